@@ -40,7 +40,7 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
-        os.path.join(CSRC, "*.h")) + [os.path.join(INCLUDE, "paged_gqa.h")]
+        os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
 def up_to_date(lib: str = LIB) -> bool:
@@ -73,7 +73,7 @@ def build(force: bool = False, verbose: bool = False, extra=(), checked: bool = 
         return obj
 
     srcs = _sources()
-    with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with ThreadPoolExecutor(max_workers=min(12, len(srcs))) as ex:
         objs = list(ex.map(compile_one, srcs))
     tmp = lib + f".tmp{os.getpid()}"
     r = subprocess.run([cc, *ARCH, "-shared", "-cudart", "static", "-Xlinker", "--exclude-libs,ALL",

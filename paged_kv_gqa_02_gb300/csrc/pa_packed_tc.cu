@@ -1,0 +1,925 @@
+// pa_packed_tc.cu -- prompt and tree attention for 16-bit Q/K/V on the
+// 5th-generation tensor cores (tcgen05 MMA, accumulators in tensor memory,
+// operands staged by TMA).  head_dim 64 or 128.
+//
+// A unit of work is 2 x 128 MMA rows of one (sequence, kv head): row tiles A
+// and B, each 128/G consecutive packed rows times the G q heads (MMA row =
+// token * G + head), against key tiles of 128.  Every K/V tile in shared
+// memory serves both row tiles and all G heads.  CTAs are persistent, one per
+// SM, and walk a list of units or, for a tree, of pieces of units:
+//   prompt: units in descending order of their key tiles, dealt out in turn;
+//           keys are the packed rows 0..t of the unit's own sequence;
+//   tree:   the CTA's share of the keys (pa_tree_plan.cuh); key tiles are the
+//           history's pages first, then the packed drafts under their mask.
+//
+// Warp roles (320 threads), joined by mbarriers; each role walks the items on
+// its own clock, so one item's loads and first products run under the last
+// one's softmax and epilogue:
+//   warps 0-3, 4-7  softmax of tile A and of tile B: a thread per MMA row
+//                   (tensor-memory lane), online softmax in base 2 whose
+//                   running max is raised only when it grows by more than
+//                   2^8, probabilities written over their scores, epilogue
+//   warp 8          finds the items, publishes them, and issues the TMA loads
+//   warp 9          owns tensor memory; issues every MMA (converged warp, one
+//                   elected lane)
+// Tensor memory (512 columns): S/P of A [0,128), of B [128,256), O of A
+// [256,256+D), O of B [256+D,256+2D).  Per key tile the MMA warp issues
+// P_A V, then A's next Q K^T once that product has read P_A (same columns),
+// then the same for B: one row tile's products run while the other's softmax
+// does.
+//
+// Probabilities enter P.V as one 16-bit value when the output is 16 bits wide
+// (each is off by half a step at most, the size of the output's own
+// rounding), and as hi + lo 16-bit parts, two products, when it is fp32.
+// Sums are taken of the fp32 probabilities.
+//
+// 0 x NaN: a masked key has probability 0, but its V may hold anything.  In a
+// key tile that is not seen whole by every row, V rows that no row sees are
+// zeroed in shared memory, and NaNs and infinities of the others too; rows
+// that do see such a value get it back in the epilogue (a rare path that
+// reads V again, and that also undoes infinity x 0 where a part of P is 0).
+#include "pa_ptx.cuh"
+#include "pa_serving.h"
+#include "pa_tc.cuh"
+#include "pa_tree_plan.cuh"
+
+#include <cudaTypedefs.h>
+
+#include <type_traits>
+
+namespace pa {
+
+namespace {
+
+constexpr int kBM = 128;  // MMA rows of a row tile
+constexpr int kBN = 128;  // keys of a tile
+constexpr int kKS = 3;    // K ring depth
+constexpr int kVS = 2;    // V ring depth
+constexpr int kIS = 2;    // items published ahead
+constexpr int kThreads = 320;
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr uint32_t kHalfBytes = kBN * 128;  // one 64-dim half of a tile
+constexpr uint64_t kWaitNs = 2000000000ull;  // a role gives up after 2 s on one barrier
+constexpr uint32_t kSleepNs = 20000;         // longest sleep inside one try_wait
+constexpr float kRescaleStep = 8.f;
+constexpr uint32_t kNegInf = 0xff800000u;
+
+struct Item {
+    TreeItem t;
+    int valid;
+};
+
+struct Bars {
+    uint64_t q_full, q_empty;
+    uint64_t k_full[kKS], k_empty[kKS], v_full[kVS], v_empty[kVS];
+    uint64_t s_full[2], p_full[2], o_done[2];  // of row tile x
+    uint64_t item_full[kIS], item_empty[kIS];
+    uint64_t mma_done, never;
+    uint32_t tmem, abort;
+    uint32_t poison[kIS];  // n + 1: item n met a NaN or infinity in a V that not every row sees
+    Item items[kIS];
+};
+
+template <int D> struct Smem {
+    static constexpr uint32_t kTileBytes = kBN * D * 2;  // one K (or V, or Q) tile
+    static constexpr uint32_t kKOff = 2 * kTileBytes;    // after Q of A and B
+    static constexpr uint32_t kVOff = kKOff + kKS * kTileBytes;
+    static constexpr uint32_t kBarOff = kVOff + kVS * kTileBytes;
+    static constexpr uint32_t kBytes = 1024 + kBarOff + sizeof(Bars);
+};
+static_assert(Smem<128>::kBytes <= 232448, "shared memory of one CTA");
+
+__device__ inline uint32_t col_s(int x) { return 128u * x; }
+template <int D> __device__ inline uint32_t col_o(int x) { return 256u + uint32_t(D) * x; }
+
+struct TcArgs {
+    PackedAttn a;
+    TreeShape shape;
+    int32_t tq, G, n_units, head_first;  // n_units: prompt, units of the longest sequence per kv head
+};
+
+__device__ inline bool wait_bar(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        if (mbar_try_wait_sleep(bar, parity, kSleepNs)) return true;
+        if (*abort_flag || globaltimer_ns() - t0 > kWaitNs) return false;
+    }
+}
+
+__device__ inline float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Pairs of fp32 in one 64-bit register pair, and their paired arithmetic.
+__device__ inline uint64_t f2_pack(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ inline void f2_unpack(uint64_t v, uint32_t& lo, uint32_t& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+}
+__device__ inline uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ inline uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ inline uint64_t f2_sub(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// The 16-bit type's packing of two fp32 (low half = first), its exact halves
+// back, and a test for NaNs and infinities: x * 0 is NaN for those alone.
+template <typename T> struct H2;
+template <> struct H2<__nv_bfloat16> {
+    __device__ static inline uint32_t pack(float a, float b) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    __device__ static inline uint64_t unpack(uint32_t h) { return f2_pack(h << 16, h & 0xffff0000u); }
+    __device__ static inline uint32_t probe(uint32_t x, uint32_t acc) {
+        const __nv_bfloat162 z = __float2bfloat162_rn(0.f);
+        const __nv_bfloat162 y = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x), z,
+                                         *reinterpret_cast<const __nv_bfloat162*>(&acc));
+        return *reinterpret_cast<const uint32_t*>(&y);
+    }
+    static constexpr uint32_t kExp = 0x7f80u;
+};
+template <> struct H2<__half> {
+    __device__ static inline uint32_t pack(float a, float b) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    __device__ static inline uint64_t unpack(uint32_t h) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        return f2_pack(__float_as_uint(f.x), __float_as_uint(f.y));
+    }
+    __device__ static inline uint32_t probe(uint32_t x, uint32_t acc) {
+        const __half2 z = __float2half2_rn(0.f);
+        const __half2 y =
+            __hfma2(*reinterpret_cast<const __half2*>(&x), z, *reinterpret_cast<const __half2*>(&acc));
+        return *reinterpret_cast<const uint32_t*>(&y);
+    }
+    static constexpr uint32_t kExp = 0x7c00u;
+};
+template <typename T> __device__ inline bool bad16(uint32_t h) { return (h & H2<T>::kExp) == H2<T>::kExp; }
+
+__device__ inline uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+__device__ inline void apply_mask(uint32_t (&r)[32], uint32_t m) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) r[k] = ((m >> k) & 1u) ? r[k] : kNegInf;
+}
+
+// Rows and key tiles of the two row tiles of an item.
+struct Shape2 {
+    int rows[2], tiles[2];
+};
+template <bool kTree> __device__ inline Shape2 shape2(const TreeItem& t, int tq) {
+    Shape2 s;
+    s.rows[0] = min(tq, t.n_rows);
+    s.rows[1] = t.n_rows - s.rows[0];
+    if (kTree) {
+        s.tiles[0] = t.b1 - t.b0;
+        s.tiles[1] = s.rows[1] > 0 ? s.tiles[0] : 0;
+    } else {  // causal: tile B may see one key tile more
+        s.tiles[0] = (t.t0 + s.rows[0] + kBN - 1) / kBN;
+        s.tiles[1] = s.rows[1] > 0 ? (t.t0 + tq + s.rows[1] + kBN - 1) / kBN : 0;
+    }
+    return s;
+}
+
+// The prompt's units in descending order of key tiles: unit i is
+// (tile pair from the last, sequence, kv head); those that their sequence
+// does not have are passed over.  CTA c takes i = c, 2n-1-c, 2n+c, ... of the
+// n CTAs, so that none gets the longer unit of every round.
+struct PromptWalk {
+    int64_t round;
+    __device__ inline bool next(const TcArgs& p, TreeItem& it, uint32_t* status) {
+        const PackedAttn& a = p.a;
+        const int64_t per = int64_t(a.Hkv) * a.r.num_seqs, all = per * p.n_units;
+        for (;; ++round) {
+            const int64_t i = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            if (round * gridDim.x >= all) return false;
+            if (i >= all) continue;
+            const int level = p.n_units - 1 - int(i / per), u = int(i % per);
+            it.g = u % a.Hkv;
+            it.seq = u / a.Hkv;
+            const int r0 = a.r.cu_lens[it.seq], r1 = a.r.cu_lens[it.seq + 1];
+            if (r0 < 0 || r1 < r0 || r1 > a.r.total_rows || r1 - r0 > a.r.max_rows) {
+                if (level == 0 && (threadIdx.x & 31) == 0) flag(status, PA_DEV_BAD_LEN);
+                continue;
+            }
+            it.T = r1 - r0;
+            it.t0 = level * 2 * p.tq;
+            if (it.t0 >= it.T) continue;
+            it.n_rows = min(2 * p.tq, it.T - it.t0);
+            it.row0 = r0 + it.t0;
+            it.L = it.nh = it.b0 = 0;
+            it.b1 = (it.t0 + it.n_rows + kBN - 1) / kBN;
+            it.slot = -1;
+            it.bad_len = false;
+            ++round;
+            return true;
+        }
+    }
+};
+
+template <typename T, int D, bool kTree, typename TOut>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKc,
+              const __grid_constant__ CUtensorMap tmVc, const __grid_constant__ TcArgs p) {
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr bool kSplit = std::is_same<TOut, float>::value;
+    constexpr int kHalves = D / 64;  // 64-dim (128-byte) halves of a row
+    constexpr uint32_t kTileBytes = Smem<D>::kTileBytes;
+    const PackedAttn& a = p.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = p.G, tq = p.tq;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* base =
+        reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sQ = base;
+    Bars& B = *reinterpret_cast<Bars*>(base + Smem<D>::kBarOff);
+    volatile uint32_t* abort_flag = &B.abort;
+    auto k_tile = [&](int st) { return base + Smem<D>::kKOff + st * kTileBytes; };
+    auto v_tile = [&](int st) { return base + Smem<D>::kVOff + st * kTileBytes; };
+
+    if (tid == 0) {
+        mbar_init(&B.q_full, 1);
+        mbar_init(&B.q_empty, 1);
+        for (int i = 0; i < kKS; ++i) {
+            mbar_init(&B.k_full[i], 1);
+            mbar_init(&B.k_empty[i], 1);
+        }
+        for (int i = 0; i < kVS; ++i) {
+            mbar_init(&B.v_full[i], 1);
+            mbar_init(&B.v_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&B.s_full[i], 1);
+            mbar_init(&B.p_full[i], 4);
+            mbar_init(&B.o_done[i], 1);
+        }
+        for (int i = 0; i < kIS; ++i) {
+            mbar_init(&B.item_full[i], 1);
+            mbar_init(&B.item_empty[i], 9);  // 8 softmax warps and the MMA warp
+            B.poison[i] = 0;
+        }
+        mbar_init(&B.mma_done, 1);
+        mbar_init(&B.never, 1);
+        B.abort = 0;
+        mbar_fence_init();
+    }
+    if (warp == kMmaWarp) {
+        tc::tmem_alloc(&B.tmem, 512);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tm = B.tmem;
+    pdl_wait_primary();
+    pdl_launch_dependents();  // after the wait: the join reads the lengths before its own
+    if (a.debug_timeout) {
+        // Testing: a wait that runs out before any copy is issued (a barrier
+        // nothing targets, no time allowed) aborts every role of the CTA.
+        if (tid == 0 && !mbar_wait_ns(&B.never, 0, 0)) {
+            *abort_flag = 1u;
+            flag(a.dev_status, PA_DEV_TIMEOUT);
+        }
+        __syncthreads();
+    }
+    auto give_up = [&]() {
+        *abort_flag = 1u;
+        flag(a.dev_status, PA_DEV_TIMEOUT);
+    };
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag));
+    };
+
+    if (warp == kProducerWarp) {
+        // ================================ producer ================================
+        if (lane == 0) {
+            tma_prefetch_desc(&tmQ);
+            tma_prefetch_desc(&tmK);
+            tma_prefetch_desc(&tmV);
+            if (kTree) {
+                tma_prefetch_desc(&tmKc);
+                tma_prefetch_desc(&tmVc);
+            }
+        }
+        TreeWalk walk;
+        PromptWalk prompt = {0};
+        if constexpr (kTree) {
+            if (blockIdx.x == 0)
+                for (int s = lane; s < p.shape.num_seqs; s += 32) {
+                    const TreeSeq q = tree_seq(p.shape, s);
+                    if (q.bad_rows || q.bad_len) flag(a.dev_status, PA_DEV_BAD_LEN);
+                }
+            walk.start(p.shape, blockIdx.x);
+        }
+        const int P = a.c.page_size;
+        const int xc_first = p.head_first;
+        int kq = 0, vq = 0, qn = 0;  // K tiles, V tiles and Qs issued
+        bool ok = !*abort_flag;
+        for (int n = 0; ok; ++n) {
+            Item it;
+            if constexpr (kTree)
+                it.valid = walk.next(p.shape, it.t);
+            else
+                it.valid = prompt.next(p, it.t, a.dev_status);
+            const int is = n % kIS;
+            if (n >= kIS) ok = wait_all(&B.item_empty[is], ((n / kIS) - 1) & 1);
+            if (!ok) break;
+            if (lane == 0) {
+                B.items[is] = it;
+                mbar_arrive(&B.item_full[is]);
+            }
+            if (!it.valid) break;
+            const TreeItem& t = it.t;
+            const Shape2 sh = shape2<kTree>(t, tq);
+            const int nt = max(sh.tiles[0], sh.tiles[1]);
+            const int32_t* table = kTree ? a.c.block_tables + int64_t(t.seq) * a.c.max_blocks : nullptr;
+            const int PT = kTree ? kBN / P : 0;
+            const int npg = kTree ? (t.L + P - 1) / P : 0;
+            for (int j = 0; j < nt; ++j) {
+                const int blk = t.b0 + j;
+                const bool hist = kTree && blk < t.nh;
+                int pg = a.c.num_pages;  // beyond the tensor: the box reads as zeros
+                if (hist) {
+                    const int idx = blk * PT + lane;
+                    if (lane < PT && idx < npg) {
+                        const int e = table[idx];
+                        if (e >= 0 && e < a.c.num_pages)
+                            pg = e;
+                        else
+                            flag(a.dev_status, PA_DEV_BAD_PAGE);
+                    }
+                }
+                const int prow = t.row0 - t.t0 + (blk - t.nh) * kBN;  // packed row of the tile's first key
+                auto load = [&](uint8_t* dst, const CUtensorMap* packed, const CUtensorMap* paged, uint64_t* bar) {
+                    if (lane == 0) mbar_arrive_expect_tx(bar, kTileBytes);  // zero-filled boxes count whole
+                    __syncwarp();
+                    if (hist) {
+                        if (lane < PT)
+#pragma unroll
+                            for (int hh = 0; hh < kHalves; ++hh)
+                                tma_load_4d(dst + hh * kHalfBytes + lane * P * 128, paged, bar, 64 * hh,
+                                            xc_first ? t.g : 0, xc_first ? 0 : t.g, pg);
+                    } else if (lane < kHalves) {
+                        tma_load_3d(dst + lane * kHalfBytes, packed, bar, 64 * lane, t.g, prow);
+                    }
+                };
+                const int sk = kq % kKS, sv = vq % kVS;
+                if (kq >= kKS) ok = wait_all(&B.k_empty[sk], ((kq / kKS) - 1) & 1);
+                if (!ok) break;
+                load(k_tile(sk), &tmK, &tmKc, &B.k_full[sk]);
+                ++kq;
+                if (j == 0) {
+                    // Q, after the item's first K tile: the last item's products may still read its place
+                    if (n > 0) ok = wait_all(&B.q_empty, (n - 1) & 1);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        const uint32_t qbytes = uint32_t(kHalves) * 128u * uint32_t(G * tq);
+                        mbar_arrive_expect_tx(&B.q_full, sh.rows[1] > 0 ? 2 * qbytes : qbytes);
+                        for (int x = 0; x < (sh.rows[1] > 0 ? 2 : 1); ++x)
+                            for (int hh = 0; hh < kHalves; ++hh)
+                                tma_load_3d(sQ + x * kTileBytes + hh * kHalfBytes, &tmQ, &B.q_full, 64 * hh,
+                                            t.g * G, t.row0 + x * tq);
+                    }
+                    ++qn;
+                }
+                if (vq >= kVS) ok = wait_all(&B.v_empty[sv], ((vq / kVS) - 1) & 1);
+                if (!ok) break;
+                load(v_tile(sv), &tmV, &tmVc, &B.v_full[sv]);
+                ++vq;
+            }
+        }
+        if (lane == 0) {
+            if (!ok) give_up();
+            // never leave the CTA with copies in flight
+            for (int j = max(0, kq - kKS); j < kq; ++j) mbar_wait_ns(&B.k_full[j % kKS], (j / kKS) & 1, kWaitNs);
+            for (int j = max(0, vq - kVS); j < vq; ++j) mbar_wait_ns(&B.v_full[j % kVS], (j / kVS) & 1, kWaitNs);
+            if (qn > 0 && !mbar_wait_ns(&B.q_full, (qn - 1) & 1, kWaitNs)) flag(a.dev_status, PA_DEV_TIMEOUT);
+        }
+    } else if (warp == kMmaWarp) {
+        // ================================== MMA ===================================
+        const uint32_t idQK = tc::idesc_f16(kBM, kBN, kBf16, false);
+        const uint32_t idPV = tc::idesc_f16(kBM, D, kBf16, true);
+        // descriptors: the high word is shared, low words advance by offset >> 4
+        const uint32_t hi_d = tc::desc_hi_sw128(1024);
+        const uint32_t q_lo = tc::desc_lo(smem_u32(sQ), 16);
+        const uint32_t k_lo = tc::desc_lo(smem_u32(k_tile(0)), 16);
+        const uint32_t v_lo = tc::desc_lo(smem_u32(v_tile(0)), kHalfBytes);
+        // S_x = Q_x K^T of K tile number kt
+        auto qk = [&](int x, int kt) {
+            const uint32_t qx = q_lo + x * (kTileBytes >> 4);
+            const uint32_t kx = k_lo + (kt % kKS) * (kTileBytes >> 4);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t off = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
+                tc::mma_ss_elect(tm + col_s(x), tc::make_desc(qx + off, hi_d), tc::make_desc(kx + off, hi_d), idQK,
+                                 ks > 0);
+            }
+            tc::commit_elect(&B.s_full[x]);
+        };
+        // O_x (+)= P_x V of V tile number vt; P of 16 keys is 8 columns, 32 keys
+        // take 16 (kSplit: 32, hi then lo)
+        auto pv = [&](int x, int vt, bool first) {
+            const uint32_t vx = v_lo + (vt % kVS) * (kTileBytes >> 4);
+            const uint32_t p_col = tm + col_s(x), o_col = tm + col_o<D>(x);
+#pragma unroll
+            for (int ks = 0; ks < kBN / 16; ++ks) {
+                const uint64_t bd = tc::make_desc(vx + ks * (2048 >> 4), hi_d);
+                if constexpr (kSplit) {
+                    const uint32_t col = p_col + 32 * (ks >> 1) + 8 * (ks & 1);
+                    tc::mma_ts_elect(o_col, col, bd, idPV, !first || ks > 0);
+                    tc::mma_ts_elect(o_col, col + 16, bd, idPV, true);
+                } else {
+                    tc::mma_ts_elect(o_col, p_col + 8 * ks, bd, idPV, !first || ks > 0);
+                }
+            }
+            tc::commit_elect(&B.o_done[x]);
+        };
+        int kt = 0, vt = 0;       // K and V tiles used
+        int sc[2] = {0, 0};       // score tiles of x issued; P.V number sc - 1 waits for them
+        bool ok = true;
+        for (int n = 0;; ++n) {
+            const int is = n % kIS;
+            ok = wait_all(&B.item_full[is], (n / kIS) & 1);
+            if (!ok) break;
+            const int valid = B.items[is].valid;
+            const Shape2 sh = shape2<kTree>(B.items[is].t, tq);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.item_empty[is]);
+            if (!valid) break;
+            const int nt = max(sh.tiles[0], sh.tiles[1]);
+            const int xl = sh.tiles[1] > 0 ? 1 : 0;  // the row tile served last
+            ok = wait_all(&B.q_full, n & 1) && wait_all(&B.k_full[kt % kKS], (kt / kKS) & 1);
+            for (int x = 0; ok && x <= xl; ++x) {
+                // P_x of the last item has been read
+                if (sc[x] > 0) ok = wait_all(&B.o_done[x], (sc[x] - 1) & 1);
+                if (!ok) break;
+                tc::fence_after_sync();
+                qk(x, kt);
+                ++sc[x];
+            }
+            if (!ok) break;
+            tc::commit_elect(&B.k_empty[kt % kKS]);
+            ++kt;
+            if (nt == 1) tc::commit_elect(&B.q_empty);
+            for (int j = 0; ok && j < nt; ++j) {
+                bool k_waited = false, v_waited = false;
+                for (int x = 0; ok && x <= xl; ++x) {
+                    if (j >= sh.tiles[x]) continue;
+                    ok = wait_all(&B.p_full[x], (sc[x] - 1) & 1);
+                    if (ok && !v_waited) ok = wait_all(&B.v_full[vt % kVS], (vt / kVS) & 1);
+                    if (!ok) break;
+                    v_waited = true;
+                    tc::fence_after_sync();
+                    pv(x, vt, j == 0);
+                    if (x == xl) tc::commit_elect(&B.v_empty[vt % kVS]);
+                    if (j + 1 < sh.tiles[x]) {
+                        if (!k_waited) ok = wait_all(&B.k_full[kt % kKS], (kt / kKS) & 1);
+                        if (ok) ok = wait_all(&B.o_done[x], (sc[x] - 1) & 1);
+                        if (!ok) break;
+                        k_waited = true;
+                        tc::fence_after_sync();
+                        qk(x, kt);
+                        ++sc[x];
+                        if (x == xl) tc::commit_elect(&B.k_empty[kt % kKS]);
+                    }
+                }
+                ++vt;
+                if (j + 1 < nt) ++kt;
+                if (ok && j + 2 == nt) tc::commit_elect(&B.q_empty);
+            }
+            if (!ok) break;
+        }
+        if (!ok && lane == 0) give_up();
+        // every MMA issued so far has finished before tensor memory is freed
+        tc::commit_elect(&B.mma_done);
+        if (!__all_sync(0xffffffffu, mbar_wait_ns(&B.mma_done, 0, kWaitNs)) && lane == 0)
+            flag(a.dev_status, PA_DEV_TIMEOUT);
+    } else {
+        // ================================= softmax =================================
+        const int x = warp >> 2;  // row tile
+        const int quad = warp & 3;
+        const int m = quad * 32 + lane;  // MMA row = tensor-memory lane
+        const uint32_t lane_addr = uint32_t(quad * 32) << 16;
+        const int tr = m / G, h = m - tr * G;
+        const float sl2 = a.scale_log2;
+        const uint32_t sbase = tm + lane_addr + col_s(x);
+        const uint32_t obase = tm + lane_addr + col_o<D>(x);
+        int sc = 0;  // score tiles taken
+        int vt = 0;  // V tiles passed
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            const int is = n % kIS;
+            ok = wait_all(&B.item_full[is], (n / kIS) & 1);
+            if (!ok) break;
+            const TreeItem t = B.items[is].t;
+            if (!B.items[is].valid) break;
+            const Shape2 sh = shape2<kTree>(t, tq);
+            const int nt = sh.tiles[x], nt_all = max(sh.tiles[0], sh.tiles[1]);
+            const bool row_ok = tr < tq && tr < sh.rows[x];
+            const int tt = t.t0 + x * tq + tr;  // the row's place in its sequence
+            const int row = t.row0 + x * tq + tr;
+            const int P = a.c.page_size;
+            const int32_t* table = kTree ? a.c.block_tables + int64_t(t.seq) * a.c.max_blocks : nullptr;
+            const int PT = kTree ? kBN / P : 0;
+            const int npg = kTree ? (t.L + P - 1) / P : 0;
+            // table entry of page `lane` of a history tile (0, a page inside the pool, past its pages)
+            auto entry = [&](int blk) -> int {
+                const int idx = blk * PT + lane;
+                return kTree && blk < t.nh && lane < PT && idx < npg ? __ldg(table + idx) : 0;
+            };
+            // packed keys that some row of the item sees
+            const int p_end = kTree ? t.T : t.t0 + t.n_rows;
+            float m_run = -INFINITY, l_run = 0.f;
+            int e_cur = entry(t.b0);
+            for (int j = 0; j < nt; ++j) {
+                const int blk = t.b0 + j;
+                const bool hist = kTree && blk < t.nh;
+                const int k0 = (blk - (hist ? 0 : t.nh)) * kBN;  // first key, of the history or the packed rows
+                const int e_nxt = kTree && j + 1 < nt ? entry(blk + 1) : 0;
+                uint32_t see[4];  // keys of this tile that the row sees
+                bool full = false;
+                if (hist) {
+                    const uint32_t pmask = __ballot_sync(0xffffffffu, e_cur >= 0 && e_cur < a.c.num_pages);
+                    full = k0 + kBN <= t.L && pmask == 0xffffffffu;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        see[c] = low_bits(t.L - k0 - 32 * c);
+                        if (P == 32)
+                            see[c] &= (pmask >> c) & 1u ? 0xffffffffu : 0u;
+                        else
+                            see[c] &= ((pmask >> (2 * c)) & 1u ? 0x0000ffffu : 0u) |
+                                      ((pmask >> (2 * c + 1)) & 1u ? 0xffff0000u : 0u);
+                    }
+                } else if constexpr (kTree) {
+                    const uint32_t* words = a.tree_mask + int64_t(row) * a.mask_words + (k0 >> 5);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        see[c] = row_ok && !t.bad_len && (k0 >> 5) + c < a.mask_words
+                                     ? __ldg(words + c) & low_bits(t.T - k0 - 32 * c)
+                                     : 0u;
+                } else {
+                    const int lim = row_ok ? tt + 1 - k0 : 0;
+                    full = lim >= kBN;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) see[c] = low_bits(lim - 32 * c);
+                }
+                e_cur = e_nxt;
+                ok = wait_all(&B.s_full[x], sc & 1);
+                if (!ok) break;
+                ++sc;
+                tc::fence_after_sync();
+
+                // ---- pass 1: row max of the raw scores (scale > 0 keeps the order)
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t r[32];
+                    tc::ld_32x32b_x32(sbase + 32 * c, r);
+                    tc::wait_ld();
+                    tc::reg_fence(r);
+                    if (!full) apply_mask(r, c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3]);
+                    float m0 = mx, m1 = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        m0 = max3(m0, __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+                        m1 = max3(m1, __uint_as_float(r[k + 2]), __uint_as_float(r[k + 3]));
+                    }
+                    mx = fmaxf(m0, m1);
+                }
+                const float mt = mx * sl2;  // -inf when nothing is visible
+                const bool need = mt > m_run + kRescaleStep;
+                const float alpha = need ? ex2(m_run - mt) : 1.f;
+                if (need) m_run = mt;
+                l_run *= alpha;
+
+                // O_x is rescaled in place: the last P_x V has finished (S_x was
+                // issued after it)
+                if (j > 0 && __any_sync(0xffffffffu, need)) {
+#pragma unroll 1
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t ro[16];
+                        tc::ld_32x32b_x16(obase + 16 * c, ro);
+                        tc::wait_ld();
+                        tc::reg_fence(ro);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) ro[k] = __float_as_uint(__uint_as_float(ro[k]) * alpha);
+                        tc::st_32x32b_x16(obase + 16 * c, ro);
+                    }
+                }
+
+                // ---- pass 2: p = 2^(s * scale_log2 - m_run) over the scores
+                const float nmu = m_run == -INFINITY ? 0.f : -m_run;
+                const uint64_t sl2_2 = f2_pack(__float_as_uint(sl2), __float_as_uint(sl2));
+                const uint64_t nmu_2 = f2_pack(__float_as_uint(nmu), __float_as_uint(nmu));
+                uint64_t sum_2 = f2_pack(0u, 0u);
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t r[32];
+                    tc::ld_32x32b_x32(sbase + 32 * c, r);
+                    tc::wait_ld();
+                    tc::reg_fence(r);
+                    if (!full) apply_mask(r, c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3]);
+#pragma unroll
+                    for (int w = 0; w < 16; ++w) {
+                        uint32_t z0, z1;
+                        f2_unpack(f2_fma(f2_pack(r[2 * w], r[2 * w + 1]), sl2_2, nmu_2), z0, z1);
+                        const float p0 = ex2(__uint_as_float(z0)), p1 = ex2(__uint_as_float(z1));
+                        const uint64_t pp = f2_pack(__float_as_uint(p0), __float_as_uint(p1));
+                        sum_2 = f2_add(sum_2, pp);
+                        r[2 * w] = H2<T>::pack(p0, p1);
+                        if constexpr (kSplit) {
+                            uint32_t d0, d1;
+                            f2_unpack(f2_sub(pp, H2<T>::unpack(r[2 * w])), d0, d1);
+                            r[2 * w + 1] = H2<T>::pack(__uint_as_float(d0), __uint_as_float(d1));
+                        }
+                    }
+                    if constexpr (kSplit) {
+                        tc::st_32x32b_x16_stride2<0>(sbase + 32 * c, r);
+                        tc::st_32x32b_x16_stride2<1>(sbase + 32 * c + 16, r);
+                    } else {
+                        tc::st_32x32b_x16_stride2<0>(sbase + 16 * c, r);
+                    }
+                }
+                uint32_t sum0, sum1;
+                f2_unpack(sum_2, sum0, sum1);
+                l_run += __uint_as_float(sum0) + __uint_as_float(sum1);
+                tc::wait_st();
+
+                // ---- V rows that not every row sees: once per key tile, by tile A's
+                // warps (by tile B's in the tile that B alone has), before their
+                // P is handed over; the MMA warp takes B's product after A's.
+                const int v_end = hist ? t.L : p_end;  // keys some row sees
+                const bool mixed = kTree ? !hist : k0 + kBN > t.t0 + 1;
+                if ((x == 0 || j >= sh.tiles[0]) && (mixed || k0 + kBN > v_end)) {
+                    const int sv = (vt + j) % kVS;
+                    ok = wait_all(&B.v_full[sv], ((vt + j) / kVS) & 1);
+                    if (!ok) break;
+                    uint8_t* vrow = v_tile(sv) + m * 128;  // a key's row, 64 dims at a time
+                    bool touched = false;
+                    if (k0 + m >= v_end) {
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c)
+                            *reinterpret_cast<uint4*>(vrow + (c >> 3) * kHalfBytes + ((c + lane) & 7) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                        touched = true;
+                    } else if (mixed) {
+                        uint32_t acc = 0u;
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c) {
+                            const uint4 w = *reinterpret_cast<const uint4*>(vrow + (c >> 3) * kHalfBytes +
+                                                                            ((c + lane) & 7) * 16);
+                            acc = H2<T>::probe(w.x, H2<T>::probe(w.y, H2<T>::probe(w.z, H2<T>::probe(w.w, acc))));
+                        }
+                        if (bad16<T>(acc) || bad16<T>(acc >> 16)) {
+                            for (int c = 0; c < D / 2; ++c) {
+                                uint32_t* w = reinterpret_cast<uint32_t*>(vrow + (c >> 5) * kHalfBytes) + (c & 31);
+                                uint32_t y = *w;
+                                if (bad16<T>(y)) y &= 0xffff0000u;
+                                if (bad16<T>(y >> 16)) y &= 0x0000ffffu;
+                                *w = y;
+                            }
+                            B.poison[is] = uint32_t(n) + 1u;
+                            touched = true;
+                        }
+                    }
+                    if (touched) fence_proxy_async_smem();
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B.p_full[x]);
+            }
+            if (!ok) break;
+            vt += nt_all;
+
+            // Puts right 32 dims of a row that sees a NaN or infinity in V: one
+            // that was kept out of P.V, or that met a zero part of P there.  What
+            // the row sees of them is the result, whatever the rest adds up to.
+            auto restore = [&](uint32_t (&r)[32], const TreeItem& it, int at, int place, int d0) {
+                float f[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) f[k] = 0.f;
+                auto add = [&](const T* v) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const float y = Elt<T>::f(v[k]);
+                        if (!isfinite(y)) f[k] += y;
+                    }
+                };
+                for (int key = it.b0 * kBN; kTree && key < min(it.L, min(it.b1, it.nh) * kBN); ++key) {
+                    const int pg = table[key / P];
+                    if (pg >= 0 && pg < a.c.num_pages)
+                        add(static_cast<const T*>(a.c.v) + int64_t(pg) * a.c.page_stride +
+                            int64_t(key % P) * a.c.token_stride + int64_t(it.g) * a.c.head_stride + d0);
+                }
+                const int k_lo = max(0, it.b0 - it.nh) * kBN;
+                const int k_hi = kTree ? min(it.T, max(0, it.b1 - it.nh) * kBN) : place + 1;
+                for (int key = k_lo; key < k_hi; ++key) {
+                    if (kTree && ((key >> 5) >= a.mask_words ||
+                                  !((a.tree_mask[int64_t(at) * a.mask_words + (key >> 5)] >> (key & 31)) & 1u)))
+                        continue;
+                    add(static_cast<const T*>(a.v) + int64_t(it.row0 - it.t0 + key) * a.r.v_stride + it.g * D + d0);
+                }
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    if (!isfinite(f[k])) r[k] = __float_as_uint(f[k]);
+            };
+
+            // ---- epilogue: O / l, or the piece's max, sum and O into its slot --------
+            if (nt > 0) {
+                ok = wait_all(&B.o_done[x], (sc - 1) & 1);
+                if (!ok) break;
+                tc::fence_after_sync();
+                const bool poison = *reinterpret_cast<volatile uint32_t*>(&B.poison[is]) == uint32_t(n) + 1u;
+                const bool piece = kTree && t.slot >= 0;
+                const float inv = piece ? 1.f : l_run == 0.f ? 0.f : 1.f / l_run;
+                const int r_unit = (x * tq + tr) * G + h;  // distribution of the unit
+                float* slot = piece ? static_cast<float*>(a.workspace) + slot_floats(2 * kBM, D) * t.slot : nullptr;
+                TOut* orow = static_cast<TOut*>(a.out) + (int64_t(row) * a.Hq + t.g * G + h) * D;
+                if (piece && row_ok) *reinterpret_cast<float2*>(slot + 2 * r_unit) = make_float2(m_run, l_run);
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t r[32];
+                    __syncwarp();  // the last round's rows may have parted
+                    tc::ld_32x32b_x32(obase + 32 * c, r);
+                    tc::wait_ld();
+                    tc::reg_fence(r);
+                    // x * 0 is NaN for NaNs and infinities alone
+                    float z = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) z = fmaf(__uint_as_float(r[k]), 0.f, z);
+                    if (row_ok && l_run == l_run && (poison || z != z)) restore(r, t, row, tt, 32 * c);
+                    if (!row_ok) continue;
+                    if (piece) {
+                        float4* dst = reinterpret_cast<float4*>(slot + 4 * kBM + int64_t(r_unit) * D + 32 * c);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            dst[k] = make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]),
+                                                 __uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3]));
+                    } else if constexpr (kSplit) {
+                        float4* dst = reinterpret_cast<float4*>(orow + 32 * c);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            dst[k] = make_float4(__uint_as_float(r[4 * k]) * inv, __uint_as_float(r[4 * k + 1]) * inv,
+                                                 __uint_as_float(r[4 * k + 2]) * inv,
+                                                 __uint_as_float(r[4 * k + 3]) * inv);
+                    } else {
+                        uint4* dst = reinterpret_cast<uint4*>(orow + 32 * c);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t y[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                y[e] = H2<T>::pack(__uint_as_float(r[8 * k + 2 * e]) * inv,
+                                                   __uint_as_float(r[8 * k + 2 * e + 1]) * inv);
+                            dst[k] = make_uint4(y[0], y[1], y[2], y[3]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.item_empty[is]);
+        }
+        if (!ok) give_up();
+    }
+
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tm, 512);
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    if (!fn) {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }
+    return fn;
+}
+
+bool encode(CUtensorMap* m, pa_dtype dt, int rank, const void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return enc && enc(m, dt == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                      const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Packed rows as (head_dim, head, row); the box is 64 dims x heads x rows.
+bool encode_rows(CUtensorMap* m, const PackedAttn& a, const void* ptr, int heads, int64_t stride, int box_heads,
+                 int box_rows) {
+    const cuuint64_t dims[3] = {cuuint64_t(a.D), cuuint64_t(heads), cuuint64_t(a.r.total_rows)};
+    const cuuint64_t strides[2] = {cuuint64_t(a.D) * 2, cuuint64_t(stride) * 2};
+    const cuuint32_t box[3] = {64, cuuint32_t(box_heads), cuuint32_t(box_rows)};
+    return encode(m, a.dtype, 3, ptr, dims, strides, box);
+}
+
+// The pool as (head_dim, kv head, slot, page), the middle two in stride order;
+// the box is one page of one kv head, 64 dims at a time.
+bool encode_pages(CUtensorMap* m, const PackedAttn& a, const void* ptr, bool head_first) {
+    const CacheArgs& c = a.c;
+    const cuuint64_t hs = cuuint64_t(c.head_stride) * 2, ts = cuuint64_t(c.token_stride) * 2;
+    const cuuint64_t nh = cuuint64_t(a.Hkv), P = cuuint64_t(c.page_size);
+    const cuuint64_t dims[4] = {cuuint64_t(a.D), head_first ? nh : P, head_first ? P : nh, cuuint64_t(c.num_pages)};
+    const cuuint64_t strides[3] = {head_first ? hs : ts, head_first ? ts : hs, cuuint64_t(c.page_stride) * 2};
+    const cuuint32_t box[4] = {64, head_first ? 1u : cuuint32_t(P), head_first ? cuuint32_t(P) : 1u, 1};
+    return encode(m, a.dtype, 4, ptr, dims, strides, box);
+}
+
+template <typename T, int D, bool kTree, typename TOut>
+cudaError_t launch_typed(const PackedAttn& a, cudaStream_t st) {
+    auto kern = packed_tc<T, D, kTree, TOut>;
+    static bool configured = false;  // benign race: every caller sets the same value
+    if (!configured) {
+        cudaError_t e =
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Smem<D>::kBytes));
+        if (e != cudaSuccess) return e;
+        configured = true;
+    }
+    TcArgs p = {};
+    p.a = a;
+    p.G = a.Hq / a.Hkv;
+    p.tq = kBM / p.G;
+    CUtensorMap mq, mk, mv, mkc, mvc;
+    if (!encode_rows(&mq, a, a.q, a.Hq, a.r.q_stride, p.G, p.tq) ||
+        !encode_rows(&mk, a, a.k, a.Hkv, a.r.k_stride, 1, kBN) ||
+        !encode_rows(&mv, a, a.v, a.Hkv, a.r.v_stride, 1, kBN))
+        return cudaErrorInvalidValue;
+    mkc = mk;
+    mvc = mv;
+    int64_t ctas;
+    if (kTree) {
+        p.head_first = a.c.head_stride <= a.c.token_stride;
+        if (!encode_pages(&mkc, a, a.c.k, p.head_first) || !encode_pages(&mvc, a, a.c.v, p.head_first))
+            return cudaErrorInvalidValue;
+        TreeShape& s = p.shape;
+        s.cu_lens = a.r.cu_lens;
+        s.context_lens = a.c.context_lens;
+        s.num_seqs = a.r.num_seqs;
+        s.total_rows = a.r.total_rows;
+        s.max_rows = a.r.max_rows;
+        s.Hkv = a.Hkv;
+        s.tu = 2 * p.tq;
+        s.kb = kBN;
+        s.n_ctas = a.n_ctas;
+        s.cap = int64_t(a.c.max_blocks) * a.c.page_size;
+        ctas = a.n_ctas;
+    } else {
+        p.n_units = (a.r.max_rows + 2 * p.tq - 1) / (2 * p.tq);
+        ctas = int64_t(p.n_units) * a.Hkv * a.r.num_seqs;
+        if (ctas > a.n_ctas) ctas = a.n_ctas;
+    }
+    cudaError_t e = launch_pdl(kern, dim3(unsigned(ctas)), dim3(kThreads), Smem<D>::kBytes, st, mq, mk, mv, mkc, mvc, p);
+    if (e != cudaSuccess || !kTree) return e;
+    return launch_pdl(tree_join<TOut, D>, dim3(a.r.total_rows, (a.Hq + kJoinWarps - 1) / kJoinWarps),
+                      dim3(kJoinWarps * 32), 0, st, p.shape, static_cast<const float*>(a.workspace),
+                      static_cast<TOut*>(a.out), a.Hq, 2 * kBM);
+}
+
+template <typename T, int D> cudaError_t launch_out(const PackedAttn& a, cudaStream_t st) {
+    if (a.out_dtype == PA_F32)
+        return a.tree_mask ? launch_typed<T, D, true, float>(a, st) : launch_typed<T, D, false, float>(a, st);
+    return a.tree_mask ? launch_typed<T, D, true, T>(a, st) : launch_typed<T, D, false, T>(a, st);
+}
+
+}  // namespace
+
+size_t tree_tc_workspace_bytes(int D, int n_ctas) {
+    return (2 * size_t(n_ctas) * slot_floats(2 * kBM, D) * sizeof(float) + 255) & ~size_t(255);
+}
+
+cudaError_t launch_packed_tc(const PackedAttn& a, cudaStream_t st) {
+    if (a.dtype == PA_BF16)
+        return a.D == 64 ? launch_out<__nv_bfloat16, 64>(a, st) : launch_out<__nv_bfloat16, 128>(a, st);
+    return a.D == 64 ? launch_out<__half, 64>(a, st) : launch_out<__half, 128>(a, st);
+}
+
+}  // namespace pa

@@ -1,0 +1,258 @@
+// pa_tree_plan.cuh -- how a tree call's work is shared out, and the join of
+// the pieces.
+//
+// A unit is (sequence, kv head, tile of `tu` drafts); its keys come in blocks
+// of `kb`, first the history's, then the drafts' own.  Units are laid end to
+// end, sequence by sequence and kv head by kv head, each as 1 + blocks
+// positions, and the line is cut into n equal shares, one for each CTA.  A
+// unit inside one share is finished there; the pieces of the others are left
+// in slots and joined in ascending CTA order.  A CTA leaves at most two
+// pieces: one of a unit that began before its share (slot 2c) and one of a
+// unit that begins in it (slot 2c + 1).
+// The partition depends on the lengths and n alone, so results repeat bit for
+// bit, and on the device only through n.
+#pragma once
+
+#include "pa_ptx.cuh"
+#include "pa_serving.h"
+
+namespace pa {
+
+namespace {  // each kernel's file has its own copy of the join
+
+constexpr int kMinShare = 2;  // positions of a share: one block and its unit's start
+
+struct TreeShape {
+    const int32_t* cu_lens;
+    const int32_t* context_lens;
+    int32_t num_seqs, total_rows, max_rows, Hkv, tu, kb, n_ctas;
+    int64_t cap;  // tokens a block table holds
+};
+
+struct TreeSeq {
+    int row0, T, L;  // T = 0: no rows, or rows that the call refuses; L = 0 with a bad length
+    bool bad_rows, bad_len;
+    int units, nh, nd, cost;  // tiles of a kv head; blocks of history and of drafts; positions of a unit
+};
+
+__device__ inline TreeSeq tree_seq(const TreeShape& a, int s) {
+    TreeSeq q;
+    const int r0 = a.cu_lens[s], r1 = a.cu_lens[s + 1];
+    q.row0 = r0;
+    q.L = a.context_lens[s];
+    q.bad_rows = r0 < 0 || r1 < r0 || r1 > a.total_rows || r1 - r0 > a.max_rows;
+    q.T = q.bad_rows ? 0 : r1 - r0;
+    q.bad_len = q.L < 0 || q.L > a.cap;
+    if (q.bad_len) q.L = 0;
+    q.units = (q.T + a.tu - 1) / a.tu;
+    q.nh = (q.L + a.kb - 1) / a.kb;
+    q.nd = (q.T + a.kb - 1) / a.kb;
+    q.cost = q.T > 0 ? 1 + q.nh + q.nd : 0;
+    return q;
+}
+
+__device__ inline int64_t tree_seq_cost(const TreeShape& a, const TreeSeq& q) {
+    return int64_t(a.Hkv) * q.units * q.cost;
+}
+
+__device__ inline int64_t warp_sum64(int64_t v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Positions of all sequences; with `before`, also of those ahead of sequence
+// s.  The whole warp.
+__device__ inline int64_t tree_total(const TreeShape& a, int s, int64_t* before) {
+    int64_t all = 0, ahead = 0;
+    for (int i = threadIdx.x & 31; i < a.num_seqs; i += 32) {
+        const int64_t c = tree_seq_cost(a, tree_seq(a, i));
+        all += c;
+        if (i < s) ahead += c;
+    }
+    if (before) *before = warp_sum64(ahead);
+    return warp_sum64(all);
+}
+
+// CTAs that take part.
+__device__ inline int tree_ctas(const TreeShape& a, int64_t total) {
+    return int(min(int64_t(a.n_ctas), max(int64_t(1), total / kMinShare)));
+}
+__device__ inline int64_t share_start(int64_t total, int n, int c) { return (total * c + n - 1) / n; }
+__device__ inline int share_owner(int64_t total, int n, int64_t p) { return int(p * n / total); }
+
+// One CTA's piece of a unit.
+struct TreeItem {
+    int seq, g, row0;         // packed row of the tile's first draft
+    int t0, n_rows;           // the tile's first draft, its drafts
+    int T, L, nh, b0, b1;     // blocks [b0, b1) of nh + nd
+    int slot;                 // -1: the whole unit
+    bool bad_len;
+};
+
+// A CTA's walk over its share; every lane of the warp holds the same state.
+struct TreeWalk {
+    int64_t at, end;     // positions left
+    int64_t seq_at;      // where the current sequence starts
+    int s, cta;
+    TreeSeq q;
+
+    __device__ inline void start(const TreeShape& a, int c) {
+        cta = c;
+        const int64_t total = tree_total(a, 0, nullptr);
+        const int n = tree_ctas(a, total);
+        at = end = 0;
+        if (c >= n || total == 0) return;
+        at = share_start(total, n, c);
+        end = share_start(total, n, c + 1);
+        seq_at = 0;
+        // the sequence that position `at` lies in, 32 at a time
+        for (int base = 0;; base += 32) {
+            const int i = base + int(threadIdx.x & 31);
+            const int64_t c1 = i < a.num_seqs ? tree_seq_cost(a, tree_seq(a, i)) : 0;
+            int64_t upto = c1;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+                if (int(threadIdx.x & 31) >= o) upto += x;
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, seq_at + upto > at);
+            if (m || base + 32 >= a.num_seqs) {
+                const int l = m ? __ffs(m) - 1 : 31;
+                s = min(base + l, a.num_seqs - 1);
+                seq_at += __shfl_sync(0xffffffffu, upto - c1, l);
+                break;
+            }
+            seq_at += __shfl_sync(0xffffffffu, upto, 31);
+        }
+        q = tree_seq(a, s);
+    }
+
+    // The next piece; false at the share's end.
+    __device__ inline bool next(const TreeShape& a, TreeItem& it) {
+        while (at < end) {
+            while (at >= seq_at + tree_seq_cost(a, q)) {  // at < end <= total: a later sequence has it
+                seq_at += tree_seq_cost(a, q);
+                q = tree_seq(a, ++s);
+            }
+            const int64_t in = at - seq_at;
+            const int unit = int(in / q.cost), o = int(in - int64_t(unit) * q.cost);
+            const int take = int(min(int64_t(q.cost - o), end - at));
+            at += take;
+            it.b0 = max(o - 1, 0);
+            it.b1 = o + take - 1;
+            if (it.b0 >= it.b1) continue;  // only the unit's first position: no block
+            const int u = unit % q.units;
+            it.seq = s;
+            it.g = unit / q.units;
+            it.t0 = u * a.tu;
+            it.n_rows = min(a.tu, q.T - it.t0);
+            it.row0 = q.row0 + it.t0;
+            it.T = q.T;
+            it.L = q.L;
+            it.nh = q.nh;
+            it.bad_len = q.bad_len;
+            const bool first = it.b0 == 0, whole = first && it.b1 == q.cost - 1;
+            it.slot = whole ? -1 : 2 * cta + (first ? 1 : 0);
+            return true;
+        }
+        return false;
+    }
+};
+
+// Lengths that a call refuses are flagged once, by CTA 0.
+__device__ inline void tree_flag_lengths(const TreeShape& a, uint32_t* status) {
+    for (int s = threadIdx.x; s < a.num_seqs; s += blockDim.x) {
+        const TreeSeq q = tree_seq(a, s);
+        if (q.bad_rows || q.bad_len) flag(status, PA_DEV_BAD_LEN);
+    }
+}
+
+// A slot holds, for each of a unit's `rows` distributions (draft * G + head),
+// the base-2 running max and the sum, then the accumulators.
+__host__ __device__ inline int64_t slot_floats(int rows, int D) { return int64_t(rows) * (D + 2); }
+
+template <typename T> __device__ inline T from_f32(float x);
+template <> __device__ inline float from_f32<float>(float x) { return x; }
+template <> __device__ inline __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <> __device__ inline __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// The join, launched with programmatic dependent launch behind the pieces'
+// kernel: one warp per (packed row, q head), CTAs of eight heads of a row.
+// It finds its pieces from the lengths before it waits; a row whose unit was
+// finished in one share returns.
+constexpr int kJoinWarps = 8;
+template <typename TOut, int D>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    tree_join(const TreeShape a, const float* slots, TOut* out, int Hq, int rows) {
+    constexpr int kV = D / 32;  // dims of a lane
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = blockIdx.x, h = int(blockIdx.y) * kJoinWarps + warp;
+    if (h >= Hq) return;
+    // the row's sequence: the lowest whose rows hold it (at most one does)
+    int s = -1;
+    for (int base = 0; base < a.num_seqs && s < 0; base += 32) {
+        const int i = base + lane;
+        const bool in = i < a.num_seqs && a.cu_lens[i] <= row && row < a.cu_lens[i + 1];
+        const unsigned m = __ballot_sync(0xffffffffu, in);
+        if (m) s = base + __ffs(m) - 1;
+    }
+    if (s < 0) return;
+    const TreeSeq q = tree_seq(a, s);
+    if (q.T == 0) return;
+    int64_t before;
+    const int64_t total = tree_total(a, s, &before);
+    const int n = tree_ctas(a, total);
+    const int G = Hq / a.Hkv, g = h / G, t = row - q.row0, u = t / a.tu;
+    const int64_t u0 = before + (int64_t(g) * q.units + u) * q.cost;
+    const int c0 = share_owner(total, n, u0 + 1), c1 = share_owner(total, n, u0 + q.cost - 1);
+    if (c0 == c1) return;
+    const int r = (t - u * a.tu) * G + (h - g * G);
+    const int64_t size = slot_floats(rows, D);
+    pdl_wait_primary();
+    auto slot_of = [&](int c) { return slots + size * (2 * c + (c == c0 ? 1 : 0)); };
+    float m_all = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) m_all = fmaxf(m_all, slot_of(c)[2 * r]);
+    m_all = warp_max(m_all);
+    float acc[kV], l = 0.f;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) acc[v] = 0.f;
+    for (int cb = c0; cb <= c1; cb += 32) {
+        float w = 0.f, lw = 0.f;
+        if (cb + lane <= c1) {
+            const float2 ml = *reinterpret_cast<const float2*>(slot_of(cb + lane) + 2 * r);
+            // a piece with no visible key has max -inf and weight 0; a NaN max cannot be (max drops NaN)
+            w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - m_all);
+            lw = ml.y * w;
+        }
+        const int nc = min(32, c1 - cb + 1);
+#pragma unroll 4
+        for (int i = 0; i < nc; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            l += __shfl_sync(0xffffffffu, lw, i);
+            const float* p = slot_of(cb + i) + 2 * rows + int64_t(r) * D + lane * kV;
+            float x[kV];
+            if constexpr (kV == 4)
+                *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(p);
+            else
+                *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(p);
+#pragma unroll
+            for (int v = 0; v < kV; ++v) acc[v] = wi == 0.f ? acc[v] : fmaf(wi, x[v], acc[v]);
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    TOut y[kV];
+#pragma unroll
+    for (int v = 0; v < kV; ++v) y[v] = from_f32<TOut>(acc[v] * inv);
+    TOut* o = out + (int64_t(row) * Hq + h) * D + lane * kV;
+    if constexpr (sizeof(y) == 16)
+        *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(y);
+    else if constexpr (sizeof(y) == 8)
+        *reinterpret_cast<uint2*>(o) = *reinterpret_cast<const uint2*>(y);
+    else
+        *reinterpret_cast<uint32_t*>(o) = *reinterpret_cast<const uint32_t*>(y);
+}
+
+}  // namespace
+
+}  // namespace pa

@@ -1,4 +1,5 @@
-"""ctypes binding of libpaged_gqa.so (see ``include/paged_gqa.h``).
+"""ctypes binding of libpaged_gqa.so (see ``include/paged_gqa.h`` and
+``include/paged_gqa_serving.h``).
 
 Argument marshalling only: every step of the attention runs in the CUDA
 library.  torch supplies device memory and the current stream.  There is no
@@ -18,6 +19,7 @@ LIB_PATH = os.environ.get("PA_GQA_LIB") or os.path.join(PKG, "libpaged_gqa.so")
 PA_F32, PA_F16, PA_BF16 = 0, 1, 2
 DTYPE_CODE = {"f32": PA_F32, "f16": PA_F16, "bf16": PA_BF16}
 PA_DEV_BAD_PAGE, PA_DEV_BAD_LEN, PA_DEV_TIMEOUT, PA_DEV_OOB = 1, 2, 4, 8
+PA_DEV_NO_PAGES, PA_DEV_BAD_INDEX = 16, 32
 PA_FORM_AUTO, PA_FORM_PAIR, PA_FORM_COUNTED = 0, 1, 2
 STATUS = {0: "PA_OK", 1: "PA_ERR_NULL", 2: "PA_ERR_SHAPE", 3: "PA_ERR_DTYPE",
           4: "PA_ERR_ALIGN", 5: "PA_ERR_WORKSPACE", 6: "PA_ERR_UNSUPPORTED", 7: "PA_ERR_CUDA"}
@@ -25,7 +27,9 @@ STATUS = {0: "PA_OK", 1: "PA_ERR_NULL", 2: "PA_ERR_SHAPE", 3: "PA_ERR_DTYPE",
 EXPORTS = ("pa_params_init", "pa_status_string", "pa_decode_plan", "pa_decode_workspace_size",
            "pa_decode", "pa_decode_partial", "pa_combine", "pa_prefill_workspace_size",
            "pa_prefill_chunk", "pa_version", "pa_decode_append", "pa_decode_noalloc",
-           "pa_build_flags", "pa_decode_kernels")
+           "pa_build_flags", "pa_decode_kernels", "pa_rows_init", "pa_prompt",
+           "pa_tree_workspace_size", "pa_tree", "pa_store", "pa_pages_workspace_size",
+           "pa_pages_resize", "pa_pages_fork", "pa_pages_compact", "pa_pages_copy")
 
 
 class PaError(RuntimeError):
@@ -47,6 +51,14 @@ class Params(ctypes.Structure):
                 ("num_splits", ctypes.c_int32), ("decode_phases", ctypes.c_int32),
                 ("decode_q_rows", ctypes.c_int32), ("sliding_window", ctypes.c_int32),
                 ("decode_form", ctypes.c_int32), ("debug_timeout", ctypes.c_int32)]
+
+
+class Rows(ctypes.Structure):
+    """Mirror of ``pa_rows``."""
+    _fields_ = [("total_rows", ctypes.c_int32), ("max_rows", ctypes.c_int32),
+                ("source_rows", ctypes.c_int32), ("mask_words", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64)]
 
 
 _lock = threading.Lock()
@@ -84,6 +96,23 @@ def load(path: str = LIB_PATH):
             for name in ("pa_decode_plan", "pa_decode", "pa_decode_append", "pa_decode_partial",
                          "pa_combine", "pa_prefill_chunk", "pa_decode_noalloc"):
                 getattr(L, name).restype = ctypes.c_int
+            R = ctypes.POINTER(Rows)
+            L.pa_rows_init.argtypes = [R]
+            L.pa_rows_init.restype = R
+            L.pa_prompt.argtypes = [P, R, vp, vp, vp, vp, vp, vp, vp]
+            L.pa_tree_workspace_size.argtypes = [P, R]
+            L.pa_tree.argtypes = [P, R, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]
+            L.pa_store.argtypes = [P, R, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+            L.pa_pages_workspace_size.argtypes = [P]
+            L.pa_pages_resize.argtypes = [P, vp, vp, vp, vp, vp, vp, sz, vp, vp]
+            L.pa_pages_fork.argtypes = [P, vp, vp, vp, vp, vp, i32, vp, vp]
+            L.pa_pages_compact.argtypes = [P, vp, vp, vp, vp, i32, vp, vp, sz, vp, vp]
+            L.pa_pages_copy.argtypes = [P, vp, vp, vp, i32, vp, vp]
+            for name in ("pa_tree_workspace_size", "pa_pages_workspace_size"):
+                getattr(L, name).restype = sz
+            for name in ("pa_prompt", "pa_tree", "pa_store", "pa_pages_resize", "pa_pages_fork",
+                         "pa_pages_compact", "pa_pages_copy"):
+                getattr(L, name).restype = ctypes.c_int
             L.pa_version.restype = i32
             if hasattr(L, "pa_build_flags"):
                 L.pa_build_flags.restype = i32
@@ -94,7 +123,8 @@ def load(path: str = LIB_PATH):
 def make_params(*, num_seqs, num_q_heads, num_kv_heads, head_dim, page_size, num_pages,
                 max_blocks_per_seq, max_context_len, scale=None, dtype="bf16", kv_dtype=None,
                 deterministic=1, num_splits=0, strides=(0, 0, 0), decode_phases=0,
-                decode_q_rows=0, sliding_window=0, decode_form=0, debug_timeout=0) -> Params:
+                decode_q_rows=0, sliding_window=0, decode_form=0, debug_timeout=0,
+                out_dtype="f32") -> Params:
     p = Params()
     load().pa_params_init(ctypes.byref(p))
     p.num_seqs, p.num_q_heads, p.num_kv_heads = num_seqs, num_q_heads, num_kv_heads
@@ -104,7 +134,7 @@ def make_params(*, num_seqs, num_q_heads, num_kv_heads, head_dim, page_size, num
     p.scale = (1.0 / math.sqrt(head_dim)) if scale is None else scale
     p.q_dtype = DTYPE_CODE[dtype]
     p.kv_dtype = DTYPE_CODE[kv_dtype or dtype]
-    p.out_dtype = PA_F32
+    p.out_dtype = DTYPE_CODE[out_dtype]
     p.deterministic, p.num_splits = deterministic, num_splits
     p.decode_phases = decode_phases
     p.decode_q_rows = decode_q_rows
@@ -269,3 +299,230 @@ def decode_noalloc(p: Params, q, k_cache, v_cache, block_tables, context_lens, o
               _ptr(context_lens), _ptr(out), _ptr(dev_status), _stream(stream)),
            "pa_decode_noalloc")
     return out
+
+
+# ---- the serving step (include/paged_gqa_serving.h) ---------------------------
+# These check what the C entry points cannot see: that each tensor has the
+# dtype and the extent that the parameters promise, on one device.
+
+def make_rows(total_rows, max_rows, *, source_rows=0, mask_words=0, q_stride=0, k_stride=0,
+              v_stride=0) -> Rows:
+    """``pa_rows``: packed rows, their bound per sequence, strides in elements (0: contiguous)."""
+    return Rows(total_rows, max_rows, source_rows, mask_words, q_stride, k_stride, v_stride)
+
+
+def prompt_params(*, num_seqs, num_q_heads, num_kv_heads, head_dim, scale=None, dtype="bf16",
+                  out_dtype="f32", debug_timeout=0) -> Params:
+    """Params of pa_prompt, which has no pages."""
+    return make_params(num_seqs=num_seqs, num_q_heads=num_q_heads, num_kv_heads=num_kv_heads,
+                       head_dim=head_dim, page_size=0, num_pages=0, max_blocks_per_seq=0,
+                       max_context_len=0, scale=scale, dtype=dtype, out_dtype=out_dtype,
+                       debug_timeout=debug_timeout)
+
+
+_TORCH_DTYPE = None
+
+
+def _torch_dtype(code):
+    global _TORCH_DTYPE
+    if _TORCH_DTYPE is None:
+        import torch
+        _TORCH_DTYPE = {PA_F32: torch.float32, PA_F16: torch.float16, PA_BF16: torch.bfloat16}
+    return _TORCH_DTYPE[code]
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _ints(t, n, device, what):
+    """Pointer of a contiguous int32 tensor of at least n elements."""
+    _need(t.element_size() == 4 and not t.is_floating_point() and t.numel() >= n and t.is_contiguous()
+          and t.device == device, f"{what}: a contiguous int32 tensor of at least {n} elements on {device}")
+    return t.data_ptr()
+
+
+def _packed(t, code, rows, heads, dim, stride, device, what):
+    """Pointer of packed rows [rows][heads][dim], ``stride`` elements between rows."""
+    _need(t.dtype is _torch_dtype(code) and t.dim() == 3 and t.shape[0] >= rows and t.shape[1] == heads
+          and t.shape[2] == dim and t.device == device
+          and (rows == 0 or (t.stride(2) == 1 and (heads == 1 or t.stride(1) == dim)
+                             and (rows == 1 or t.stride(0) == (stride or heads * dim)))),
+          f"{what}: [{rows}][{heads}][{dim}] {_torch_dtype(code)}, rows {stride or heads * dim} elements apart, "
+          f"on {device}")
+    return t.data_ptr()
+
+
+def _pool(t, p, device, what):
+    """Pointer of a K or V pool: the last slot of the last head and page lies inside the tensor's storage."""
+    hs = p.head_stride or p.head_dim
+    ts = p.token_stride or p.num_kv_heads * hs
+    ps = p.page_stride or p.page_size * ts
+    last = (p.num_pages - 1) * ps + (p.page_size - 1) * ts + (p.num_kv_heads - 1) * hs + p.head_dim
+    _need(t.dtype is _torch_dtype(p.kv_dtype) and t.device == device
+          and t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() >= last,
+          f"{what}: {last} elements of {_torch_dtype(p.kv_dtype)} on {device}")
+    return t.data_ptr()
+
+
+def _status(t, device):
+    return None if t is None else _ints(t, 1, device, "dev_status")
+
+
+class _on:
+    """The device of a call's tensors made current, and the stream's handle."""
+    __slots__ = ("device", "stream", "guard")
+
+    def __init__(self, t, stream):
+        _need(t.is_cuda, "tensors must be on a CUDA device")
+        self.device, self.stream, self.guard = t.device, stream, None
+
+    def __enter__(self):
+        import torch
+        if torch.cuda.current_device() != self.device.index:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _packed_out(p, r, q, out):
+    import torch
+    if out is None:
+        return torch.zeros((r.total_rows, p.num_q_heads, p.head_dim), dtype=_torch_dtype(p.out_dtype),
+                           device=q.device)
+    _packed(out, p.out_dtype, r.total_rows, p.num_q_heads, p.head_dim, 0, q.device, "out")
+    return out
+
+
+def prompt(p: Params, r: Rows, q, k, v, cu_lens, out=None, dev_status=None, stream=None):
+    """Causal attention over whole packed prompts; q [rows][Hq][D], k and v
+    [rows][Hkv][D] -> out [rows][Hq][D] in p.out_dtype.  Rows behind the last
+    sequence keep what ``out`` held (zeros when it is made here)."""
+    n, d, hkv, dev = r.total_rows, p.head_dim, p.num_kv_heads, q.device
+    with _on(q, stream) as st:
+        out = _packed_out(p, r, q, out)
+        _check(load().pa_prompt(p, r, _packed(q, p.q_dtype, n, p.num_q_heads, d, r.q_stride, dev, "q"),
+                                _packed(k, p.kv_dtype, n, hkv, d, r.k_stride, dev, "k"),
+                                _packed(v, p.kv_dtype, n, hkv, d, r.v_stride, dev, "v"),
+                                _ints(cu_lens, p.num_seqs + 1, dev, "cu_lens"), out.data_ptr(),
+                                _status(dev_status, dev), st), "pa_prompt")
+    return out
+
+
+def tree_workspace_size(p: Params, r: Rows) -> int:
+    return int(load().pa_tree_workspace_size(p, r))
+
+
+def tree(p: Params, r: Rows, q, k, v, cu_lens, tree_mask, k_cache, v_cache, block_tables,
+         context_lens, out=None, workspace=None, dev_status=None, stream=None):
+    """Attention of drafted tokens over the paged history and one another:
+    packed q, k, v as in ``prompt``, tree_mask [rows][mask_words] int32."""
+    import torch
+    n, d, hkv, dev, b = r.total_rows, p.head_dim, p.num_kv_heads, q.device, p.num_seqs
+    with _on(q, stream) as st:
+        out = _packed_out(p, r, q, out)
+        if workspace is None:
+            workspace = torch.empty(max(tree_workspace_size(p, r), 1), dtype=torch.uint8, device=dev)
+        _need(workspace.device == dev and workspace.is_contiguous(), f"workspace: contiguous, on {dev}")
+        words = r.mask_words or (r.max_rows + 31) // 32
+        _check(load().pa_tree(p, r, _packed(q, p.q_dtype, n, p.num_q_heads, d, r.q_stride, dev, "q"),
+                              _packed(k, p.kv_dtype, n, hkv, d, r.k_stride, dev, "k"),
+                              _packed(v, p.kv_dtype, n, hkv, d, r.v_stride, dev, "v"),
+                              _ints(cu_lens, b + 1, dev, "cu_lens"), _ints(tree_mask, n * words, dev, "tree_mask"),
+                              _pool(k_cache, p, dev, "k_cache"), _pool(v_cache, p, dev, "v_cache"),
+                              _ints(block_tables, b * p.max_blocks_per_seq, dev, "block_tables"),
+                              _ints(context_lens, b, dev, "context_lens"), out.data_ptr(), workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size(), _status(dev_status, dev), st),
+               "pa_tree")
+    return out
+
+
+def store(p: Params, r: Rows, k, v, cu_lens, k_cache, v_cache, block_tables, context_lens,
+          row_index=None, dev_status=None, stream=None):
+    """Writes packed K/V rows (or, with row_index, chosen rows of them) to
+    each sequence's last positions; k_cache and v_cache change in place."""
+    n, d, hkv, dev, b = r.total_rows, p.head_dim, p.num_kv_heads, k.device, p.num_seqs
+    src = r.source_rows or n
+    with _on(k, stream) as st:
+        _check(load().pa_store(p, r, _packed(k, p.kv_dtype, src, hkv, d, r.k_stride, dev, "k"),
+                               _packed(v, p.kv_dtype, src, hkv, d, r.v_stride, dev, "v"),
+                               _ints(cu_lens, b + 1, dev, "cu_lens"),
+                               None if row_index is None else _ints(row_index, n, dev, "row_index"),
+                               _pool(k_cache, p, dev, "k_cache"), _pool(v_cache, p, dev, "v_cache"),
+                               _ints(block_tables, b * p.max_blocks_per_seq, dev, "block_tables"),
+                               _ints(context_lens, b, dev, "context_lens"), _status(dev_status, dev), st),
+               "pa_store")
+
+
+def pages_workspace_size(p: Params) -> int:
+    return int(load().pa_pages_workspace_size(p))
+
+
+def _bookkeeping(p, refcounts, block_tables, context_lens):
+    dev = refcounts.device
+    return (_ints(refcounts, p.num_pages, dev, "refcounts"),
+            _ints(block_tables, p.num_seqs * p.max_blocks_per_seq, dev, "block_tables"),
+            _ints(context_lens, p.num_seqs, dev, "context_lens"))
+
+
+def _scratch(p, workspace, dev):
+    import torch
+    if workspace is None:
+        workspace = torch.empty(max(pages_workspace_size(p), 1), dtype=torch.uint8, device=dev)
+    _need(workspace.device == dev and workspace.is_contiguous(), f"workspace: contiguous, on {dev}")
+    return workspace
+
+
+def pages_resize(p: Params, refcounts, block_tables, context_lens, new_lens, pairs, workspace=None,
+                 dev_status=None, stream=None):
+    """Reserves, trims and frees pages: sequence s goes to new_lens[s] tokens
+    (negative: left alone).  pairs [num_seqs][2] gets the copies to make."""
+    dev = refcounts.device
+    with _on(refcounts, stream) as st:
+        ws = _scratch(p, workspace, dev)
+        _check(load().pa_pages_resize(p, *_bookkeeping(p, refcounts, block_tables, context_lens),
+                                      _ints(new_lens, p.num_seqs, dev, "new_lens"),
+                                      _ints(pairs, 2 * p.num_seqs, dev, "pairs"), ws.data_ptr(),
+                                      ws.numel() * ws.element_size(), _status(dev_status, dev), st),
+               "pa_pages_resize")
+
+
+def pages_fork(p: Params, refcounts, block_tables, context_lens, src, dst, dev_status=None, stream=None):
+    """Makes each empty sequence dst[i] a copy of src[i] that shares its pages."""
+    dev = refcounts.device
+    with _on(refcounts, stream) as st:
+        n = dst.numel()
+        _check(load().pa_pages_fork(p, *_bookkeeping(p, refcounts, block_tables, context_lens),
+                                    _ints(src, n, dev, "src"), _ints(dst, n, dev, "dst"), n,
+                                    _status(dev_status, dev), st), "pa_pages_fork")
+
+
+def pages_compact(p: Params, refcounts, block_tables, context_lens, pairs, num_moves, workspace=None,
+                  dev_status=None, stream=None):
+    """Moves live pages to the low end of the pool, at most len(pairs) of
+    them; pairs [n][2] gets the copies to make, num_moves [1] their number."""
+    dev = refcounts.device
+    with _on(refcounts, stream) as st:
+        ws = _scratch(p, workspace, dev)
+        n = pairs.numel() // 2
+        _check(load().pa_pages_compact(p, *_bookkeeping(p, refcounts, block_tables, context_lens),
+                                       _ints(pairs, 2 * n, dev, "pairs"), n,
+                                       _ints(num_moves, 1, dev, "num_moves"), ws.data_ptr(),
+                                       ws.numel() * ws.element_size(), _status(dev_status, dev), st),
+               "pa_pages_compact")
+
+
+def pages_copy(p: Params, k_cache, v_cache, pairs, dev_status=None, stream=None):
+    """Copies page pairs[i][0] to pairs[i][1] in one layer's K and V; negative pairs are passed over."""
+    dev = k_cache.device
+    with _on(k_cache, stream) as st:
+        n = pairs.numel() // 2
+        _check(load().pa_pages_copy(p, _pool(k_cache, p, dev, "k_cache"), _pool(v_cache, p, dev, "v_cache"),
+                                    _ints(pairs, 2 * n, dev, "pairs"), n, _status(dev_status, dev), st),
+               "pa_pages_copy")
