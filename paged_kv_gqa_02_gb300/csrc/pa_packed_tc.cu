@@ -2,31 +2,37 @@
 // 5th-generation tensor cores (tcgen05 MMA, accumulators in tensor memory,
 // operands staged by TMA).  head_dim 64 or 128.
 //
-// A unit of work is 2 x 128 MMA rows of one (sequence, kv head): row tiles A
-// and B, each 128/G consecutive packed rows times the G q heads (MMA row =
+// A unit of work is up to 2 x 128 MMA rows of one (sequence, kv head): row tiles
+// A and B, each 128/G consecutive packed rows times the G q heads (MMA row =
 // token * G + head), against key tiles of 128.  Every K/V tile in shared
-// memory serves both row tiles and all G heads.  CTAs are persistent, one per
-// SM, and walk a list of units or, for a tree, of pieces of units:
+// memory serves both row tiles and all G heads.  A unit that fills one row
+// tile only is worked on by both sides all the same: side A takes the even key
+// tiles and side B the odd ones, each with its own O, max and sum, and the
+// epilogue joins them ("twin").  CTAs are persistent, one per SM, and walk a
+// list of units or, for a tree, of pieces of units:
 //   prompt: units in descending order of their key tiles, dealt out in turn;
 //           keys are the packed rows 0..t of the unit's own sequence;
 //   tree:   the CTA's share of the keys (pa_tree_plan.cuh); key tiles are the
 //           history's pages first, then the packed drafts under their mask.
 //
-// Warp roles (320 threads), joined by mbarriers; each role walks the items on
-// its own clock, so one item's loads and first products run under the last
-// one's softmax and epilogue:
-//   warps 0-3, 4-7  softmax of tile A and of tile B: a thread per MMA row
-//                   (tensor-memory lane), online softmax in base 2 whose
-//                   running max is raised only when it grows by more than
-//                   2^8, probabilities written over their scores, epilogue
+// Warp roles, joined by mbarriers; each role walks the items on its own clock,
+// so one item's loads and first products run under the last one's softmax and
+// epilogue:
+//   warps 0-3, 4-7  softmax of side A and of side B: a thread per MMA row
+//                   (tensor-memory lane), probabilities written over their
+//                   scores, epilogue
 //   warp 8          finds the items, publishes them, and issues the TMA loads
 //   warp 9          owns tensor memory; issues every MMA (converged warp, one
 //                   elected lane)
+//   warp 10         cleans V tiles that not every row sees whole (below)
 // Tensor memory (512 columns): S/P of A [0,128), of B [128,256), O of A
-// [256,256+D), O of B [256+D,256+2D).  Per key tile the MMA warp issues
-// P_A V, then A's next Q K^T once that product has read P_A (same columns),
-// then the same for B: one row tile's products run while the other's softmax
-// does.
+// [256,256+D), O of B [256+D,256+2D).  Per key tile the MMA warp issues P V and,
+// once that product has read P (same columns), the next Q K^T, for A and B in
+// turn: one side's products run while the other's softmax does.
+//
+// Softmax: a row's 128 scores are read from tensor memory into registers in one
+// go; online, in base 2, with a running max that is raised, and O rescaled,
+// only when it grows by more than 2^8.
 //
 // Probabilities enter P.V as one 16-bit value when the output is 16 bits wide
 // (each is off by half a step at most, the size of the output's own
@@ -56,12 +62,15 @@ constexpr int kBN = 128;  // keys of a tile
 constexpr int kKS = 3;    // K ring depth
 constexpr int kVS = 2;    // V ring depth
 constexpr int kIS = 2;    // items published ahead
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;  // three warpgroups
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 128;  // a thread; 2 x 208 + 88 = 3 x 168, the launch's
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
+constexpr int kCleanWarp = 10;
 constexpr uint32_t kHalfBytes = kBN * 128;  // one 64-dim half of a tile
 constexpr uint64_t kWaitNs = 2000000000ull;  // a role gives up after 2 s on one barrier
-constexpr uint32_t kSleepNs = 20000;         // longest sleep inside one try_wait
+constexpr uint32_t kSleepNs = 20000;  // longest sleep inside one try_wait
+constexpr int kWaitSlices = int(kWaitNs / kSleepNs);
 constexpr float kRescaleStep = 8.f;
 constexpr uint32_t kNegInf = 0xff800000u;
 
@@ -72,13 +81,15 @@ struct Item {
 
 struct Bars {
     uint64_t q_full, q_empty;
-    uint64_t k_full[kKS], k_empty[kKS], v_full[kVS], v_empty[kVS];
+    uint64_t k_full[kKS], k_empty[kKS], v_full[kVS], v_clean[kVS], v_empty[kVS];
     uint64_t s_full[2], p_full[2], o_done[2];  // of row tile x
     uint64_t item_full[kIS], item_empty[kIS];
+    uint64_t side_b, side_w;  // twin: `side` holds B's figures; the weights
     uint64_t mma_done, never;
     uint32_t tmem, abort;
     uint32_t poison[kIS];  // n + 1: item n met a NaN or infinity in a V that not every row sees
     Item items[kIS];
+    float2 side[kBM];  // twin: B's max and sum, then both sides' weights, of each row
 };
 
 template <int D> struct Smem {
@@ -96,9 +107,13 @@ template <int D> __device__ inline uint32_t col_o(int x) { return 256u + uint32_
 struct TcArgs {
     PackedAttn a;
     TreeShape shape;
-    int32_t tq, G, n_units, head_first;  // n_units: prompt, units of the longest sequence per kv head
+    int32_t tq, G, head_first;
+    int32_t tu, n_units;  // prompt: rows of a unit; units of the longest sequence per kv head
 };
 
+// Waits for a phase, suspended in slices of up to kSleepNs, kWaitSlices of them
+// at most, or until another role has given up.  Kept short: every role's waits
+// are copies of it, and instruction fetch is what the MMA warp waits for most.
 __device__ inline bool wait_bar(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
@@ -181,49 +196,97 @@ __device__ inline void apply_mask(uint32_t (&r)[32], uint32_t m) {
     for (int k = 0; k < 32; ++k) r[k] = ((m >> k) & 1u) ? r[k] : kNegInf;
 }
 
-// Rows and key tiles of the two row tiles of an item.
-struct Shape2 {
-    int rows[2], tiles[2];
+__device__ inline float max32(const uint32_t (&r)[32]) {
+    float m0 = __uint_as_float(r[0]), m1 = __uint_as_float(r[1]);
+#pragma unroll
+    for (int k = 2; k < 30; k += 4) {
+        m0 = max3(m0, __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+        m1 = max3(m1, __uint_as_float(r[k + 2]), __uint_as_float(r[k + 3]));
+    }
+    return max3(fmaxf(m0, m1), __uint_as_float(r[30]), __uint_as_float(r[31]));
+}
+
+// A warp's 32 rows x kN 16-byte pieces, a row a lane, written so that four lanes
+// write 64 consecutive bytes of a row: a store of a piece a lane touches 32
+// lines and takes as long as four of these.  In groups of four lanes, lane b
+// gets piece b of each of the group's rows (two rounds of exchanges).
+// row(i) is the address of the group's i-th row, or nullptr where it is none.
+template <int kN, typename Row> __device__ inline void store_rows4(uint4 (&v)[kN], int lane, Row row) {
+    const bool up1 = lane & 1, up2 = lane & 2;
+    auto swap = [&](uint4& a, uint4& b, bool up, int mask) {  // gives a (up) or b, takes the partner's
+        uint4 x = up ? a : b;
+        x.x = __shfl_xor_sync(0xffffffffu, x.x, mask);
+        x.y = __shfl_xor_sync(0xffffffffu, x.y, mask);
+        x.z = __shfl_xor_sync(0xffffffffu, x.z, mask);
+        x.w = __shfl_xor_sync(0xffffffffu, x.w, mask);
+        if (up)
+            a = x;
+        else
+            b = x;
+    };
+#pragma unroll
+    for (int g = 0; g < kN; g += 4) {
+        swap(v[g], v[g + 1], up1, 1);
+        swap(v[g + 2], v[g + 3], up1, 1);
+        swap(v[g], v[g + 2], up2, 2);
+        swap(v[g + 1], v[g + 3], up2, 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint4* at = row(i);
+            if (at) at[g + (lane & 3)] = v[g + i];
+        }
+    }
+}
+
+// What the two sides of an item do: their rows and key tiles.  Tile i of side x
+// is the item's tile i, or 2 i + x of a twin, whose sides share A's rows.
+struct Sides {
+    int rows[2], tiles[2], nt;
+    bool twin;
+    __device__ inline int tile(int x, int i) const { return twin ? 2 * i + x : i; }
 };
-template <bool kTree> __device__ inline Shape2 shape2(const TreeItem& t, int tq) {
-    Shape2 s;
+template <bool kTree> __device__ inline Sides sides_of(const TreeItem& t, int tq) {
+    Sides s;
+    s.nt = t.b1 - t.b0;
     s.rows[0] = min(tq, t.n_rows);
     s.rows[1] = t.n_rows - s.rows[0];
-    if (kTree) {
-        s.tiles[0] = t.b1 - t.b0;
-        s.tiles[1] = s.rows[1] > 0 ? s.tiles[0] : 0;
-    } else {  // causal: tile B may see one key tile more
-        s.tiles[0] = (t.t0 + s.rows[0] + kBN - 1) / kBN;
-        s.tiles[1] = s.rows[1] > 0 ? (t.t0 + tq + s.rows[1] + kBN - 1) / kBN : 0;
+    s.twin = s.rows[1] == 0 && s.nt > 1;
+    if (s.twin) {
+        s.rows[1] = s.rows[0];
+        s.tiles[0] = (s.nt + 1) >> 1;
+        s.tiles[1] = s.nt >> 1;
+    } else {  // causal: tile B may see one key tile more than A
+        s.tiles[0] = kTree ? s.nt : (t.t0 + s.rows[0] + kBN - 1) / kBN;
+        s.tiles[1] = s.rows[1] > 0 ? s.nt : 0;
     }
     return s;
 }
 
 // The prompt's units in descending order of key tiles: unit i is
-// (tile pair from the last, sequence, kv head); those that their sequence
-// does not have are passed over.  CTA c takes i = c, 2n-1-c, 2n+c, ... of the
-// n CTAs, so that none gets the longer unit of every round.
+// (level from the last, sequence, kv head); those that their sequence does not
+// have are passed over.  CTA c takes i = c, 2n-1-c, 2n+c, ... of the n CTAs, so
+// that none gets the longer unit of every round.
 struct PromptWalk {
-    int64_t round;
+    int round;
     __device__ inline bool next(const TcArgs& p, TreeItem& it, uint32_t* status) {
         const PackedAttn& a = p.a;
-        const int64_t per = int64_t(a.Hkv) * a.r.num_seqs, all = per * p.n_units;
+        const int per = a.Hkv * a.r.num_seqs, all = per * p.n_units, n = gridDim.x, c = blockIdx.x;
         for (;; ++round) {
-            const int64_t i = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-            if (round * gridDim.x >= all) return false;
+            if (round * n >= all) return false;
+            const int i = round * n + ((round & 1) ? n - 1 - c : c);
             if (i >= all) continue;
-            const int level = p.n_units - 1 - int(i / per), u = int(i % per);
-            it.g = u % a.Hkv;
+            const int level = p.n_units - 1 - i / per, u = i % per;
             it.seq = u / a.Hkv;
+            it.g = u - it.seq * a.Hkv;
             const int r0 = a.r.cu_lens[it.seq], r1 = a.r.cu_lens[it.seq + 1];
             if (r0 < 0 || r1 < r0 || r1 > a.r.total_rows || r1 - r0 > a.r.max_rows) {
                 if (level == 0 && (threadIdx.x & 31) == 0) flag(status, PA_DEV_BAD_LEN);
                 continue;
             }
             it.T = r1 - r0;
-            it.t0 = level * 2 * p.tq;
+            it.t0 = level * p.tu;
             if (it.t0 >= it.T) continue;
-            it.n_rows = min(2 * p.tq, it.T - it.t0);
+            it.n_rows = min(p.tu, it.T - it.t0);
             it.row0 = r0 + it.t0;
             it.L = it.nh = it.b0 = 0;
             it.b1 = (it.t0 + it.n_rows + kBN - 1) / kBN;
@@ -234,6 +297,9 @@ struct PromptWalk {
         }
     }
 };
+
+template <int N> __device__ inline void regs_grow() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ inline void regs_shrink() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 template <typename T, int D, bool kTree, typename TOut>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -266,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kVS; ++i) {
             mbar_init(&B.v_full[i], 1);
+            mbar_init(&B.v_clean[i], 1);
             mbar_init(&B.v_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -275,9 +342,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kIS; ++i) {
             mbar_init(&B.item_full[i], 1);
-            mbar_init(&B.item_empty[i], 9);  // 8 softmax warps and the MMA warp
+            mbar_init(&B.item_empty[i], 10);  // 8 softmax warps, the MMA warp, the V warp
             B.poison[i] = 0;
         }
+        mbar_init(&B.side_b, 4);
+        mbar_init(&B.side_w, 4);
         mbar_init(&B.mma_done, 1);
         mbar_init(&B.never, 1);
         B.abort = 0;
@@ -306,12 +375,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 1u;
         flag(a.dev_status, PA_DEV_TIMEOUT);
     };
-    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag));
     };
-
     if (warp == kProducerWarp) {
         // ================================ producer ================================
+        regs_shrink<kOtherRegs>();
         if (lane == 0) {
             tma_prefetch_desc(&tmQ);
             tma_prefetch_desc(&tmK);
@@ -350,8 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!it.valid) break;
             const TreeItem& t = it.t;
-            const Shape2 sh = shape2<kTree>(t, tq);
-            const int nt = max(sh.tiles[0], sh.tiles[1]);
+            const Sides sd = sides_of<kTree>(t, tq);
+            const int nt = sd.nt, n_q = t.n_rows > tq ? 2 : 1;  // row tiles
             const int32_t* table = kTree ? a.c.block_tables + int64_t(t.seq) * a.c.max_blocks : nullptr;
             const int PT = kTree ? kBN / P : 0;
             const int npg = kTree ? (t.L + P - 1) / P : 0;
@@ -394,8 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     if (lane == 0) {
                         const uint32_t qbytes = uint32_t(kHalves) * 128u * uint32_t(G * tq);
-                        mbar_arrive_expect_tx(&B.q_full, sh.rows[1] > 0 ? 2 * qbytes : qbytes);
-                        for (int x = 0; x < (sh.rows[1] > 0 ? 2 : 1); ++x)
+                        mbar_arrive_expect_tx(&B.q_full, n_q * qbytes);
+                        for (int x = 0; x < n_q; ++x)
                             for (int hh = 0; hh < kHalves; ++hh)
                                 tma_load_3d(sQ + x * kTileBytes + hh * kHalfBytes, &tmQ, &B.q_full, 64 * hh,
                                             t.g * G, t.row0 + x * tq);
@@ -417,6 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kMmaWarp) {
         // ================================== MMA ===================================
+        regs_shrink<kOtherRegs>();
         const uint32_t idQK = tc::idesc_f16(kBM, kBN, kBf16, false);
         const uint32_t idPV = tc::idesc_f16(kBM, D, kBf16, true);
         // descriptors: the high word is shared, low words advance by offset >> 4
@@ -424,10 +494,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t q_lo = tc::desc_lo(smem_u32(sQ), 16);
         const uint32_t k_lo = tc::desc_lo(smem_u32(k_tile(0)), 16);
         const uint32_t v_lo = tc::desc_lo(smem_u32(v_tile(0)), kHalfBytes);
-        // S_x = Q_x K^T of K tile number kt
-        auto qk = [&](int x, int kt) {
-            const uint32_t qx = q_lo + x * (kTileBytes >> 4);
-            const uint32_t kx = k_lo + (kt % kKS) * (kTileBytes >> 4);
+        // S_x = Q K^T of row tile qt and K tile number t
+        auto qk = [&](int x, int qt, int t) {
+            const uint32_t qx = q_lo + qt * (kTileBytes >> 4);
+            const uint32_t kx = k_lo + (t % kKS) * (kTileBytes >> 4);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 const uint32_t off = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
@@ -436,10 +506,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc::commit_elect(&B.s_full[x]);
         };
-        // O_x (+)= P_x V of V tile number vt; P of 16 keys is 8 columns, 32 keys
-        // take 16 (kSplit: 32, hi then lo)
-        auto pv = [&](int x, int vt, bool first) {
-            const uint32_t vx = v_lo + (vt % kVS) * (kTileBytes >> 4);
+        // O_x (+)= P_x V of V tile number t.  16 keys: 8 columns of P, 2048 bytes
+        // of V; P of 32 keys takes 16 columns (kSplit: 32, hi then lo, a product each)
+        auto pv = [&](int x, int t, bool first) {
+            const uint32_t vx = v_lo + (t % kVS) * (kTileBytes >> 4);
             const uint32_t p_col = tm + col_s(x), o_col = tm + col_o<D>(x);
 #pragma unroll
             for (int ks = 0; ks < kBN / 16; ++ks) {
@@ -454,68 +524,169 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc::commit_elect(&B.o_done[x]);
         };
-        int kt = 0, vt = 0;       // K and V tiles used
-        int sc[2] = {0, 0};       // score tiles of x issued; P.V number sc - 1 waits for them
+        auto have_k = [&](int t) { return wait_all(&B.k_full[t % kKS], (t / kKS) & 1); };
+        auto have_v = [&](int t) { return wait_all(&B.v_clean[t % kVS], (t / kVS) & 1); };
+        int kt = 0;          // K and V tiles of the items before
+        int sc[2] = {0, 0};  // score tiles of x issued; P_x V number sc - 1 waits for its P
         bool ok = true;
+        // This warp's own instructions are what a key tile's round waits for most,
+        // so the common item has a loop to itself, and waits and commits that
+        // nothing hangs on are put behind a P V, where the warp would wait anyway.
         for (int n = 0;; ++n) {
             const int is = n % kIS;
             ok = wait_all(&B.item_full[is], (n / kIS) & 1);
             if (!ok) break;
             const int valid = B.items[is].valid;
-            const Shape2 sh = shape2<kTree>(B.items[is].t, tq);
+            const Sides sd = sides_of<kTree>(B.items[is].t, tq);
             __syncwarp();
             if (lane == 0) mbar_arrive(&B.item_empty[is]);
             if (!valid) break;
-            const int nt = max(sh.tiles[0], sh.tiles[1]);
-            const int xl = sh.tiles[1] > 0 ? 1 : 0;  // the row tile served last
-            ok = wait_all(&B.q_full, n & 1) && wait_all(&B.k_full[kt % kKS], (kt / kKS) & 1);
-            for (int x = 0; ok && x <= xl; ++x) {
-                // P_x of the last item has been read
-                if (sc[x] > 0) ok = wait_all(&B.o_done[x], (sc[x] - 1) & 1);
-                if (!ok) break;
-                tc::fence_after_sync();
-                qk(x, kt);
-                ++sc[x];
-            }
-            if (!ok) break;
-            tc::commit_elect(&B.k_empty[kt % kKS]);
-            ++kt;
-            if (nt == 1) tc::commit_elect(&B.q_empty);
-            for (int j = 0; ok && j < nt; ++j) {
-                bool k_waited = false, v_waited = false;
-                for (int x = 0; ok && x <= xl; ++x) {
-                    if (j >= sh.tiles[x]) continue;
-                    ok = wait_all(&B.p_full[x], (sc[x] - 1) & 1);
-                    if (ok && !v_waited) ok = wait_all(&B.v_full[vt % kVS], (vt / kVS) & 1);
+            const int nt = sd.nt;
+            ok = wait_all(&B.q_full, n & 1) && have_k(kt);
+            if (sd.twin) {  // side x: tiles x, x + 2, ...
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (ok && x == 1) ok = have_k(kt + 1);
+                    if (ok && sc[x] > 0) ok = wait_all(&B.o_done[x], (sc[x] - 1) & 1);  // the last item's P V
                     if (!ok) break;
-                    v_waited = true;
                     tc::fence_after_sync();
-                    pv(x, vt, j == 0);
-                    if (x == xl) tc::commit_elect(&B.v_empty[vt % kVS]);
-                    if (j + 1 < sh.tiles[x]) {
-                        if (!k_waited) ok = wait_all(&B.k_full[kt % kKS], (kt / kKS) & 1);
-                        if (ok) ok = wait_all(&B.o_done[x], (sc[x] - 1) & 1);
+                    qk(x, 0, kt + x);
+                    ++sc[x];
+                    tc::commit_elect(&B.k_empty[(kt + x) % kKS]);
+                }
+                if (nt == 2) tc::commit_elect(&B.q_empty);
+                ok = ok && have_v(kt);
+                for (int j = 0; ok && j < nt; j += 2) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int t = kt + j + x;
+                        if (j + x >= nt) break;
+                        ok = wait_all(&B.p_full[x], (sc[x] - 1) & 1);
                         if (!ok) break;
-                        k_waited = true;
                         tc::fence_after_sync();
-                        qk(x, kt);
-                        ++sc[x];
-                        if (x == xl) tc::commit_elect(&B.k_empty[kt % kKS]);
+                        pv(x, t, j == 0);
+                        tc::commit_elect(&B.v_empty[t % kVS]);
+                        if (j + x + 1 < nt) ok = have_v(t + 1);
+                        if (j + x + 2 < nt) {
+                            ok = ok && have_k(t + 2) && wait_all(&B.o_done[x], (sc[x] - 1) & 1);
+                            if (!ok) break;
+                            tc::fence_after_sync();
+                            qk(x, 0, t + 2);
+                            ++sc[x];
+                            tc::commit_elect(&B.k_empty[(t + 2) % kKS]);
+                            if (j + x + 3 == nt) tc::commit_elect(&B.q_empty);
+                        }
                     }
                 }
-                ++vt;
-                if (j + 1 < nt) ++kt;
-                if (ok && j + 2 == nt) tc::commit_elect(&B.q_empty);
+            } else {
+                const int xl = sd.tiles[1] > 0 ? 1 : 0;  // the side served last
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (!ok || x > xl) break;
+                    if (sc[x] > 0) ok = wait_all(&B.o_done[x], (sc[x] - 1) & 1);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    qk(x, x, kt);
+                    ++sc[x];
+                }
+                tc::commit_elect(&B.k_empty[kt % kKS]);
+                if (nt == 1) tc::commit_elect(&B.q_empty);
+                ok = ok && have_v(kt);
+                for (int j = 0; ok && j < nt; ++j) {
+                    const int t = kt + j;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (j >= sd.tiles[x]) continue;
+                        ok = wait_all(&B.p_full[x], (sc[x] - 1) & 1);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        pv(x, t, j == 0);
+                        const bool more = j + 1 < nt;
+                        if (more && (x == 0 || j >= sd.tiles[0])) ok = have_k(t + 1);
+                        if (x == xl) {
+                            tc::commit_elect(&B.v_empty[t % kVS]);
+                            if (ok && more) ok = have_v(t + 1);
+                        }
+                        if (!ok) break;
+                        if (j + 1 < sd.tiles[x]) {
+                            ok = wait_all(&B.o_done[x], (sc[x] - 1) & 1);
+                            if (!ok) break;
+                            tc::fence_after_sync();
+                            qk(x, x, t + 1);
+                            ++sc[x];
+                            if (x == xl) tc::commit_elect(&B.k_empty[(t + 1) % kKS]);
+                        }
+                    }
+                    if (ok && j + 2 == nt) tc::commit_elect(&B.q_empty);
+                }
             }
             if (!ok) break;
+            kt += nt;
         }
         if (!ok && lane == 0) give_up();
         // every MMA issued so far has finished before tensor memory is freed
         tc::commit_elect(&B.mma_done);
         if (!__all_sync(0xffffffffu, mbar_wait_ns(&B.mma_done, 0, kWaitNs)) && lane == 0)
             flag(a.dev_status, PA_DEV_TIMEOUT);
+    } else if (warp == kCleanWarp) {
+        // ================================= V rows ==================================
+        regs_shrink<kOtherRegs>();
+        int vt = 0;
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            const int is = n % kIS;
+            ok = wait_all(&B.item_full[is], (n / kIS) & 1);
+            if (!ok || !B.items[is].valid) break;
+            const TreeItem t = B.items[is].t;
+            for (int j = 0; j < t.b1 - t.b0; ++j, ++vt) {
+                const int blk = t.b0 + j, sv = vt % kVS;
+                const bool hist = kTree && blk < t.nh;
+                const int k0 = (blk - (hist ? 0 : t.nh)) * kBN;
+                const int v_end = hist ? t.L : kTree ? t.T : t.t0 + t.n_rows;  // keys that some row sees
+                const bool mixed = kTree ? !hist : k0 + kBN > t.t0 + 1;        // keys that only some rows see
+                ok = wait_all(&B.v_full[sv], (vt / kVS) & 1);
+                if (!ok) break;
+                if (mixed || k0 + kBN > v_end) {
+                    for (int r = lane; r < kBN; r += 32) {
+                        uint8_t* row = v_tile(sv) + r * 128;  // a key's row, 64 dims at a time
+                        if (k0 + r >= v_end) {
+#pragma unroll
+                            for (int c = 0; c < D / 8; ++c)
+                                *reinterpret_cast<uint4*>(row + (c >> 3) * kHalfBytes + ((c + lane) & 7) * 16) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                        } else if (mixed) {
+                            uint32_t acc = 0u;
+#pragma unroll
+                            for (int c = 0; c < D / 8; ++c) {
+                                const uint4 w = *reinterpret_cast<const uint4*>(row + (c >> 3) * kHalfBytes +
+                                                                                ((c + lane) & 7) * 16);
+                                acc = H2<T>::probe(w.x, H2<T>::probe(w.y, H2<T>::probe(w.z, H2<T>::probe(w.w, acc))));
+                            }
+                            if (bad16<T>(acc) || bad16<T>(acc >> 16)) {
+                                for (int c = 0; c < D / 2; ++c) {
+                                    uint32_t* w = reinterpret_cast<uint32_t*>(row + (c >> 5) * kHalfBytes) + (c & 31);
+                                    uint32_t y = *w;
+                                    if (bad16<T>(y)) y &= 0xffff0000u;
+                                    if (bad16<T>(y >> 16)) y &= 0x0000ffffu;
+                                    *w = y;
+                                }
+                                B.poison[is] = uint32_t(n) + 1u;
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B.v_clean[sv]);
+            }
+            if (ok && lane == 0) mbar_arrive(&B.item_empty[is]);
+        }
+        if (!ok && lane == 0) give_up();
+    } else if (warp > kCleanWarp) {
+        regs_shrink<kOtherRegs>();  // an idle warp: the whole warpgroup gives
     } else {
         // ================================= softmax =================================
+        regs_grow<kSoftmaxRegs>();
         const int x = warp >> 2;  // row tile
         const int quad = warp & 3;
         const int m = quad * 32 + lane;  // MMA row = tensor-memory lane
@@ -524,8 +695,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sl2 = a.scale_log2;
         const uint32_t sbase = tm + lane_addr + col_s(x);
         const uint32_t obase = tm + lane_addr + col_o<D>(x);
-        int sc = 0;  // score tiles taken
-        int vt = 0;  // V tiles passed
+        int sc = 0, sc_other = 0;  // score tiles of this side and of the other before this item
+        int twins = 0;       // twins before it
         bool ok = true;
         for (int n = 0; ok; ++n) {
             const int is = n % kIS;
@@ -533,11 +704,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             const TreeItem t = B.items[is].t;
             if (!B.items[is].valid) break;
-            const Shape2 sh = shape2<kTree>(t, tq);
-            const int nt = sh.tiles[x], nt_all = max(sh.tiles[0], sh.tiles[1]);
-            const bool row_ok = tr < tq && tr < sh.rows[x];
-            const int tt = t.t0 + x * tq + tr;  // the row's place in its sequence
-            const int row = t.row0 + x * tq + tr;
+            const Sides sd = sides_of<kTree>(t, tq);
+            const int nt = x ? sd.tiles[1] : sd.tiles[0];
+            const bool row_ok = tr < tq && tr < (x ? sd.rows[1] : sd.rows[0]);
+            const int tile_row = (sd.twin ? 0 : x * tq) + tr;
+            const int tt = t.t0 + tile_row;  // the row's place in its sequence
+            const int row = t.row0 + tile_row;
             const int P = a.c.page_size;
             const int32_t* table = kTree ? a.c.block_tables + int64_t(t.seq) * a.c.max_blocks : nullptr;
             const int PT = kTree ? kBN / P : 0;
@@ -547,15 +719,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int idx = blk * PT + lane;
                 return kTree && blk < t.nh && lane < PT && idx < npg ? __ldg(table + idx) : 0;
             };
-            // packed keys that some row of the item sees
-            const int p_end = kTree ? t.T : t.t0 + t.n_rows;
             float m_run = -INFINITY, l_run = 0.f;
-            int e_cur = entry(t.b0);
-            for (int j = 0; j < nt; ++j) {
-                const int blk = t.b0 + j;
+            int e_cur = entry(t.b0 + sd.tile(x, 0));
+            for (int i = 0; i < nt; ++i) {
+                const int blk = t.b0 + sd.tile(x, i);
                 const bool hist = kTree && blk < t.nh;
                 const int k0 = (blk - (hist ? 0 : t.nh)) * kBN;  // first key, of the history or the packed rows
-                const int e_nxt = kTree && j + 1 < nt ? entry(blk + 1) : 0;
+                const int e_nxt = kTree && i + 1 < nt ? entry(t.b0 + sd.tile(x, i + 1)) : 0;
                 uint32_t see[4];  // keys of this tile that the row sees
                 bool full = false;
                 if (hist) {
@@ -584,132 +754,85 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < 4; ++c) see[c] = low_bits(lim - 32 * c);
                 }
                 e_cur = e_nxt;
-                ok = wait_all(&B.s_full[x], sc & 1);
+                ok = wait_all(&B.s_full[x], (sc + i) & 1);
                 if (!ok) break;
-                ++sc;
                 tc::fence_after_sync();
 
-                // ---- pass 1: row max of the raw scores (scale > 0 keeps the order)
-                float mx = -INFINITY;
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t r[32];
-                    tc::ld_32x32b_x32(sbase + 32 * c, r);
+                // ---- p = 2^(s * scale_log2 - m_run) of the row's 128 scores
+                uint32_t r[4][32];
+                float sum;
+                {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tc::ld_32x32b_x32(sbase + 32 * c, r[c]);
                     tc::wait_ld();
-                    tc::reg_fence(r);
-                    if (!full) apply_mask(r, c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3]);
-                    float m0 = mx, m1 = -INFINITY;
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        m0 = max3(m0, __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
-                        m1 = max3(m1, __uint_as_float(r[k + 2]), __uint_as_float(r[k + 3]));
+                    for (int c = 0; c < 4; ++c) {
+                        tc::reg_fence(r[c]);
+                        if (!full) apply_mask(r[c], see[c]);
                     }
-                    mx = fmaxf(m0, m1);
-                }
-                const float mt = mx * sl2;  // -inf when nothing is visible
-                const bool need = mt > m_run + kRescaleStep;
-                const float alpha = need ? ex2(m_run - mt) : 1.f;
-                if (need) m_run = mt;
-                l_run *= alpha;
-
-                // O_x is rescaled in place: the last P_x V has finished (S_x was
-                // issued after it)
-                if (j > 0 && __any_sync(0xffffffffu, need)) {
-#pragma unroll 1
-                    for (int c = 0; c < D / 16; ++c) {
-                        uint32_t ro[16];
-                        tc::ld_32x32b_x16(obase + 16 * c, ro);
-                        tc::wait_ld();
-                        tc::reg_fence(ro);
+                    float mx[4];
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) ro[k] = __float_as_uint(__uint_as_float(ro[k]) * alpha);
-                        tc::st_32x32b_x16(obase + 16 * c, ro);
-                    }
-                }
-
-                // ---- pass 2: p = 2^(s * scale_log2 - m_run) over the scores
-                const float nmu = m_run == -INFINITY ? 0.f : -m_run;
-                const uint64_t sl2_2 = f2_pack(__float_as_uint(sl2), __float_as_uint(sl2));
-                const uint64_t nmu_2 = f2_pack(__float_as_uint(nmu), __float_as_uint(nmu));
-                uint64_t sum_2 = f2_pack(0u, 0u);
+                    for (int c = 0; c < 4; ++c) mx[c] = max32(r[c]);
+                    const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
+                    const bool need = mt > m_run + kRescaleStep;
+                    // raise the max and rescale O in place: the last P V has
+                    // finished (these scores were issued after it)
+                    const float alpha = need ? ex2(m_run - mt) : 1.f;
+                    if (need) m_run = mt;
+                    l_run *= alpha;
+                    if (i > 0 && __any_sync(0xffffffffu, need)) {
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t r[32];
-                    tc::ld_32x32b_x32(sbase + 32 * c, r);
-                    tc::wait_ld();
-                    tc::reg_fence(r);
-                    if (!full) apply_mask(r, c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3]);
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t ro[16];
+                            tc::ld_32x32b_x16(obase + 16 * c, ro);
+                            tc::wait_ld();
+                            tc::reg_fence(ro);
 #pragma unroll
-                    for (int w = 0; w < 16; ++w) {
-                        uint32_t z0, z1;
-                        f2_unpack(f2_fma(f2_pack(r[2 * w], r[2 * w + 1]), sl2_2, nmu_2), z0, z1);
-                        const float p0 = ex2(__uint_as_float(z0)), p1 = ex2(__uint_as_float(z1));
-                        const uint64_t pp = f2_pack(__float_as_uint(p0), __float_as_uint(p1));
-                        sum_2 = f2_add(sum_2, pp);
-                        r[2 * w] = H2<T>::pack(p0, p1);
-                        if constexpr (kSplit) {
-                            uint32_t d0, d1;
-                            f2_unpack(f2_sub(pp, H2<T>::unpack(r[2 * w])), d0, d1);
-                            r[2 * w + 1] = H2<T>::pack(__uint_as_float(d0), __uint_as_float(d1));
+                            for (int k = 0; k < 16; ++k) ro[k] = __float_as_uint(__uint_as_float(ro[k]) * alpha);
+                            tc::st_32x32b_x16(obase + 16 * c, ro);
                         }
                     }
-                    if constexpr (kSplit) {
-                        tc::st_32x32b_x16_stride2<0>(sbase + 32 * c, r);
-                        tc::st_32x32b_x16_stride2<1>(sbase + 32 * c + 16, r);
-                    } else {
-                        tc::st_32x32b_x16_stride2<0>(sbase + 16 * c, r);
-                    }
-                }
-                uint32_t sum0, sum1;
-                f2_unpack(sum_2, sum0, sum1);
-                l_run += __uint_as_float(sum0) + __uint_as_float(sum1);
-                tc::wait_st();
-
-                // ---- V rows that not every row sees: once per key tile, by tile A's
-                // warps (by tile B's in the tile that B alone has), before their
-                // P is handed over; the MMA warp takes B's product after A's.
-                const int v_end = hist ? t.L : p_end;  // keys some row sees
-                const bool mixed = kTree ? !hist : k0 + kBN > t.t0 + 1;
-                if ((x == 0 || j >= sh.tiles[0]) && (mixed || k0 + kBN > v_end)) {
-                    const int sv = (vt + j) % kVS;
-                    ok = wait_all(&B.v_full[sv], ((vt + j) / kVS) & 1);
-                    if (!ok) break;
-                    uint8_t* vrow = v_tile(sv) + m * 128;  // a key's row, 64 dims at a time
-                    bool touched = false;
-                    if (k0 + m >= v_end) {
+                                    const float nmu = m_run == -INFINITY ? 0.f : -m_run;  // nothing seen yet: weights 0, not NaN
+                    const uint64_t sl2_2 = f2_pack(__float_as_uint(sl2), __float_as_uint(sl2));
+                    const uint64_t nmu_2 = f2_pack(__float_as_uint(nmu), __float_as_uint(nmu));
+                    uint64_t sum_2[2] = {f2_pack(0u, 0u), f2_pack(0u, 0u)};
 #pragma unroll
-                        for (int c = 0; c < D / 8; ++c)
-                            *reinterpret_cast<uint4*>(vrow + (c >> 3) * kHalfBytes + ((c + lane) & 7) * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
-                        touched = true;
-                    } else if (mixed) {
-                        uint32_t acc = 0u;
+                    for (int c = 0; c < 4; ++c) {
 #pragma unroll
-                        for (int c = 0; c < D / 8; ++c) {
-                            const uint4 w = *reinterpret_cast<const uint4*>(vrow + (c >> 3) * kHalfBytes +
-                                                                            ((c + lane) & 7) * 16);
-                            acc = H2<T>::probe(w.x, H2<T>::probe(w.y, H2<T>::probe(w.z, H2<T>::probe(w.w, acc))));
-                        }
-                        if (bad16<T>(acc) || bad16<T>(acc >> 16)) {
-                            for (int c = 0; c < D / 2; ++c) {
-                                uint32_t* w = reinterpret_cast<uint32_t*>(vrow + (c >> 5) * kHalfBytes) + (c & 31);
-                                uint32_t y = *w;
-                                if (bad16<T>(y)) y &= 0xffff0000u;
-                                if (bad16<T>(y >> 16)) y &= 0x0000ffffu;
-                                *w = y;
+                        for (int w = 0; w < 16; ++w) {
+                            uint32_t z0, z1;
+                            f2_unpack(f2_fma(f2_pack(r[c][2 * w], r[c][2 * w + 1]), sl2_2, nmu_2), z0, z1);
+                            const float p0 = ex2(__uint_as_float(z0)), p1 = ex2(__uint_as_float(z1));
+                            const uint64_t pp = f2_pack(__float_as_uint(p0), __float_as_uint(p1));
+                            sum_2[w & 1] = f2_add(sum_2[w & 1], pp);
+                            r[c][2 * w] = H2<T>::pack(p0, p1);
+                            if constexpr (kSplit) {
+                                uint32_t d0, d1;
+                                f2_unpack(f2_sub(pp, H2<T>::unpack(r[c][2 * w])), d0, d1);
+                                r[c][2 * w + 1] = H2<T>::pack(__uint_as_float(d0), __uint_as_float(d1));
                             }
-                            B.poison[is] = uint32_t(n) + 1u;
-                            touched = true;
                         }
                     }
-                    if (touched) fence_proxy_async_smem();
+                    uint32_t s0, s1;
+                    f2_unpack(f2_add(sum_2[0], sum_2[1]), s0, s1);
+                    sum = __uint_as_float(s0) + __uint_as_float(s1);
                 }
+                l_run += sum;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if constexpr (kSplit) {
+                        tc::st_32x32b_x16_stride2<0>(sbase + 32 * c, r[c]);
+                        tc::st_32x32b_x16_stride2<1>(sbase + 32 * c + 16, r[c]);
+                    } else {
+                        tc::st_32x32b_x16_stride2<0>(sbase + 16 * c, r[c]);
+                    }
+                }
+                tc::wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&B.p_full[x]);
             }
             if (!ok) break;
-            vt += nt_all;
 
             // Puts right 32 dims of a row that sees a NaN or infinity in V: one
             // that was kept out of P.V, or that met a zero part of P there.  What
@@ -744,55 +867,107 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!isfinite(f[k])) r[k] = __float_as_uint(f[k]);
             };
 
-            // ---- epilogue: O / l, or the piece's max, sum and O into its slot --------
+            // ---- epilogue: O / l, or the piece's max, sum and O into its slot.  A
+            // twin's rows are joined: each side writes half of the dims.
+            sc += nt;
+            sc_other += x ? sd.tiles[0] : sd.tiles[1];
             if (nt > 0) {
                 ok = wait_all(&B.o_done[x], (sc - 1) & 1);
+                if (ok && sd.twin) ok = wait_all(&B.o_done[1 - x], (sc_other - 1) & 1);
                 if (!ok) break;
                 tc::fence_after_sync();
                 const bool poison = *reinterpret_cast<volatile uint32_t*>(&B.poison[is]) == uint32_t(n) + 1u;
                 const bool piece = kTree && t.slot >= 0;
-                const float inv = piece ? 1.f : l_run == 0.f ? 0.f : 1.f / l_run;
-                const int r_unit = (x * tq + tr) * G + h;  // distribution of the unit
+                float2 w = make_float2(1.f, 0.f);  // what side A's (or the only) O counts, and side B's
+                if (sd.twin) {  // threads m of both sides hold the same row: B's figures, then A's verdict
+                    if (x == 1) {
+                        B.side[m] = make_float2(m_run, l_run);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&B.side_b);
+                    } else {
+                        ok = wait_all(&B.side_b, twins & 1);
+                        if (!ok) break;
+                        const float2 o = B.side[m];
+                        const float top = fmaxf(m_run, o.x), base = top == -INFINITY ? 0.f : top;
+                        w = make_float2(ex2(m_run - base), ex2(o.x - base));
+                        // max drops NaN, so a sum may be NaN beside a max of -inf
+                        l_run = (l_run == 0.f ? 0.f : l_run * (m_run == -INFINITY ? 1.f : w.x)) +
+                                (o.y == 0.f ? 0.f : o.y * (o.x == -INFINITY ? 1.f : w.y));
+                        m_run = top;
+                    }
+                }
+                if (!piece && (x == 0 || !sd.twin)) {
+                    const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+                    w.x *= inv;
+                    w.y *= inv;
+                }
+                if (sd.twin) {
+                    if (x == 0) {
+                        B.side[m] = w;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&B.side_w);
+                    } else {
+                        ok = wait_all(&B.side_w, twins & 1);
+                        if (!ok) break;
+                        w = B.side[m];
+                    }
+                    ++twins;
+                }
+                const int r_unit = tile_row * G + h;  // distribution of the unit
                 float* slot = piece ? static_cast<float*>(a.workspace) + slot_floats(2 * kBM, D) * t.slot : nullptr;
                 TOut* orow = static_cast<TOut*>(a.out) + (int64_t(row) * a.Hq + t.g * G + h) * D;
-                if (piece && row_ok) *reinterpret_cast<float2*>(slot + 2 * r_unit) = make_float2(m_run, l_run);
+                if (piece && row_ok && (x == 0 || !sd.twin))
+                    *reinterpret_cast<float2*>(slot + 2 * r_unit) = make_float2(m_run, l_run);
+                const int c_lo = sd.twin ? x * (D / 64) : 0, c_hi = sd.twin ? c_lo + D / 64 : D / 32;
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
+                for (int c = c_lo; c < c_hi; ++c) {
                     uint32_t r[32];
-                    __syncwarp();  // the last round's rows may have parted
-                    tc::ld_32x32b_x32(obase + 32 * c, r);
-                    tc::wait_ld();
-                    tc::reg_fence(r);
+                    if (sd.twin) {
+                        uint32_t o[32];
+                        tc::ld_32x32b_x32(tm + lane_addr + col_o<D>(0) + 32 * c, r);
+                        tc::ld_32x32b_x32(tm + lane_addr + col_o<D>(1) + 32 * c, o);
+                        tc::wait_ld();
+                        tc::reg_fence(r);
+                        tc::reg_fence(o);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            r[k] = __float_as_uint(
+                                fmaf(__uint_as_float(r[k]), w.x, __uint_as_float(o[k]) * w.y));
+                    } else {
+                        tc::ld_32x32b_x32(obase + 32 * c, r);
+                        tc::wait_ld();
+                        tc::reg_fence(r);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * w.x);
+                    }
                     // x * 0 is NaN for NaNs and infinities alone
                     float z = 0.f;
 #pragma unroll
                     for (int k = 0; k < 32; ++k) z = fmaf(__uint_as_float(r[k]), 0.f, z);
-                    if (row_ok && l_run == l_run && (poison || z != z)) restore(r, t, row, tt, 32 * c);
-                    if (!row_ok) continue;
-                    if (piece) {
-                        float4* dst = reinterpret_cast<float4*>(slot + 4 * kBM + int64_t(r_unit) * D + 32 * c);
+                    if (row_ok && w.x == w.x && (poison || z != z)) restore(r, t, row, tt, 32 * c);
+                    __syncwarp();
+                    // row i of this lane's group of four: its lane's own dst
+                    auto row_at = [&](int i, uint64_t mine) {
+                        return reinterpret_cast<uint4*>(__shfl_sync(0xffffffffu, mine, (lane & 28) + i));
+                    };
+                    if (piece || kSplit) {
+                        const uint64_t mine = reinterpret_cast<uint64_t>(
+                            !row_ok ? nullptr : (piece ? slot + 4 * kBM + int64_t(r_unit) * D : reinterpret_cast<float*>(orow)) + 32 * c);
+                        uint4 y[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            dst[k] = make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]),
-                                                 __uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3]));
-                    } else if constexpr (kSplit) {
-                        float4* dst = reinterpret_cast<float4*>(orow + 32 * c);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            dst[k] = make_float4(__uint_as_float(r[4 * k]) * inv, __uint_as_float(r[4 * k + 1]) * inv,
-                                                 __uint_as_float(r[4 * k + 2]) * inv,
-                                                 __uint_as_float(r[4 * k + 3]) * inv);
+                        for (int k = 0; k < 8; ++k) y[k] = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+                        store_rows4(y, lane, [&](int i) { return row_at(i, mine); });
                     } else {
-                        uint4* dst = reinterpret_cast<uint4*>(orow + 32 * c);
+                        const uint64_t mine = reinterpret_cast<uint64_t>(row_ok ? orow + 32 * c : nullptr);
+                        uint4 y[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            uint32_t y[4];
+                            uint32_t* w4 = &y[k].x;
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                y[e] = H2<T>::pack(__uint_as_float(r[8 * k + 2 * e]) * inv,
-                                                   __uint_as_float(r[8 * k + 2 * e + 1]) * inv);
-                            dst[k] = make_uint4(y[0], y[1], y[2], y[3]);
+                                w4[e] = H2<T>::pack(__uint_as_float(r[8 * k + 2 * e]), __uint_as_float(r[8 * k + 2 * e + 1]));
                         }
+                        store_rows4(y, lane, [&](int i) { return row_at(i, mine); });
                     }
                 }
             }
@@ -893,8 +1068,13 @@ cudaError_t launch_typed(const PackedAttn& a, cudaStream_t st) {
         s.cap = int64_t(a.c.max_blocks) * a.c.page_size;
         ctas = a.n_ctas;
     } else {
-        p.n_units = (a.r.max_rows + 2 * p.tq - 1) / (2 * p.tq);
-        ctas = int64_t(p.n_units) * a.Hkv * a.r.num_seqs;
+        // Two row tiles share their K/V tiles; one alone makes twice as many, half
+        // as long units: for calls that would leave half of the SMs idle.
+        const int64_t per = int64_t(a.Hkv) * a.r.num_seqs;
+        const int pairs = (a.r.max_rows + 2 * p.tq - 1) / (2 * p.tq);
+        p.tu = per * pairs <= a.n_ctas / 2 ? p.tq : 2 * p.tq;
+        p.n_units = (a.r.max_rows + p.tu - 1) / p.tu;
+        ctas = per * p.n_units;
         if (ctas > a.n_ctas) ctas = a.n_ctas;
     }
     cudaError_t e = launch_pdl(kern, dim3(unsigned(ctas)), dim3(kThreads), Smem<D>::kBytes, st, mq, mk, mv, mkc, mvc, p);

@@ -159,6 +159,10 @@ PA_EXPORT pa_status pa_prompt(const pa_params* p, const pa_rows* r, const void* 
     if (st != PA_OK) return st;
     if ((st = check_rows(p, r, &a.r)) != PA_OK) return st;
     if (r->total_rows == 0) return PA_OK;
+    // the kernels number their tiles of 64 or 128 (row, head) pairs in 32 bits
+    const int tile = 64 / (p->num_q_heads / p->num_kv_heads);
+    if (((a.r.max_rows + tile - 1) / tile) * int64_t(p->num_kv_heads) * p->num_seqs > (1 << 30))
+        return PA_ERR_UNSUPPORTED;
     if (!q || !k || !v || !cu_lens || !out) return PA_ERR_NULL;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(cu_lens, 4))
         return PA_ERR_ALIGN;

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import sys
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -320,83 +321,96 @@ def prompt_params(*, num_seqs, num_q_heads, num_kv_heads, head_dim, scale=None, 
                        debug_timeout=debug_timeout)
 
 
-_TORCH_DTYPE = None
+_DTYPES = ()
 
 
-def _torch_dtype(code):
-    global _TORCH_DTYPE
-    if _TORCH_DTYPE is None:
+def _dtypes():
+    """torch's dtypes by dtype code, then int32."""
+    global _DTYPES
+    if not _DTYPES:
         import torch
-        _TORCH_DTYPE = {PA_F32: torch.float32, PA_F16: torch.float16, PA_BF16: torch.bfloat16}
-    return _TORCH_DTYPE[code]
+        _DTYPES = (torch.float32, torch.float16, torch.bfloat16, torch.int32)
+    return _DTYPES
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+# The messages are put together only when a check fails, and each property of a
+# tensor is asked for once: a small call's kernels take less time than careless
+# checks would.
 
-
-def _ints(t, n, device, what):
-    """Pointer of a contiguous int32 tensor of at least n elements."""
-    _need(t.element_size() == 4 and not t.is_floating_point() and t.numel() >= n and t.is_contiguous()
-          and t.device == device, f"{what}: a contiguous int32 tensor of at least {n} elements on {device}")
+def _ints(t, n, dev, what):
+    """Pointer of a contiguous int32 tensor of at least n elements on device number dev."""
+    if t.get_device() != dev or t.dtype is not _dtypes()[3] or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous int32 tensor of at least {n} elements on cuda:{dev}")
     return t.data_ptr()
 
 
-def _packed(t, code, rows, heads, dim, stride, device, what):
-    """Pointer of packed rows [rows][heads][dim], ``stride`` elements between rows."""
-    _need(t.dtype is _torch_dtype(code) and t.dim() == 3 and t.shape[0] >= rows and t.shape[1] == heads
-          and t.shape[2] == dim and t.device == device
-          and (rows == 0 or (t.stride(2) == 1 and (heads == 1 or t.stride(1) == dim)
-                             and (rows == 1 or t.stride(0) == (stride or heads * dim)))),
-          f"{what}: [{rows}][{heads}][{dim}] {_torch_dtype(code)}, rows {stride or heads * dim} elements apart, "
-          f"on {device}")
+def _packed(t, code, rows, heads, dim, stride, dev, what):
+    """Pointer of packed rows [rows or more][heads][dim], ``stride`` elements between rows."""
+    shape = t.shape
+    if (t.get_device() != dev or t.dtype is not _dtypes()[code] or len(shape) != 3 or shape[0] < rows
+            or shape[1] != heads or shape[2] != dim
+            or not (t.is_contiguous() if stride in (0, heads * dim) else t.stride() == (stride, dim, 1))):
+        raise ValueError(f"{what}: [{rows}][{heads}][{dim}] of {_dtypes()[code]}, rows "
+                         f"{stride or heads * dim} elements apart, on cuda:{dev}")
     return t.data_ptr()
 
 
-def _pool(t, p, device, what):
-    """Pointer of a K or V pool: the last slot of the last head and page lies inside the tensor's storage."""
-    hs = p.head_stride or p.head_dim
-    ts = p.token_stride or p.num_kv_heads * hs
-    ps = p.page_stride or p.page_size * ts
-    last = (p.num_pages - 1) * ps + (p.page_size - 1) * ts + (p.num_kv_heads - 1) * hs + p.head_dim
-    _need(t.dtype is _torch_dtype(p.kv_dtype) and t.device == device
-          and t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() >= last,
-          f"{what}: {last} elements of {_torch_dtype(p.kv_dtype)} on {device}")
+def _pool(t, p, dev, what):
+    """Pointer of a K or V pool: the last slot of the last head and page lies inside the tensor."""
+    last = p.num_pages * p.page_size * p.num_kv_heads * p.head_dim
+    if p.head_stride or p.token_stride or p.page_stride:
+        hs = p.head_stride or p.head_dim
+        ts = p.token_stride or p.num_kv_heads * hs
+        ps = p.page_stride or p.page_size * ts
+        last = (p.num_pages - 1) * ps + (p.page_size - 1) * ts + (p.num_kv_heads - 1) * hs + p.head_dim
+    if (t.get_device() != dev or t.dtype is not _dtypes()[p.kv_dtype]
+            or (t.numel() < last if t.is_contiguous() else _elements_behind(t) < last)):
+        raise ValueError(f"{what}: {last} elements of {_dtypes()[p.kv_dtype]} on cuda:{dev}")
     return t.data_ptr()
 
 
-def _status(t, device):
-    return None if t is None else _ints(t, 1, device, "dev_status")
+def _elements_behind(t):
+    """Elements of t's storage from its first one on."""
+    return t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
 
 
-class _on:
-    """The device of a call's tensors made current, and the stream's handle."""
-    __slots__ = ("device", "stream", "guard")
-
-    def __init__(self, t, stream):
-        _need(t.is_cuda, "tensors must be on a CUDA device")
-        self.device, self.stream, self.guard = t.device, stream, None
-
-    def __enter__(self):
-        import torch
-        if torch.cuda.current_device() != self.device.index:
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
-        return s.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _scratch(t, dev):
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor on cuda:{dev}")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _packed_out(p, r, q, out):
+def _status(t, dev):
+    return None if t is None else _ints(t, 1, dev, "dev_status")
+
+
+def _call(name, dev, stream, *args):
+    """The entry point with device number dev current, on the given stream or that device's current one."""
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    torch = sys.modules["torch"]  # the tensors came from it
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _call(name, dev, stream, *args)
+    # the current stream's handle as torch's own generated launchers get it: torch.cuda.current_stream()
+    # builds a Stream object first, which takes longer (2.8 us) than a kernel's launch
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    code = getattr(_lib or load(), name)(*args, handle)
+    if code:
+        raise PaError(code, name)
+
+
+def _new(make, size, dtype, like, stream):
+    """A tensor made for a call on `stream`: filled there, and not handed out again before the call has run."""
+    import torch
+    with torch.cuda.stream(stream):  # None: the current one
+        return make(size, dtype=dtype, device=like.device)
+
+
+def _packed_out(p, r, q, out, stream):
     import torch
     if out is None:
-        return torch.zeros((r.total_rows, p.num_q_heads, p.head_dim), dtype=_torch_dtype(p.out_dtype),
-                           device=q.device)
-    _packed(out, p.out_dtype, r.total_rows, p.num_q_heads, p.head_dim, 0, q.device, "out")
+        out = _new(torch.zeros, (r.total_rows, p.num_q_heads, p.head_dim), _dtypes()[p.out_dtype], q, stream)
     return out
 
 
@@ -404,14 +418,12 @@ def prompt(p: Params, r: Rows, q, k, v, cu_lens, out=None, dev_status=None, stre
     """Causal attention over whole packed prompts; q [rows][Hq][D], k and v
     [rows][Hkv][D] -> out [rows][Hq][D] in p.out_dtype.  Rows behind the last
     sequence keep what ``out`` held (zeros when it is made here)."""
-    n, d, hkv, dev = r.total_rows, p.head_dim, p.num_kv_heads, q.device
-    with _on(q, stream) as st:
-        out = _packed_out(p, r, q, out)
-        _check(load().pa_prompt(p, r, _packed(q, p.q_dtype, n, p.num_q_heads, d, r.q_stride, dev, "q"),
-                                _packed(k, p.kv_dtype, n, hkv, d, r.k_stride, dev, "k"),
-                                _packed(v, p.kv_dtype, n, hkv, d, r.v_stride, dev, "v"),
-                                _ints(cu_lens, p.num_seqs + 1, dev, "cu_lens"), out.data_ptr(),
-                                _status(dev_status, dev), st), "pa_prompt")
+    n, d, hq, hkv, dev = r.total_rows, p.head_dim, p.num_q_heads, p.num_kv_heads, q.get_device()
+    out = _packed_out(p, r, q, out, stream)
+    _call("pa_prompt", dev, stream, p, r,
+          _packed(q, p.q_dtype, n, hq, d, r.q_stride, dev, "q"), _packed(k, p.kv_dtype, n, hkv, d, r.k_stride, dev, "k"),
+          _packed(v, p.kv_dtype, n, hkv, d, r.v_stride, dev, "v"), _ints(cu_lens, p.num_seqs + 1, dev, "cu_lens"),
+          _packed(out, p.out_dtype, n, hq, d, 0, dev, "out"), _status(dev_status, dev))
     return out
 
 
@@ -423,23 +435,18 @@ def tree(p: Params, r: Rows, q, k, v, cu_lens, tree_mask, k_cache, v_cache, bloc
          context_lens, out=None, workspace=None, dev_status=None, stream=None):
     """Attention of drafted tokens over the paged history and one another:
     packed q, k, v as in ``prompt``, tree_mask [rows][mask_words] int32."""
-    import torch
-    n, d, hkv, dev, b = r.total_rows, p.head_dim, p.num_kv_heads, q.device, p.num_seqs
-    with _on(q, stream) as st:
-        out = _packed_out(p, r, q, out)
-        if workspace is None:
-            workspace = torch.empty(max(tree_workspace_size(p, r), 1), dtype=torch.uint8, device=dev)
-        _need(workspace.device == dev and workspace.is_contiguous(), f"workspace: contiguous, on {dev}")
-        words = r.mask_words or (r.max_rows + 31) // 32
-        _check(load().pa_tree(p, r, _packed(q, p.q_dtype, n, p.num_q_heads, d, r.q_stride, dev, "q"),
-                              _packed(k, p.kv_dtype, n, hkv, d, r.k_stride, dev, "k"),
-                              _packed(v, p.kv_dtype, n, hkv, d, r.v_stride, dev, "v"),
-                              _ints(cu_lens, b + 1, dev, "cu_lens"), _ints(tree_mask, n * words, dev, "tree_mask"),
-                              _pool(k_cache, p, dev, "k_cache"), _pool(v_cache, p, dev, "v_cache"),
-                              _ints(block_tables, b * p.max_blocks_per_seq, dev, "block_tables"),
-                              _ints(context_lens, b, dev, "context_lens"), out.data_ptr(), workspace.data_ptr(),
-                              workspace.numel() * workspace.element_size(), _status(dev_status, dev), st),
-               "pa_tree")
+    n, d, hq, hkv, dev, b = r.total_rows, p.head_dim, p.num_q_heads, p.num_kv_heads, q.get_device(), p.num_seqs
+    out = _packed_out(p, r, q, out, stream)
+    if workspace is None:
+        workspace = _new_scratch(tree_workspace_size(p, r), q, stream)
+    words = r.mask_words or (r.max_rows + 31) // 32
+    _call("pa_tree", dev, stream, p, r,
+          _packed(q, p.q_dtype, n, hq, d, r.q_stride, dev, "q"), _packed(k, p.kv_dtype, n, hkv, d, r.k_stride, dev, "k"),
+          _packed(v, p.kv_dtype, n, hkv, d, r.v_stride, dev, "v"), _ints(cu_lens, b + 1, dev, "cu_lens"),
+          _ints(tree_mask, n * words, dev, "tree_mask"), _pool(k_cache, p, dev, "k_cache"),
+          _pool(v_cache, p, dev, "v_cache"), _ints(block_tables, b * p.max_blocks_per_seq, dev, "block_tables"),
+          _ints(context_lens, b, dev, "context_lens"), _packed(out, p.out_dtype, n, hq, d, 0, dev, "out"),
+          *_scratch(workspace, dev), _status(dev_status, dev))
     return out
 
 
@@ -447,82 +454,65 @@ def store(p: Params, r: Rows, k, v, cu_lens, k_cache, v_cache, block_tables, con
           row_index=None, dev_status=None, stream=None):
     """Writes packed K/V rows (or, with row_index, chosen rows of them) to
     each sequence's last positions; k_cache and v_cache change in place."""
-    n, d, hkv, dev, b = r.total_rows, p.head_dim, p.num_kv_heads, k.device, p.num_seqs
+    n, d, hkv, dev, b = r.total_rows, p.head_dim, p.num_kv_heads, k.get_device(), p.num_seqs
     src = r.source_rows or n
-    with _on(k, stream) as st:
-        _check(load().pa_store(p, r, _packed(k, p.kv_dtype, src, hkv, d, r.k_stride, dev, "k"),
-                               _packed(v, p.kv_dtype, src, hkv, d, r.v_stride, dev, "v"),
-                               _ints(cu_lens, b + 1, dev, "cu_lens"),
-                               None if row_index is None else _ints(row_index, n, dev, "row_index"),
-                               _pool(k_cache, p, dev, "k_cache"), _pool(v_cache, p, dev, "v_cache"),
-                               _ints(block_tables, b * p.max_blocks_per_seq, dev, "block_tables"),
-                               _ints(context_lens, b, dev, "context_lens"), _status(dev_status, dev), st),
-               "pa_store")
+    _call("pa_store", dev, stream, p, r,
+          _packed(k, p.kv_dtype, src, hkv, d, r.k_stride, dev, "k"),
+          _packed(v, p.kv_dtype, src, hkv, d, r.v_stride, dev, "v"), _ints(cu_lens, b + 1, dev, "cu_lens"),
+          None if row_index is None else _ints(row_index, n, dev, "row_index"), _pool(k_cache, p, dev, "k_cache"),
+          _pool(v_cache, p, dev, "v_cache"), _ints(block_tables, b * p.max_blocks_per_seq, dev, "block_tables"),
+          _ints(context_lens, b, dev, "context_lens"), _status(dev_status, dev))
 
 
 def pages_workspace_size(p: Params) -> int:
     return int(load().pa_pages_workspace_size(p))
 
 
-def _bookkeeping(p, refcounts, block_tables, context_lens):
-    dev = refcounts.device
+def _new_scratch(n, like, stream):
+    import torch
+    return _new(torch.empty, max(n, 1), torch.uint8, like, stream)
+
+
+def _bookkeeping(p, refcounts, block_tables, context_lens, dev):
     return (_ints(refcounts, p.num_pages, dev, "refcounts"),
             _ints(block_tables, p.num_seqs * p.max_blocks_per_seq, dev, "block_tables"),
             _ints(context_lens, p.num_seqs, dev, "context_lens"))
-
-
-def _scratch(p, workspace, dev):
-    import torch
-    if workspace is None:
-        workspace = torch.empty(max(pages_workspace_size(p), 1), dtype=torch.uint8, device=dev)
-    _need(workspace.device == dev and workspace.is_contiguous(), f"workspace: contiguous, on {dev}")
-    return workspace
 
 
 def pages_resize(p: Params, refcounts, block_tables, context_lens, new_lens, pairs, workspace=None,
                  dev_status=None, stream=None):
     """Reserves, trims and frees pages: sequence s goes to new_lens[s] tokens
     (negative: left alone).  pairs [num_seqs][2] gets the copies to make."""
-    dev = refcounts.device
-    with _on(refcounts, stream) as st:
-        ws = _scratch(p, workspace, dev)
-        _check(load().pa_pages_resize(p, *_bookkeeping(p, refcounts, block_tables, context_lens),
-                                      _ints(new_lens, p.num_seqs, dev, "new_lens"),
-                                      _ints(pairs, 2 * p.num_seqs, dev, "pairs"), ws.data_ptr(),
-                                      ws.numel() * ws.element_size(), _status(dev_status, dev), st),
-               "pa_pages_resize")
+    dev = refcounts.get_device()
+    if workspace is None:
+        workspace = _new_scratch(pages_workspace_size(p), refcounts, stream)
+    _call("pa_pages_resize", dev, stream, p,
+          *_bookkeeping(p, refcounts, block_tables, context_lens, dev), _ints(new_lens, p.num_seqs, dev, "new_lens"),
+          _ints(pairs, 2 * p.num_seqs, dev, "pairs"), *_scratch(workspace, dev), _status(dev_status, dev))
 
 
 def pages_fork(p: Params, refcounts, block_tables, context_lens, src, dst, dev_status=None, stream=None):
     """Makes each empty sequence dst[i] a copy of src[i] that shares its pages."""
-    dev = refcounts.device
-    with _on(refcounts, stream) as st:
-        n = dst.numel()
-        _check(load().pa_pages_fork(p, *_bookkeeping(p, refcounts, block_tables, context_lens),
-                                    _ints(src, n, dev, "src"), _ints(dst, n, dev, "dst"), n,
-                                    _status(dev_status, dev), st), "pa_pages_fork")
+    dev, n = refcounts.get_device(), dst.numel()
+    _call("pa_pages_fork", dev, stream, p,
+          *_bookkeeping(p, refcounts, block_tables, context_lens, dev), _ints(src, n, dev, "src"),
+          _ints(dst, n, dev, "dst"), n, _status(dev_status, dev))
 
 
 def pages_compact(p: Params, refcounts, block_tables, context_lens, pairs, num_moves, workspace=None,
                   dev_status=None, stream=None):
     """Moves live pages to the low end of the pool, at most len(pairs) of
     them; pairs [n][2] gets the copies to make, num_moves [1] their number."""
-    dev = refcounts.device
-    with _on(refcounts, stream) as st:
-        ws = _scratch(p, workspace, dev)
-        n = pairs.numel() // 2
-        _check(load().pa_pages_compact(p, *_bookkeeping(p, refcounts, block_tables, context_lens),
-                                       _ints(pairs, 2 * n, dev, "pairs"), n,
-                                       _ints(num_moves, 1, dev, "num_moves"), ws.data_ptr(),
-                                       ws.numel() * ws.element_size(), _status(dev_status, dev), st),
-               "pa_pages_compact")
+    dev, n = refcounts.get_device(), pairs.numel() // 2
+    if workspace is None:
+        workspace = _new_scratch(pages_workspace_size(p), refcounts, stream)
+    _call("pa_pages_compact", dev, stream, p,
+          *_bookkeeping(p, refcounts, block_tables, context_lens, dev), _ints(pairs, 2 * n, dev, "pairs"), n,
+          _ints(num_moves, 1, dev, "num_moves"), *_scratch(workspace, dev), _status(dev_status, dev))
 
 
 def pages_copy(p: Params, k_cache, v_cache, pairs, dev_status=None, stream=None):
     """Copies page pairs[i][0] to pairs[i][1] in one layer's K and V; negative pairs are passed over."""
-    dev = k_cache.device
-    with _on(k_cache, stream) as st:
-        n = pairs.numel() // 2
-        _check(load().pa_pages_copy(p, _pool(k_cache, p, dev, "k_cache"), _pool(v_cache, p, dev, "v_cache"),
-                                    _ints(pairs, 2 * n, dev, "pairs"), n, _status(dev_status, dev), st),
-               "pa_pages_copy")
+    dev, n = k_cache.get_device(), pairs.numel() // 2
+    _call("pa_pages_copy", dev, stream, p, _pool(k_cache, p, dev, "k_cache"),
+          _pool(v_cache, p, dev, "v_cache"), _ints(pairs, 2 * n, dev, "pairs"), n, _status(dev_status, dev))
