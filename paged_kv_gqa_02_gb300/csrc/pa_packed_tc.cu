@@ -69,7 +69,7 @@ constexpr int kMmaWarp = 9;
 constexpr int kCleanWarp = 10;
 constexpr uint32_t kHalfBytes = kBN * 128;  // one 64-dim half of a tile
 constexpr uint64_t kWaitNs = 2000000000ull;  // a role gives up after 2 s on one barrier
-constexpr uint32_t kSleepNs = 20000;  // longest sleep inside one try_wait
+constexpr uint32_t kSleepNs = 20000;        // longest sleep inside one try_wait
 constexpr int kWaitSlices = int(kWaitNs / kSleepNs);
 constexpr float kRescaleStep = 8.f;
 constexpr uint32_t kNegInf = 0xff800000u;
@@ -111,16 +111,35 @@ struct TcArgs {
     int32_t tu, n_units;  // prompt: rows of a unit; units of the longest sequence per kv head
 };
 
-// Waits for a phase, suspended in slices of up to kSleepNs, kWaitSlices of them
-// at most, or until another role has given up.  Kept short: every role's waits
-// are copies of it, and instruction fetch is what the MMA warp waits for most.
+// Waits for a phase: one suspended try, then others of up to kSleepNs each, a
+// bounded number of them, until another role has given up.  Kept short: every
+// wait is a copy of this, and the SM's instruction cache is small.
 __device__ inline bool wait_bar(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
     if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < kWaitSlices; ++i) {
         if (mbar_try_wait_sleep(bar, parity, kSleepNs)) return true;
-        if (*abort_flag || globaltimer_ns() - t0 > kWaitNs) return false;
+        if (*abort_flag) return false;
     }
+    return false;
+}
+
+// MMA and commit by the lane for which `e` is 1, chosen once: an election inside
+// each MMA made a product of eight 3.8 KB of code and the MMA warp's pace the
+// kernel's (8192 rows, 64/8 heads: 744 against 714 us).
+__device__ inline uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+    return r;
+}
+__device__ inline void mma_ss1(uint32_t d, uint64_t a, uint64_t b, uint32_t i, bool acc, uint32_t e) {
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(i), "r"(acc ? 1u : 0u), "r"(e) : "memory");
+}
+__device__ inline void mma_ts1(uint32_t d, uint32_t a, uint64_t b, uint32_t i, bool acc, uint32_t e) {
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(i), "r"(acc ? 1u : 0u), "r"(e) : "memory");
+}
+__device__ inline void commit1(uint64_t* bar, uint32_t e) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(e) : "memory");
 }
 
 __device__ inline float max3(float a, float b, float c) {
@@ -271,6 +290,7 @@ struct PromptWalk {
     __device__ inline bool next(const TcArgs& p, TreeItem& it, uint32_t* status) {
         const PackedAttn& a = p.a;
         const int per = a.Hkv * a.r.num_seqs, all = per * p.n_units, n = gridDim.x, c = blockIdx.x;
+#pragma unroll 1
         for (;; ++round) {
             if (round * n >= all) return false;
             const int i = round * n + ((round & 1) ? n - 1 - c : c);
@@ -394,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         PromptWalk prompt = {0};
         if constexpr (kTree) {
             if (blockIdx.x == 0)
+#pragma unroll 1
                 for (int s = lane; s < p.shape.num_seqs; s += 32) {
                     const TreeSeq q = tree_seq(p.shape, s);
                     if (q.bad_rows || q.bad_len) flag(a.dev_status, PA_DEV_BAD_LEN);
@@ -424,6 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t* table = kTree ? a.c.block_tables + int64_t(t.seq) * a.c.max_blocks : nullptr;
             const int PT = kTree ? kBN / P : 0;
             const int npg = kTree ? (t.L + P - 1) / P : 0;
+#pragma unroll 1
             for (int j = 0; j < nt; ++j) {
                 const int blk = t.b0 + j;
                 const bool hist = kTree && blk < t.nh;
@@ -480,13 +502,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             if (!ok) give_up();
             // never leave the CTA with copies in flight
+#pragma unroll 1
             for (int j = max(0, kq - kKS); j < kq; ++j) mbar_wait_ns(&B.k_full[j % kKS], (j / kKS) & 1, kWaitNs);
+#pragma unroll 1
             for (int j = max(0, vq - kVS); j < vq; ++j) mbar_wait_ns(&B.v_full[j % kVS], (j / kVS) & 1, kWaitNs);
             if (qn > 0 && !mbar_wait_ns(&B.q_full, (qn - 1) & 1, kWaitNs)) flag(a.dev_status, PA_DEV_TIMEOUT);
         }
     } else if (warp == kMmaWarp) {
         // ================================== MMA ===================================
         regs_shrink<kOtherRegs>();
+        const uint32_t el = elect_one();
         const uint32_t idQK = tc::idesc_f16(kBM, kBN, kBf16, false);
         const uint32_t idPV = tc::idesc_f16(kBM, D, kBf16, true);
         // descriptors: the high word is shared, low words advance by offset >> 4
@@ -501,10 +526,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 const uint32_t off = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
-                tc::mma_ss_elect(tm + col_s(x), tc::make_desc(qx + off, hi_d), tc::make_desc(kx + off, hi_d), idQK,
-                                 ks > 0);
+                mma_ss1(tm + col_s(x), tc::make_desc(qx + off, hi_d), tc::make_desc(kx + off, hi_d), idQK,
+                                 ks > 0, el);
             }
-            tc::commit_elect(&B.s_full[x]);
+            commit1(&B.s_full[x], el);
         };
         // O_x (+)= P_x V of V tile number t.  16 keys: 8 columns of P, 2048 bytes
         // of V; P of 32 keys takes 16 columns (kSplit: 32, hi then lo, a product each)
@@ -516,116 +541,103 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t bd = tc::make_desc(vx + ks * (2048 >> 4), hi_d);
                 if constexpr (kSplit) {
                     const uint32_t col = p_col + 32 * (ks >> 1) + 8 * (ks & 1);
-                    tc::mma_ts_elect(o_col, col, bd, idPV, !first || ks > 0);
-                    tc::mma_ts_elect(o_col, col + 16, bd, idPV, true);
+                    mma_ts1(o_col, col, bd, idPV, !first || ks > 0, el);
+                    mma_ts1(o_col, col + 16, bd, idPV, true, el);
                 } else {
-                    tc::mma_ts_elect(o_col, p_col + 8 * ks, bd, idPV, !first || ks > 0);
+                    mma_ts1(o_col, p_col + 8 * ks, bd, idPV, !first || ks > 0, el);
                 }
             }
-            tc::commit_elect(&B.o_done[x]);
+            commit1(&B.o_done[x], el);
         };
         auto have_k = [&](int t) { return wait_all(&B.k_full[t % kKS], (t / kKS) & 1); };
         auto have_v = [&](int t) { return wait_all(&B.v_clean[t % kVS], (t / kVS) & 1); };
         int kt = 0;          // K and V tiles of the items before
         int sc[2] = {0, 0};  // score tiles of x issued; P_x V number sc - 1 waits for its P
-        bool ok = true;
-        // This warp's own instructions are what a key tile's round waits for most,
-        // so the common item has a loop to itself, and waits and commits that
-        // nothing hangs on are put behind a P V, where the warp would wait anyway.
-        for (int n = 0;; ++n) {
-            const int is = n % kIS;
-            ok = wait_all(&B.item_full[is], (n / kIS) & 1);
-            if (!ok) break;
-            const int valid = B.items[is].valid;
-            const Sides sd = sides_of<kTree>(B.items[is].t, tq);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&B.item_empty[is]);
-            if (!valid) break;
-            const int nt = sd.nt;
-            ok = wait_all(&B.q_full, n & 1) && have_k(kt);
-            if (sd.twin) {  // side x: tiles x, x + 2, ...
+        // The pair of an item's side x with tile t: P V, and behind it, where this
+        // warp would wait anyway, the commits and the next tiles' waits.
+        auto take_p = [&](int x, int t, bool first) {
+            if (!wait_all(&B.p_full[x], (sc[x] - 1) & 1)) return false;
+            tc::fence_after_sync();
+            pv(x, t, first);
+            return true;
+        };
+        // Q K^T of the side's next tile takes the place of its P (of the last
+        // item's, at first): once that P V is done
+        auto next_s = [&](int x, int qt, int t) {
+            if (sc[x] > 0 && !wait_all(&B.o_done[x], (sc[x] - 1) & 1)) return false;
+            tc::fence_after_sync();
+            qk(x, qt, t);
+            ++sc[x];
+            return true;
+        };
+        auto run_twin = [&](int nt) {  // side x: tiles x, x + 2, ...
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (x == 1 && !have_k(kt + 1)) return false;
+                if (!next_s(x, 0, kt + x)) return false;
+                commit1(&B.k_empty[(kt + x) % kKS], el);
+            }
+            if (nt == 2) commit1(&B.q_empty, el);
+            if (!have_v(kt)) return false;
+#pragma unroll 1
+            for (int j = 0; j < nt; j += 2) {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    if (ok && x == 1) ok = have_k(kt + 1);
-                    if (ok && sc[x] > 0) ok = wait_all(&B.o_done[x], (sc[x] - 1) & 1);  // the last item's P V
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    qk(x, 0, kt + x);
-                    ++sc[x];
-                    tc::commit_elect(&B.k_empty[(kt + x) % kKS]);
-                }
-                if (nt == 2) tc::commit_elect(&B.q_empty);
-                ok = ok && have_v(kt);
-                for (int j = 0; ok && j < nt; j += 2) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int t = kt + j + x;
-                        if (j + x >= nt) break;
-                        ok = wait_all(&B.p_full[x], (sc[x] - 1) & 1);
-                        if (!ok) break;
-                        tc::fence_after_sync();
-                        pv(x, t, j == 0);
-                        tc::commit_elect(&B.v_empty[t % kVS]);
-                        if (j + x + 1 < nt) ok = have_v(t + 1);
-                        if (j + x + 2 < nt) {
-                            ok = ok && have_k(t + 2) && wait_all(&B.o_done[x], (sc[x] - 1) & 1);
-                            if (!ok) break;
-                            tc::fence_after_sync();
-                            qk(x, 0, t + 2);
-                            ++sc[x];
-                            tc::commit_elect(&B.k_empty[(t + 2) % kKS]);
-                            if (j + x + 3 == nt) tc::commit_elect(&B.q_empty);
-                        }
+                    const int t = kt + j + x;
+                    if (j + x >= nt) return true;
+                    if (!take_p(x, t, j == 0)) return false;
+                    commit1(&B.v_empty[t % kVS], el);
+                    if (j + x + 1 < nt && !have_v(t + 1)) return false;
+                    if (j + x + 2 < nt) {
+                        if (!have_k(t + 2) || !next_s(x, 0, t + 2)) return false;
+                        commit1(&B.k_empty[(t + 2) % kKS], el);
+                        if (j + x + 3 == nt) commit1(&B.q_empty, el);
                     }
-                }
-            } else {
-                const int xl = sd.tiles[1] > 0 ? 1 : 0;  // the side served last
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (!ok || x > xl) break;
-                    if (sc[x] > 0) ok = wait_all(&B.o_done[x], (sc[x] - 1) & 1);
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    qk(x, x, kt);
-                    ++sc[x];
-                }
-                tc::commit_elect(&B.k_empty[kt % kKS]);
-                if (nt == 1) tc::commit_elect(&B.q_empty);
-                ok = ok && have_v(kt);
-                for (int j = 0; ok && j < nt; ++j) {
-                    const int t = kt + j;
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        if (j >= sd.tiles[x]) continue;
-                        ok = wait_all(&B.p_full[x], (sc[x] - 1) & 1);
-                        if (!ok) break;
-                        tc::fence_after_sync();
-                        pv(x, t, j == 0);
-                        const bool more = j + 1 < nt;
-                        if (more && (x == 0 || j >= sd.tiles[0])) ok = have_k(t + 1);
-                        if (x == xl) {
-                            tc::commit_elect(&B.v_empty[t % kVS]);
-                            if (ok && more) ok = have_v(t + 1);
-                        }
-                        if (!ok) break;
-                        if (j + 1 < sd.tiles[x]) {
-                            ok = wait_all(&B.o_done[x], (sc[x] - 1) & 1);
-                            if (!ok) break;
-                            tc::fence_after_sync();
-                            qk(x, x, t + 1);
-                            ++sc[x];
-                            if (x == xl) tc::commit_elect(&B.k_empty[(t + 1) % kKS]);
-                        }
-                    }
-                    if (ok && j + 2 == nt) tc::commit_elect(&B.q_empty);
                 }
             }
-            if (!ok) break;
-            kt += nt;
-        }
-        if (!ok && lane == 0) give_up();
+            return true;
+        };
+        auto run_pair = [&](const Sides& sd) {  // both sides take every tile (A alone, where there is no B)
+            const int nt = sd.nt;
+            const bool two = sd.tiles[1] > 0;
+            if (!next_s(0, 0, kt) || (two && !next_s(1, 1, kt))) return false;
+            commit1(&B.k_empty[kt % kKS], el);
+            if (nt == 1) commit1(&B.q_empty, el);
+            if (!have_v(kt)) return false;
+#pragma unroll 1
+            for (int j = 0; j < nt; ++j) {
+                const int t = kt + j;
+                const bool more = j + 1 < nt;
+                if (j < sd.tiles[0] && !take_p(0, t, j == 0)) return false;
+                if (more && !have_k(t + 1)) return false;
+                if (j + 1 < sd.tiles[0] && !next_s(0, 0, t + 1)) return false;
+                if (two && !take_p(1, t, j == 0)) return false;
+                commit1(&B.v_empty[t % kVS], el);
+                if (!more) return true;
+                if (!have_v(t + 1) || (two && !next_s(1, 1, t + 1))) return false;
+                commit1(&B.k_empty[(t + 1) % kKS], el);
+                if (j + 2 == nt) commit1(&B.q_empty, el);
+            }
+            return true;
+        };
+        auto run = [&]() {
+#pragma unroll 1
+            for (int n = 0;; ++n) {
+                const int is = n % kIS;
+                if (!wait_all(&B.item_full[is], (n / kIS) & 1)) return false;
+                const int valid = B.items[is].valid;
+                const Sides sd = sides_of<kTree>(B.items[is].t, tq);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B.item_empty[is]);
+                if (!valid) return true;
+                if (!wait_all(&B.q_full, n & 1) || !have_k(kt)) return false;
+                if (!(sd.twin ? run_twin(sd.nt) : run_pair(sd))) return false;
+                kt += sd.nt;
+            }
+        };
+        if (!run() && lane == 0) give_up();
         // every MMA issued so far has finished before tensor memory is freed
-        tc::commit_elect(&B.mma_done);
+        commit1(&B.mma_done, el);
         if (!__all_sync(0xffffffffu, mbar_wait_ns(&B.mma_done, 0, kWaitNs)) && lane == 0)
             flag(a.dev_status, PA_DEV_TIMEOUT);
     } else if (warp == kCleanWarp) {
@@ -638,6 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = wait_all(&B.item_full[is], (n / kIS) & 1);
             if (!ok || !B.items[is].valid) break;
             const TreeItem t = B.items[is].t;
+#pragma unroll 1
             for (int j = 0; j < t.b1 - t.b0; ++j, ++vt) {
                 const int blk = t.b0 + j, sv = vt % kVS;
                 const bool hist = kTree && blk < t.nh;
@@ -647,6 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = wait_all(&B.v_full[sv], (vt / kVS) & 1);
                 if (!ok) break;
                 if (mixed || k0 + kBN > v_end) {
+#pragma unroll 1
                     for (int r = lane; r < kBN; r += 32) {
                         uint8_t* row = v_tile(sv) + r * 128;  // a key's row, 64 dims at a time
                         if (k0 + r >= v_end) {
@@ -663,6 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 acc = H2<T>::probe(w.x, H2<T>::probe(w.y, H2<T>::probe(w.z, H2<T>::probe(w.w, acc))));
                             }
                             if (bad16<T>(acc) || bad16<T>(acc >> 16)) {
+#pragma unroll 1
                                 for (int c = 0; c < D / 2; ++c) {
                                     uint32_t* w = reinterpret_cast<uint32_t*>(row + (c >> 5) * kHalfBytes) + (c & 31);
                                     uint32_t y = *w;
@@ -721,6 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             float m_run = -INFINITY, l_run = 0.f;
             int e_cur = entry(t.b0 + sd.tile(x, 0));
+#pragma unroll 1
             for (int i = 0; i < nt; ++i) {
                 const int blk = t.b0 + sd.tile(x, i);
                 const bool hist = kTree && blk < t.nh;
@@ -838,29 +854,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             // that was kept out of P.V, or that met a zero part of P there.  What
             // the row sees of them is the result, whatever the rest adds up to.
             auto restore = [&](uint32_t (&r)[32], const TreeItem& it, int at, int place, int d0) {
-                float f[32];
-#pragma unroll
+                float f[32];  // rolled loops and local memory: rare, and small code
+#pragma unroll 1
                 for (int k = 0; k < 32; ++k) f[k] = 0.f;
-                auto add = [&](const T* v) {
-#pragma unroll
+                const int n_hist = kTree ? max(0, min(it.L, min(it.b1, it.nh) * kBN) - it.b0 * kBN) : 0;
+                const int k_lo = max(0, it.b0 - it.nh) * kBN;
+                const int k_hi = kTree ? min(it.T, max(0, it.b1 - it.nh) * kBN) : place + 1;
+#pragma unroll 1
+                for (int i = 0; i < n_hist + max(0, k_hi - k_lo); ++i) {
+                    const T* v;
+                    if (kTree && i < n_hist) {
+                        const int key = it.b0 * kBN + i, pg = table[key / P];
+                        if (pg < 0 || pg >= a.c.num_pages) continue;
+                        v = static_cast<const T*>(a.c.v) + int64_t(pg) * a.c.page_stride +
+                            int64_t(key % P) * a.c.token_stride + int64_t(it.g) * a.c.head_stride + d0;
+                    } else {
+                        const int key = k_lo + i - n_hist;
+                        if (kTree && ((key >> 5) >= a.mask_words ||
+                                      !((a.tree_mask[int64_t(at) * a.mask_words + (key >> 5)] >> (key & 31)) & 1u)))
+                            continue;
+                        v = static_cast<const T*>(a.v) + int64_t(it.row0 - it.t0 + key) * a.r.v_stride + it.g * D + d0;
+                    }
+#pragma unroll 1
                     for (int k = 0; k < 32; ++k) {
                         const float y = Elt<T>::f(v[k]);
                         if (!isfinite(y)) f[k] += y;
                     }
-                };
-                for (int key = it.b0 * kBN; kTree && key < min(it.L, min(it.b1, it.nh) * kBN); ++key) {
-                    const int pg = table[key / P];
-                    if (pg >= 0 && pg < a.c.num_pages)
-                        add(static_cast<const T*>(a.c.v) + int64_t(pg) * a.c.page_stride +
-                            int64_t(key % P) * a.c.token_stride + int64_t(it.g) * a.c.head_stride + d0);
-                }
-                const int k_lo = max(0, it.b0 - it.nh) * kBN;
-                const int k_hi = kTree ? min(it.T, max(0, it.b1 - it.nh) * kBN) : place + 1;
-                for (int key = k_lo; key < k_hi; ++key) {
-                    if (kTree && ((key >> 5) >= a.mask_words ||
-                                  !((a.tree_mask[int64_t(at) * a.mask_words + (key >> 5)] >> (key & 31)) & 1u)))
-                        continue;
-                    add(static_cast<const T*>(a.v) + int64_t(it.row0 - it.t0 + key) * a.r.v_stride + it.g * D + d0);
                 }
 #pragma unroll
                 for (int k = 0; k < 32; ++k)

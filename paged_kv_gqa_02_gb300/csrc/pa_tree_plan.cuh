@@ -65,6 +65,7 @@ __device__ inline int64_t warp_sum64(int64_t v) {
 // s.  The whole warp.
 __device__ inline int64_t tree_total(const TreeShape& a, int s, int64_t* before) {
     int64_t all = 0, ahead = 0;
+#pragma unroll 1
     for (int i = threadIdx.x & 31; i < a.num_seqs; i += 32) {
         const int64_t c = tree_seq_cost(a, tree_seq(a, i));
         all += c;
@@ -107,6 +108,7 @@ struct TreeWalk {
         end = share_start(total, n, c + 1);
         seq_at = 0;
         // the sequence that position `at` lies in, 32 at a time
+#pragma unroll 1
         for (int base = 0;; base += 32) {
             const int i = base + int(threadIdx.x & 31);
             const int64_t c1 = i < a.num_seqs ? tree_seq_cost(a, tree_seq(a, i)) : 0;
@@ -130,7 +132,9 @@ struct TreeWalk {
 
     // The next piece; false at the share's end.
     __device__ inline bool next(const TreeShape& a, TreeItem& it) {
+#pragma unroll 1
         while (at < end) {
+#pragma unroll 1
             while (at >= seq_at + tree_seq_cost(a, q)) {  // at < end <= total: a later sequence has it
                 seq_at += tree_seq_cost(a, q);
                 q = tree_seq(a, ++s);
@@ -191,6 +195,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     if (h >= Hq) return;
     // the row's sequence: the lowest whose rows hold it (at most one does)
     int s = -1;
+#pragma unroll 1
     for (int base = 0; base < a.num_seqs && s < 0; base += 32) {
         const int i = base + lane;
         const bool in = i < a.num_seqs && a.cu_lens[i] <= row && row < a.cu_lens[i + 1];
@@ -212,11 +217,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     pdl_wait_primary();
     auto slot_of = [&](int c) { return slots + size * (2 * c + (c == c0 ? 1 : 0)); };
     float m_all = -INFINITY;
+#pragma unroll 1
     for (int c = c0 + lane; c <= c1; c += 32) m_all = fmaxf(m_all, slot_of(c)[2 * r]);
     m_all = warp_max(m_all);
     float acc[kV], l = 0.f;
 #pragma unroll
     for (int v = 0; v < kV; ++v) acc[v] = 0.f;
+#pragma unroll 1
     for (int cb = c0; cb <= c1; cb += 32) {
         float w = 0.f, lw = 0.f;
         if (cb + lane <= c1) {
