@@ -166,6 +166,11 @@ __device__ inline uint64_t f2_add(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+__device__ inline uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 __device__ inline uint64_t f2_sub(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -743,10 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int k0 = (blk - (hist ? 0 : t.nh)) * kBN;  // first key, of the history or the packed rows
                 const int e_nxt = kTree && i + 1 < nt ? entry(t.b0 + sd.tile(x, i + 1)) : 0;
                 uint32_t see[4];  // keys of this tile that the row sees
-                bool full = false;
                 if (hist) {
                     const uint32_t pmask = __ballot_sync(0xffffffffu, e_cur >= 0 && e_cur < a.c.num_pages);
-                    full = k0 + kBN <= t.L && pmask == 0xffffffffu;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         see[c] = low_bits(t.L - k0 - 32 * c);
@@ -765,7 +768,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      : 0u;
                 } else {
                     const int lim = row_ok ? tt + 1 - k0 : 0;
-                    full = lim >= kBN;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) see[c] = low_bits(lim - 32 * c);
                 }
@@ -784,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         tc::reg_fence(r[c]);
-                        if (!full) apply_mask(r[c], see[c]);
+                        if (see[c] != 0xffffffffu) apply_mask(r[c], see[c]);
                     }
                     float mx[4];
 #pragma unroll
@@ -941,29 +943,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int c = c_lo; c < c_hi; ++c) {
                     uint32_t r[32];
+                    tc::ld_32x32b_x32((sd.twin ? tm + lane_addr + col_o<D>(0) : obase) + 32 * c, r);
+                    const uint64_t wx = f2_pack(__float_as_uint(w.x), __float_as_uint(w.x));
+                    uint64_t z = 0;  // x * 0 is NaN for NaNs and infinities alone
                     if (sd.twin) {
                         uint32_t o[32];
-                        tc::ld_32x32b_x32(tm + lane_addr + col_o<D>(0) + 32 * c, r);
                         tc::ld_32x32b_x32(tm + lane_addr + col_o<D>(1) + 32 * c, o);
                         tc::wait_ld();
                         tc::reg_fence(r);
                         tc::reg_fence(o);
+                        const uint64_t wy = f2_pack(__float_as_uint(w.y), __float_as_uint(w.y));
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            r[k] = __float_as_uint(
-                                fmaf(__uint_as_float(r[k]), w.x, __uint_as_float(o[k]) * w.y));
+                        for (int k = 0; k < 32; k += 2) {
+                            const uint64_t y = f2_fma(f2_pack(o[k], o[k + 1]), wy, f2_mul(f2_pack(r[k], r[k + 1]), wx));
+                            f2_unpack(y, r[k], r[k + 1]);
+                            z = f2_fma(y, 0ull, z);
+                        }
                     } else {
-                        tc::ld_32x32b_x32(obase + 32 * c, r);
                         tc::wait_ld();
                         tc::reg_fence(r);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * w.x);
+                        for (int k = 0; k < 32; k += 2) {
+                            const uint64_t y = f2_mul(f2_pack(r[k], r[k + 1]), wx);
+                            f2_unpack(y, r[k], r[k + 1]);
+                            z = f2_fma(y, 0ull, z);
+                        }
                     }
-                    // x * 0 is NaN for NaNs and infinities alone
-                    float z = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) z = fmaf(__uint_as_float(r[k]), 0.f, z);
-                    if (row_ok && w.x == w.x && (poison || z != z)) restore(r, t, row, tt, 32 * c);
+                    uint32_t z0, z1;
+                    f2_unpack(z, z0, z1);
+                    const float zz = __uint_as_float(z0) + __uint_as_float(z1);
+                    if (row_ok && w.x == w.x && (poison || zz != zz)) restore(r, t, row, tt, 32 * c);
                     __syncwarp();
                     // row i of this lane's group of four: its lane's own dst
                     auto row_at = [&](int i, uint64_t mine) {

@@ -35,20 +35,23 @@ struct TreeSeq {
     int units, nh, nd, cost;  // tiles of a kv head; blocks of history and of drafts; positions of a unit
 };
 
-__device__ inline TreeSeq tree_seq(const TreeShape& a, int s) {
+// Sequence s from its lengths (no loads).
+__device__ inline TreeSeq tree_seq_of(const TreeShape& a, int r0, int r1, int L) {
     TreeSeq q;
-    const int r0 = a.cu_lens[s], r1 = a.cu_lens[s + 1];
     q.row0 = r0;
-    q.L = a.context_lens[s];
+    q.L = L;
     q.bad_rows = r0 < 0 || r1 < r0 || r1 > a.total_rows || r1 - r0 > a.max_rows;
     q.T = q.bad_rows ? 0 : r1 - r0;
-    q.bad_len = q.L < 0 || q.L > a.cap;
+    q.bad_len = L < 0 || L > a.cap;
     if (q.bad_len) q.L = 0;
     q.units = (q.T + a.tu - 1) / a.tu;
     q.nh = (q.L + a.kb - 1) / a.kb;
     q.nd = (q.T + a.kb - 1) / a.kb;
     q.cost = q.T > 0 ? 1 + q.nh + q.nd : 0;
     return q;
+}
+__device__ inline TreeSeq tree_seq(const TreeShape& a, int s) {
+    return tree_seq_of(a, a.cu_lens[s], a.cu_lens[s + 1], a.context_lens[s]);
 }
 
 __device__ inline int64_t tree_seq_cost(const TreeShape& a, const TreeSeq& q) {
@@ -79,8 +82,12 @@ __device__ inline int64_t tree_total(const TreeShape& a, int s, int64_t* before)
 __device__ inline int tree_ctas(const TreeShape& a, int64_t total) {
     return int(min(int64_t(a.n_ctas), max(int64_t(1), total / kMinShare)));
 }
-__device__ inline int64_t share_start(int64_t total, int n, int c) { return (total * c + n - 1) / n; }
-__device__ inline int share_owner(int64_t total, int n, int64_t p) { return int(p * n / total); }
+// 64-bit division takes long; the usual operands fit 32 bits.
+__device__ inline int64_t div_pos(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
+}
+__device__ inline int64_t share_start(int64_t total, int n, int c) { return div_pos(total * c + n - 1, n); }
+__device__ inline int share_owner(int64_t total, int n, int64_t p) { return int(div_pos(p * n, total)); }
 
 // One CTA's piece of a unit.
 struct TreeItem {
@@ -91,16 +98,44 @@ struct TreeItem {
     bool bad_len;
 };
 
-// A CTA's walk over its share; every lane of the warp holds the same state.
+// A CTA's walk over its share, by one whole warp whose lanes hold the same
+// state, but for the lengths of 32 sequences, one a lane: a call of up to 32
+// sequences reads them once, in one round of loads.
 struct TreeWalk {
-    int64_t at, end;     // positions left
-    int64_t seq_at;      // where the current sequence starts
+    int64_t at, end;  // positions left
+    int64_t seq_at;   // where the current sequence starts
     int s, cta;
     TreeSeq q;
+    int base, lane_r0, lane_r1, lane_L;  // lengths of sequence base + lane
+
+    __device__ inline void load(const TreeShape& a, int b) {
+        base = b;
+        const int i = b + int(threadIdx.x & 31);
+        const bool in = i < a.num_seqs;
+        lane_r0 = in ? a.cu_lens[i] : 0;
+        lane_r1 = in ? a.cu_lens[i + 1] : 0;
+        lane_L = in ? a.context_lens[i] : 0;
+    }
+    __device__ inline TreeSeq get(const TreeShape& a, int i) {
+        const int l = i - base;
+        return tree_seq_of(a, __shfl_sync(0xffffffffu, lane_r0, l), __shfl_sync(0xffffffffu, lane_r1, l),
+                           __shfl_sync(0xffffffffu, lane_L, l));
+    }
+    __device__ inline int64_t lane_cost(const TreeShape& a) {  // 0 past the last sequence: it has no rows
+        return tree_seq_cost(a, tree_seq_of(a, lane_r0, lane_r1, lane_L));
+    }
 
     __device__ inline void start(const TreeShape& a, int c) {
         cta = c;
-        const int64_t total = tree_total(a, 0, nullptr);
+        int64_t all = 0;
+        load(a, 0);
+        all = lane_cost(a);
+#pragma unroll 1
+        for (int b = 32; b < a.num_seqs; b += 32) {
+            load(a, b);
+            all += lane_cost(a);
+        }
+        const int64_t total = warp_sum64(all);
         const int n = tree_ctas(a, total);
         at = end = 0;
         if (c >= n || total == 0) return;
@@ -108,26 +143,27 @@ struct TreeWalk {
         end = share_start(total, n, c + 1);
         seq_at = 0;
         // the sequence that position `at` lies in, 32 at a time
+        if (base != 0) load(a, 0);
 #pragma unroll 1
-        for (int base = 0;; base += 32) {
-            const int i = base + int(threadIdx.x & 31);
-            const int64_t c1 = i < a.num_seqs ? tree_seq_cost(a, tree_seq(a, i)) : 0;
-            int64_t upto = c1;
+        for (;;) {
+            const int64_t own = lane_cost(a);
+            int64_t upto = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
                 if (int(threadIdx.x & 31) >= o) upto += x;
             }
             const unsigned m = __ballot_sync(0xffffffffu, seq_at + upto > at);
-            if (m || base + 32 >= a.num_seqs) {
-                const int l = m ? __ffs(m) - 1 : 31;
-                s = min(base + l, a.num_seqs - 1);
-                seq_at += __shfl_sync(0xffffffffu, upto - c1, l);
+            if (m) {
+                const int l = __ffs(m) - 1;
+                s = base + l;
+                seq_at += __shfl_sync(0xffffffffu, upto - own, l);
                 break;
             }
-            seq_at += __shfl_sync(0xffffffffu, upto, 31);
+            seq_at += __shfl_sync(0xffffffffu, upto, 31);  // at < total: a later window has it
+            load(a, base + 32);
         }
-        q = tree_seq(a, s);
+        q = get(a, s);
     }
 
     // The next piece; false at the share's end.
@@ -137,19 +173,19 @@ struct TreeWalk {
 #pragma unroll 1
             while (at >= seq_at + tree_seq_cost(a, q)) {  // at < end <= total: a later sequence has it
                 seq_at += tree_seq_cost(a, q);
-                q = tree_seq(a, ++s);
+                if (++s - base == 32) load(a, s);
+                q = get(a, s);
             }
             const int64_t in = at - seq_at;
-            const int unit = int(in / q.cost), o = int(in - int64_t(unit) * q.cost);
+            const int unit = int(div_pos(in, q.cost)), o = int(in - int64_t(unit) * q.cost);
             const int take = int(min(int64_t(q.cost - o), end - at));
             at += take;
             it.b0 = max(o - 1, 0);
             it.b1 = o + take - 1;
             if (it.b0 >= it.b1) continue;  // only the unit's first position: no block
-            const int u = unit % q.units;
-            it.seq = s;
             it.g = unit / q.units;
-            it.t0 = u * a.tu;
+            it.seq = s;
+            it.t0 = (unit - it.g * q.units) * a.tu;
             it.n_rows = min(a.tu, q.T - it.t0);
             it.row0 = q.row0 + it.t0;
             it.T = q.T;
@@ -233,18 +269,27 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
             lw = ml.y * w;
         }
         const int nc = min(32, c1 - cb + 1);
-#pragma unroll 4
-        for (int i = 0; i < nc; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, w, i);
-            l += __shfl_sync(0xffffffffu, lw, i);
-            const float* p = slot_of(cb + i) + 2 * rows + int64_t(r) * D + lane * kV;
-            float x[kV];
-            if constexpr (kV == 4)
-                *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(p);
-            else
-                *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(p);
+        // eight pieces' loads at a time in flight
+#pragma unroll 1
+        for (int i = 0; i < nc; i += 8) {
+            float x[8][kV];
 #pragma unroll
-            for (int v = 0; v < kV; ++v) acc[v] = wi == 0.f ? acc[v] : fmaf(wi, x[v], acc[v]);
+            for (int e = 0; e < 8; ++e) {
+                if (i + e >= nc) continue;
+                const float* p = slot_of(cb + i + e) + 2 * rows + int64_t(r) * D + lane * kV;
+                if constexpr (kV == 4)
+                    *reinterpret_cast<float4*>(x[e]) = *reinterpret_cast<const float4*>(p);
+                else
+                    *reinterpret_cast<float2*>(x[e]) = *reinterpret_cast<const float2*>(p);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (i + e >= nc) continue;
+                const float wi = __shfl_sync(0xffffffffu, w, i + e);
+                l += __shfl_sync(0xffffffffu, lw, i + e);
+#pragma unroll
+                for (int v = 0; v < kV; ++v) acc[v] = wi == 0.f ? acc[v] : fmaf(wi, x[e][v], acc[v]);
+            }
         }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
