@@ -357,12 +357,14 @@ template <int D> cudaError_t launch(const PackedAttn& a, cudaStream_t st) {
     s.max_rows = a.r.max_rows;
     s.Hkv = a.Hkv;
     s.tu = tq;
+    s.tile = tq;
     s.kb = kKB;
+    s.start = 1;
     s.n_ctas = a.n_ctas;
     s.cap = int64_t(a.c.max_blocks) * a.c.page_size;
     cudaError_t e = launch_pdl(packed_f32<D, true>, dim3(a.n_ctas), dim3(kThr), sm, st, a, s, 0);
     if (e != cudaSuccess) return e;
-    return launch_pdl(tree_join<float, D>, dim3(a.r.total_rows, (a.Hq + kJoinWarps - 1) / kJoinWarps),
+    return launch_pdl(tree_join<float, D>, join_grid(a.r.total_rows, a.Hq),
                       dim3(kJoinWarps * 32), 0, st, s, static_cast<const float*>(a.workspace),
                       static_cast<float*>(a.out), a.Hq, kM);
 }

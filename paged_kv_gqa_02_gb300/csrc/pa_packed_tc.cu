@@ -8,9 +8,9 @@
 // memory serves both row tiles and all G heads.  A unit that fills one row
 // tile only is worked on by both sides all the same: side A takes the even key
 // tiles and side B the odd ones, each with its own O, max and sum, and the
-// epilogue joins them ("twin").  CTAs are persistent, one per SM, and walk a
-// list of units or, for a tree, of pieces of units:
-//   prompt: units in descending order of their key tiles, dealt out in turn;
+// epilogue joins them ("twin").  CTAs are persistent, one per SM, and work
+// through units or, for a tree, pieces of units:
+//   prompt: units in descending order of their key tiles, taken one by one;
 //           keys are the packed rows 0..t of the unit's own sequence;
 //   tree:   the CTA's share of the keys (pa_tree_plan.cuh); key tiles are the
 //           history's pages first, then the packed drafts under their mask.
@@ -51,6 +51,7 @@
 
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <type_traits>
 
 namespace pa {
@@ -71,6 +72,9 @@ constexpr uint32_t kHalfBytes = kBN * 128;  // one 64-dim half of a tile
 constexpr uint64_t kWaitNs = 2000000000ull;  // a role gives up after 2 s on one barrier
 constexpr uint32_t kSleepNs = 20000;        // longest sleep inside one try_wait
 constexpr int kWaitSlices = int(kWaitNs / kSleepNs);
+// What a tree's unit costs apart from its key tiles, in key tiles of a twin
+// (0.9 us each; 1.75 us with two row tiles): start, joins and epilogue, 4.5 us
+constexpr int kUnitStart = 5;
 constexpr float kRescaleStep = 8.f;
 constexpr uint32_t kNegInf = 0xff800000u;
 
@@ -84,6 +88,8 @@ struct Bars {
     uint64_t k_full[kKS], k_empty[kKS], v_full[kVS], v_clean[kVS], v_empty[kVS];
     uint64_t s_full[2], p_full[2], o_done[2];  // of row tile x
     uint64_t item_full[kIS], item_empty[kIS];
+    uint64_t unit_asked;      // prompt: the next unit's number has arrived
+    alignas(16) uint4 unit;
     uint64_t side_b, side_w;  // twin: `side` holds B's figures; the weights
     uint64_t mma_done, never;
     uint32_t tmem, abort;
@@ -286,42 +292,100 @@ template <bool kTree> __device__ inline Sides sides_of(const TreeItem& t, int tq
     return s;
 }
 
-// The prompt's units in descending order of key tiles: unit i is
-// (level from the last, sequence, kv head); those that their sequence does not
-// have are passed over.  CTA c takes i = c, 2n-1-c, 2n+c, ... of the n CTAs, so
-// that none gets the longer unit of every round.
-struct PromptWalk {
-    int round;
-    __device__ inline bool next(const TcArgs& p, TreeItem& it, uint32_t* status) {
+// A prompt's units, numbered in descending order of key tiles: by level (the
+// tile of rows, from the last), then sequence, then kv head.  The grid has a CTA
+// for each number there can be; the SMs hold one CTA each, and a CTA that is
+// done asks the hardware to cancel the launch of a waiting one and takes its
+// number, so that the longest units come first and none waits for a CTA that
+// drew longer ones (numbers dealt out in turn instead: the ragged batch's CTAs
+// ended between 95 and 180 us).
+struct PromptUnits {
+    int lane_n;  // units of sequence `lane`, in calls of up to 32
+    __device__ inline int units(const TcArgs& p, int s) {
         const PackedAttn& a = p.a;
-        const int per = a.Hkv * a.r.num_seqs, all = per * p.n_units, n = gridDim.x, c = blockIdx.x;
+        if (s >= a.r.num_seqs) return 0;
+        const int r0 = a.r.cu_lens[s], r1 = a.r.cu_lens[s + 1];
+        if (r0 < 0 || r1 < r0 || r1 > a.r.total_rows || r1 - r0 > a.r.max_rows) return 0;
+        return (r1 - r0 + p.tu - 1) / p.tu;
+    }
+    __device__ inline void start(const TcArgs& p) { lane_n = units(p, threadIdx.x & 31); }
+    __device__ inline int lane_units(const TcArgs& p, int base) {
+        return p.a.r.num_seqs <= 32 ? lane_n : units(p, base + int(threadIdx.x & 31));
+    }
+    // units at `level` and above, of all sequences
+    __device__ inline int above(const TcArgs& p, int level) {
+        int n = 0;
 #pragma unroll 1
-        for (;; ++round) {
-            if (round * n >= all) return false;
-            const int i = round * n + ((round & 1) ? n - 1 - c : c);
-            if (i >= all) continue;
-            const int level = p.n_units - 1 - i / per, u = i % per;
-            it.seq = u / a.Hkv;
-            it.g = u - it.seq * a.Hkv;
-            const int r0 = a.r.cu_lens[it.seq], r1 = a.r.cu_lens[it.seq + 1];
-            if (r0 < 0 || r1 < r0 || r1 > a.r.total_rows || r1 - r0 > a.r.max_rows) {
-                if (level == 0 && (threadIdx.x & 31) == 0) flag(status, PA_DEV_BAD_LEN);
-                continue;
-            }
-            it.T = r1 - r0;
-            it.t0 = level * p.tu;
-            if (it.t0 >= it.T) continue;
-            it.n_rows = min(p.tu, it.T - it.t0);
-            it.row0 = r0 + it.t0;
-            it.L = it.nh = it.b0 = 0;
-            it.b1 = (it.t0 + it.n_rows + kBN - 1) / kBN;
-            it.slot = -1;
-            it.bad_len = false;
-            ++round;
-            return true;
+        for (int b = 0; b < p.a.r.num_seqs; b += 32) n += max(0, lane_units(p, b) - level);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+        return n;
+    }
+    // Unit number i; false where there are not so many.
+    __device__ inline bool get(const TcArgs& p, int i, TreeItem& it) {
+        const PackedAttn& a = p.a;
+        const int k = i / a.Hkv;
+        if (k >= above(p, 0)) return false;
+        int lo = 0, hi = p.n_units - 1;  // the highest level with more than k units at and above it
+#pragma unroll 1
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (above(p, mid) > k)
+                lo = mid;
+            else
+                hi = mid - 1;
         }
+        int rank = k - above(p, lo + 1);  // among the sequences that reach this level
+#pragma unroll 1
+        for (int b = 0;; b += 32) {
+            unsigned m = __ballot_sync(0xffffffffu, lane_units(p, b) > lo);
+            if (rank < __popc(m)) {
+#pragma unroll 1
+                for (; rank > 0; --rank) m &= m - 1;
+                it.seq = b + __ffs(m) - 1;
+                break;
+            }
+            rank -= __popc(m);
+        }
+        const int r0 = a.r.cu_lens[it.seq];
+        it.g = i - k * a.Hkv;
+        it.T = a.r.cu_lens[it.seq + 1] - r0;
+        it.t0 = lo * p.tu;
+        it.n_rows = min(p.tu, it.T - it.t0);
+        it.row0 = r0 + it.t0;
+        it.L = it.nh = it.b0 = 0;
+        it.b1 = (it.t0 + it.n_rows + kBN - 1) / kBN;
+        it.slot = -1;
+        it.bad_len = false;
+        return true;
     }
 };
+
+// Asks for the number of a CTA that has not been launched; the answer (16 bytes)
+// arrives on `bar`.  Not to be asked again after a refusal.
+__device__ inline void ask_unit(uint4* answer, uint64_t* bar) {
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            smem_u32(answer)),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+// The number, or -1 for a refusal.
+__device__ inline int answered_unit(uint4* answer) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+        "ld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, h;\n\t}"
+        : "=r"(got), "=r"(x)
+        : "r"(smem_u32(answer))
+        : "memory");
+    fence_proxy_async_smem();  // read before the next answer is written there
+    return got ? int(x) : -1;
+}
 
 template <int N> __device__ inline void regs_grow() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ inline void regs_shrink() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -370,6 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&B.item_empty[i], 10);  // 8 softmax warps, the MMA warp, the V warp
             B.poison[i] = 0;
         }
+        mbar_init(&B.unit_asked, 1);
         mbar_init(&B.side_b, 4);
         mbar_init(&B.side_w, 4);
         mbar_init(&B.mma_done, 1);
@@ -416,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         TreeWalk walk;
-        PromptWalk prompt = {0};
+        PromptUnits units;
         if constexpr (kTree) {
             if (blockIdx.x == 0)
 #pragma unroll 1
@@ -425,17 +490,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (q.bad_rows || q.bad_len) flag(a.dev_status, PA_DEV_BAD_LEN);
                 }
             walk.start(p.shape, blockIdx.x);
+        } else {
+            if (blockIdx.x == 0)
+#pragma unroll 1
+                for (int s = lane; s < a.r.num_seqs; s += 32) {
+                    const int r0 = a.r.cu_lens[s], r1 = a.r.cu_lens[s + 1];
+                    if (r0 < 0 || r1 < r0 || r1 > a.r.total_rows || r1 - r0 > a.r.max_rows)
+                        flag(a.dev_status, PA_DEV_BAD_LEN);
+                }
+            units.start(p);
         }
         const int P = a.c.page_size;
         const int xc_first = p.head_first;
         int kq = 0, vq = 0, qn = 0;  // K tiles, V tiles and Qs issued
-        bool ok = !*abort_flag;
+        int items = 0;               // units asked for
+        bool ok = !*abort_flag, asked = false;
+#pragma unroll 1
         for (int n = 0; ok; ++n) {
             Item it;
-            if constexpr (kTree)
+            if constexpr (kTree) {
                 it.valid = walk.next(p.shape, it.t);
-            else
-                it.valid = prompt.next(p, it.t, a.dev_status);
+            } else {
+                int i = blockIdx.x;
+                if (n > 0) {  // asked for before the last item's last tile
+                    ok = wait_all(&B.unit_asked, (n - 1) & 1);
+                    if (!ok) break;
+                    asked = false;
+                    i = answered_unit(&B.unit);
+                }
+                // past the last unit, all that wait are past it too
+                it.valid = i >= 0 && units.get(p, i, it.t);
+            }
             const int is = n % kIS;
             if (n >= kIS) ok = wait_all(&B.item_empty[is], ((n / kIS) - 1) & 1);
             if (!ok) break;
@@ -452,6 +537,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int npg = kTree ? (t.L + P - 1) / P : 0;
 #pragma unroll 1
             for (int j = 0; j < nt; ++j) {
+                if (!kTree && j == nt - 1) {
+                    if (lane == 0) ask_unit(&B.unit, &B.unit_asked);
+                    asked = true;
+                    ++items;
+                }
                 const int blk = t.b0 + j;
                 const bool hist = kTree && blk < t.nh;
                 int pg = a.c.num_pages;  // beyond the tensor: the box reads as zeros
@@ -507,6 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             if (!ok) give_up();
             // never leave the CTA with copies in flight
+            if (asked) mbar_wait_ns(&B.unit_asked, (items - 1) & 1, kWaitNs);
 #pragma unroll 1
             for (int j = max(0, kq - kKS); j < kq; ++j) mbar_wait_ns(&B.k_full[j % kKS], (j / kKS) & 1, kWaitNs);
 #pragma unroll 1
@@ -1091,7 +1182,9 @@ cudaError_t launch_typed(const PackedAttn& a, cudaStream_t st) {
         s.max_rows = a.r.max_rows;
         s.Hkv = a.Hkv;
         s.tu = 2 * p.tq;
+        s.tile = p.tq;
         s.kb = kBN;
+        s.start = kUnitStart;
         s.n_ctas = a.n_ctas;
         s.cap = int64_t(a.c.max_blocks) * a.c.page_size;
         ctas = a.n_ctas;
@@ -1102,12 +1195,12 @@ cudaError_t launch_typed(const PackedAttn& a, cudaStream_t st) {
         const int pairs = (a.r.max_rows + 2 * p.tq - 1) / (2 * p.tq);
         p.tu = per * pairs <= a.n_ctas / 2 ? p.tq : 2 * p.tq;
         p.n_units = (a.r.max_rows + p.tu - 1) / p.tu;
-        ctas = per * p.n_units;
-        if (ctas > a.n_ctas) ctas = a.n_ctas;
+        // one for each unit there can be: a sequence's last may be partly filled
+        ctas = std::min(per * p.n_units, int64_t(a.Hkv) * (a.r.total_rows / p.tu + a.r.num_seqs));
     }
     cudaError_t e = launch_pdl(kern, dim3(unsigned(ctas)), dim3(kThreads), Smem<D>::kBytes, st, mq, mk, mv, mkc, mvc, p);
     if (e != cudaSuccess || !kTree) return e;
-    return launch_pdl(tree_join<TOut, D>, dim3(a.r.total_rows, (a.Hq + kJoinWarps - 1) / kJoinWarps),
+    return launch_pdl(tree_join<TOut, D>, join_grid(a.r.total_rows, a.Hq),
                       dim3(kJoinWarps * 32), 0, st, p.shape, static_cast<const float*>(a.workspace),
                       static_cast<TOut*>(a.out), a.Hq, 2 * kBM);
 }

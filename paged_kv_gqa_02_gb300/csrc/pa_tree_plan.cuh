@@ -3,12 +3,16 @@
 //
 // A unit is (sequence, kv head, tile of `tu` drafts); its keys come in blocks
 // of `kb`, first the history's, then the drafts' own.  Units are laid end to
-// end, sequence by sequence and kv head by kv head, each as 1 + blocks
-// positions, and the line is cut into n equal shares, one for each CTA.  A
-// unit inside one share is finished there; the pieces of the others are left
-// in slots and joined in ascending CTA order.  A CTA leaves at most two
-// pieces: one of a unit that began before its share (slot 2c) and one of a
-// unit that begins in it (slot 2c + 1).
+// end, sequence by sequence and kv head by kv head, each as `start` positions
+// and then, for a block, one position or, in a sequence whose units hold more
+// than `tile` drafts, two: what starting and ending a unit and what a block
+// cost beside one another.  The line is cut into n equal shares, one for each
+// CTA; a block is the share's that holds its first position.  A unit inside one
+// share is finished there; the pieces of the others are left in slots and
+// joined in ascending CTA order.  A CTA leaves at most two pieces: one of a
+// unit that began before its share (slot 2c) and one of a unit that begins in
+// it (slot 2c + 1).  Shares have two positions at least, so that none lies
+// inside a unit without one of its blocks.
 // The partition depends on the lengths and n alone, so results repeat bit for
 // bit, and on the device only through n.
 #pragma once
@@ -20,19 +24,20 @@ namespace pa {
 
 namespace {  // each kernel's file has its own copy of the join
 
-constexpr int kMinShare = 2;  // positions of a share: one block and its unit's start
+constexpr int kMinShare = 2;  // positions of a share
 
 struct TreeShape {
     const int32_t* cu_lens;
     const int32_t* context_lens;
-    int32_t num_seqs, total_rows, max_rows, Hkv, tu, kb, n_ctas;
+    int32_t num_seqs, total_rows, max_rows, Hkv, tu, tile, kb, start, n_ctas;
     int64_t cap;  // tokens a block table holds
 };
 
 struct TreeSeq {
     int row0, T, L;  // T = 0: no rows, or rows that the call refuses; L = 0 with a bad length
     bool bad_rows, bad_len;
-    int units, nh, nd, cost;  // tiles of a kv head; blocks of history and of drafts; positions of a unit
+    int units, nh, nd;   // tiles of a kv head; blocks of history and of drafts
+    int width, cost;     // positions of a block and of a unit
 };
 
 // Sequence s from its lengths (no loads).
@@ -47,7 +52,8 @@ __device__ inline TreeSeq tree_seq_of(const TreeShape& a, int r0, int r1, int L)
     q.units = (q.T + a.tu - 1) / a.tu;
     q.nh = (q.L + a.kb - 1) / a.kb;
     q.nd = (q.T + a.kb - 1) / a.kb;
-    q.cost = q.T > 0 ? 1 + q.nh + q.nd : 0;
+    q.width = q.T > a.tile ? 2 : 1;
+    q.cost = q.T > 0 ? a.start + q.width * (q.nh + q.nd) : 0;
     return q;
 }
 __device__ inline TreeSeq tree_seq(const TreeShape& a, int s) {
@@ -180,9 +186,10 @@ struct TreeWalk {
             const int unit = int(div_pos(in, q.cost)), o = int(in - int64_t(unit) * q.cost);
             const int take = int(min(int64_t(q.cost - o), end - at));
             at += take;
-            it.b0 = max(o - 1, 0);
-            it.b1 = o + take - 1;
-            if (it.b0 >= it.b1) continue;  // only the unit's first position: no block
+            // blocks whose first position, start + width * b, is in [o, o + take)
+            it.b0 = max(o - a.start + q.width - 1, 0) / q.width;
+            it.b1 = max(o + take - a.start + q.width - 1, 0) / q.width;
+            if (it.b0 >= it.b1) continue;  // of the unit's start only
             it.g = unit / q.units;
             it.seq = s;
             it.t0 = (unit - it.g * q.units) * a.tu;
@@ -192,7 +199,7 @@ struct TreeWalk {
             it.L = q.L;
             it.nh = q.nh;
             it.bad_len = q.bad_len;
-            const bool first = it.b0 == 0, whole = first && it.b1 == q.cost - 1;
+            const bool first = it.b0 == 0, whole = first && it.b1 == q.nh + q.nd;
             it.slot = whole ? -1 : 2 * cta + (first ? 1 : 0);
             return true;
         }
@@ -218,17 +225,22 @@ template <> __device__ inline __half from_f32<__half>(float x) { return __float2
 template <> __device__ inline __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
 // The join, launched with programmatic dependent launch behind the pieces'
-// kernel: one warp per (packed row, q head), CTAs of eight heads of a row.
-// It finds its pieces from the lengths before it waits; a row whose unit was
-// finished in one share returns.
+// kernel: one CTA per packed row, or where that leaves SMs idle several, a warp
+// per q head and round.  The lengths are read before it waits; a row whose unit
+// was finished in one share has nothing to do.
 constexpr int kJoinWarps = 8;
+// CTAs of a row: with eight an SM there is one round of CTAs, each of which pays
+// for reading the lengths (tree of 64 rows, 64 heads: 30 us with a CTA per 8 heads)
+inline dim3 join_grid(int rows, int Hq) {
+    const int most = (Hq + kJoinWarps - 1) / kJoinWarps, fit = 152 * 8 / rows;
+    return dim3(rows, fit < 1 ? 1 : fit < most ? fit : most);
+}
 template <typename TOut, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     tree_join(const TreeShape a, const float* slots, TOut* out, int Hq, int rows) {
     constexpr int kV = D / 32;  // dims of a lane
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row = blockIdx.x, h = int(blockIdx.y) * kJoinWarps + warp;
-    if (h >= Hq) return;
+    const int row = blockIdx.x;
     // the row's sequence: the lowest whose rows hold it (at most one does)
     int s = -1;
 #pragma unroll 1
@@ -238,71 +250,79 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         const unsigned m = __ballot_sync(0xffffffffu, in);
         if (m) s = base + __ffs(m) - 1;
     }
-    if (s < 0) return;
-    const TreeSeq q = tree_seq(a, s);
-    if (q.T == 0) return;
-    int64_t before;
-    const int64_t total = tree_total(a, s, &before);
-    const int n = tree_ctas(a, total);
-    const int G = Hq / a.Hkv, g = h / G, t = row - q.row0, u = t / a.tu;
-    const int64_t u0 = before + (int64_t(g) * q.units + u) * q.cost;
-    const int c0 = share_owner(total, n, u0 + 1), c1 = share_owner(total, n, u0 + q.cost - 1);
-    if (c0 == c1) return;
-    const int r = (t - u * a.tu) * G + (h - g * G);
-    const int64_t size = slot_floats(rows, D);
-    pdl_wait_primary();
-    auto slot_of = [&](int c) { return slots + size * (2 * c + (c == c0 ? 1 : 0)); };
-    float m_all = -INFINITY;
-#pragma unroll 1
-    for (int c = c0 + lane; c <= c1; c += 32) m_all = fmaxf(m_all, slot_of(c)[2 * r]);
-    m_all = warp_max(m_all);
-    float acc[kV], l = 0.f;
-#pragma unroll
-    for (int v = 0; v < kV; ++v) acc[v] = 0.f;
-#pragma unroll 1
-    for (int cb = c0; cb <= c1; cb += 32) {
-        float w = 0.f, lw = 0.f;
-        if (cb + lane <= c1) {
-            const float2 ml = *reinterpret_cast<const float2*>(slot_of(cb + lane) + 2 * r);
-            // a piece with no visible key has max -inf and weight 0; a NaN max cannot be (max drops NaN)
-            w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - m_all);
-            lw = ml.y * w;
-        }
-        const int nc = min(32, c1 - cb + 1);
-        // eight pieces' loads at a time in flight
-#pragma unroll 1
-        for (int i = 0; i < nc; i += 8) {
-            float x[8][kV];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (i + e >= nc) continue;
-                const float* p = slot_of(cb + i + e) + 2 * rows + int64_t(r) * D + lane * kV;
-                if constexpr (kV == 4)
-                    *reinterpret_cast<float4*>(x[e]) = *reinterpret_cast<const float4*>(p);
-                else
-                    *reinterpret_cast<float2*>(x[e]) = *reinterpret_cast<const float2*>(p);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (i + e >= nc) continue;
-                const float wi = __shfl_sync(0xffffffffu, w, i + e);
-                l += __shfl_sync(0xffffffffu, lw, i + e);
-#pragma unroll
-                for (int v = 0; v < kV; ++v) acc[v] = wi == 0.f ? acc[v] : fmaf(wi, x[e][v], acc[v]);
-            }
-        }
+    TreeSeq q = {};
+    int64_t before = 0, total = 0;
+    if (s >= 0) {
+        q = tree_seq(a, s);
+        total = tree_total(a, s, &before);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    TOut y[kV];
+    // by every CTA: were none to wait, this grid could end before the one it joins for
+    pdl_wait_primary();
+    if (q.T == 0) return;
+    const int n = tree_ctas(a, total);
+    const int G = Hq / a.Hkv, t = row - q.row0, u = t / a.tu;
+#pragma unroll 1
+    for (int h = int(blockIdx.y) * kJoinWarps + warp; h < Hq; h += int(gridDim.y) * kJoinWarps) {
+        const int g = h / G;
+        const int64_t u0 = before + (int64_t(g) * q.units + u) * q.cost;
+        const int64_t b0 = u0 + a.start;  // the first block's position
+        const int c0 = share_owner(total, n, b0), c1 = share_owner(total, n, b0 + q.width * (q.nh + q.nd - 1));
+        if (c0 == c1) continue;
+        const int r = (t - u * a.tu) * G + (h - g * G);
+        const int64_t size = slot_floats(rows, D);
+        auto slot_of = [&](int c) { return slots + size * (2 * c + (c == c0 ? 1 : 0)); };
+        float m_all = -INFINITY;
+#pragma unroll 1
+        for (int c = c0 + lane; c <= c1; c += 32) m_all = fmaxf(m_all, slot_of(c)[2 * r]);
+        m_all = warp_max(m_all);
+        float acc[kV], l = 0.f;
 #pragma unroll
-    for (int v = 0; v < kV; ++v) y[v] = from_f32<TOut>(acc[v] * inv);
-    TOut* o = out + (int64_t(row) * Hq + h) * D + lane * kV;
-    if constexpr (sizeof(y) == 16)
-        *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(y);
-    else if constexpr (sizeof(y) == 8)
-        *reinterpret_cast<uint2*>(o) = *reinterpret_cast<const uint2*>(y);
-    else
-        *reinterpret_cast<uint32_t*>(o) = *reinterpret_cast<const uint32_t*>(y);
+        for (int v = 0; v < kV; ++v) acc[v] = 0.f;
+#pragma unroll 1
+        for (int cb = c0; cb <= c1; cb += 32) {
+            float w = 0.f, lw = 0.f;
+            if (cb + lane <= c1) {
+                const float2 ml = *reinterpret_cast<const float2*>(slot_of(cb + lane) + 2 * r);
+                // a piece with no visible key has max -inf and weight 0; a NaN max cannot be (max drops NaN)
+                w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - m_all);
+                lw = ml.y * w;
+            }
+            const int nc = min(32, c1 - cb + 1);
+            // eight pieces' loads at a time in flight
+#pragma unroll 1
+            for (int i = 0; i < nc; i += 8) {
+                float x[8][kV];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (i + e >= nc) continue;
+                    const float* p = slot_of(cb + i + e) + 2 * rows + int64_t(r) * D + lane * kV;
+                    if constexpr (kV == 4)
+                        *reinterpret_cast<float4*>(x[e]) = *reinterpret_cast<const float4*>(p);
+                    else
+                        *reinterpret_cast<float2*>(x[e]) = *reinterpret_cast<const float2*>(p);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (i + e >= nc) continue;
+                    const float wi = __shfl_sync(0xffffffffu, w, i + e);
+                    l += __shfl_sync(0xffffffffu, lw, i + e);
+#pragma unroll
+                    for (int v = 0; v < kV; ++v) acc[v] = wi == 0.f ? acc[v] : fmaf(wi, x[e][v], acc[v]);
+                }
+            }
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        TOut y[kV];
+#pragma unroll
+        for (int v = 0; v < kV; ++v) y[v] = from_f32<TOut>(acc[v] * inv);
+        TOut* o = out + (int64_t(row) * Hq + h) * D + lane * kV;
+        if constexpr (sizeof(y) == 16)
+            *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(y);
+        else if constexpr (sizeof(y) == 8)
+            *reinterpret_cast<uint2*>(o) = *reinterpret_cast<const uint2*>(y);
+        else
+            *reinterpret_cast<uint32_t*>(o) = *reinterpret_cast<const uint32_t*>(y);
+    }
 }
 
 }  // namespace
