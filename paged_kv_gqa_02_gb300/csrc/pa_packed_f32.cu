@@ -78,10 +78,16 @@ __global__ void __launch_bounds__(kThr, 1) packed_f32(const PackedAttn a, const 
 
     TreeWalk walk;
     TreeItem it;
+    // what there is to join here; first that there is nothing
+    auto put_join = [&](int4 u) {
+        if (tid == 0) tree_joins(a.workspace, kM, D, a.n_ctas)[blockIdx.x] = u;
+    };
     if constexpr (kTree) {
         if (blockIdx.x == 0) tree_flag_lengths(shape, a.dev_status);
         walk.start(shape, blockIdx.x);
-        if (!walk.next(shape, it)) return;
+        const bool any = walk.next(shape, it);
+        if (!any || !begins(it)) put_join(make_int4(0, 0, 0, 0));
+        if (!any) return;
     } else {
         // blockIdx.x = (tile from the last) x (sequence, kv head)
         const int per = a.Hkv * a.r.num_seqs;
@@ -105,6 +111,7 @@ __global__ void __launch_bounds__(kThr, 1) packed_f32(const PackedAttn a, const 
     }
 
     for (;;) {  // the items of the share (prompt: one)
+        if (kTree && begins(it)) put_join(join_of(it));
         const float* kp = static_cast<const float*>(a.k) + int64_t(it.row0 - it.t0) * a.r.k_stride + it.g * D;
         const float* vp = static_cast<const float*>(a.v) + int64_t(it.row0 - it.t0) * a.r.v_stride + it.g * D;
         const float* kc = nullptr;
@@ -364,16 +371,12 @@ template <int D> cudaError_t launch(const PackedAttn& a, cudaStream_t st) {
     s.cap = int64_t(a.c.max_blocks) * a.c.page_size;
     cudaError_t e = launch_pdl(packed_f32<D, true>, dim3(a.n_ctas), dim3(kThr), sm, st, a, s, 0);
     if (e != cudaSuccess) return e;
-    return launch_pdl(tree_join<float, D>, join_grid(a.r.total_rows, a.Hq),
-                      dim3(kJoinWarps * 32), 0, st, s, static_cast<const float*>(a.workspace),
-                      static_cast<float*>(a.out), a.Hq, kM);
+    return launch_join<float, D>(s, a, kM, st);
 }
 
 }  // namespace
 
-size_t tree_f32_workspace_bytes(int D, int n_ctas) {
-    return (2 * size_t(n_ctas) * slot_floats(kM, D) * sizeof(float) + 255) & ~size_t(255);
-}
+size_t tree_f32_workspace_bytes(int D, int n_ctas) { return tree_workspace_bytes(kM, D, n_ctas); }
 
 cudaError_t launch_packed_f32(const PackedAttn& a, cudaStream_t st) {
     return a.D == 64 ? launch<64>(a, st) : launch<128>(a, st);

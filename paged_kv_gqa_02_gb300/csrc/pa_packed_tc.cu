@@ -504,12 +504,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int xc_first = p.head_first;
         int kq = 0, vq = 0, qn = 0;  // K tiles, V tiles and Qs issued
         int items = 0;               // units asked for
-        bool ok = !*abort_flag, asked = false;
+        bool ok = !*abort_flag, asked = false, joins = false;
 #pragma unroll 1
         for (int n = 0; ok; ++n) {
             Item it;
             if constexpr (kTree) {
                 it.valid = walk.next(p.shape, it.t);
+                if (it.valid ? begins(it.t) : !joins) {  // what there is to join here, or that there is nothing
+                    if (lane == 0)
+                        tree_joins(a.workspace, 2 * kBM, D, a.n_ctas)[blockIdx.x] =
+                            it.valid ? join_of(it.t) : make_int4(0, 0, 0, 0);
+                    joins = true;
+                }
             } else {
                 int i = blockIdx.x;
                 if (n > 0) {  // asked for before the last item's last tile
@@ -595,6 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (lane == 0) {
+            if (kTree && !joins)  // gave up
+                tree_joins(a.workspace, 2 * kBM, D, a.n_ctas)[blockIdx.x] = make_int4(0, 0, 0, 0);
             if (!ok) give_up();
             // never leave the CTA with copies in flight
             if (asked) mbar_wait_ns(&B.unit_asked, (items - 1) & 1, kWaitNs);
@@ -1200,9 +1208,7 @@ cudaError_t launch_typed(const PackedAttn& a, cudaStream_t st) {
     }
     cudaError_t e = launch_pdl(kern, dim3(unsigned(ctas)), dim3(kThreads), Smem<D>::kBytes, st, mq, mk, mv, mkc, mvc, p);
     if (e != cudaSuccess || !kTree) return e;
-    return launch_pdl(tree_join<TOut, D>, join_grid(a.r.total_rows, a.Hq),
-                      dim3(kJoinWarps * 32), 0, st, p.shape, static_cast<const float*>(a.workspace),
-                      static_cast<TOut*>(a.out), a.Hq, 2 * kBM);
+    return launch_join<TOut, D>(p.shape, a, 2 * kBM, st);
 }
 
 template <typename T, int D> cudaError_t launch_out(const PackedAttn& a, cudaStream_t st) {
@@ -1213,9 +1219,7 @@ template <typename T, int D> cudaError_t launch_out(const PackedAttn& a, cudaStr
 
 }  // namespace
 
-size_t tree_tc_workspace_bytes(int D, int n_ctas) {
-    return (2 * size_t(n_ctas) * slot_floats(2 * kBM, D) * sizeof(float) + 255) & ~size_t(255);
-}
+size_t tree_tc_workspace_bytes(int D, int n_ctas) { return tree_workspace_bytes(2 * kBM, D, n_ctas); }
 
 cudaError_t launch_packed_tc(const PackedAttn& a, cudaStream_t st) {
     if (a.dtype == PA_BF16)

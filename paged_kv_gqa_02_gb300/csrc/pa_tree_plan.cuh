@@ -20,6 +20,8 @@
 #include "pa_ptx.cuh"
 #include "pa_serving.h"
 
+#include <algorithm>
+
 namespace pa {
 
 namespace {  // each kernel's file has its own copy of the join
@@ -70,20 +72,6 @@ __device__ inline int64_t warp_sum64(int64_t v) {
     return v;
 }
 
-// Positions of all sequences; with `before`, also of those ahead of sequence
-// s.  The whole warp.
-__device__ inline int64_t tree_total(const TreeShape& a, int s, int64_t* before) {
-    int64_t all = 0, ahead = 0;
-#pragma unroll 1
-    for (int i = threadIdx.x & 31; i < a.num_seqs; i += 32) {
-        const int64_t c = tree_seq_cost(a, tree_seq(a, i));
-        all += c;
-        if (i < s) ahead += c;
-    }
-    if (before) *before = warp_sum64(ahead);
-    return warp_sum64(all);
-}
-
 // CTAs that take part.
 __device__ inline int tree_ctas(const TreeShape& a, int64_t total) {
     return int(min(int64_t(a.n_ctas), max(int64_t(1), total / kMinShare)));
@@ -101,6 +89,7 @@ struct TreeItem {
     int t0, n_rows;           // the tile's first draft, its drafts
     int T, L, nh, b0, b1;     // blocks [b0, b1) of nh + nd
     int slot;                 // -1: the whole unit
+    int last;                 // of a unit's first piece: the CTA of its last one
     bool bad_len;
 };
 
@@ -110,7 +99,8 @@ struct TreeItem {
 struct TreeWalk {
     int64_t at, end;  // positions left
     int64_t seq_at;   // where the current sequence starts
-    int s, cta;
+    int64_t total;
+    int s, cta, n;
     TreeSeq q;
     int base, lane_r0, lane_r1, lane_L;  // lengths of sequence base + lane
 
@@ -141,8 +131,8 @@ struct TreeWalk {
             load(a, b);
             all += lane_cost(a);
         }
-        const int64_t total = warp_sum64(all);
-        const int n = tree_ctas(a, total);
+        total = warp_sum64(all);
+        n = tree_ctas(a, total);
         at = end = 0;
         if (c >= n || total == 0) return;
         at = share_start(total, n, c);
@@ -201,6 +191,9 @@ struct TreeWalk {
             it.bad_len = q.bad_len;
             const bool first = it.b0 == 0, whole = first && it.b1 == q.nh + q.nd;
             it.slot = whole ? -1 : 2 * cta + (first ? 1 : 0);
+            it.last = cta;
+            if (first && !whole)  // the last block's first position
+                it.last = share_owner(total, n, seq_at + int64_t(unit) * q.cost + a.start + q.width * (q.nh + q.nd - 1));
             return true;
         }
         return false;
@@ -219,103 +212,116 @@ __device__ inline void tree_flag_lengths(const TreeShape& a, uint32_t* status) {
 // the base-2 running max and the sum, then the accumulators.
 __host__ __device__ inline int64_t slot_floats(int rows, int D) { return int64_t(rows) * (D + 2); }
 
+// The workspace: two slots for each CTA, then for each CTA the unit to join that
+// begins in its share (one at most): its first packed row, kv head, drafts (0:
+// none), and the CTA of its last piece.
+__host__ __device__ inline size_t tree_workspace_bytes(int rows, int D, int n_ctas) {
+    return (size_t(n_ctas) * (2 * slot_floats(rows, D) * sizeof(float) + sizeof(int4)) + 255) & ~size_t(255);
+}
+__device__ inline int4* tree_joins(void* workspace, int rows, int D, int n_ctas) {
+    return reinterpret_cast<int4*>(static_cast<float*>(workspace) + 2 * slot_floats(rows, D) * n_ctas);
+}
+__device__ inline bool begins(const TreeItem& it) { return it.slot >= 0 && (it.slot & 1); }
+__device__ inline int4 join_of(const TreeItem& it) { return make_int4(it.row0, it.g, it.n_rows, it.last); }
+
 template <typename T> __device__ inline T from_f32(float x);
 template <> __device__ inline float from_f32<float>(float x) { return x; }
 template <> __device__ inline __half from_f32<__half>(float x) { return __float2half_rn(x); }
 template <> __device__ inline __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
 // The join, launched with programmatic dependent launch behind the pieces'
-// kernel: one CTA per packed row, or where that leaves SMs idle several, a warp
-// per q head and round.  The lengths are read before it waits; a row whose unit
-// was finished in one share has nothing to do.
-constexpr int kJoinWarps = 8;
-// CTAs of a row: with eight an SM there is one round of CTAs, each of which pays
-// for reading the lengths (tree of 64 rows, 64 heads: 30 us with a CTA per 8 heads)
-inline dim3 join_grid(int rows, int Hq) {
-    const int most = (Hq + kJoinWarps - 1) / kJoinWarps, fit = 152 * 8 / rows;
-    return dim3(rows, fit < 1 ? 1 : fit < most ? fit : most);
-}
-template <typename TOut, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32)
-    tree_join(const TreeShape a, const float* slots, TOut* out, int Hq, int rows) {
+// kernel, which leaves it a list of what to join.  CTAs of eight warps over a
+// unit's distributions, `per` for each warp one after the other.  Pieces are
+// taken in ascending CTA order, kP at a time in flight, against a running max.
+// A small call has many pieces for each of few distributions and waits for its
+// loads: sixteen in flight, a distribution a warp.  A large one has two or three
+// pieces for each of many and is bound by its instructions (36 us with sixteen
+// steps for each, 64 rows x 8, 64 heads): four in flight, four distributions a
+// warp.
+template <typename TOut, int D, int kP>
+__global__ void __launch_bounds__(256)
+    tree_join(float* slots, TOut* out, int Hq, int G, int rows, int per, int n_ctas) {
     constexpr int kV = D / 32;  // dims of a lane
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row = blockIdx.x;
-    // the row's sequence: the lowest whose rows hold it (at most one does)
-    int s = -1;
-#pragma unroll 1
-    for (int base = 0; base < a.num_seqs && s < 0; base += 32) {
-        const int i = base + lane;
-        const bool in = i < a.num_seqs && a.cu_lens[i] <= row && row < a.cu_lens[i + 1];
-        const unsigned m = __ballot_sync(0xffffffffu, in);
-        if (m) s = base + __ffs(m) - 1;
-    }
-    TreeSeq q = {};
-    int64_t before = 0, total = 0;
-    if (s >= 0) {
-        q = tree_seq(a, s);
-        total = tree_total(a, s, &before);
-    }
-    // by every CTA: were none to wait, this grid could end before the one it joins for
     pdl_wait_primary();
-    if (q.T == 0) return;
-    const int n = tree_ctas(a, total);
-    const int G = Hq / a.Hkv, t = row - q.row0, u = t / a.tu;
+    // the blockIdx.x-th entry of the list that has something to join
+    __shared__ int count[8], found;
+    const int4* list = tree_joins(slots, rows, D, n_ctas);
+    int left = blockIdx.x;
+    if (threadIdx.x == 0) found = -1;
 #pragma unroll 1
-    for (int h = int(blockIdx.y) * kJoinWarps + warp; h < Hq; h += int(gridDim.y) * kJoinWarps) {
-        const int g = h / G;
-        const int64_t u0 = before + (int64_t(g) * q.units + u) * q.cost;
-        const int64_t b0 = u0 + a.start;  // the first block's position
-        const int c0 = share_owner(total, n, b0), c1 = share_owner(total, n, b0 + q.width * (q.nh + q.nd - 1));
-        if (c0 == c1) continue;
-        const int r = (t - u * a.tu) * G + (h - g * G);
-        const int64_t size = slot_floats(rows, D);
-        auto slot_of = [&](int c) { return slots + size * (2 * c + (c == c0 ? 1 : 0)); };
-        float m_all = -INFINITY;
+    for (int base = 0; base < n_ctas; base += 256) {
+        const int i = base + int(threadIdx.x);
+        const bool has = i < n_ctas && list[i].z > 0;
+        const unsigned m = __ballot_sync(0xffffffffu, has);
+        if (lane == 0) count[warp] = __popc(m);
+        __syncthreads();
+        int at = __popc(m & ((1u << lane) - 1u)), all = 0;
+        for (int w = 0; w < 8; ++w) {
+            at += w < warp ? count[w] : 0;
+            all += count[w];
+        }
+        if (has && at == left) found = i;
+        left -= all;
+        __syncthreads();
+    }
+    if (found < 0) return;
+    const int4 u = list[found];
+    const int valid = u.z * G, c0 = found, c1 = u.w;
+    const int64_t size = slot_floats(rows, D);
+    // a piece's slot: the unit's first CTA left it in its second
+    const float* first = slots + size * (2 * c0 + 1);
+    const float* later = slots + size * (2 * c0);  // + 2 * size for each CTA on
 #pragma unroll 1
-        for (int c = c0 + lane; c <= c1; c += 32) m_all = fmaxf(m_all, slot_of(c)[2 * r]);
-        m_all = warp_max(m_all);
-        float acc[kV], l = 0.f;
+    for (int k = 0; k < per; ++k) {
+        const int r = (int(blockIdx.y) * 8 + warp) * per + k;
+        if (r >= valid) return;
+        float acc[kV], m_run = -INFINITY, l_run = 0.f;
 #pragma unroll
         for (int v = 0; v < kV; ++v) acc[v] = 0.f;
 #pragma unroll 1
-        for (int cb = c0; cb <= c1; cb += 32) {
-            float w = 0.f, lw = 0.f;
-            if (cb + lane <= c1) {
-                const float2 ml = *reinterpret_cast<const float2*>(slot_of(cb + lane) + 2 * r);
-                // a piece with no visible key has max -inf and weight 0; a NaN max cannot be (max drops NaN)
-                w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - m_all);
-                lw = ml.y * w;
+        for (int c = c0; c <= c1; c += kP) {
+            const int np = min(kP, c1 - c + 1);
+            float2 ml = make_float2(-INFINITY, 0.f);  // of piece `lane`
+            auto slot_of = [&](int i) { return c + i == c0 ? first : later + 2 * size * (c + i - c0); };
+            if (lane < np) ml = *reinterpret_cast<const float2*>(slot_of(lane) + 2 * r);
+            float x[kP][kV];
+#pragma unroll
+            for (int i = 0; i < kP; ++i) {
+                if (i >= np) break;
+                const float* p = slot_of(i) + 2 * rows + int64_t(r) * D + lane * kV;
+                if constexpr (kV == 4)
+                    *reinterpret_cast<float4*>(x[i]) = *reinterpret_cast<const float4*>(p);
+                else
+                    *reinterpret_cast<float2*>(x[i]) = *reinterpret_cast<const float2*>(p);
             }
-            const int nc = min(32, c1 - cb + 1);
-            // eight pieces' loads at a time in flight
-#pragma unroll 1
-            for (int i = 0; i < nc; i += 8) {
-                float x[8][kV];
+            const float m_new = fmaxf(m_run, warp_max(ml.x));
+            const float base = m_new == -INFINITY ? 0.f : m_new;
+            const float old = ex2(m_run - base);
+            m_run = m_new;
+            // a piece with nothing visible has max -inf and sum 0: weight 0.  With
+            // a sum that is not 0 its scores were NaN, which the max drops.
+            const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - base);
+            l_run *= old;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (i + e >= nc) continue;
-                    const float* p = slot_of(cb + i + e) + 2 * rows + int64_t(r) * D + lane * kV;
-                    if constexpr (kV == 4)
-                        *reinterpret_cast<float4*>(x[e]) = *reinterpret_cast<const float4*>(p);
-                    else
-                        *reinterpret_cast<float2*>(x[e]) = *reinterpret_cast<const float2*>(p);
-                }
+            for (int v = 0; v < kV; ++v) acc[v] *= old;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (i + e >= nc) continue;
-                    const float wi = __shfl_sync(0xffffffffu, w, i + e);
-                    l += __shfl_sync(0xffffffffu, lw, i + e);
+            for (int i = 0; i < kP; ++i) {
+                if (i >= np) break;
+                const float wi = __shfl_sync(0xffffffffu, w, i), li = __shfl_sync(0xffffffffu, ml.y, i);
+                if (wi != 0.f) {
+                    l_run = fmaf(wi, li, l_run);
 #pragma unroll
-                    for (int v = 0; v < kV; ++v) acc[v] = wi == 0.f ? acc[v] : fmaf(wi, x[e][v], acc[v]);
+                    for (int v = 0; v < kV; ++v) acc[v] = fmaf(wi, x[i][v], acc[v]);
                 }
             }
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int t = r / G;
+        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
         TOut y[kV];
 #pragma unroll
         for (int v = 0; v < kV; ++v) y[v] = from_f32<TOut>(acc[v] * inv);
-        TOut* o = out + (int64_t(row) * Hq + h) * D + lane * kV;
+        TOut* o = out + (int64_t(u.x + t) * Hq + u.y * G + (r - t * G)) * D + lane * kV;
         if constexpr (sizeof(y) == 16)
             *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(y);
         else if constexpr (sizeof(y) == 8)
@@ -323,6 +329,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         else
             *reinterpret_cast<uint32_t*>(o) = *reinterpret_cast<const uint32_t*>(y);
     }
+}
+// Launches it: one distribution a warp while that makes no more CTAs with work
+// than run at once, four otherwise.
+template <typename TOut, int D>
+inline cudaError_t launch_join(const TreeShape& a, const PackedAttn& p, int rows, cudaStream_t st) {
+    const int64_t units = int64_t(a.Hkv) * (a.total_rows / a.tu + std::min(a.num_seqs, a.total_rows));
+    const int G = p.Hq / p.Hkv, most = std::min(a.tu, a.max_rows) * G;  // a unit's distributions
+    const int per = units * ((most + 7) / 8) <= 152 * 4 ? 1 : 4;
+    return launch_pdl(per == 1 ? tree_join<TOut, D, 16> : tree_join<TOut, D, 4>,
+                      dim3(unsigned(std::min(units, int64_t(a.n_ctas))), (most + 8 * per - 1) / (8 * per)), dim3(256), 0, st,
+                      static_cast<float*>(p.workspace), static_cast<TOut*>(p.out), p.Hq, G, rows, per, a.n_ctas);
 }
 
 }  // namespace
