@@ -336,7 +336,7 @@ template <typename TOut, int D>
 inline cudaError_t launch_join(const TreeShape& a, const PackedAttn& p, int rows, cudaStream_t st) {
     const int64_t units = int64_t(a.Hkv) * (a.total_rows / a.tu + std::min(a.num_seqs, a.total_rows));
     const int G = p.Hq / p.Hkv, most = std::min(a.tu, a.max_rows) * G;  // a unit's distributions
-    const int per = units * ((most + 7) / 8) <= 152 * 4 ? 1 : 4;
+    const int per = units * ((most + 7) / 8) <= 152 * 4 ? 1 : 2;
     return launch_pdl(per == 1 ? tree_join<TOut, D, 16> : tree_join<TOut, D, 4>,
                       dim3(unsigned(std::min(units, int64_t(a.n_ctas))), (most + 8 * per - 1) / (8 * per)), dim3(256), 0, st,
                       static_cast<float*>(p.workspace), static_cast<TOut*>(p.out), p.Hq, G, rows, per, a.n_ctas);
