@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(kThr, 1) packed_f32(const PackedAttn a, const 
             trow[i] = r / G;
             rok[i] = r < tq * G && trow[i] < it.n_rows;
         }
+        const bool live = (tid >> 5) * 8 < it.n_rows * G;
         float o[4][4 * kDv];
         float m_run[4], l_part[4];  // l_part: this thread's keys only
 #pragma unroll
@@ -217,14 +218,15 @@ __global__ void __launch_bounds__(kThr, 1) packed_f32(const PackedAttn a, const 
             // a packed block that some row of the tile sees only in part
             const bool part = !hist && (kTree || (b + 1) * kKB > it.t0 + 1);
 
-            // ---- scores: s[i][k] = q(ty*4+i) . k(tx+16k) ---------------------------
+            // ---- scores: s[i][k] = q(ty*4+i) . k(tx+16k), by warps that have a
+            // distribution (a small tree fills few of the tile's) ------------------
             float s[4][4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) s[i][k] = 0.f;
 #pragma unroll 4
-            for (int d = 0; d < D; d += 4) {
+            for (int d = live ? 0 : D; d < D; d += 4) {
                 float4 qv[4], kv[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(q_s + (ty * 4 + i) * kLd + d);
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(kThr, 1) packed_f32(const PackedAttn a, const 
             // a NaN or infinity in its V stays out of the rows that do not see it.
             auto pv = [&](auto skip_zero) {
 #pragma unroll 4
-                for (int j = 0; j < kKB; ++j) {
+                for (int j = live ? 0 : kKB; j < kKB; ++j) {
                     const float4 p = *reinterpret_cast<const float4*>(p_t + j * kPld + ty * 4);
                     const float pr[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
@@ -364,9 +366,10 @@ template <int D> cudaError_t launch(const PackedAttn& a, cudaStream_t st) {
     s.max_rows = a.r.max_rows;
     s.Hkv = a.Hkv;
     s.tu = tq;
-    s.tile = tq;
+    s.tile = 0x7fffffff;  // a unit is one tile: its blocks cost the same
     s.kb = kKB;
     s.start = 1;
+    s.min_share = 1;
     s.n_ctas = a.n_ctas;
     s.cap = int64_t(a.c.max_blocks) * a.c.page_size;
     cudaError_t e = launch_pdl(packed_f32<D, true>, dim3(a.n_ctas), dim3(kThr), sm, st, a, s, 0);

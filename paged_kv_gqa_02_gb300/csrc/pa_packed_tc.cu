@@ -1193,6 +1193,7 @@ cudaError_t launch_typed(const PackedAttn& a, cudaStream_t st) {
         s.tile = p.tq;
         s.kb = kBN;
         s.start = kUnitStart;
+        s.min_share = 2;  // a key tile for each side
         s.n_ctas = a.n_ctas;
         s.cap = int64_t(a.c.max_blocks) * a.c.page_size;
         ctas = a.n_ctas;

@@ -11,8 +11,8 @@
 // share is finished there; the pieces of the others are left in slots and
 // joined in ascending CTA order.  A CTA leaves at most two pieces: one of a
 // unit that began before its share (slot 2c) and one of a unit that begins in
-// it (slot 2c + 1).  Shares have two positions at least, so that none lies
-// inside a unit without one of its blocks.
+// it (slot 2c + 1).  Shares have `min_share` positions at least, two where a
+// block has two, so that none lies inside a unit without one of its blocks.
 // The partition depends on the lengths and n alone, so results repeat bit for
 // bit, and on the device only through n.
 #pragma once
@@ -26,12 +26,10 @@ namespace pa {
 
 namespace {  // each kernel's file has its own copy of the join
 
-constexpr int kMinShare = 2;  // positions of a share
-
 struct TreeShape {
     const int32_t* cu_lens;
     const int32_t* context_lens;
-    int32_t num_seqs, total_rows, max_rows, Hkv, tu, tile, kb, start, n_ctas;
+    int32_t num_seqs, total_rows, max_rows, Hkv, tu, tile, kb, start, min_share, n_ctas;
     int64_t cap;  // tokens a block table holds
 };
 
@@ -74,7 +72,7 @@ __device__ inline int64_t warp_sum64(int64_t v) {
 
 // CTAs that take part.
 __device__ inline int tree_ctas(const TreeShape& a, int64_t total) {
-    return int(min(int64_t(a.n_ctas), max(int64_t(1), total / kMinShare)));
+    return int(min(int64_t(a.n_ctas), max(int64_t(1), total / a.min_share)));
 }
 // 64-bit division takes long; the usual operands fit 32 bits.
 __device__ inline int64_t div_pos(int64_t a, int64_t b) {
