@@ -50,7 +50,8 @@ extern "C" {
  * or less than none is skipped, its rows left as they were (PA_DEV_BAD_LEN);
  * rows that ends out of order give to two sequences hold either's result. */
 typedef struct {
-    int32_t total_rows;  /* rows of the packed tensors; 0: nothing to do         */
+    int32_t total_rows;  /* rows of the packed tensors, at most 2^30; 0: nothing
+                            to do                                                */
     int32_t max_rows;    /* host bound on the rows of one sequence               */
     int32_t source_rows; /* pa_store with row_index: rows of k and v; 0 means
                             total_rows                                           */

@@ -12,6 +12,7 @@ namespace {
 
 constexpr int kRefSms = 152;         // shares of a deterministic tree call
 constexpr int kMaxTreeRows = 1024;   // drafts of one sequence
+constexpr int kMaxRows = 1 << 30;    // packed rows: sums with a tile stay in 32 bits
 
 int elt_bytes(pa_dtype d) { return d == PA_F32 ? 4 : 2; }
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -68,6 +69,7 @@ pa_status check_cache(const pa_params* p, pa::CacheArgs* c) {
 pa_status check_rows(const pa_params* p, const pa_rows* r, pa::RowArgs* a) {
     if (r->total_rows < 0 || r->max_rows < 0 || (r->total_rows > 0 && r->max_rows < 1)) return PA_ERR_SHAPE;
     if (r->source_rows < 0 || r->mask_words < 0) return PA_ERR_SHAPE;
+    if (r->total_rows > kMaxRows) return PA_ERR_UNSUPPORTED;
     const int64_t D = p->head_dim, nq = D * p->num_q_heads, nk = D * p->num_kv_heads;
     a->num_seqs = p->num_seqs;
     a->total_rows = r->total_rows;
@@ -93,7 +95,7 @@ pa_status check_tree(const pa_params* p, const pa_rows* r, pa::PackedAttn* a) {
     if (p->num_splits != 0 || p->sliding_window != 0 || p->decode_q_rows > 1) return PA_ERR_UNSUPPORTED;
     if (a->r.max_rows > kMaxTreeRows) return PA_ERR_UNSUPPORTED;
     const int words = (a->r.max_rows + 31) / 32;
-    a->mask_words = r->mask_words ? r->mask_words : (r->max_rows + 31) / 32;
+    a->mask_words = r->mask_words ? r->mask_words : int((int64_t(r->max_rows) + 31) / 32);
     if (a->mask_words < words) return PA_ERR_SHAPE;
     a->n_ctas = share_ctas(p);
     return PA_OK;
