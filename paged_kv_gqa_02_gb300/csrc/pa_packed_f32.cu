@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThr, 1) packed_f32(const PackedAttn a, const 
     const int G = a.Hq / a.Hkv;
     const int tq = kM / G;  // packed rows of a tile
     pdl_wait_primary();
-    pdl_launch_dependents();  // after the wait: the join reads the lengths before its own
+    pdl_launch_dependents();  // after the wait, so that nothing overtakes what it waited for
 
     TreeWalk walk;
     TreeItem it;

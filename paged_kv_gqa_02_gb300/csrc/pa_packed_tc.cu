@@ -64,7 +64,8 @@ constexpr int kKS = 3;    // K ring depth
 constexpr int kVS = 2;    // V ring depth
 constexpr int kIS = 2;    // items published ahead
 constexpr int kThreads = 384;  // three warpgroups
-constexpr int kSoftmaxRegs = 184, kOtherRegs = 128;  // a thread; 2 x 208 + 88 = 3 x 168, the launch's
+// registers of a thread: 2 x 184 + 128 of the launch's 3 x 168 (208 + 88 was slower: the others spilled)
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 128;
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
 constexpr int kCleanWarp = 10;
@@ -292,31 +293,34 @@ template <bool kTree> __device__ inline Sides sides_of(const TreeItem& t, int tq
     return s;
 }
 
-// A prompt's units, numbered in descending order of key tiles: by level (the
-// tile of rows, from the last), then sequence, then kv head.  The grid has a CTA
-// for each number there can be; the SMs hold one CTA each, and a CTA that is
-// done asks the hardware to cancel the launch of a waiting one and takes its
-// number, so that the longest units come first and none waits for a CTA that
-// drew longer ones (numbers dealt out in turn instead: the ragged batch's CTAs
-// ended between 95 and 180 us).
+// A prompt's units, numbered.  Up to 32 sequences: in descending order of key
+// tiles, by level (the tile of rows, from the last), then sequence, then kv head.
+// More: by sequence, then level from the last, then kv head, as finding a level
+// would mean counting all sequences again for each unit.  The grid has a CTA for
+// each number there can be; an SM holds one, and a CTA that is done asks the
+// hardware to cancel the launch of a waiting one and takes its number, so that
+// the longest units come first and none waits for a CTA that drew longer ones
+// (numbers dealt out in turn instead: the ragged batch's CTAs ended between 95
+// and 180 us).
 struct PromptUnits {
-    int lane_n;  // units of sequence `lane`, in calls of up to 32
-    __device__ inline int units(const TcArgs& p, int s) {
+    int base, first;  // the window of 32 sequences at hand; units of those before it
+    int lane_n;       // units of sequence base + lane
+    __device__ inline void load(const TcArgs& p, int b) {
         const PackedAttn& a = p.a;
-        if (s >= a.r.num_seqs) return 0;
-        const int r0 = a.r.cu_lens[s], r1 = a.r.cu_lens[s + 1];
-        if (r0 < 0 || r1 < r0 || r1 > a.r.total_rows || r1 - r0 > a.r.max_rows) return 0;
-        return (r1 - r0 + p.tu - 1) / p.tu;
+        const int s = b + int(threadIdx.x & 31);
+        base = b;
+        lane_n = 0;
+        if (s < a.r.num_seqs) {
+            const int r0 = a.r.cu_lens[s], r1 = a.r.cu_lens[s + 1];
+            if (r0 >= 0 && r1 >= r0 && r1 <= a.r.total_rows && r1 - r0 <= a.r.max_rows)
+                lane_n = (r1 - r0 + p.tu - 1) / p.tu;
+        }
     }
-    __device__ inline void start(const TcArgs& p) { lane_n = units(p, threadIdx.x & 31); }
-    __device__ inline int lane_units(const TcArgs& p, int base) {
-        return p.a.r.num_seqs <= 32 ? lane_n : units(p, base + int(threadIdx.x & 31));
+    __device__ inline void start(const TcArgs& p) {
+        first = 0;
+        load(p, 0);
     }
-    // units at `level` and above, of all sequences
-    __device__ inline int above(const TcArgs& p, int level) {
-        int n = 0;
-#pragma unroll 1
-        for (int b = 0; b < p.a.r.num_seqs; b += 32) n += max(0, lane_units(p, b) - level);
+    static __device__ inline int warp_add(int n) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
         return n;
@@ -325,37 +329,53 @@ struct PromptUnits {
     __device__ inline bool get(const TcArgs& p, int i, TreeItem& it) {
         const PackedAttn& a = p.a;
         const int k = i / a.Hkv;
-        if (k >= above(p, 0)) return false;
-        int lo = 0, hi = p.n_units - 1;  // the highest level with more than k units at and above it
+        int level;
+        if (a.r.num_seqs <= 32) {
+            if (k >= warp_add(lane_n)) return false;
+            int lo = 0, hi = p.n_units - 1;  // the highest level with more than k units at and above it
 #pragma unroll 1
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (above(p, mid) > k)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        int rank = k - above(p, lo + 1);  // among the sequences that reach this level
-#pragma unroll 1
-        for (int b = 0;; b += 32) {
-            unsigned m = __ballot_sync(0xffffffffu, lane_units(p, b) > lo);
-            if (rank < __popc(m)) {
-#pragma unroll 1
-                for (; rank > 0; --rank) m &= m - 1;
-                it.seq = b + __ffs(m) - 1;
-                break;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (warp_add(max(0, lane_n - mid)) > k)
+                    lo = mid;
+                else
+                    hi = mid - 1;
             }
-            rank -= __popc(m);
+            level = lo;
+            int rank = k - warp_add(max(0, lane_n - lo - 1));  // among the sequences that reach this level
+            unsigned m = __ballot_sync(0xffffffffu, lane_n > lo);
+#pragma unroll 1
+            for (; rank > 0; --rank) m &= m - 1;
+            it.seq = __ffs(m) - 1;
+        } else {
+            if (k < first) start(p);  // numbers mostly rise
+            int all;
+#pragma unroll 1
+            while (k >= first + (all = warp_add(lane_n))) {
+                if (base + 32 >= a.r.num_seqs) return false;
+                first += all;
+                load(p, base + 32);
+            }
+            int upto = lane_n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (int(threadIdx.x & 31) >= o) upto += y;
+            }
+            const int l = __ffs(__ballot_sync(0xffffffffu, first + upto > k)) - 1;
+            it.seq = base + l;
+            level = first + __shfl_sync(0xffffffffu, upto, l) - 1 - k;  // the sequence's last unit first
         }
         const int r0 = a.r.cu_lens[it.seq];
         it.g = i - k * a.Hkv;
         it.T = a.r.cu_lens[it.seq + 1] - r0;
-        it.t0 = lo * p.tu;
+        it.t0 = level * p.tu;
         it.n_rows = min(p.tu, it.T - it.t0);
         it.row0 = r0 + it.t0;
         it.L = it.nh = it.b0 = 0;
         it.b1 = (it.t0 + it.n_rows + kBN - 1) / kBN;
         it.slot = -1;
+        it.last = 0;
         it.bad_len = false;
         return true;
     }
@@ -451,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_after_sync();
     const uint32_t tm = B.tmem;
     pdl_wait_primary();
-    pdl_launch_dependents();  // after the wait: the join reads the lengths before its own
+    pdl_launch_dependents();  // after the wait, so that nothing overtakes what it waited for
     if (a.debug_timeout) {
         // Testing: a wait that runs out before any copy is issued (a barrier
         // nothing targets, no time allowed) aborts every role of the CTA.
@@ -630,8 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 const uint32_t off = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
-                mma_ss1(tm + col_s(x), tc::make_desc(qx + off, hi_d), tc::make_desc(kx + off, hi_d), idQK,
-                                 ks > 0, el);
+                mma_ss1(tm + col_s(x), tc::make_desc(qx + off, hi_d), tc::make_desc(kx + off, hi_d), idQK, ks > 0, el);
             }
             commit1(&B.s_full[x], el);
         };
@@ -657,8 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto have_v = [&](int t) { return wait_all(&B.v_clean[t % kVS], (t / kVS) & 1); };
         int kt = 0;          // K and V tiles of the items before
         int sc[2] = {0, 0};  // score tiles of x issued; P_x V number sc - 1 waits for its P
-        // The pair of an item's side x with tile t: P V, and behind it, where this
-        // warp would wait anyway, the commits and the next tiles' waits.
+        // P V of side x with tile t.  Behind it, where this warp would wait anyway,
+        // stand the commits and the next tiles' waits.
         auto take_p = [&](int x, int t, bool first) {
             if (!wait_all(&B.p_full[x], (sc[x] - 1) & 1)) return false;
             tc::fence_after_sync();
@@ -806,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ================================= softmax =================================
         regs_grow<kSoftmaxRegs>();
-        const int x = warp >> 2;  // row tile
+        const int x = warp >> 2;  // side
         const int quad = warp & 3;
         const int m = quad * 32 + lane;  // MMA row = tensor-memory lane
         const uint32_t lane_addr = uint32_t(quad * 32) << 16;
@@ -815,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t sbase = tm + lane_addr + col_s(x);
         const uint32_t obase = tm + lane_addr + col_o<D>(x);
         int sc = 0, sc_other = 0;  // score tiles of this side and of the other before this item
-        int twins = 0;       // twins before it
+        int twins = 0;             // twins before it
         bool ok = true;
         for (int n = 0; ok; ++n) {
             const int is = n % kIS;
@@ -1071,7 +1090,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t z0, z1;
                     f2_unpack(z, z0, z1);
                     const float zz = __uint_as_float(z0) + __uint_as_float(z1);
-                    if (row_ok && w.x == w.x && (poison || zz != zz)) restore(r, t, row, tt, 32 * c);
+                    if (row_ok && !t.bad_len && w.x == w.x && (poison || zz != zz)) restore(r, t, row, tt, 32 * c);
                     __syncwarp();
                     // row i of this lane's group of four: its lane's own dst
                     auto row_at = [&](int i, uint64_t mine) {

@@ -121,14 +121,10 @@ struct TreeWalk {
 
     __device__ inline void start(const TreeShape& a, int c) {
         cta = c;
-        int64_t all = 0;
         load(a, 0);
-        all = lane_cost(a);
-#pragma unroll 1
-        for (int b = 32; b < a.num_seqs; b += 32) {
-            load(a, b);
-            all += lane_cost(a);
-        }
+        int64_t all = lane_cost(a);
+#pragma unroll 4
+        for (int i = 32 + int(threadIdx.x & 31); i < a.num_seqs; i += 32) all += tree_seq_cost(a, tree_seq(a, i));
         total = warp_sum64(all);
         n = tree_ctas(a, total);
         at = end = 0;
@@ -137,7 +133,6 @@ struct TreeWalk {
         end = share_start(total, n, c + 1);
         seq_at = 0;
         // the sequence that position `at` lies in, 32 at a time
-        if (base != 0) load(a, 0);
 #pragma unroll 1
         for (;;) {
             const int64_t own = lane_cost(a);

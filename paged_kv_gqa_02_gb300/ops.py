@@ -321,16 +321,20 @@ def prompt_params(*, num_seqs, num_q_heads, num_kv_heads, head_dim, scale=None, 
                        debug_timeout=debug_timeout)
 
 
-_DTYPES = ()
+_DTYPES, _I32 = (), None  # torch's dtypes by dtype code, and its int32, once known
 
 
 def _dtypes():
-    """torch's dtypes by dtype code, then int32."""
-    global _DTYPES
+    global _DTYPES, _I32
     if not _DTYPES:
         import torch
-        _DTYPES = (torch.float32, torch.float16, torch.bfloat16, torch.int32)
+        _DTYPES, _I32 = (torch.float32, torch.float16, torch.bfloat16), torch.int32
     return _DTYPES
+
+
+def _int32():
+    _dtypes()
+    return _I32
 
 
 # The messages are put together only when a check fails, and each property of a
@@ -339,7 +343,7 @@ def _dtypes():
 
 def _ints(t, n, dev, what):
     """Pointer of a contiguous int32 tensor of at least n elements on device number dev."""
-    if t.get_device() != dev or t.dtype is not _dtypes()[3] or t.numel() < n or not t.is_contiguous():
+    if t.dtype is not (_I32 or _int32()) or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous int32 tensor of at least {n} elements on cuda:{dev}")
     return t.data_ptr()
 

@@ -319,3 +319,35 @@ def test_a_wait_that_runs_out_is_reported(op):
         ops.tree(p, r, q, k, v, c, mask, pool.k, pool.v, pool.tables, pool.context, dev_status=status)
     assert int(status.item()) & ops.PA_DEV_TIMEOUT
     run_prompt([300], "bf16", "bf16", 8, 2, 64)
+
+
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+@pytest.mark.parametrize("n", (33, 70))
+def test_prompt_many_sequences(dtype, n):
+    """More sequences than a warp has lanes, some empty, some of several units."""
+    run_prompt([0 if i % 5 == 3 else (i * 53) % 190 + (400 if i == 40 else 0) for i in range(n)], dtype, dtype, 8, 2, 64, pad=2)
+
+
+def test_tree_bad_length_beside_bad_values():
+    """A sequence whose length is refused is zeros even where its drafts' V are not finite."""
+    pool, p, r, q, k, v, c, mask, clean = run_tree([60, 40], [9, 6], "bf16", "bf16", 4, 2, 64, 16)
+    v[3, 0, 1] = float("nan")
+    pool.context[0] = -1
+    out = ops.tree(p, r, q, k, v, c, mask, pool.k, pool.v, pool.tables, pool.context)
+    assert (out[:9] == 0).all() and torch.equal(out[9:], clean[9:])
+
+
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+def test_tree_workspace_holds_nothing_over(dtype):
+    """A workspace full of another call's pieces gives the bits that a filled one gives."""
+    kw = dict(dtype=dtype, out_dtype=dtype, hq=8, hkv=2, d=64, page=16)
+    a = run_tree([900, 33, 0], [20, 40, 7], seed=3, **kw)
+    b = run_tree([64, 2000, 7], [33, 64, 30], seed=4, **kw)
+    ws = torch.empty(max(ops.tree_workspace_size(m[1], m[2]) for m in (a, b)), dtype=torch.uint8, device="cuda")
+    for m in (a, b, a, b, b):
+        pool, p, r, q, k, v, c, mask, first = m
+        out = ops.tree(p, r, q, k, v, c, mask, pool.k, pool.v, pool.tables, pool.context, workspace=ws)
+        assert torch.equal(out, first)
+    ws.fill_(127)
+    pool, p, r, q, k, v, c, mask, first = a
+    assert torch.equal(ops.tree(p, r, q, k, v, c, mask, pool.k, pool.v, pool.tables, pool.context, workspace=ws), first)
