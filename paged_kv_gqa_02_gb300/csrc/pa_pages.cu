@@ -394,10 +394,10 @@ template <bool kFlat> __global__ void __launch_bounds__(kCopyThr) pages_copy(con
     for (int64_t i0 = int(blockIdx.x) / a.parts; i0 < a.n; i0 += int64_t(32) * step) {
         const int64_t mine = i0 + int64_t(lane) * step;
         const int2 read = mine < a.n ? pairs[mine] : make_int2(-1, -1);
-        const bool real = read.x >= 0 && read.y >= 0 && read.x != read.y;
+        const bool real = read.x >= 0 && read.y >= 0;
         const bool in = real && read.x < a.num_pages && read.y < a.num_pages;
         if (real && !in && threadIdx.x < 32) flag(a.dev_status, PA_DEV_BAD_INDEX);
-        for (unsigned m = __ballot_sync(0xffffffffu, in); m; m &= m - 1) {
+        for (unsigned m = __ballot_sync(0xffffffffu, in && read.x != read.y); m; m &= m - 1) {
             const int l = __ffs(m) - 1;
             const int2 p = make_int2(__shfl_sync(0xffffffffu, read.x, l), __shfl_sync(0xffffffffu, read.y, l));
             const int c0 = part * (kCopyThr * kCopyPer) + int(threadIdx.x);
@@ -470,8 +470,9 @@ __global__ void __launch_bounds__(kStoreThr) store_rows(const StoreArgs a) {
     const int s = lo;
     if (s >= a.num_seqs) return;  // behind the last sequence
     const int r0 = a.cu_lens[s], r1 = a.cu_lens[s + 1], L = a.context_lens[s];
+    if (row < r0) return;  // before the first sequence (ends out of order are flagged above)
     const int n = r1 - r0;
-    if (r0 < 0 || row < r0 || row >= r1 || r1 > a.total_rows || n > a.max_rows || L < n ||
+    if (r0 < 0 || row >= r1 || r1 > a.total_rows || n > a.max_rows || L < n ||
         L > int64_t(a.max_blocks) * a.page_size) {
         if (lane == 0) flag(a.dev_status, PA_DEV_BAD_LEN);
         return;

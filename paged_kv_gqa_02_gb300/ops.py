@@ -368,8 +368,10 @@ def _pool(t, p, dev, what):
         ps = p.page_stride or p.page_size * ts
         last = (p.num_pages - 1) * ps + (p.page_size - 1) * ts + (p.num_kv_heads - 1) * hs + p.head_dim
     if (t.get_device() != dev or t.dtype is not _dtypes()[p.kv_dtype]
-            or (t.numel() < last if t.is_contiguous() else _elements_behind(t) < last)):
-        raise ValueError(f"{what}: {last} elements of {_dtypes()[p.kv_dtype]} on cuda:{dev}")
+            or (t.numel() < last if t.is_contiguous()
+                else not (p.head_stride or p.token_stride or p.page_stride) or _elements_behind(t) < last)):
+        raise ValueError(f"{what}: {last} elements of {_dtypes()[p.kv_dtype]} on cuda:{dev}, contiguous unless "
+                         "the parameters give strides")
     return t.data_ptr()
 
 

@@ -260,6 +260,10 @@ def test_python_checks_see_what_the_library_cannot():
     assert ops._pool(pool, p, dev, "k") == pool.data_ptr()
     with pytest.raises(ValueError):
         ops._pool(pool[:2], p, dev, "k")
+    layers = torch.zeros(3, 2, 16, 2, 64, dtype=torch.bfloat16)  # two layers' pages side by side
+    with pytest.raises(ValueError):
+        ops._pool(layers[:, 1], p, dev, "k")
+    assert ops._pool(layers[:, 1], params(num_pages=3, strides=(2 * 16 * 128, 128, 64)), dev, "k")
     head_major = params(num_pages=3, strides=(2 * 16 * 64, 64, 16 * 64))
     assert ops._pool(torch.zeros(3, 2, 16, 64, dtype=torch.bfloat16), head_major, dev, "k")
     with pytest.raises(ValueError):

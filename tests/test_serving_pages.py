@@ -104,6 +104,24 @@ def test_store_refused_rows():
         assert torch.equal(got.nan_to_num(9.0), w.nan_to_num(9.0))
 
 
+def test_store_leaves_rows_before_the_first_sequence():
+    gen = torch.Generator().manual_seed(15)
+    pool = ref.Pool([20, 5], 16, 2, 64, "bf16", gen)
+    k, v = (torch.randn((9, 2, 64), generator=gen).to(torch.bfloat16).cuda() for _ in range(2))
+    want = [x.clone() for x in pool.kv]
+    for s, (row, n, L) in enumerate([(3, 4, 20), (7, 1, 5)]):
+        for i in range(n):
+            pos = L - n + i
+            for w, x in zip(want, (k, v)):
+                w[pool.tables[s, pos // 16].long(), pos % 16] = x[row + i]
+    status = status_word()
+    ops.store(pool.params(2), ops.make_rows(9, 4), k, v, i32([3, 7, 8]), pool.k, pool.v, pool.tables, pool.context,
+              dev_status=status)
+    assert int(status.item()) == 0
+    for got, w in zip(pool.kv, want):
+        assert torch.equal(got.nan_to_num(9.0), w.nan_to_num(9.0))
+
+
 # ---- bookkeeping -----------------------------------------------------------------
 
 class Device:
@@ -247,6 +265,16 @@ def test_copy(dtype, page, hkv, d, head_major):
     assert int(status.item()) == ops.PA_DEV_BAD_INDEX
     for got, w in zip(pool.kv, want):
         assert torch.equal(got, w)
+
+
+def test_copy_flags_a_pair_outside_the_pool_that_goes_nowhere():
+    pool = torch.ones(3, 16, 2, 64, dtype=torch.bfloat16, device="cuda")
+    p = params(1, 3, 1)
+    for pair, want in (([7, 7], ops.PA_DEV_BAD_INDEX), ([1, 1], 0), ([-1, 9], 0), ([0, 3], ops.PA_DEV_BAD_INDEX)):
+        status = status_word()
+        ops.pages_copy(p, pool, pool.clone(), i32([pair]), dev_status=status)
+        assert int(status.item()) == want, pair
+        assert (pool == 1).all()
 
 
 def test_page_calls_replay():
