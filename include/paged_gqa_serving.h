@@ -45,10 +45,12 @@ extern "C" {
 
 /* Packed rows: sequence s owns rows cu_lens[s] .. cu_lens[s+1]-1 of q, k, v
  * and out; cu_lens is [num_seqs + 1] int32 on the device, ascending from a
- * value >= 0.  Rows behind the last sequence's are neither read nor written.
- * A sequence whose rows leave [0, total_rows] or number more than max_rows
- * or less than none is skipped, its rows left as they were (PA_DEV_BAD_LEN);
- * rows that ends out of order give to two sequences hold either's result. */
+ * value >= 0.  Rows before the first sequence's and behind the last one's
+ * have no part in any result and are not written.  A sequence whose rows
+ * leave [0, total_rows] or number more than max_rows or less than none is
+ * skipped, its rows left as they were (PA_DEV_BAD_LEN).  Where ends descend
+ * (flagged too), rows can belong to several sequences, and each row of the
+ * call holds one of its sequences' results or is left as it was. */
 typedef struct {
     int32_t total_rows;  /* rows of the packed tensors, at most 2^30; 0: nothing
                             to do                                                */
@@ -86,7 +88,7 @@ pa_status pa_prompt(const pa_params *p, const pa_rows *r, const void *q, const v
 /* -------------------------------------------------------------------- tree
  * T_s drafts of sequence s (its packed rows) over a history of
  * L_s = context_lens[s] cached tokens, 0 <= L_s <= max_blocks_per_seq *
- * page_size; the history does not hold the drafts, whose K/V come packed in
+ * page_size and at most 2^30; the history does not hold the drafts, whose K/V come packed in
  * k and v.  Row t attends every history key, and draft j < T_s where bit
  * j % 32 of word j / 32 of its mask row is set (its own bit is not implied).
  *   tree_mask: [total_rows][mask_words] 32-bit words.

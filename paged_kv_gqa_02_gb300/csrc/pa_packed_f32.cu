@@ -371,7 +371,7 @@ template <int D> cudaError_t launch(const PackedAttn& a, cudaStream_t st) {
     s.start = 1;
     s.min_share = 1;
     s.n_ctas = a.n_ctas;
-    s.cap = int64_t(a.c.max_blocks) * a.c.page_size;
+    s.cap = a.max_history;
     cudaError_t e = launch_pdl(packed_f32<D, true>, dim3(a.n_ctas), dim3(kThr), sm, st, a, s, 0);
     if (e != cudaSuccess) return e;
     return launch_join<float, D>(s, a, kM, st);

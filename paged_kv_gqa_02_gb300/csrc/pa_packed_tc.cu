@@ -928,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc::st_32x32b_x16(obase + 16 * c, ro);
                         }
                     }
-                                    const float nmu = m_run == -INFINITY ? 0.f : -m_run;  // nothing seen yet: weights 0, not NaN
+                    const float nmu = m_run == -INFINITY ? 0.f : -m_run;  // nothing seen yet: weights 0, not NaN
                     const uint64_t sl2_2 = f2_pack(__float_as_uint(sl2), __float_as_uint(sl2));
                     const uint64_t nmu_2 = f2_pack(__float_as_uint(nmu), __float_as_uint(nmu));
                     uint64_t sum_2[2] = {f2_pack(0u, 0u), f2_pack(0u, 0u)};
@@ -970,37 +970,69 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
 
-            // Puts right 32 dims of a row that sees a NaN or infinity in V: one
-            // that was kept out of P.V, or that met a zero part of P there.  What
-            // the row sees of them is the result, whatever the rest adds up to.
-            auto restore = [&](uint32_t (&r)[32], const TreeItem& it, int at, int place, int d0) {
+            // Puts right 32 dims of the rows that `mine` marks, which may see a NaN or
+            // infinity in V: one that was kept out of P.V, or that met a zero part
+            // of P there.  What a row sees of them is the result, whatever the rest
+            // adds up to.  The whole warp looks for them, a key a lane, as there are
+            // few or one alone makes all that a row sees NaN (20000 rows, 2/1 heads of
+            // 64, a NaN in one of them: 0.55 ms, 0.23 ms without it; when each row went
+            // through its keys by itself, 45 ms).
+            auto restore = [&](uint32_t (&r)[32], const TreeItem& it, int at, int place, int d0, bool mine) {
                 float f[32];  // rolled loops and local memory: rare, and small code
 #pragma unroll 1
                 for (int k = 0; k < 32; ++k) f[k] = 0.f;
                 const int n_hist = kTree ? max(0, min(it.L, min(it.b1, it.nh) * kBN) - it.b0 * kBN) : 0;
                 const int k_lo = max(0, it.b0 - it.nh) * kBN;
-                const int k_hi = kTree ? min(it.T, max(0, it.b1 - it.nh) * kBN) : place + 1;
+                const int k_hi = kTree ? min(it.T, max(0, it.b1 - it.nh) * kBN) : it.t0 + it.n_rows;
+                const int n_keys = n_hist + max(0, k_hi - k_lo);
+                bool left = mine;  // false once all that can follow changes nothing
 #pragma unroll 1
-                for (int i = 0; i < n_hist + max(0, k_hi - k_lo); ++i) {
-                    const T* v;
+                for (int i0 = 0; i0 < n_keys && __any_sync(0xffffffffu, left); i0 += 32) {
+                    const int i = i0 + lane;
+                    const T* v = nullptr;
                     if (kTree && i < n_hist) {
                         const int key = it.b0 * kBN + i, pg = table[key / P];
-                        if (pg < 0 || pg >= a.c.num_pages) continue;
-                        v = static_cast<const T*>(a.c.v) + int64_t(pg) * a.c.page_stride +
-                            int64_t(key % P) * a.c.token_stride + int64_t(it.g) * a.c.head_stride + d0;
-                    } else {
-                        const int key = k_lo + i - n_hist;
-                        if (kTree && ((key >> 5) >= a.mask_words ||
-                                      !((a.tree_mask[int64_t(at) * a.mask_words + (key >> 5)] >> (key & 31)) & 1u)))
-                            continue;
-                        v = static_cast<const T*>(a.v) + int64_t(it.row0 - it.t0 + key) * a.r.v_stride + it.g * D + d0;
+                        if (pg >= 0 && pg < a.c.num_pages)
+                            v = static_cast<const T*>(a.c.v) + int64_t(pg) * a.c.page_stride +
+                                int64_t(key % P) * a.c.token_stride + int64_t(it.g) * a.c.head_stride + d0;
+                    } else if (i < n_keys) {
+                        v = static_cast<const T*>(a.v) + int64_t(it.row0 - it.t0 + k_lo + i - n_hist) * a.r.v_stride +
+                            it.g * D + d0;
                     }
+                    uint32_t acc = 0u;
+                    if (v) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint4 w = reinterpret_cast<const uint4*>(v)[c];
+                            acc = H2<T>::probe(w.x, H2<T>::probe(w.y, H2<T>::probe(w.z, H2<T>::probe(w.w, acc))));
+                        }
+                    }
+                    unsigned m = __ballot_sync(0xffffffffu, bad16<T>(acc) || bad16<T>(acc >> 16));
 #pragma unroll 1
-                    for (int k = 0; k < 32; ++k) {
-                        const float y = Elt<T>::f(v[k]);
-                        if (!isfinite(y)) f[k] += y;
+                    for (; m; m &= m - 1) {
+                        const int l = __ffs(m) - 1, key = k_lo + i0 + l - n_hist;
+                        const T* u = reinterpret_cast<const T*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(v), l));
+                        bool sees = left;
+                        if (i0 + l >= n_hist) {
+                            if constexpr (kTree)
+                                sees = sees && (key >> 5) < a.mask_words &&
+                                       ((a.tree_mask[int64_t(at) * a.mask_words + (key >> 5)] >> (key & 31)) & 1u);
+                            else
+                                sees = sees && key <= place;
+                        }
+                        if (!__any_sync(0xffffffffu, sees)) continue;
+                        const float y = Elt<T>::f(u[lane]);  // a dim a lane
+                        if (__all_sync(0xffffffffu, y != y) && sees) left = false;
+                        unsigned dims = __ballot_sync(0xffffffffu, !isfinite(y));
+#pragma unroll 1
+                        for (; dims; dims &= dims - 1) {
+                            const int k = __ffs(dims) - 1;
+                            const float z = __shfl_sync(0xffffffffu, y, k);
+                            if (sees) f[k] += z;
+                        }
                     }
                 }
+                if (!mine) return;
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
                     if (!isfinite(f[k])) r[k] = __float_as_uint(f[k]);
@@ -1090,7 +1122,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t z0, z1;
                     f2_unpack(z, z0, z1);
                     const float zz = __uint_as_float(z0) + __uint_as_float(z1);
-                    if (row_ok && !t.bad_len && w.x == w.x && (poison || zz != zz)) restore(r, t, row, tt, 32 * c);
+                    const bool fix = row_ok && !t.bad_len && w.x == w.x && (poison || zz != zz);
+                    if (__any_sync(0xffffffffu, fix)) restore(r, t, row, tt, 32 * c, fix);
                     __syncwarp();
                     // row i of this lane's group of four: its lane's own dst
                     auto row_at = [&](int i, uint64_t mine) {
@@ -1214,7 +1247,7 @@ cudaError_t launch_typed(const PackedAttn& a, cudaStream_t st) {
         s.start = kUnitStart;
         s.min_share = 2;  // a key tile for each side
         s.n_ctas = a.n_ctas;
-        s.cap = int64_t(a.c.max_blocks) * a.c.page_size;
+        s.cap = a.max_history;
         ctas = a.n_ctas;
     } else {
         // Two row tiles share their K/V tiles; one alone makes twice as many, half

@@ -40,6 +40,7 @@ struct PackedAttn {
     // tree only
     const uint32_t* tree_mask;  // nullptr: prompt
     int32_t mask_words;
+    int32_t max_history;  // what a block table holds, 2^30 at most
     CacheArgs c;
     int32_t n_ctas;
     void* workspace;

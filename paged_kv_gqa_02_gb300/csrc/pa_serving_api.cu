@@ -13,10 +13,11 @@ namespace {
 constexpr int kRefSms = 152;         // shares of a deterministic tree call
 constexpr int kMaxTreeRows = 1024;   // drafts of one sequence
 constexpr int kMaxRows = 1 << 30;    // packed rows: sums with a tile stay in 32 bits
+constexpr int64_t kMaxHistory = 1 << 30;  // tokens before a tree, for the same reason
 
 int elt_bytes(pa_dtype d) { return d == PA_F32 ? 4 : 2; }
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-size_t known_dtype(pa_dtype d) { return d >= PA_F32 && d <= PA_BF16; }
+bool known_dtype(pa_dtype d) { return d >= PA_F32 && d <= PA_BF16; }
 
 int device_sms() {
     int dev = 0, n = 0;
@@ -97,6 +98,8 @@ pa_status check_tree(const pa_params* p, const pa_rows* r, pa::PackedAttn* a) {
     const int words = (a->r.max_rows + 31) / 32;
     a->mask_words = r->mask_words ? r->mask_words : int((int64_t(r->max_rows) + 31) / 32);
     if (a->mask_words < words) return PA_ERR_SHAPE;
+    const int64_t cap = int64_t(p->max_blocks_per_seq) * p->page_size;
+    a->max_history = int(cap < kMaxHistory ? cap : kMaxHistory);
     a->n_ctas = share_ctas(p);
     return PA_OK;
 }

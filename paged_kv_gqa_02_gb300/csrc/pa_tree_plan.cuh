@@ -30,7 +30,7 @@ struct TreeShape {
     const int32_t* cu_lens;
     const int32_t* context_lens;
     int32_t num_seqs, total_rows, max_rows, Hkv, tu, tile, kb, start, min_share, n_ctas;
-    int64_t cap;  // tokens a block table holds
+    int32_t cap;  // longest history: what a block table holds, 2^30 at most
 };
 
 struct TreeSeq {
@@ -229,7 +229,7 @@ template <> __device__ inline __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { r
 // A small call has many pieces for each of few distributions and waits for its
 // loads: sixteen in flight, a distribution a warp.  A large one has two or three
 // pieces for each of many and is bound by its instructions (36 us with sixteen
-// steps for each, 64 rows x 8, 64 heads): four in flight, four distributions a
+// steps for each, 64 rows x 8, 64 heads): four in flight, two distributions a
 // warp.
 template <typename TOut, int D, int kP>
 __global__ void __launch_bounds__(256)
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(256)
     }
 }
 // Launches it: one distribution a warp while that makes no more CTAs with work
-// than run at once, four otherwise.
+// than run at once, two otherwise.
 template <typename TOut, int D>
 inline cudaError_t launch_join(const TreeShape& a, const PackedAttn& p, int rows, cudaStream_t st) {
     const int64_t units = int64_t(a.Hkv) * (a.total_rows / a.tu + std::min(a.num_seqs, a.total_rows));

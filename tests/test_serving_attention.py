@@ -351,3 +351,88 @@ def test_tree_workspace_holds_nothing_over(dtype):
     ws.fill_(127)
     pool, p, r, q, k, v, c, mask, first = a
     assert torch.equal(ops.tree(p, r, q, k, v, c, mask, pool.k, pool.v, pool.tables, pool.context, workspace=ws), first)
+
+
+@pytest.mark.parametrize("op", ("prompt", "tree"))
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+def test_rows_before_the_first_sequence(op, dtype):
+    """Ends that start above 0: the rows before them have no part in the call."""
+    lens, first, total = [40, 9], 5, 57
+    q, k, v = packed(total, 4, 2, 64, dtype, 8)
+    for x in (q, k, v):
+        x[:first], x[first + 49:] = float("nan"), float("nan")
+    c = ref.cu(lens) + first
+    out, status = torch.full_like(q, 7.0), torch.zeros(1, dtype=torch.int32, device="cuda")
+    mine = slice(first, first + 49)
+    if op == "prompt":
+        p = ops.prompt_params(num_seqs=2, num_q_heads=4, num_kv_heads=2, head_dim=64, dtype=dtype, out_dtype=dtype)
+        ops.prompt(p, ops.make_rows(total, 40), q, k, v, c, out=out, dev_status=status)
+        want, tol = ref.prompt_ref(q[mine], k[mine], v[mine], lens, p.scale, dtype, dtype)
+    else:
+        gen = torch.Generator().manual_seed(9)
+        pool = ref.Pool([70, 3], 16, 2, 64, dtype, gen)
+        p = pool.params(4, out_dtype=dtype)
+        mask = ref.random_mask([first] + lens + [3], 2, gen)
+        ops.tree(p, ops.make_rows(total, 40), q, k, v, c, mask, pool.k, pool.v, pool.tables, pool.context, out=out,
+                 dev_status=status)
+        want, tol = ref.tree_ref(q[mine], k[mine], v[mine], lens, mask[mine].contiguous(), *pool.kv, pool.tables, [70, 3],
+                                 p.scale, dtype, dtype)
+    assert int(status.item()) == 0
+    ref.assert_close(out[mine], want, tol)
+    assert (out[:first] == 7.0).all() and (out[first + 49:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", ("f32", "f16"))
+def test_tree_histories_past_their_limit(dtype):
+    """A block table may hold more than 2^30 tokens; a history may not be that long."""
+    hq, blocks = 4, 1 << 27  # of 16 slots: 2^31
+    q, k, v = packed(3, hq, 2, 64, dtype, 4)
+    pool = torch.zeros(2, 16, 2, 64, dtype=ref.DT[dtype], device="cuda")
+    tables = torch.zeros(1, blocks, dtype=torch.int32, device="cuda")
+    p = ops.make_params(num_seqs=1, num_q_heads=hq, num_kv_heads=2, head_dim=64, page_size=16, num_pages=2,
+                        max_blocks_per_seq=blocks, max_context_len=0, dtype=dtype, out_dtype=dtype)
+    r, mask = ops.make_rows(3, 3), torch.ones(3, 1, dtype=torch.int32, device="cuda")
+    for n in ((1 << 30) + 1, (1 << 31) - 1):
+        out, status = torch.full_like(q, 7.0), torch.zeros(1, dtype=torch.int32, device="cuda")
+        ops.tree(p, r, q, k, v, ref.cu([3]), mask, pool, pool, tables, torch.tensor([n], dtype=torch.int32, device="cuda"),
+                 out=out, dev_status=status)
+        assert int(status.item()) == ops.PA_DEV_BAD_LEN
+        assert (out == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ("f16", "bf16"))
+@pytest.mark.parametrize("out_dtype", ("f32", None))
+def test_long_prompt_with_bad_values(dtype, out_dtype):
+    """Rows find the values that are not finite among many keys without the call taking hundreds of times as long."""
+    n, d, out_dtype = 20000, 64, out_dtype or dtype
+    q, k, v = packed(n, 2, 1, d, dtype, 6)
+    p = ops.prompt_params(num_seqs=1, num_q_heads=2, num_kv_heads=1, head_dim=d, dtype=dtype, out_dtype=out_dtype)
+    r, c = ops.make_rows(n, n), ref.cu([n])
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def timed():
+        ops.prompt(p, r, q, k, v, c, dev_status=status)
+        e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        e[0].record()
+        out = ops.prompt(p, r, q, k, v, c, dev_status=status)
+        e[1].record()
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        return out, e[0].elapsed_time(e[1])
+    clean, t0 = timed()
+    v[3, 0, 7] = float("nan")
+    v[40:, 0, 9] = float("inf")       # a dim that overflows from there on
+    v[9000, 0, 40] = -float("inf")
+    v[9500, 0, 40] = float("inf")     # and their sum
+    out, t1 = timed()
+    want = clean.clone()
+    want[3:, :, 7], want[40:, :, 9] = float("nan"), float("inf")
+    want[9000:, :, 40] = -float("inf")
+    want[9500:, :, 40] = float("nan")
+    same = (out == want) | (out.isnan() & want.isnan())
+    assert same.all(), f"{int((~same).sum())} elements"
+    assert t1 < 60 * t0 + 5, f"{t0} ms, {t1} ms with values that are not finite"
+    v[5:] = float("nan")              # all that a bad token leaves in the layers behind it
+    out, t1 = timed()
+    assert out[5:].isnan().all()
+    assert t1 < 60 * t0 + 5, f"{t0} ms, {t1} ms with NaNs behind row 5"
