@@ -63,6 +63,7 @@ constexpr int kBN = 128;  // keys of a tile
 constexpr int kKS = 3;    // K ring depth
 constexpr int kVS = 2;    // V ring depth
 constexpr int kIS = 2;    // items published ahead
+constexpr int kAsk = 8;   // CTAs that one past the last unit cancels at a time
 constexpr int kThreads = 384;  // three warpgroups
 // registers of a thread: 2 x 184 + 128 of the launch's 3 x 168 (208 + 88 was slower: the others spilled)
 constexpr int kSoftmaxRegs = 184, kOtherRegs = 128;
@@ -89,8 +90,8 @@ struct Bars {
     uint64_t k_full[kKS], k_empty[kKS], v_full[kVS], v_clean[kVS], v_empty[kVS];
     uint64_t s_full[2], p_full[2], o_done[2];  // of row tile x
     uint64_t item_full[kIS], item_empty[kIS];
-    uint64_t unit_asked;      // prompt: the next unit's number has arrived
-    alignas(16) uint4 unit;
+    uint64_t unit_asked;      // prompt: the units' numbers asked for have arrived
+    alignas(16) uint4 unit[kAsk];
     uint64_t side_b, side_w;  // twin: `side` holds B's figures; the weights
     uint64_t mma_done, never;
     uint32_t tmem, abort;
@@ -381,13 +382,14 @@ struct PromptUnits {
     }
 };
 
-// Asks for the number of a CTA that has not been launched; the answer (16 bytes)
-// arrives on `bar`.  Not to be asked again after a refusal.
-__device__ inline void ask_unit(uint4* answer, uint64_t* bar) {
-    mbar_arrive_expect_tx(bar, 16);
-    asm volatile(
+// Asks for the numbers of n CTAs that have not been launched; the answers (16
+// bytes each) arrive on `bar`.  Not to be asked again after a refusal.
+__device__ inline void ask_units(uint4* answer, int n, uint64_t* bar) {
+    mbar_arrive_expect_tx(bar, 16 * n);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) asm volatile(
         "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-            smem_u32(answer)),
+            smem_u32(answer + i)),
         "r"(smem_u32(bar))
         : "memory");
 }
@@ -523,8 +525,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int P = a.c.page_size;
         const int xc_first = p.head_first;
         int kq = 0, vq = 0, qn = 0;  // K tiles, V tiles and Qs issued
-        int items = 0;               // units asked for
-        bool ok = !*abort_flag, asked = false, joins = false;
+        int asks = 0, batch = 1;     // times that numbers were asked for, how many last
+        int number = lane == 0 ? int(blockIdx.x) : -1;  // units' numbers at hand, one a lane
+        bool ok = !*abort_flag, asked = false, refused = false, joins = false;
 #pragma unroll 1
         for (int n = 0; ok; ++n) {
             Item it;
@@ -537,15 +540,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                     joins = true;
                 }
             } else {
-                int i = blockIdx.x;
-                if (n > 0) {  // asked for before the last item's last tile
-                    ok = wait_all(&B.unit_asked, (n - 1) & 1);
-                    if (!ok) break;
-                    asked = false;
-                    i = answered_unit(&B.unit);
+                // A CTA whose number is past the last unit cancels those that wait, as
+                // they are past it too, until there are none: quicker than their launch
+                // (one prompt of 100 rows, 64/8 heads, replayed on a graph of 32768: 100
+                // us with each launched, 22 us so).
+                it.valid = 0;
+#pragma unroll 1
+                while (ok) {
+                    const unsigned m = __ballot_sync(0xffffffffu, number >= 0);
+                    if (m) {
+                        const int l = __ffs(m) - 1, i = __shfl_sync(0xffffffffu, number, l);
+                        if (lane == l) number = -1;
+                        it.valid = units.get(p, i, it.t);
+                        if (it.valid) break;
+                    } else if (refused) {
+                        break;
+                    } else {
+                        if (!asked) {  // else before the last item's last tile
+                            batch = kAsk;
+                            if (lane == 0) ask_units(B.unit, batch, &B.unit_asked);
+                            ++asks;
+                            asked = true;
+                        }
+                        ok = wait_all(&B.unit_asked, (asks - 1) & 1);
+                        if (!ok) break;
+                        asked = false;
+                        if (lane < batch) number = answered_unit(&B.unit[lane]);
+                        refused = __any_sync(0xffffffffu, lane < batch && number < 0);
+                    }
                 }
-                // past the last unit, all that wait are past it too
-                it.valid = i >= 0 && units.get(p, i, it.t);
+                if (!ok) break;
             }
             const int is = n % kIS;
             if (n >= kIS) ok = wait_all(&B.item_empty[is], ((n / kIS) - 1) & 1);
@@ -564,9 +588,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int j = 0; j < nt; ++j) {
                 if (!kTree && j == nt - 1) {
-                    if (lane == 0) ask_unit(&B.unit, &B.unit_asked);
-                    asked = true;
-                    ++items;
+                    // unless there are numbers at hand or none left (a warp-wide test)
+                    if (!refused && !__any_sync(0xffffffffu, number >= 0)) {
+                        batch = 1;
+                        if (lane == 0) ask_units(B.unit, batch, &B.unit_asked);
+                        ++asks;
+                        asked = true;
+                    }
                 }
                 const int blk = t.b0 + j;
                 const bool hist = kTree && blk < t.nh;
@@ -625,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tree_joins(a.workspace, 2 * kBM, D, a.n_ctas)[blockIdx.x] = make_int4(0, 0, 0, 0);
             if (!ok) give_up();
             // never leave the CTA with copies in flight
-            if (asked) mbar_wait_ns(&B.unit_asked, (items - 1) & 1, kWaitNs);
+            if (asked) mbar_wait_ns(&B.unit_asked, (asks - 1) & 1, kWaitNs);
 #pragma unroll 1
             for (int j = max(0, kq - kKS); j < kq; ++j) mbar_wait_ns(&B.k_full[j % kKS], (j / kKS) & 1, kWaitNs);
 #pragma unroll 1

@@ -436,3 +436,30 @@ def test_long_prompt_with_bad_values(dtype, out_dtype):
     out, t1 = timed()
     assert out[5:].isnan().all()
     assert t1 < 60 * t0 + 5, f"{t0} ms, {t1} ms with NaNs behind row 5"
+
+
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+@pytest.mark.parametrize("n", (2, 40))
+def test_prompt_graph_for_many_more_rows(dtype, n):
+    """A graph captured for 6000 rows, replayed with few, with none, and with all of them."""
+    hq, hkv, d, total = 6, 3, 64, 6000
+    q, k, v = packed(total, hq, hkv, d, dtype, n)
+    p = ops.prompt_params(num_seqs=n, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, dtype=dtype, out_dtype=dtype)
+    r, c = ops.make_rows(total, total), ref.cu([0] * n)
+    out, status = torch.zeros_like(q), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ops.prompt(p, r, q, k, v, c, out=out, dev_status=status)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ops.prompt(p, r, q, k, v, c, out=out, dev_status=status)
+    for lens in ([0] * (n - 1) + [70], [0] * n, [33] * n, [total - n + 1] + [1] * (n - 1), [1] * n):
+        c.copy_(ref.cu(lens))
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        m = sum(lens)
+        assert (out[m:] == 7.0).all()
+        if m:
+            want, tol = ref.prompt_ref(q[:m], k[:m], v[:m], lens, p.scale, dtype, dtype)
+            ref.assert_close(out[:m], want, tol, f"{lens[:2]}")
