@@ -15,8 +15,9 @@
 // loads) on long prompts; the dependent chain of loads on short calls.  fp32
 // stays off the tensor cores: one tf32 product keeps 11 bits.
 //
-// Prompt: one CTA per tile, latest rows (most keys) first.  Tree: one CTA per
+// Prompt: one CTA per tile (pa_prompt_plan.cuh), latest rows (most keys) first.  Tree: one CTA per
 // share of the keys (pa_tree_plan.cuh).
+#include "pa_prompt_plan.cuh"
 #include "pa_ptx.cuh"
 #include "pa_serving.h"
 #include "pa_tree_plan.cuh"
@@ -58,7 +59,7 @@ template <int D> struct Tile {
 };
 
 template <int D, bool kTree>
-__global__ void __launch_bounds__(kThr, 1) packed_f32(const PackedAttn a, const TreeShape shape, int n_tiles) {
+__global__ void __launch_bounds__(kThr, 1) packed_f32(const PackedAttn a, const TreeShape shape, const PromptShape prompt, int n_tiles) {
     using S = Tile<D>;
     constexpr int kLd = S::kLd, kPld = S::kPld;
     constexpr int kDv = D / 64;                // float4 columns of O a thread owns
@@ -88,6 +89,15 @@ __global__ void __launch_bounds__(kThr, 1) packed_f32(const PackedAttn a, const 
         const bool any = walk.next(shape, it);
         if (!any || !begins(it)) put_join(make_int4(0, 0, 0, 0));
         if (!any) return;
+    } else if (n_tiles == 0) {  // blockIdx.x is the unit's number; every warp finds it
+        PromptUnits units;
+        units.start(prompt);
+        if (blockIdx.x == 0)
+            for (int s = tid; s < a.r.num_seqs; s += kThr) {
+                const int r0 = a.r.cu_lens[s], r1 = a.r.cu_lens[s + 1];
+                if (r0 < 0 || r1 < r0 || r1 > a.r.total_rows || r1 - r0 > a.r.max_rows) flag(a.dev_status, PA_DEV_BAD_LEN);
+            }
+        if (!units.get(prompt, blockIdx.x, it)) return;
     } else {
         // blockIdx.x = (tile from the last) x (sequence, kv head)
         const int per = a.Hkv * a.r.num_seqs;
@@ -357,7 +367,15 @@ template <int D> cudaError_t launch(const PackedAttn& a, cudaStream_t st) {
     if (!a.tree_mask) {
         const int64_t tiles = (int64_t(a.r.max_rows) + tq - 1) / tq, ctas = tiles * a.Hkv * a.r.num_seqs;
         if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-        return launch_pdl(packed_f32<D, false>, dim3(unsigned(ctas)), dim3(kThr), sm, st, a, s, int(tiles));
+        // A CTA for each tile of each (sequence, kv head), where few of them can be
+        // empty; else one for each unit's number, which each CTA takes some time to
+        // find, about that of an empty CTA for every 32 sequences (2000 rows and 31
+        // prompts of 10, 64/8 heads, 64000 tiles of which 2500 hold rows: 2039 us
+        // without numbers, 1864 with).
+        const PromptShape numbered = prompt_shape(a, tq, kKB);
+        const bool direct = ctas <= prompt_numbers(numbered) * (2 + a.r.num_seqs / 32);
+        return launch_pdl(packed_f32<D, false>, dim3(unsigned(direct ? ctas : prompt_numbers(numbered))), dim3(kThr), sm, st,
+                          a, s, numbered, direct ? int(tiles) : 0);
     }
     s.cu_lens = a.r.cu_lens;
     s.context_lens = a.c.context_lens;
@@ -372,7 +390,7 @@ template <int D> cudaError_t launch(const PackedAttn& a, cudaStream_t st) {
     s.min_share = 1;
     s.n_ctas = a.n_ctas;
     s.cap = a.max_history;
-    cudaError_t e = launch_pdl(packed_f32<D, true>, dim3(a.n_ctas), dim3(kThr), sm, st, a, s, 0);
+    cudaError_t e = launch_pdl(packed_f32<D, true>, dim3(a.n_ctas), dim3(kThr), sm, st, a, s, PromptShape{}, 0);
     if (e != cudaSuccess) return e;
     return launch_join<float, D>(s, a, kM, st);
 }

@@ -44,6 +44,7 @@
 // zeroed in shared memory, and NaNs and infinities of the others too; rows
 // that do see such a value get it back in the epilogue (a rare path that
 // reads V again, and that also undoes infinity x 0 where a part of P is 0).
+#include "pa_prompt_plan.cuh"
 #include "pa_ptx.cuh"
 #include "pa_serving.h"
 #include "pa_tc.cuh"
@@ -115,8 +116,8 @@ template <int D> __device__ inline uint32_t col_o(int x) { return 256u + uint32_
 struct TcArgs {
     PackedAttn a;
     TreeShape shape;
+    PromptShape prompt;
     int32_t tq, G, head_first;
-    int32_t tu, n_units;  // prompt: rows of a unit; units of the longest sequence per kv head
 };
 
 // Waits for a phase: one suspended try, then others of up to kSleepNs each, a
@@ -294,94 +295,12 @@ template <bool kTree> __device__ inline Sides sides_of(const TreeItem& t, int tq
     return s;
 }
 
-// A prompt's units, numbered.  Up to 32 sequences: in descending order of key
-// tiles, by level (the tile of rows, from the last), then sequence, then kv head.
-// More: by sequence, then level from the last, then kv head, as finding a level
-// would mean counting all sequences again for each unit.  The grid has a CTA for
-// each number there can be; an SM holds one, and a CTA that is done asks the
-// hardware to cancel the launch of a waiting one and takes its number, so that
-// the longest units come first and none waits for a CTA that drew longer ones
-// (numbers dealt out in turn instead: the ragged batch's CTAs ended between 95
-// and 180 us).
-struct PromptUnits {
-    int base, first;  // the window of 32 sequences at hand; units of those before it
-    int lane_n;       // units of sequence base + lane
-    __device__ inline void load(const TcArgs& p, int b) {
-        const PackedAttn& a = p.a;
-        const int s = b + int(threadIdx.x & 31);
-        base = b;
-        lane_n = 0;
-        if (s < a.r.num_seqs) {
-            const int r0 = a.r.cu_lens[s], r1 = a.r.cu_lens[s + 1];
-            if (r0 >= 0 && r1 >= r0 && r1 <= a.r.total_rows && r1 - r0 <= a.r.max_rows)
-                lane_n = (r1 - r0 + p.tu - 1) / p.tu;
-        }
-    }
-    __device__ inline void start(const TcArgs& p) {
-        first = 0;
-        load(p, 0);
-    }
-    static __device__ inline int warp_add(int n) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-        return n;
-    }
-    // Unit number i; false where there are not so many.
-    __device__ inline bool get(const TcArgs& p, int i, TreeItem& it) {
-        const PackedAttn& a = p.a;
-        const int k = i / a.Hkv;
-        int level;
-        if (a.r.num_seqs <= 32) {
-            if (k >= warp_add(lane_n)) return false;
-            int lo = 0, hi = p.n_units - 1;  // the highest level with more than k units at and above it
-#pragma unroll 1
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (warp_add(max(0, lane_n - mid)) > k)
-                    lo = mid;
-                else
-                    hi = mid - 1;
-            }
-            level = lo;
-            int rank = k - warp_add(max(0, lane_n - lo - 1));  // among the sequences that reach this level
-            unsigned m = __ballot_sync(0xffffffffu, lane_n > lo);
-#pragma unroll 1
-            for (; rank > 0; --rank) m &= m - 1;
-            it.seq = __ffs(m) - 1;
-        } else {
-            if (k < first) start(p);  // numbers mostly rise
-            int all;
-#pragma unroll 1
-            while (k >= first + (all = warp_add(lane_n))) {
-                if (base + 32 >= a.r.num_seqs) return false;
-                first += all;
-                load(p, base + 32);
-            }
-            int upto = lane_n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, upto, o);
-                if (int(threadIdx.x & 31) >= o) upto += y;
-            }
-            const int l = __ffs(__ballot_sync(0xffffffffu, first + upto > k)) - 1;
-            it.seq = base + l;
-            level = first + __shfl_sync(0xffffffffu, upto, l) - 1 - k;  // the sequence's last unit first
-        }
-        const int r0 = a.r.cu_lens[it.seq];
-        it.g = i - k * a.Hkv;
-        it.T = a.r.cu_lens[it.seq + 1] - r0;
-        it.t0 = level * p.tu;
-        it.n_rows = min(p.tu, it.T - it.t0);
-        it.row0 = r0 + it.t0;
-        it.L = it.nh = it.b0 = 0;
-        it.b1 = (it.t0 + it.n_rows + kBN - 1) / kBN;
-        it.slot = -1;
-        it.last = 0;
-        it.bad_len = false;
-        return true;
-    }
-};
-
+// A prompt's grid has a CTA for each unit's number there can be; an SM holds one,
+// and a CTA that is done asks the hardware to cancel the launch of a waiting one
+// and takes its number, so that the longest units come first and none waits for
+// a CTA that drew longer ones (numbers dealt out in turn instead: the ragged
+// batch's CTAs ended between 95 and 180 us).
+//
 // Asks for the numbers of n CTAs that have not been launched; the answers (16
 // bytes each) arrive on `bar`.  Not to be asked again after a refusal.
 __device__ inline void ask_units(uint4* answer, int n, uint64_t* bar) {
@@ -520,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (r0 < 0 || r1 < r0 || r1 > a.r.total_rows || r1 - r0 > a.r.max_rows)
                         flag(a.dev_status, PA_DEV_BAD_LEN);
                 }
-            units.start(p);
+            units.start(p.prompt);
         }
         const int P = a.c.page_size;
         const int xc_first = p.head_first;
@@ -551,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (m) {
                         const int l = __ffs(m) - 1, i = __shfl_sync(0xffffffffu, number, l);
                         if (lane == l) number = -1;
-                        it.valid = units.get(p, i, it.t);
+                        it.valid = units.get(p.prompt, i, it.t);
                         if (it.valid) break;
                     } else if (refused) {
                         break;
@@ -1282,10 +1201,8 @@ cudaError_t launch_typed(const PackedAttn& a, cudaStream_t st) {
         // as long units: for calls that would leave half of the SMs idle.
         const int64_t per = int64_t(a.Hkv) * a.r.num_seqs;
         const int pairs = (a.r.max_rows + 2 * p.tq - 1) / (2 * p.tq);
-        p.tu = per * pairs <= a.n_ctas / 2 ? p.tq : 2 * p.tq;
-        p.n_units = (a.r.max_rows + p.tu - 1) / p.tu;
-        // one for each unit there can be: a sequence's last may be partly filled
-        ctas = std::min(per * p.n_units, int64_t(a.Hkv) * (a.r.total_rows / p.tu + a.r.num_seqs));
+        p.prompt = prompt_shape(a, per * pairs <= a.n_ctas / 2 ? p.tq : 2 * p.tq, kBN);
+        ctas = prompt_numbers(p.prompt);
     }
     cudaError_t e = launch_pdl(kern, dim3(unsigned(ctas)), dim3(kThreads), Smem<D>::kBytes, st, mq, mk, mv, mkc, mvc, p);
     if (e != cudaSuccess || !kTree) return e;
