@@ -1197,11 +1197,20 @@ cudaError_t launch_typed(const PackedAttn& a, cudaStream_t st) {
         s.cap = a.max_history;
         ctas = a.n_ctas;
     } else {
-        // Two row tiles share their K/V tiles; one alone makes twice as many, half
-        // as long units: for calls that would leave half of the SMs idle.
-        const int64_t per = int64_t(a.Hkv) * a.r.num_seqs;
-        const int pairs = (a.r.max_rows + 2 * p.tq - 1) / (2 * p.tq);
-        p.prompt = prompt_shape(a, per * pairs <= a.n_ctas / 2 ? p.tq : 2 * p.tq, kBN);
+        // Two row tiles share their K/V tiles; one alone makes twice as many units,
+        // half as long.  The longest unit bounds a call with few, the work one with
+        // many: which form ends first is reckoned from the rows (us: a key tile of
+        // one or two row tiles, a unit's start and end, a third of a unit for CTAs
+        // that end apart; causal units see half of the longest one's tiles on
+        // average).  Measured, one against two, 16/2 heads of 128: 2500 rows 31.7,
+        // 38.5; 4000 rows 61.9, 57.1; 8/8 heads of 64: 4000 rows 32.8, 56.8.
+        const float tiles = float((int64_t(a.r.max_rows) + kBN - 1) / kBN);
+        auto ends = [&](int tu, float tile) {
+            const float units = float(a.Hkv) * float((int64_t(a.r.total_rows) + tu - 1) / tu);
+            const float mean = tile * (tiles + 1.f) * 0.5f + 4.f;
+            return std::max(tile * tiles + 4.f, units * mean / float(a.n_ctas) + mean / 3.f);
+        };
+        p.prompt = prompt_shape(a, ends(p.tq, 0.9f) < ends(2 * p.tq, 1.75f) ? p.tq : 2 * p.tq, kBN);
         ctas = prompt_numbers(p.prompt);
     }
     cudaError_t e = launch_pdl(kern, dim3(unsigned(ctas)), dim3(kThreads), Smem<D>::kBytes, st, mq, mk, mv, mkc, mvc, p);

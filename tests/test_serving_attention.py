@@ -463,3 +463,11 @@ def test_prompt_graph_for_many_more_rows(dtype, n):
         if m:
             want, tol = ref.prompt_ref(q[:m], k[:m], v[:m], lens, p.scale, dtype, dtype)
             ref.assert_close(out[:m], want, tol, f"{lens[:2]}")
+
+
+@pytest.mark.parametrize("dtype,out_dtype", TYPES)
+@pytest.mark.parametrize("d", (64, 128))
+@pytest.mark.parametrize("hq,hkv", [(16, 8), (32, 8)])
+def test_prompt_few_and_many_units(dtype, out_dtype, d, hq, hkv):
+    """Of the 16-bit kernel: units of one tile of rows, and of two."""
+    run_prompt([1100, 5, 700], dtype, out_dtype, hq, hkv, d, pad=1)
