@@ -94,6 +94,7 @@ struct Bars {
     uint64_t unit_asked;      // prompt: the units' numbers asked for have arrived
     alignas(16) uint4 unit[kAsk];
     uint64_t side_b, side_w;  // twin: `side` holds B's figures; the weights
+    uint64_t twin_read;       // twin: side B has read A's O
     uint64_t mma_done, never;
     uint32_t tmem, abort;
     uint32_t poison[kIS];  // n + 1: item n met a NaN or infinity in a V that not every row sees
@@ -378,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&B.unit_asked, 1);
         mbar_init(&B.side_b, 4);
         mbar_init(&B.side_w, 4);
+        mbar_init(&B.twin_read, 4);
         mbar_init(&B.mma_done, 1);
         mbar_init(&B.never, 1);
         B.abort = 0;
@@ -623,10 +625,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto have_v = [&](int t) { return wait_all(&B.v_clean[t % kVS], (t / kVS) & 1); };
         int kt = 0;          // K and V tiles of the items before
         int sc[2] = {0, 0};  // score tiles of x issued; P_x V number sc - 1 waits for its P
+        int twins = 0;       // twins before this item
+        bool behind_twin = false;
         // P V of side x with tile t.  Behind it, where this warp would wait anyway,
         // stand the commits and the next tiles' waits.
         auto take_p = [&](int x, int t, bool first) {
             if (!wait_all(&B.p_full[x], (sc[x] - 1) & 1)) return false;
+            // Side B of a twin reads A's O too, which A's P of the next item does not
+            // wait for.  (A has read B's O by then: its P comes first in every item.)
+            if (x == 0 && first && behind_twin && !wait_all(&B.twin_read, (twins - 1) & 1)) return false;
             tc::fence_after_sync();
             pv(x, t, first);
             return true;
@@ -702,6 +709,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!valid) return true;
                 if (!wait_all(&B.q_full, n & 1) || !have_k(kt)) return false;
                 if (!(sd.twin ? run_twin(sd.nt) : run_pair(sd))) return false;
+                behind_twin = sd.twin;
+                twins += sd.twin;
                 kt += sd.nt;
             }
         };
@@ -1095,6 +1104,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         store_rows4(y, lane, [&](int i) { return row_at(i, mine); });
                     }
+                }
+                if (sd.twin && x == 1) {
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&B.twin_read);
                 }
             }
             __syncwarp();
