@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(kScanThr) pages_resize(const PagesCall c, cons
     const int L = c.context_lens[s], N = new_lens[s], P = c.page_size;
     const int64_t cap = int64_t(c.max_blocks) * P;
     int32_t* pair = pairs + 2 * int64_t(s);
+    __syncthreads();  // every thread has read L, which the first one writes
     if (L < 0 || L > cap || N > cap || N < 0) {
         if (tid < 2) pair[tid] = -1;
         return;
