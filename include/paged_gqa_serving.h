@@ -154,8 +154,9 @@ size_t pa_pages_workspace_size(const pa_params *p);
  *  - a sequence whose pages do not suffice, counting those that the
  *    sequences before it asked for, is left as it was (PA_DEV_NO_PAGES);
  *    one whose old or new length is out of range too (PA_DEV_BAD_LEN).
- * A released table entry outside the pool, or of a page with refcount 0, is
- * passed over (PA_DEV_BAD_PAGE).  pairs: [num_seqs][2]. */
+ * A released table entry outside the pool, of a page that was free when the
+ * call began or of one whose refcount falls to 0 before it, is passed over
+ * (PA_DEV_BAD_PAGE).  pairs: [num_seqs][2]. */
 pa_status pa_pages_resize(const pa_params *p, int32_t *refcounts, int32_t *block_tables,
                           int32_t *context_lens, const int32_t *new_lens, int32_t *pairs,
                           void *workspace, size_t workspace_bytes, uint32_t *dev_status,

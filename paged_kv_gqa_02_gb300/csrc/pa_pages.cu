@@ -23,13 +23,15 @@ constexpr int kWarps = kScanThr / 32;
 
 // Workspace: inclusive needs of each sequence within its block of 256 and
 // block totals (64 bits: absurd lengths must not wrap), then in 32 bits chunk
-// counts, chunk lists (free pages) and the page map of compact.
+// counts, chunk lists (free pages), and the page map of compact or, of resize,
+// a bit for each page that was free when the call began.
 struct PagesWs {
     int64_t* need;
     int64_t* block_need;
     int32_t* count;
     int32_t* list;
     int32_t* map;
+    uint32_t* was_free;  // in the map's place
 };
 __host__ __device__ inline int n_chunks(int pages) { return (pages + kChunk - 1) / kChunk; }
 __host__ __device__ inline int n_blocks(int seqs) { return (seqs + kScanThr - 1) / kScanThr; }
@@ -40,6 +42,7 @@ __host__ __device__ inline PagesWs ws_of(void* ws, int seqs, int pages) {
     w.count = reinterpret_cast<int32_t*>(w.block_need + n_blocks(seqs));
     w.list = w.count + n_chunks(pages);
     w.map = w.list + int64_t(n_chunks(pages)) * kChunk;
+    w.was_free = reinterpret_cast<uint32_t*>(w.map);
     return w;
 }
 
@@ -122,6 +125,7 @@ __global__ void __launch_bounds__(kScanThr) pages_scan(const PagesCall c, const 
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             if (free_[i]) list[at + __popc(m[i] & ((1u << lane) - 1u))] = base + 32 * i + lane;
+            if (new_lens && lane == 0 && base + 32 * i < c.num_pages) w.was_free[base / 32 + i] = m[i];
             at += __popc(m[i]);
         }
         if (tid == 0) w.count[blockIdx.x] = all;
@@ -170,9 +174,10 @@ __device__ inline int free_page(const PagesWs& w, const int* pre, int n, int k) 
     return w.list[int64_t(lo) * kChunk + (k - pre[lo])];
 }
 
-// Gives back one hold on a table entry.
-__device__ inline void release(const PagesCall& c, int pg) {
-    if (pg < 0 || pg >= c.num_pages) {
+// Gives back one hold on a table entry.  A page that was free when the call
+// began may be another sequence's by now: no hold on it is given back.
+__device__ inline void release(const PagesCall& c, const PagesWs& w, int pg) {
+    if (pg < 0 || pg >= c.num_pages || ((w.was_free[pg >> 5] >> (pg & 31)) & 1u)) {
         flag(c.dev_status, PA_DEV_BAD_PAGE);
     } else if (atomicSub(c.refcounts + pg, 1) <= 0) {
         atomicAdd(c.refcounts + pg, 1);
@@ -225,7 +230,7 @@ __global__ void __launch_bounds__(kScanThr) pages_resize(const PagesCall c, cons
             to = free_page(w, pre, nc, first);
             row[b] = to;
             atomicAdd(c.refcounts + to, 1);
-            atomicSub(c.refcounts + from, 1);
+            release(c, w, from);  // shared by more entries than it counts: flagged
         }
         pair[0] = from;
         pair[1] = to;
@@ -237,7 +242,7 @@ __global__ void __launch_bounds__(kScanThr) pages_resize(const PagesCall c, cons
         atomicAdd(c.refcounts + pg, 1);
     }
     for (int b = has + tid; b < had; b += kScanThr) {
-        release(c, row[b]);
+        release(c, w, row[b]);
         row[b] = -1;
     }
 }

@@ -58,3 +58,28 @@ def test_long_sequences_freed_and_shrunk_release_every_page():
             assert b.ref.tolist() == m.ref and b.lens.tolist() == m.lens and b.pairs.tolist() == want
             assert b.tables.tolist() == m.tables
         assert int(b.ref.abs().sum()) == 0 and (b.tables == -1).all()
+
+
+@pytest.mark.parametrize("last", (1, 5999))
+def test_an_entry_that_names_a_free_page_takes_no_hold_from_its_new_owner(last):
+    """Sequence 0 is handed page 0 while the last one gives back an entry that names it without a hold:
+    whichever comes first, the page is sequence 0's and the entry is flagged."""
+    b = Books(last + 1, 40, 3)
+    b.tables[last, 0], b.tables[last, 1] = 0, 7
+    b.lens[last], b.ref[7] = 32, 1
+    for _ in range(3):
+        tables, lens, counts = b.tables.clone(), b.lens.clone(), b.ref.clone()
+        assert b.resize([20] + [-1] * (last - 1) + [0]) == ops.PA_DEV_BAD_PAGE
+        assert b.ref.tolist() == [1, 1] + [0] * 38
+        assert b.tables[0].tolist() == [0, 1, -1] and (b.tables[last] == -1).all()
+        b.tables.copy_(tables), b.lens.copy_(lens), b.ref.copy_(counts)
+
+
+def test_more_sharers_than_a_page_counts_leave_no_negative_count():
+    """Three entries name a page of refcount 2: each sequence that grows gets its own page, the third hold is flagged."""
+    b = Books(3, 10, 2)
+    b.tables[:, 0], b.lens[:] = 4, 5
+    b.ref[4] = 2
+    assert b.resize([6, 7, 8]) == ops.PA_DEV_BAD_PAGE
+    assert b.ref.tolist() == [1, 1, 1] + [0] * 7
+    assert b.pairs.tolist() == [[4, 0], [4, 1], [4, 2]] and b.tables[:, 0].tolist() == [0, 1, 2]
