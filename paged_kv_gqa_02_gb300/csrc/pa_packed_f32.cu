@@ -17,6 +17,7 @@
 //
 // Prompt: one CTA per tile (pa_prompt_plan.cuh), latest rows (most keys) first.  Tree: one CTA per
 // share of the keys (pa_tree_plan.cuh).
+#include "pa_device.h"
 #include "pa_prompt_plan.cuh"
 #include "pa_ptx.cuh"
 #include "pa_serving.h"
@@ -355,14 +356,10 @@ __global__ void __launch_bounds__(kThr, 1) packed_f32(const PackedAttn a, const 
 template <int D> cudaError_t launch(const PackedAttn& a, cudaStream_t st) {
     const size_t sm = Tile<D>::kBytes;
     const int G = a.Hq / a.Hkv, tq = kM / G;
-    static bool configured = false;  // benign race: every caller sets the same value
-    if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(packed_f32<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sm));
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(packed_f32<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sm));
-        if (e != cudaSuccess) return e;
-        configured = true;
-    }
+    static std::atomic<uint64_t> allowed[2] = {};
+    cudaError_t e = a.tree_mask ? allow_shared_memory(reinterpret_cast<const void*>(packed_f32<D, true>), sm, allowed[1])
+                                : allow_shared_memory(reinterpret_cast<const void*>(packed_f32<D, false>), sm, allowed[0]);
+    if (e != cudaSuccess) return e;
     TreeShape s = {};
     if (!a.tree_mask) {
         const int64_t tiles = (int64_t(a.r.max_rows) + tq - 1) / tq, ctas = tiles * a.Hkv * a.r.num_seqs;
@@ -390,7 +387,7 @@ template <int D> cudaError_t launch(const PackedAttn& a, cudaStream_t st) {
     s.min_share = 1;
     s.n_ctas = a.n_ctas;
     s.cap = a.max_history;
-    cudaError_t e = launch_pdl(packed_f32<D, true>, dim3(a.n_ctas), dim3(kThr), sm, st, a, s, PromptShape{}, 0);
+    e = launch_pdl(packed_f32<D, true>, dim3(a.n_ctas), dim3(kThr), sm, st, a, s, PromptShape{}, 0);
     if (e != cudaSuccess) return e;
     return launch_join<float, D>(s, a, kM, st);
 }

@@ -44,6 +44,7 @@
 // zeroed in shared memory, and NaNs and infinities of the others too; rows
 // that do see such a value get it back in the epilogue (a rare path that
 // reads V again, and that also undoes infinity x 0 where a part of P is 0).
+#include "pa_device.h"
 #include "pa_prompt_plan.cuh"
 #include "pa_ptx.cuh"
 #include "pa_serving.h"
@@ -53,6 +54,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 namespace pa {
@@ -1126,14 +1128,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};  // the driver's, the same for every thread
+    PFN_cuTensorMapEncodeTiled_v12000 fn = known.load(std::memory_order_relaxed);
     if (!fn) {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult q;
         if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
                 cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
+            q == cudaDriverEntryPointSuccess) {
             fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+            known.store(fn, std::memory_order_relaxed);
+        }
     }
     return fn;
 }
@@ -1172,13 +1177,9 @@ bool encode_pages(CUtensorMap* m, const PackedAttn& a, const void* ptr, bool hea
 template <typename T, int D, bool kTree, typename TOut>
 cudaError_t launch_typed(const PackedAttn& a, cudaStream_t st) {
     auto kern = packed_tc<T, D, kTree, TOut>;
-    static bool configured = false;  // benign race: every caller sets the same value
-    if (!configured) {
-        cudaError_t e =
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Smem<D>::kBytes));
-        if (e != cudaSuccess) return e;
-        configured = true;
-    }
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kern), Smem<D>::kBytes, allowed);
+    if (e != cudaSuccess) return e;
     TcArgs p = {};
     p.a = a;
     p.G = a.Hq / a.Hkv;
@@ -1227,7 +1228,7 @@ cudaError_t launch_typed(const PackedAttn& a, cudaStream_t st) {
         p.prompt = prompt_shape(a, ends(p.tq, 0.9f) < ends(2 * p.tq, 1.75f) ? p.tq : 2 * p.tq, kBN);
         ctas = prompt_numbers(p.prompt);
     }
-    cudaError_t e = launch_pdl(kern, dim3(unsigned(ctas)), dim3(kThreads), Smem<D>::kBytes, st, mq, mk, mv, mkc, mvc, p);
+    e = launch_pdl(kern, dim3(unsigned(ctas)), dim3(kThreads), Smem<D>::kBytes, st, mq, mk, mv, mkc, mvc, p);
     if (e != cudaSuccess || !kTree) return e;
     return launch_join<TOut, D>(p.shape, a, 2 * kBM, st);
 }
