@@ -32,7 +32,7 @@
 //
 // Softmax: a row's 128 scores are read from tensor memory into registers in one
 // go; online, in base 2, with a running max that is raised, and O rescaled,
-// only when it grows by more than 2^8.
+// only when it grows by more than 2^8 (fp16: 2^4, below).
 //
 // Large scores: a weight is 2^(s * scale_log2 - max) in one fused step, whose
 // product is not rounded while the max's was.  All weights of a row share the
@@ -90,7 +90,6 @@ constexpr int kWaitSlices = int(kWaitNs / kSleepNs);
 // What a tree's unit costs apart from its key tiles, in key tiles of a twin
 // (0.9 us each; 1.75 us with two row tiles): start, joins and epilogue, 4.5 us
 constexpr int kUnitStart = 5;
-constexpr float kRescaleStep = 8.f;
 constexpr uint32_t kNegInf = 0xff800000u;
 
 struct Item {
@@ -216,6 +215,7 @@ template <> struct H2<__nv_bfloat16> {
     }
     static constexpr uint32_t kExp = 0x7f80u;
     static constexpr float kWide = 268435456.f;  // 2^28: below it half a step is 8 of exponent at most
+    static constexpr float kShift = 0.f, kStep = 8.f;
 };
 template <> struct H2<__half> {
     __device__ static inline uint32_t pack(float a, float b) {
@@ -233,7 +233,14 @@ template <> struct H2<__half> {
         return *reinterpret_cast<const uint32_t*>(&y);
     }
     static constexpr uint32_t kExp = 0x7c00u;
-    static constexpr float kWide = 33554432.f;  // 2^25: below it half a step is 1 of exponent at most
+    static constexpr float kWide = 16777216.f;  // 2^24: below it half a step is 1/2 of exponent at most
+    // Weights below 2^-25, half of the least subnormal, are 0 in P but not in the
+    // sum: were the max's weight 1, a history of 2^20 tokens just below would lose
+    // 3% of a row.  It is 2^10 here and grows to 2^14 before the max is raised (2^15.5
+    // with what rounding adds, of 65504): what a key loses is 2^-35 of the max's
+    // weight at most.  (2^12, raised from 2^14 on, raised it too often: 34.2 us a
+    // prompt of 1641 rows instead of 32.7.)
+    static constexpr float kShift = 10.f, kStep = 4.f;
 };
 template <typename T> __device__ inline bool bad16(uint32_t h) { return (h & H2<T>::kExp) == H2<T>::kExp; }
 
@@ -881,8 +888,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) mx[c] = max32(r[c]);
                     const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-                    const float mt = top * (fabsf(top * sl2) < H2<T>::kWide ? sl2 : sl2_wide);
-                    const bool need = mt - m_run > kRescaleStep;  // false for two infinities of a sign
+                    const float low = top * sl2 - H2<T>::kShift;
+                    const float mt = fabsf(low) < H2<T>::kWide ? low : top * sl2_wide;
+                    const bool need = mt - m_run > H2<T>::kStep;  // false for two infinities of a sign
                     // raise the max and rescale O in place: the last P V has
                     // finished (these scores were issued after it)
                     const float alpha = need ? ex2(m_run - mt) : 1.f;
