@@ -74,12 +74,15 @@ pa_rows *pa_rows_init(pa_rows *r);
  * out [total_rows][Hq][D] contiguous in out_dtype: PA_F32, or the dtype of q.
  * Uses of p: num_seqs, num_q_heads, num_kv_heads (ratio at most 16),
  * head_dim 64 or 128, scale (> 0), q_dtype == kv_dtype, out_dtype,
- * debug_timeout; its page fields are ignored.  num_seqs <= 65535.
+ * deterministic, debug_timeout; its page fields are ignored.  num_seqs <= 65535.
  * Scores, softmax statistics and accumulators are fp32.  With 16-bit inputs
  * the probabilities enter P.V in 16 bits when out is 16 bits wide, and as a
  * sum of two 16-bit parts when out is PA_F32.
  * A NaN or infinity in k or v reaches only the rows that attend it (and all
  * of them, a weight that underflows to zero aside).
+ * A row's bits depend on its own sequence and, with 16-bit inputs, on
+ * total_rows and max_rows: they choose how rows are grouped, for the device's
+ * number of SMs or, with deterministic = 1, for 152.
  * q, k, v, out 16-byte aligned; strides multiples of 16 bytes. */
 pa_status pa_prompt(const pa_params *p, const pa_rows *r, const void *q, const void *k,
                     const void *v, const int32_t *cu_lens, void *out, uint32_t *dev_status,

@@ -10,7 +10,7 @@
 
 namespace {
 
-constexpr int kRefSms = 152;         // shares of a deterministic tree call
+constexpr int kRefSms = 152;         // SMs that a deterministic call is laid out for
 constexpr int kMaxTreeRows = 1024;   // drafts of one sequence
 constexpr int kMaxRows = 1 << 30;    // packed rows: sums with a tile stay in 32 bits
 constexpr int64_t kMaxHistory = 1 << 30;  // tokens before a tree, for the same reason
@@ -178,7 +178,7 @@ PA_EXPORT pa_status pa_prompt(const pa_params* p, const pa_rows* r, const void* 
     a.v = v;
     a.out = out;
     a.dev_status = dev_status;
-    a.n_ctas = device_sms();
+    a.n_ctas = share_ctas(p);
     return launch_packed(a, stream);
 }
 
