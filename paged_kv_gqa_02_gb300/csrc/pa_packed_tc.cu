@@ -90,7 +90,7 @@ constexpr int kWaitSlices = int(kWaitNs / kSleepNs);
 // What a tree's unit costs apart from its key tiles, in key tiles of a twin
 // (0.9 us each; 1.75 us with two row tiles): start, joins and epilogue, 4.5 us
 constexpr int kUnitStart = 5;
-constexpr uint32_t kNegInf = 0xff800000u;
+constexpr uint32_t kNegInf = 0xff800000u, kPosInf = 0x7f800000u, kNan = 0x7fffffffu;
 
 struct Item {
     TreeItem t;
@@ -954,14 +954,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Puts right 32 dims of the rows that `mine` marks, which may see a NaN or
             // infinity in V: one that was kept out of P.V, or that met a zero part
             // of P there.  What a row sees of them is the result, whatever the rest
-            // adds up to.  The whole warp looks for them, a key a lane, as there are
-            // few or one alone makes all that a row sees NaN (20000 rows, 2/1 heads of
-            // 64, a NaN in one of them: 0.55 ms, 0.23 ms without it; when each row went
-            // through its keys by itself, 45 ms).
+            // adds up to.  The whole warp looks for them, a key a lane, and each row
+            // keeps a bit for each kind and dim (20000 rows, 2/1 heads of 64, a NaN in
+            // one of them: 0.45 ms, 0.21 ms without it, 45 ms when each row went
+            // through its keys by itself; infinities in all: 3.1 ms, 47 ms when the
+            // dims were added up one after another, at heads of 128 7.2 and 263).
             auto restore = [&](uint32_t (&r)[32], const TreeItem& it, int at, int place, int d0, bool mine) {
-                float f[32];  // rolled loops and local memory: rare, and small code
-#pragma unroll 1
-                for (int k = 0; k < 32; ++k) f[k] = 0.f;
+                uint32_t nan = 0u, pos = 0u, neg = 0u;  // what the row has seen: a bit a dim
                 const int n_hist = kTree ? max(0, min(it.L, min(it.b1, it.nh) * kBN) - it.b0 * kBN) : 0;
                 const int k_lo = max(0, it.b0 - it.nh) * kBN;
                 const int k_hi = kTree ? min(it.T, max(0, it.b1 - it.nh) * kBN) : it.t0 + it.n_rows;
@@ -1003,20 +1002,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (!__any_sync(0xffffffffu, sees)) continue;
                         const float y = Elt<T>::f(u[lane]);  // a dim a lane
-                        if (__all_sync(0xffffffffu, y != y) && sees) left = false;
-                        unsigned dims = __ballot_sync(0xffffffffu, !isfinite(y));
-#pragma unroll 1
-                        for (; dims; dims &= dims - 1) {
-                            const int k = __ffs(dims) - 1;
-                            const float z = __shfl_sync(0xffffffffu, y, k);
-                            if (sees) f[k] += z;
+                        const uint32_t yn = __ballot_sync(0xffffffffu, y != y);
+                        const uint32_t yp = __ballot_sync(0xffffffffu, y == INFINITY);
+                        const uint32_t ym = __ballot_sync(0xffffffffu, y == -INFINITY);
+                        if (sees) {
+                            pos |= yp;
+                            neg |= ym;
+                            nan |= yn | (pos & neg);
+                            left = nan != 0xffffffffu;
                         }
                     }
                 }
                 if (!mine) return;
 #pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    if (!isfinite(f[k])) r[k] = __float_as_uint(f[k]);
+                for (int k = 0; k < 32; ++k) {
+                    if ((pos >> k) & 1u) r[k] = kPosInf;
+                    if ((neg >> k) & 1u) r[k] = kNegInf;
+                    if ((nan >> k) & 1u) r[k] = kNan;
+                }
             };
 
             // ---- epilogue: O / l, or the piece's max, sum and O into its slot.  A

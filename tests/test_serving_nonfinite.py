@@ -101,3 +101,26 @@ def test_tree_keeps_the_other_dims(dtype, out_dtype, d, dims):
                 spot[dim] = value
                 check(go(), clean, sees, dim, value)
                 spot[dim] = kept
+
+
+@pytest.mark.parametrize("dtype,out_dtype", TYPES[1:])
+def test_infinities_everywhere(dtype, out_dtype):
+    """Every row sums what it sees: an infinity of its sign, or NaN where it sees both, in every dim."""
+    n, hq, hkv, d = 3000, 4, 2, 128
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    q, k, v = normal(gen, n, hq, d, dtype=dtype), normal(gen, n, hkv, d, dtype=dtype), normal(gen, n, hkv, d, dtype=dtype)
+    p = ops.prompt_params(num_seqs=1, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, dtype=dtype, out_dtype=out_dtype)
+    first = torch.randint(0, n, (hkv, d), generator=gen, device="cuda")   # from here on +inf
+    other = torch.randint(0, 4 * n, (hkv, d), generator=gen, device="cuda")  # here -inf
+    at = torch.arange(n, device="cuda")[:, None, None]
+    clean = ops.prompt(p, ops.make_rows(n, n), q, k, v, ref.cu([n]))
+    v = torch.where(at >= first, torch.full_like(v, float("inf")), v)
+    v = torch.where(at == other, torch.full_like(v, -float("inf")), v)
+    out = ops.prompt(p, ops.make_rows(n, n), q, k, v, ref.cu([n]))
+    up, down = ((v == x).cumsum(0) > 0 for x in (float("inf"), -float("inf")))
+    up, down = (x.repeat_interleave(hq // hkv, 1) for x in (up, down))
+    want = torch.where(up, torch.full_like(clean, float("inf")), clean)
+    want = torch.where(down, torch.full_like(clean, -float("inf")), want)
+    want = torch.where(up & down, torch.full_like(clean, float("nan")), want)
+    same = (out == want) | (out.isnan() & want.isnan())
+    assert same.all(), f"{int((~same).sum())} elements"
