@@ -348,6 +348,14 @@ def _ints(t, n, dev, what):
     return t.data_ptr()
 
 
+def _table(t, rows, width, dev, what):
+    """Pointer of an int32 table of ``rows`` rows or more, each ``width`` wide: flat, or with that last dimension."""
+    at, shape = _ints(t, rows * width, dev, what), t.shape
+    if len(shape) > 1 and shape[-1] != width:
+        raise ValueError(f"{what}: rows of {width} elements, not {shape[-1]}")
+    return at
+
+
 def _packed(t, code, rows, heads, dim, stride, dev, what):
     """Pointer of packed rows [rows or more][heads][dim], ``stride`` elements between rows."""
     shape = t.shape
@@ -449,8 +457,8 @@ def tree(p: Params, r: Rows, q, k, v, cu_lens, tree_mask, k_cache, v_cache, bloc
     _call("pa_tree", dev, stream, p, r,
           _packed(q, p.q_dtype, n, hq, d, r.q_stride, dev, "q"), _packed(k, p.kv_dtype, n, hkv, d, r.k_stride, dev, "k"),
           _packed(v, p.kv_dtype, n, hkv, d, r.v_stride, dev, "v"), _ints(cu_lens, b + 1, dev, "cu_lens"),
-          _ints(tree_mask, n * words, dev, "tree_mask"), _pool(k_cache, p, dev, "k_cache"),
-          _pool(v_cache, p, dev, "v_cache"), _ints(block_tables, b * p.max_blocks_per_seq, dev, "block_tables"),
+          _table(tree_mask, n, words, dev, "tree_mask"), _pool(k_cache, p, dev, "k_cache"),
+          _pool(v_cache, p, dev, "v_cache"), _table(block_tables, b, p.max_blocks_per_seq, dev, "block_tables"),
           _ints(context_lens, b, dev, "context_lens"), _packed(out, p.out_dtype, n, hq, d, 0, dev, "out"),
           *_scratch(workspace, dev), _status(dev_status, dev))
     return out
@@ -466,7 +474,7 @@ def store(p: Params, r: Rows, k, v, cu_lens, k_cache, v_cache, block_tables, con
           _packed(k, p.kv_dtype, src, hkv, d, r.k_stride, dev, "k"),
           _packed(v, p.kv_dtype, src, hkv, d, r.v_stride, dev, "v"), _ints(cu_lens, b + 1, dev, "cu_lens"),
           None if row_index is None else _ints(row_index, n, dev, "row_index"), _pool(k_cache, p, dev, "k_cache"),
-          _pool(v_cache, p, dev, "v_cache"), _ints(block_tables, b * p.max_blocks_per_seq, dev, "block_tables"),
+          _pool(v_cache, p, dev, "v_cache"), _table(block_tables, b, p.max_blocks_per_seq, dev, "block_tables"),
           _ints(context_lens, b, dev, "context_lens"), _status(dev_status, dev))
 
 
@@ -481,7 +489,7 @@ def _new_scratch(n, like, stream):
 
 def _bookkeeping(p, refcounts, block_tables, context_lens, dev):
     return (_ints(refcounts, p.num_pages, dev, "refcounts"),
-            _ints(block_tables, p.num_seqs * p.max_blocks_per_seq, dev, "block_tables"),
+            _table(block_tables, p.num_seqs, p.max_blocks_per_seq, dev, "block_tables"),
             _ints(context_lens, p.num_seqs, dev, "context_lens"))
 
 
@@ -494,7 +502,7 @@ def pages_resize(p: Params, refcounts, block_tables, context_lens, new_lens, pai
         workspace = _new_scratch(pages_workspace_size(p), refcounts, stream)
     _call("pa_pages_resize", dev, stream, p,
           *_bookkeeping(p, refcounts, block_tables, context_lens, dev), _ints(new_lens, p.num_seqs, dev, "new_lens"),
-          _ints(pairs, 2 * p.num_seqs, dev, "pairs"), *_scratch(workspace, dev), _status(dev_status, dev))
+          _table(pairs, p.num_seqs, 2, dev, "pairs"), *_scratch(workspace, dev), _status(dev_status, dev))
 
 
 def pages_fork(p: Params, refcounts, block_tables, context_lens, src, dst, dev_status=None, stream=None):
@@ -513,7 +521,7 @@ def pages_compact(p: Params, refcounts, block_tables, context_lens, pairs, num_m
     if workspace is None:
         workspace = _new_scratch(pages_workspace_size(p), refcounts, stream)
     _call("pa_pages_compact", dev, stream, p,
-          *_bookkeeping(p, refcounts, block_tables, context_lens, dev), _ints(pairs, 2 * n, dev, "pairs"), n,
+          *_bookkeeping(p, refcounts, block_tables, context_lens, dev), _table(pairs, n, 2, dev, "pairs"), n,
           _ints(num_moves, 1, dev, "num_moves"), *_scratch(workspace, dev), _status(dev_status, dev))
 
 
@@ -521,4 +529,4 @@ def pages_copy(p: Params, k_cache, v_cache, pairs, dev_status=None, stream=None)
     """Copies page pairs[i][0] to pairs[i][1] in one layer's K and V; negative pairs are passed over."""
     dev, n = k_cache.get_device(), pairs.numel() // 2
     _call("pa_pages_copy", dev, stream, p, _pool(k_cache, p, dev, "k_cache"),
-          _pool(v_cache, p, dev, "v_cache"), _ints(pairs, 2 * n, dev, "pairs"), n, _status(dev_status, dev))
+          _pool(v_cache, p, dev, "v_cache"), _table(pairs, n, 2, dev, "pairs"), n, _status(dev_status, dev))
