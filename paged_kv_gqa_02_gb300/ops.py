@@ -349,11 +349,13 @@ def _ints(t, n, dev, what):
 
 
 def _table(t, rows, width, dev, what):
-    """Pointer of an int32 table of ``rows`` rows or more, each ``width`` wide: flat, or with that last dimension."""
-    at, shape = _ints(t, rows * width, dev, what), t.shape
-    if len(shape) > 1 and shape[-1] != width:
-        raise ValueError(f"{what}: rows of {width} elements, not {shape[-1]}")
-    return at
+    """Pointer of a contiguous int32 table of ``rows`` rows or more, each ``width`` wide: flat, or with that last dimension."""
+    shape = t.shape
+    if (t.dtype is not (_I32 or _int32()) or t.get_device() != dev or not t.is_contiguous()
+            or (shape[0] < rows or shape[1] != width if len(shape) == 2
+                else t.numel() < rows * width or len(shape) > 1 and shape[-1] != width)):
+        raise ValueError(f"{what}: a contiguous int32 tensor of at least {rows} rows of {width} elements on cuda:{dev}")
+    return t.data_ptr()
 
 
 def _packed(t, code, rows, heads, dim, stride, dev, what):
@@ -402,8 +404,8 @@ def _call(name, dev, stream, *args):
     """The entry point with device number dev current, on the given stream or that device's current one."""
     if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
-    torch = sys.modules["torch"]  # the tensors came from it
-    if torch.cuda.current_device() != dev:
+    torch = sys.modules["torch"]  # the tensors came from it, and so CUDA is set up
+    if torch._C._cuda_getDevice() != dev:  # torch.cuda.current_device() asks whether it is
         with torch.cuda.device(dev):
             return _call(name, dev, stream, *args)
     # the current stream's handle as torch's own generated launchers get it: torch.cuda.current_stream()
