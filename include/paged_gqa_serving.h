@@ -49,8 +49,9 @@ extern "C" {
  * have no part in any result and are not written.  A sequence whose rows
  * leave [0, total_rows] or number more than max_rows or less than none is
  * skipped, its rows left as they were (PA_DEV_BAD_LEN).  Where ends descend
- * (flagged too), rows can belong to several sequences, and each row of the
- * call holds one of its sequences' results or is left as it was. */
+ * (flagged too), rows can belong to several sequences: each element of such a
+ * row is one of its sequences' results or left as it was, and which may
+ * depend on timing. */
 typedef struct {
     int32_t total_rows;  /* rows of the packed tensors, at most 2^30; 0: nothing
                             to do                                                */
@@ -76,8 +77,9 @@ pa_rows *pa_rows_init(pa_rows *r);
  * head_dim 64 or 128, scale (> 0), q_dtype == kv_dtype, out_dtype,
  * deterministic, debug_timeout; its page fields are ignored.  num_seqs <= 65535.
  * Scores, softmax statistics and accumulators are fp32.  With 16-bit inputs
- * the probabilities enter P.V in 16 bits when out is 16 bits wide, and as a
- * sum of two 16-bit parts when out is PA_F32.
+ * the probabilities enter P.V in 16 bits when out is 16 bits wide, each off by
+ * half a step at most, and as a sum of two 16-bit parts when out is PA_F32: a
+ * caller who wants 16-bit results to the last step takes PA_F32 and rounds.
  * A NaN or infinity in k or v reaches only the rows that attend it (and all
  * of them, a weight that underflows to zero aside).
  * A row's bits depend on its own sequence and, with 16-bit inputs, on
@@ -153,7 +155,9 @@ size_t pa_pages_workspace_size(const pa_params *p);
  *    the page is shared (refcount > 1 when the call began), is replaced by
  *    a fresh one, taken before the sequence's other pages, and
  *    pairs[s] = (shared, fresh); otherwise pairs[s] = (-1, -1).  Run
- *    pa_pages_copy on pairs in every layer before the next write;
+ *    pa_pages_copy on pairs in every layer before the next write.  Each
+ *    sharer that the call resizes gets a page of its own, so one that they
+ *    all leave is free afterwards;
  *  - a sequence whose pages do not suffice, counting those that the
  *    sequences before it asked for, is left as it was (PA_DEV_NO_PAGES);
  *    one whose old or new length is out of range too (PA_DEV_BAD_LEN).
