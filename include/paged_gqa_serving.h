@@ -12,10 +12,17 @@
  *   pa_pages_fork     let sequences share another's pages
  *   pa_pages_compact  move the live pages to the low end of the pool
  *   pa_pages_copy     copy pages of one layer's K and V
+ *   pa_rotate         norms and rotation of queries and keys, and their store
+ *   pa_verify         which drafts the target's distribution accepts
+ *   pa_key_weights    the attention weight that each cached key has gathered
+ *   pa_evict          drop the keys that gathered least
  *
- * A step of a serving loop: pa_pages_resize reserves room; pa_prompt and
- * pa_store take a prompt in (pa_store once per layer); then, per token or
- * per drafted tree, pa_decode / pa_tree, and pa_store of what was accepted.
+ * A step of a serving loop: pa_pages_resize reserves room; pa_rotate,
+ * pa_prompt and pa_store take a prompt in (once per layer; pa_rotate can
+ * store the rows itself); then, per token or per drafted tree, pa_decode /
+ * pa_tree, pa_verify, and pa_store of what was accepted.  A cache with a
+ * budget calls pa_key_weights after the store and, when it is full, pa_evict
+ * per layer and pa_pages_resize once.
  * pa_pages_resize and pa_pages_compact change only the bookkeeping, once
  * per step; the (source, destination) pairs that they report go to
  * pa_pages_copy once per layer, before anything else touches the pages.
@@ -41,7 +48,9 @@ extern "C" {
 
 /* Bits OR-ed into *dev_status, beside PA_DEV_BAD_PAGE and the others. */
 #define PA_DEV_NO_PAGES 16u  /* pa_pages_resize: not enough free pages for a sequence */
-#define PA_DEV_BAD_INDEX 32u /* a row index, sequence index or page of a pair out of range */
+#define PA_DEV_BAD_INDEX 32u /* a row index, sequence index, position, token, parent or page of a pair out of range */
+#define PA_DEV_BAD_VALUE 64u /* pa_verify: a row of logits without a finite largest value, or random numbers that choose nothing */
+#define PA_DEV_SHARED_PAGE 128u /* pa_evict: a page to be written has another holder */
 
 /* Packed rows: sequence s owns rows cu_lens[s] .. cu_lens[s+1]-1 of q, k, v
  * and out; cu_lens is [num_seqs + 1] int32 on the device, ascending from a
@@ -200,6 +209,150 @@ pa_status pa_pages_compact(const pa_params *p, int32_t *refcounts, int32_t *bloc
  * resize and compact never have one that does). */
 pa_status pa_pages_copy(const pa_params *p, void *k_cache, void *v_cache, const int32_t *pairs,
                         int32_t n, uint32_t *dev_status, pa_stream_t stream);
+
+/* ------------------------------------------------------------------ rotate
+ * How pa_rotate turns the heads. */
+typedef struct {
+    int32_t rotary_dim;  /* leading dims of a head that turn, a multiple of 16, at
+                            most D; 0: none (norms and store alone)               */
+    int32_t interleaved; /* 0: dim i turns with i + rotary_dim / 2; 1: 2i with 2i + 1 */
+    int32_t axes;        /* rows of positions, 1 to 3; 0 means 1                  */
+    int32_t sections[3]; /* axes > 1: the first sections[0] pairs follow axis 0,
+                            the next sections[1] axis 1, and so on; their sum is
+                            rotary_dim / 2.  axes <= 1: zeros                      */
+    int32_t table_rows;  /* rows of the table: positions are below it             */
+    float eps;           /* of the norms                                          */
+    int64_t q_out_stride, k_out_stride; /* elements from a row to the next; 0:
+                            contiguous.  Heads are D apart                         */
+} pa_rope;
+
+/* Zeroes *t, eps = 1e-6.  Returns t. */
+pa_rope *pa_rope_init(pa_rope *t);
+
+/* For each packed row and head x of q and k:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight        (y = x where the weight is NULL)
+ *   pair i < rotary_dim / 2 at position n:  c = table[n][i], w = table[n][rotary_dim / 2 + i]
+ *   (y_a, y_b) -> (c y_a - w y_b, w y_a + c y_b)
+ * computed in fp32 and rounded once.  q goes to q_out, k to k_out (where it is
+ * not NULL) and, where k_cache is not NULL, k and the rows of v as they are
+ * into the pages, to each sequence's last positions as in pa_store
+ * (context_lens counts the rows).
+ *   q_weight, k_weight: [D] in q_dtype, 16-byte aligned, either may be NULL
+ *   table: [table_rows][rotary_dim] f32, cosines and sines of the angles, 16-byte aligned
+ *   positions: [axes][total_rows] int32; NULL: the row's place in its sequence,
+ *     context_lens[s] - n_s + t, on every axis
+ *   q_out, k_out: may be q and k themselves, with the same stride; no other overlap
+ * context_lens may be NULL with positions and no cache; v, v_cache and
+ * block_tables without a cache.  k_out and k_cache may not both be NULL.
+ * A position outside [0, table_rows) leaves its row out everywhere
+ * (PA_DEV_BAD_INDEX); lengths out of range leave a sequence out
+ * (PA_DEV_BAD_LEN); a page outside the pool leaves out the store of the row
+ * (PA_DEV_BAD_PAGE).  head_dim 64, 128 or 256. */
+pa_status pa_rotate(const pa_params *p, const pa_rows *r, const pa_rope *t, const void *q, const void *k,
+                    const void *v, const int32_t *cu_lens, const float *table, const int32_t *positions,
+                    const int32_t *context_lens, const void *q_weight, const void *k_weight, void *q_out,
+                    void *k_out, void *k_cache, void *v_cache, const int32_t *block_tables,
+                    uint32_t *dev_status, pa_stream_t stream);
+
+/* ------------------------------------------------------------------ verify
+ * Which tokens of a drafted tree the target's distribution accepts.  The
+ * packed rows of a sequence are the tokens whose logits the target has
+ * computed: row 0 is the last chosen token, which is certain, the others are
+ * drafts, each behind an earlier row of its sequence, its parent.
+ *   logits:       [total_rows][vocab] of the target in q_dtype, r->q_stride
+ *                 elements from a row to the next (0: vocab)
+ *   draft_logits: the same of the distributions that the drafts were drawn from
+ *                 (independently: the children of a row from its row), stride
+ *                 r->k_stride; rows without children are not read.  NULL: each
+ *                 draft was certain to its drafter
+ *   tokens, parents: [total_rows] int32; parents count within the sequence,
+ *                 0 <= parents[t] < t; row 0's are not read
+ *   temperature:  [num_seqs] f32; logits are divided by it; not above 0: greedy
+ *   uniform:      [total_rows] f32 in [0, 1), one for each draft
+ *   noise:        [num_seqs][vocab] f32, independent exponential numbers above 0
+ * From row 0 on, with p = softmax(target), q = softmax(draft) of the row (q
+ * the certain token itself without draft_logits), its children are tried in
+ * ascending order: child c is accepted when p(c) > 0 and uniform q(c) < p(c),
+ * and the walk goes on from it; else p becomes max(p - q, 0), normalised
+ * (left as it is where nothing remains).  Where no child is accepted, the next
+ * token is the one with the largest p(i) / noise(i), ties to the lowest: the
+ * tokens then follow the target's distribution.  Greedy: a child is accepted
+ * when it is the target's largest logit, the next token is that one, ties to
+ * the lowest; neither random numbers nor draft_logits are read.
+ *   accepted:    [total_rows] int32: the packed rows of the accepted tokens, row
+ *                0 of each sequence among them, sequence after sequence, then -1
+ *   accepted_cu: [num_seqs + 1] int32: where each sequence's begin.  The two are
+ *                the row_index and cu_lens of pa_store
+ *   next_tokens: [num_seqs] int32
+ *   new_lens:    [num_seqs] int32, context_lens[s] plus the accepted rows, for
+ *                pa_pages_resize; both may be NULL
+ * A sequence without rows, or with lengths out of range (PA_DEV_BAD_LEN),
+ * accepts nothing, its next token is -1.  A draft whose token or parent is out
+ * of range is passed over (PA_DEV_BAD_INDEX).  A visited row without a finite
+ * largest logit (a NaN or +infinity, all -infinity) ends the walk with next
+ * token -1 (PA_DEV_BAD_VALUE), as do random numbers that choose none.
+ * -infinity in other logits is a probability of zero.
+ * Uses of p: num_seqs, q_dtype.  vocab >= 1, max_rows <= 1024; logits and
+ * noise aligned to their elements. */
+pa_status pa_verify(const pa_params *p, const pa_rows *r, int32_t vocab, const void *logits,
+                    const void *draft_logits, const int32_t *tokens, const int32_t *parents,
+                    const int32_t *cu_lens, const float *temperature, const float *uniform,
+                    const float *noise, const int32_t *context_lens, int32_t *accepted,
+                    int32_t *accepted_cu, int32_t *next_tokens, int32_t *new_lens, uint32_t *dev_status,
+                    pa_stream_t stream);
+
+/* ------------------------------------------------------------- key weights
+ * What each cached key gathers of its sequence's rows' attention:
+ *   weights[s][g][j] = decay weights[s][g][j]
+ *     + sum over rows t and q heads h of kv head g of
+ *       exp(scale q[t,h].k_j) / sum_{i <= e_t} exp(scale q[t,h].k_i)   for j <= e_t
+ * with row t of T_s seeing keys 0 ..= e_t = context_lens[s] - T_s + t, as in
+ * pa_prefill_chunk (T_s = 1: a decode step); the rows' own K is in the pages.
+ *   weights: [num_seqs][num_kv_heads][max_blocks_per_seq * page_size] f32.  What
+ *     stood at the last T_s positions is not read, nor anything where decay is 0;
+ *     places from context_lens[s] on are left as they were
+ * decay in [0, 1].  A sequence without rows is left as it was.  Keys in pages
+ * outside the pool take no part (PA_DEV_BAD_PAGE), theirs is decay alone.  A
+ * score of -infinity weighs nothing; a NaN or +infinity makes what its row
+ * adds NaN.  Sums, largest scores and weights are fp32.
+ * Uses of p as in pa_tree (head_dim 64 or 128; out_dtype is not used; no
+ * windows, splits or decode_q_rows); max_context_len is a bound on
+ * every context_lens[s] (0: what a table holds): longer ones are
+ * PA_DEV_BAD_LEN, their weights left as they were.
+ * workspace: pa_key_weights_workspace_size bytes, 256-byte aligned (0: invalid). */
+size_t pa_key_weights_workspace_size(const pa_params *p, const pa_rows *r);
+
+pa_status pa_key_weights(const pa_params *p, const pa_rows *r, const void *q, const int32_t *cu_lens,
+                         const void *k_cache, const int32_t *block_tables, const int32_t *context_lens,
+                         float decay, float *weights, void *workspace, size_t workspace_bytes,
+                         uint32_t *dev_status, pa_stream_t stream);
+
+/* ------------------------------------------------------------------- evict
+ * Takes each sequence s with 0 <= keep_lens[s] < context_lens[s] down to
+ * n = keep_lens[s] keys, each kv head for itself: its last r = min(recent, n)
+ * keys stay, its first f = min(first, n - r), and of the others the n - r - f
+ * with the largest weights (ties to the lowest position; a NaN counts as
+ * -infinity).  They keep their order and move together to slots 0 .. n-1.
+ *   kept:        [num_seqs][num_kv_heads][max_blocks_per_seq * page_size] int32:
+ *                entry j < n is the slot that key j came from
+ *   weights_out: as weights; entry j < n is key j's weight
+ *   new_lens:    [num_seqs] int32: n, or -1 where nothing was evicted
+ * Sequences with keep_lens[s] negative or not below context_lens[s] keep all:
+ * kept and weights_out are filled as for n = context_lens[s].  Entries from n
+ * on are left as they were.  weights_out must not overlap weights.
+ * context_lens and the tables stay as they are: after the last layer,
+ * pa_pages_resize with new_lens trims every sequence and frees its pages.
+ * refcounts ([num_pages], may be NULL): a sequence of which a page from slot f
+ * to slot n - 1 has more than one holder is not evicted (PA_DEV_SHARED_PAGE).
+ * Without them no such page may belong to two sequences.  Keys whose old or new
+ * page is outside the pool do not move (PA_DEV_BAD_PAGE); a length out of range
+ * leaves the sequence out, new_lens -1 (PA_DEV_BAD_LEN).
+ * Uses of p: num_seqs, num_kv_heads, head_dim (64, 128, 256), kv_dtype and the
+ * pages.  max_blocks_per_seq * page_size is at most 2^22. */
+pa_status pa_evict(const pa_params *p, void *k_cache, void *v_cache, const int32_t *block_tables,
+                   const int32_t *context_lens, const int32_t *refcounts, const float *weights,
+                   const int32_t *keep_lens, int32_t first, int32_t recent, float *weights_out,
+                   int32_t *kept, int32_t *new_lens, uint32_t *dev_status, pa_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,310 @@
+// pa_evict.cu -- eviction of the keys that gathered the least attention.
+//
+// Selection: a cluster of CTAs for each (sequence, kv head).  The weights are
+// taken as ordered 32-bit keys; four passes of eight bits find the key of the
+// last one that stays, from histograms that the cluster's CTAs add up, and how
+// many of its equals stay with it.  Then each CTA numbers the keys of its run
+// that stay, in order, and writes where they came from and what they weigh.
+//
+// Move: key j comes from slot kept[j] >= j, so a CTA that takes a column of
+// the rows (some 16-byte units of K or of V of one kv head) can work its way up
+// tile by tile, reading a tile before it writes it: what a tile overwrites
+// belongs to keys that it or an earlier tile has read.  Columns do not meet, so
+// they are what the work is split over, and no second copy is needed.
+#include <cooperative_groups.h>
+
+#include "pa_ptx.cuh"
+#include "pa_serving.h"
+
+namespace pa {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kSelThr = 512;
+constexpr int kSelWarps = kSelThr / 32;
+constexpr int kSelMaxCluster = 8;
+constexpr int kBins = 256;
+constexpr int kMoveThr = 256;
+constexpr int kMovePer = 4;  // rows that a thread has in flight
+
+// What happens to a sequence.
+struct Cut {
+    int L, n, first, recent;  // keys before and after; which stay whatever their weight
+    bool cut, bad;
+};
+
+__device__ inline Cut cut_of(const EvictCall& a, int s) {
+    Cut c;
+    c.L = a.c.context_lens[s];
+    const int keep = a.keep_lens[s];
+    c.bad = c.L < 0 || c.L > int64_t(a.c.max_blocks) * a.c.page_size;
+    if (c.bad) c.L = 0;
+    c.cut = !c.bad && keep >= 0 && keep < c.L;
+    c.n = c.cut ? keep : c.L;
+    c.recent = min(a.recent, c.n);
+    c.first = min(a.first, c.n - c.recent);
+    return c;
+}
+
+// Order of weights as unsigned numbers; NaN as -infinity, -0 as 0.
+__device__ inline uint32_t ordered(float w) {
+    if (!(w == w)) w = -INFINITY;
+    const uint32_t b = __float_as_uint(w + 0.f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+__global__ void __launch_bounds__(kSelThr) evict_select(const EvictCall a) {
+    __shared__ int hist[kBins];
+    __shared__ int totals[kBins];
+    __shared__ int sums[2][kSelWarps];
+    __shared__ int mine[2];      // keys of the CTA's run that equal the last one; that stay for certain
+    __shared__ int found[2];     // a digit, and how many keys are still to be chosen among its own
+    __shared__ int shared_page;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const int unit = int(blockIdx.x) / C;
+    const int s = unit / a.Hkv, g = unit - s * a.Hkv;
+    Cut c = cut_of(a, s);
+    if (tid == 0) shared_page = 0;
+    __syncthreads();
+    if (c.cut && a.refcounts) {  // pages that would be written
+        bool held = false;
+        for (int b = c.first / a.c.page_size + tid; b < (c.n + a.c.page_size - 1) / a.c.page_size; b += kSelThr) {
+            const int pg = a.c.block_tables[int64_t(s) * a.c.max_blocks + b];
+            held |= pg >= 0 && pg < a.c.num_pages && a.refcounts[pg] > 1;
+        }
+        if (held) shared_page = 1;
+    }
+    __syncthreads();
+    const bool kept_whole = shared_page != 0;
+    if (kept_whole) c.cut = false, c.n = c.L;
+    if (g == 0 && rank == 0 && tid == 0) {
+        a.new_lens[s] = c.cut ? c.n : -1;
+        if (c.bad) flag(a.dev_status, PA_DEV_BAD_LEN);
+        if (kept_whole) flag(a.dev_status, PA_DEV_SHARED_PAGE);
+    }
+    const int64_t slots = int64_t(a.c.max_blocks) * a.c.page_size;
+    const float* w = a.weights + unit * slots;
+    float* w_out = a.weights_out + unit * slots;
+    int32_t* kept = a.kept + unit * slots;
+    if (!c.cut) {
+        for (int j = rank * kSelThr + tid; j < c.L; j += C * kSelThr) {
+            kept[j] = j;
+            w_out[j] = w[j];
+        }
+        return;
+    }
+    // the middle: keys that stay by weight, `want` of them
+    const int m0 = c.first, m1 = c.L - c.recent;
+    int want = c.n - c.first - c.recent;
+    // the CTA's run of all slots
+    const int run = ((c.L + C - 1) / C + kSelThr - 1) / kSelThr * kSelThr;
+    const int lo = min(c.L, rank * run), hi = min(c.L, lo + run);
+    uint32_t prefix = 0;  // the leading digits of the last key that stays
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        for (int b = tid; b < kBins; b += kSelThr) hist[b] = 0;
+        __syncthreads();
+        for (int j = max(lo, m0) + tid; j < min(hi, m1); j += kSelThr) {
+            const uint32_t k = ordered(w[j]);
+            if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255], 1);
+        }
+        cluster.sync();
+        if (tid < kBins) {
+            int n = 0;
+            for (int r = 0; r < C; ++r) n += cluster.map_shared_rank(hist, r)[tid];
+            totals[tid] = n;
+        }
+        __syncthreads();
+        if (warp == 0) {  // from the largest digit down: where the count reaches `want`
+            int above = 0, part[kBins / 32], sum = 0;
+#pragma unroll
+            for (int i = 0; i < kBins / 32; ++i) {
+                part[i] = totals[kBins - 1 - (lane * (kBins / 32) + i)];
+                sum += part[i];
+            }
+            int v = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += x;
+            }
+            above = v - sum;
+            if (lane == 0) found[0] = 0, found[1] = 0;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < kBins / 32; ++i) {
+                if (above < want && want <= above + part[i]) {
+                    found[0] = kBins - 1 - (lane * (kBins / 32) + i);
+                    found[1] = want - above;
+                }
+                above += part[i];
+            }
+        }
+        cluster.sync();  // the others have read this histogram, the CTA its digit
+        prefix |= uint32_t(found[0]) << shift;
+        want = found[1];
+        __syncthreads();
+    }
+    // keys above the last one stay, and the first `want` equal to it; none where none is wanted
+    const bool any = c.n - c.first - c.recent > 0;
+    auto sure = [&](int j, uint32_t k) { return j < m0 || j >= m1 || (any && k > prefix); };
+    auto equal = [&](int j, uint32_t k) { return any && j >= m0 && j < m1 && k == prefix; };
+    int eq = 0, st = 0;
+    for (int j = lo + tid; j < hi; j += kSelThr) {
+        const uint32_t k = ordered(w[j]);
+        eq += equal(j, k);
+        st += sure(j, k);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        eq += __shfl_xor_sync(0xffffffffu, eq, o);
+        st += __shfl_xor_sync(0xffffffffu, st, o);
+    }
+    if (lane == 0) sums[0][warp] = eq, sums[1][warp] = st;
+    __syncthreads();
+    if (tid < 2) {
+        int n = 0;
+        for (int i = 0; i < kSelWarps; ++i) n += sums[tid][i];
+        mine[tid] = n;
+    }
+    cluster.sync();
+    int eq_at = 0, st_at = 0;  // equals and certain ones before the tile
+    for (int r = 0; r < rank; ++r) {
+        eq_at += cluster.map_shared_rank(mine, r)[0];
+        st_at += cluster.map_shared_rank(mine, r)[1];
+    }
+    for (int j0 = lo; j0 < hi; j0 += kSelThr) {
+        const int j = j0 + tid;
+        const float x = j < hi ? w[j] : 0.f;
+        const uint32_t k = ordered(x);
+        const bool e = j < hi && equal(j, k), su = j < hi && sure(j, k);
+        const unsigned em = __ballot_sync(0xffffffffu, e), sm = __ballot_sync(0xffffffffu, su);
+        __syncthreads();
+        if (lane == 0) sums[0][warp] = __popc(em), sums[1][warp] = __popc(sm);
+        __syncthreads();
+        int eb = eq_at, sb = st_at;
+        for (int i = 0; i < kSelWarps; ++i) {
+            if (i < warp) eb += sums[0][i], sb += sums[1][i];
+            eq_at += sums[0][i];
+            st_at += sums[1][i];
+        }
+        const unsigned below = (1u << lane) - 1u;
+        eb += __popc(em & below);
+        sb += __popc(sm & below);
+        if (su || (e && eb < want)) {
+            const int to = sb + min(eb, want);
+            kept[to] = j;
+            w_out[to] = x;
+        }
+    }
+    cluster.sync();  // nobody leaves while another may read its counts
+}
+
+struct MoveArgs {
+    uint4* k;
+    uint4* v;
+    int64_t page_stride, token_stride, head_stride;  // 16-byte units
+    const int32_t* block_tables;
+    const int32_t* kept;
+    const int32_t* new_lens;
+    uint32_t* dev_status;
+    int32_t Hkv, max_blocks, page_size, page_shift, num_pages;
+    int32_t parts, width;  // columns of a row, and their 16-byte units
+};
+
+__global__ void __launch_bounds__(kMoveThr) evict_move(const MoveArgs a) {
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    int id = int(blockIdx.x);
+    const int part = id % a.parts;
+    id /= a.parts;
+    uint4* pool = id & 1 ? a.v : a.k;
+    const int unit = id >> 1, s = unit / a.Hkv, g = unit - s * a.Hkv;
+    const int n = a.new_lens[s];
+    if (n <= 0) return;
+    const int32_t* table = a.block_tables + int64_t(s) * a.max_blocks;
+    const int32_t* kept = a.kept + unit * (int64_t(a.max_blocks) * a.page_size);
+    const int per = kMoveThr / a.width;  // rows of a step; a tile has kMovePer steps
+    const int sub = threadIdx.x % a.width, mine = threadIdx.x / a.width;
+    const int64_t off = g * a.head_stride + part * a.width + sub;
+    auto place = [&](int slot) -> int64_t {
+        const int pg = table[slot >> a.page_shift];
+        if (pg < 0 || pg >= a.num_pages) return -1;
+        return pg * a.page_stride + (slot & (a.page_size - 1)) * a.token_stride + off;
+    };
+    for (int j0 = 0; j0 < n; j0 += per * kMovePer) {
+        uint4 x[kMovePer];
+        int64_t to[kMovePer];
+#pragma unroll
+        for (int i = 0; i < kMovePer; ++i) {
+            const int j = j0 + i * per + mine;
+            to[i] = -1;
+            if (j < n) {
+                const int from = kept[j];
+                if (from != j) {
+                    const int64_t src = place(from);
+                    to[i] = place(j);
+                    if (src < 0 || to[i] < 0) {
+                        flag(a.dev_status, PA_DEV_BAD_PAGE);
+                        to[i] = -1;
+                    } else {
+                        x[i] = pool[src];
+                    }
+                }
+            }
+        }
+        __syncthreads();  // the tile is read
+#pragma unroll
+        for (int i = 0; i < kMovePer; ++i)
+            if (to[i] >= 0) pool[to[i]] = x[i];
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const EvictCall& c, cudaStream_t st) {
+    const int units = c.num_seqs * c.Hkv;
+    int size = kSelMaxCluster;
+    while (size > 1 && int64_t(units) * size > 2 * 152) size /= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(units) * size);
+    cfg.blockDim = dim3(kSelThr);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = size;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select, c);
+    if (e != cudaSuccess) return e;
+    MoveArgs a;
+    a.k = static_cast<uint4*>(const_cast<void*>(c.c.k));
+    a.v = static_cast<uint4*>(const_cast<void*>(c.c.v));
+    a.page_stride = c.c.page_stride * c.elt_bytes / 16;
+    a.token_stride = c.c.token_stride * c.elt_bytes / 16;
+    a.head_stride = c.c.head_stride * c.elt_bytes / 16;
+    a.block_tables = c.c.block_tables;
+    a.kept = c.kept;
+    a.new_lens = c.new_lens;
+    a.dev_status = c.dev_status;
+    a.Hkv = c.Hkv;
+    a.max_blocks = c.c.max_blocks;
+    a.page_size = c.c.page_size;
+    a.page_shift = c.c.page_size == 16 ? 4 : 5;
+    a.num_pages = c.c.num_pages;
+    const int row = c.D * c.elt_bytes / 16;  // 16-byte units, a power of two from 8 to 64
+    a.width = row;
+    while (a.width > 4 && int64_t(units) * 2 * (row / a.width) < 2 * 152) a.width /= 2;  // a column is 64 bytes at least
+    a.parts = row / a.width;
+    return launch_pdl(evict_move, dim3(unsigned(units) * 2 * a.parts), dim3(kMoveThr), 0, st, a);
+}
+
+}  // namespace pa

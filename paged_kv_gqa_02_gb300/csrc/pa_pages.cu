@@ -11,6 +11,7 @@
 //
 // The copies are bound by HBM: 16-byte loads, eight in flight per thread.
 #include "pa_ptx.cuh"
+#include "pa_rows.cuh"
 #include "pa_serving.h"
 
 namespace pa {
@@ -457,23 +458,10 @@ struct StoreArgs {
 __global__ void __launch_bounds__(kStoreThr) store_rows(const StoreArgs a) {
     pdl_wait_primary();
     const int lane = threadIdx.x & 31;
-    if (blockIdx.x == 0)  // a sequence without rows of its own is seen by nobody else
-        for (int s = threadIdx.x; s < a.num_seqs; s += kStoreThr) {
-            const int r0 = a.cu_lens[s], r1 = a.cu_lens[s + 1];
-            if (r0 < 0 || r1 < r0 || r1 > a.total_rows || r1 - r0 > a.max_rows) flag(a.dev_status, PA_DEV_BAD_LEN);
-        }
+    if (blockIdx.x == 0) flag_bad_rows(a.cu_lens, a.num_seqs, a.total_rows, a.max_rows, a.dev_status);
     const int row = int(blockIdx.x) * (kStoreThr / 32) + int(threadIdx.x >> 5);
     if (row >= a.total_rows) return;
-    // the sequence: the number of ends at or before the row, 32 probes at a time
-    int lo = 0, hi = a.num_seqs;
-    while (lo < hi) {
-        const int step = (hi - lo + 31) / 32;
-        const int at = lo + step * (lane + 1) - 1;  // the last of each of 32 runs
-        const int k = __popc(__ballot_sync(0xffffffffu, at < hi && a.cu_lens[at + 1] <= row));
-        lo = min(lo + step * k, hi);
-        hi = min(hi, lo + step - 1);
-    }
-    const int s = lo;
+    const int s = seq_of_row(a.cu_lens, a.num_seqs, row, lane);
     if (s >= a.num_seqs) return;  // behind the last sequence
     const int r0 = a.cu_lens[s], r1 = a.cu_lens[s + 1], L = a.context_lens[s];
     if (row < r0) return;  // before the first sequence (ends out of order are flagged above)

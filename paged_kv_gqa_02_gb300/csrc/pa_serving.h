@@ -80,6 +80,78 @@ cudaError_t launch_pages_compact(const PagesCall& c, int32_t* pairs, int max_mov
 cudaError_t launch_pages_copy(const CacheArgs& c, int Hkv, int D, int elt_bytes, const int32_t* pairs, int n,
                               uint32_t* dev_status, cudaStream_t st);
 
+// Rotation, draft verification, key weights and eviction.
+struct RotateCall {
+    RowArgs r;
+    pa_rope t;  // resolved: axes >= 1, strides in elements
+    const void* q;
+    const void* k;
+    const void* v;
+    const void* q_weight;
+    const void* k_weight;
+    void* q_out;
+    void* k_out;
+    const float* table;
+    const int32_t* positions;
+    pa_dtype dtype;
+    int32_t Hq, Hkv, D;
+    CacheArgs c;  // k == nullptr: no store
+    uint32_t* dev_status;
+};
+cudaError_t launch_rotate(const RotateCall& c, cudaStream_t st);
+
+struct VerifyCall {
+    const int32_t* cu_lens;
+    const void* logits;
+    const void* draft;  // nullptr: certain drafts
+    const int32_t* tokens;
+    const int32_t* parents;
+    const float* temperature;
+    const float* uniform;
+    const float* noise;
+    const int32_t* context_lens;
+    int32_t* accepted;
+    int32_t* accepted_cu;
+    int32_t* next_tokens;
+    int32_t* new_lens;
+    int64_t logits_stride, draft_stride;
+    int32_t num_seqs, total_rows, max_rows, vocab;
+    pa_dtype dtype;
+    uint32_t* dev_status;
+};
+cudaError_t launch_verify(const VerifyCall& c, cudaStream_t st);
+
+struct KeyWeightsCall {
+    RowArgs r;
+    const void* q;
+    CacheArgs c;  // v unused
+    float* weights;
+    pa_dtype dtype;
+    int32_t Hq, Hkv, D;
+    int32_t max_len;  // longest context taken
+    int32_t n_ctas;
+    float scale_log2, decay;
+    void* workspace;
+    uint32_t* dev_status;
+    int32_t debug_timeout;
+};
+size_t key_weights_workspace_bytes(const KeyWeightsCall& c);
+cudaError_t launch_key_weights(const KeyWeightsCall& c, cudaStream_t st);
+
+struct EvictCall {
+    CacheArgs c;  // k, v written
+    const int32_t* refcounts;
+    const float* weights;
+    const int32_t* keep_lens;
+    float* weights_out;
+    int32_t* kept;
+    int32_t* new_lens;
+    int32_t num_seqs, Hkv, D, elt_bytes, first, recent;
+    uint32_t* dev_status;
+};
+constexpr int64_t kMaxEvictSlots = 1 << 22;  // slots of a block table that pa_evict takes
+cudaError_t launch_evict(const EvictCall& c, cudaStream_t st);
+
 // A launch that may start while the kernel before it drains; its kernel waits
 // (griddepcontrol.wait) before it touches global memory.
 template <typename... P, typename... A>

@@ -20,7 +20,7 @@ LIB_PATH = os.environ.get("PA_GQA_LIB") or os.path.join(PKG, "libpaged_gqa.so")
 PA_F32, PA_F16, PA_BF16 = 0, 1, 2
 DTYPE_CODE = {"f32": PA_F32, "f16": PA_F16, "bf16": PA_BF16}
 PA_DEV_BAD_PAGE, PA_DEV_BAD_LEN, PA_DEV_TIMEOUT, PA_DEV_OOB = 1, 2, 4, 8
-PA_DEV_NO_PAGES, PA_DEV_BAD_INDEX = 16, 32
+PA_DEV_NO_PAGES, PA_DEV_BAD_INDEX, PA_DEV_BAD_VALUE, PA_DEV_SHARED_PAGE = 16, 32, 64, 128
 PA_FORM_AUTO, PA_FORM_PAIR, PA_FORM_COUNTED = 0, 1, 2
 STATUS = {0: "PA_OK", 1: "PA_ERR_NULL", 2: "PA_ERR_SHAPE", 3: "PA_ERR_DTYPE",
           4: "PA_ERR_ALIGN", 5: "PA_ERR_WORKSPACE", 6: "PA_ERR_UNSUPPORTED", 7: "PA_ERR_CUDA"}
@@ -30,7 +30,8 @@ EXPORTS = ("pa_params_init", "pa_status_string", "pa_decode_plan", "pa_decode_wo
            "pa_prefill_chunk", "pa_version", "pa_decode_append", "pa_decode_noalloc",
            "pa_build_flags", "pa_decode_kernels", "pa_rows_init", "pa_prompt",
            "pa_tree_workspace_size", "pa_tree", "pa_store", "pa_pages_workspace_size",
-           "pa_pages_resize", "pa_pages_fork", "pa_pages_compact", "pa_pages_copy")
+           "pa_pages_resize", "pa_pages_fork", "pa_pages_compact", "pa_pages_copy", "pa_rope_init",
+           "pa_rotate", "pa_verify", "pa_key_weights_workspace_size", "pa_key_weights", "pa_evict")
 
 
 class PaError(RuntimeError):
@@ -60,6 +61,13 @@ class Rows(ctypes.Structure):
                 ("source_rows", ctypes.c_int32), ("mask_words", ctypes.c_int32),
                 ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
                 ("v_stride", ctypes.c_int64)]
+
+
+class Rope(ctypes.Structure):
+    """Mirror of ``pa_rope``."""
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("sections", ctypes.c_int32 * 3), ("table_rows", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("q_out_stride", ctypes.c_int64), ("k_out_stride", ctypes.c_int64)]
 
 
 _lock = threading.Lock()
@@ -109,10 +117,19 @@ def load(path: str = LIB_PATH):
             L.pa_pages_fork.argtypes = [P, vp, vp, vp, vp, vp, i32, vp, vp]
             L.pa_pages_compact.argtypes = [P, vp, vp, vp, vp, i32, vp, vp, sz, vp, vp]
             L.pa_pages_copy.argtypes = [P, vp, vp, vp, i32, vp, vp]
-            for name in ("pa_tree_workspace_size", "pa_pages_workspace_size"):
+            T = ctypes.POINTER(Rope)
+            L.pa_rope_init.argtypes = [T]
+            L.pa_rope_init.restype = T
+            L.pa_rotate.argtypes = [P, R, T] + [vp] * 16
+            L.pa_verify.argtypes = [P, R, i32] + [vp] * 15
+            L.pa_key_weights_workspace_size.argtypes = [P, R]
+            L.pa_key_weights.argtypes = [P, R, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, sz, vp, vp]
+            L.pa_evict.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp]
+            for name in ("pa_tree_workspace_size", "pa_pages_workspace_size", "pa_key_weights_workspace_size"):
                 getattr(L, name).restype = sz
             for name in ("pa_prompt", "pa_tree", "pa_store", "pa_pages_resize", "pa_pages_fork",
-                         "pa_pages_compact", "pa_pages_copy"):
+                         "pa_pages_compact", "pa_pages_copy", "pa_rotate", "pa_verify", "pa_key_weights",
+                         "pa_evict"):
                 getattr(L, name).restype = ctypes.c_int
             L.pa_version.restype = i32
             if hasattr(L, "pa_build_flags"):
@@ -341,6 +358,13 @@ def _int32():
 # tensor is asked for once: a small call's kernels take less time than careless
 # checks would.
 
+def _floats(t, n, dev, what):
+    """Pointer of a contiguous float32 tensor of at least n elements on device number dev."""
+    if t.dtype is not _dtypes()[0] or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous float32 tensor of at least {n} elements on cuda:{dev}")
+    return t.data_ptr()
+
+
 def _ints(t, n, dev, what):
     """Pointer of a contiguous int32 tensor of at least n elements on device number dev."""
     if t.dtype is not (_I32 or _int32()) or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
@@ -532,3 +556,154 @@ def pages_copy(p: Params, k_cache, v_cache, pairs, dev_status=None, stream=None)
     dev, n = k_cache.get_device(), pairs.numel() // 2
     _call("pa_pages_copy", dev, stream, p, _pool(k_cache, p, dev, "k_cache"),
           _pool(v_cache, p, dev, "v_cache"), _table(pairs, n, 2, dev, "pairs"), n, _status(dev_status, dev))
+
+
+# ---- around the step's attention: rotation, verification, key weights, eviction ----
+
+def make_rope(rotary_dim, *, table_rows=0, interleaved=False, eps=1e-6, sections=None, q_out_stride=0,
+              k_out_stride=0) -> Rope:
+    """``pa_rope``; sections (pairs that follow each axis of the positions) where there are several axes."""
+    axes = len(sections) if sections else 1
+    if axes > 3:
+        raise ValueError("sections: at most three axes")
+    three = (ctypes.c_int32 * 3)(*(sections if axes > 1 else ()))
+    return Rope(rotary_dim, int(interleaved), axes, three, table_rows, eps, q_out_stride, k_out_stride)
+
+
+def _norm_weight(t, p, dev, what):
+    if t is None:
+        return None
+    if t.dtype is not _dtypes()[p.q_dtype] or t.get_device() != dev or t.numel() != p.head_dim or not t.is_contiguous():
+        raise ValueError(f"{what}: {p.head_dim} contiguous elements of {_dtypes()[p.q_dtype]} on cuda:{dev}")
+    return t.data_ptr()
+
+
+def rotate(p: Params, r: Rows, rope: Rope, q, k, cu_lens, table=None, *, v=None, positions=None, context_lens=None,
+           q_weight=None, k_weight=None, q_out=None, k_out=None, k_cache=None, v_cache=None, block_tables=None,
+           dev_status=None, stream=None):
+    """Norms and rotation of packed queries and keys: q [rows][Hq][D] -> q_out, k [rows][Hkv][D] -> k_out and,
+    with a cache, k and v into the pages as ``store`` does.  Returns (q_out, k_out); q_out is made where it is
+    None (zeros behind the last sequence), k_out too where there is no cache."""
+    n, d, hq, hkv, dev, b = r.total_rows, p.head_dim, p.num_q_heads, p.num_kv_heads, q.get_device(), p.num_seqs
+    if q_out is None:
+        q_out = _new_rows(n, hq, d, rope.q_out_stride, q, stream)
+    if k_out is None and k_cache is None:
+        k_out = _new_rows(n, hkv, d, rope.k_out_stride, k, stream)
+    cache = (None, None, None)
+    if k_cache is not None:
+        cache = (_pool(k_cache, p, dev, "k_cache"), _pool(v_cache, p, dev, "v_cache"),
+                 _table(block_tables, b, p.max_blocks_per_seq, dev, "block_tables"))
+    _call("pa_rotate", dev, stream, p, r, rope,
+          _packed(q, p.q_dtype, n, hq, d, r.q_stride, dev, "q"), _packed(k, p.kv_dtype, n, hkv, d, r.k_stride, dev, "k"),
+          None if v is None else _packed(v, p.kv_dtype, n, hkv, d, r.v_stride, dev, "v"),
+          _ints(cu_lens, b + 1, dev, "cu_lens"),
+          None if table is None else _floats(table, rope.table_rows * rope.rotary_dim, dev, "table"),
+          None if positions is None else _table(positions, max(rope.axes, 1), n, dev, "positions"),
+          None if context_lens is None else _ints(context_lens, b, dev, "context_lens"),
+          _norm_weight(q_weight, p, dev, "q_weight"), _norm_weight(k_weight, p, dev, "k_weight"),
+          _packed(q_out, p.q_dtype, n, hq, d, rope.q_out_stride, dev, "q_out"),
+          None if k_out is None else _packed(k_out, p.kv_dtype, n, hkv, d, rope.k_out_stride, dev, "k_out"),
+          *cache, _status(dev_status, dev))
+    return q_out, k_out
+
+
+def _new_rows(n, heads, dim, stride, like, stream):
+    import torch
+    stride = stride or heads * dim
+    flat = _new(torch.zeros, n * stride, like.dtype, like, stream)
+    return flat.as_strided((n, heads, dim), (stride, dim, 1))
+
+
+def verify_params(*, num_seqs, dtype="bf16") -> Params:
+    """Params of pa_verify, which has neither heads nor pages."""
+    return make_params(num_seqs=num_seqs, num_q_heads=0, num_kv_heads=0, head_dim=0, page_size=0, num_pages=0,
+                       max_blocks_per_seq=0, max_context_len=0, scale=1.0, dtype=dtype)
+
+
+def _logits(t, code, rows, vocab, stride, dev, what):
+    """Pointer of logits [rows or more][vocab], ``stride`` elements between rows."""
+    if (t.dtype is not _dtypes()[code] or t.get_device() != dev or t.dim() != 2 or t.shape[0] < rows
+            or t.shape[1] != vocab or t.stride() != (stride or vocab, 1) and t.numel() and (t.shape[0] > 1 or vocab > 1)):
+        raise ValueError(f"{what}: [{rows}][{vocab}] of {_dtypes()[code]}, rows {stride or vocab} elements apart, "
+                         f"on cuda:{dev}")
+    return t.data_ptr()
+
+
+def verify(p: Params, r: Rows, logits, draft_logits, tokens, parents, cu_lens, temperature, uniform, noise,
+           context_lens=None, accepted=None, accepted_cu=None, next_tokens=None, new_lens=None, dev_status=None,
+           stream=None):
+    """Which drafts the target's logits [rows][vocab] accept, and the token behind them.  draft_logits None: the
+    drafts were certain.  Returns (accepted, accepted_cu, next_tokens, new_lens): the row_index and cu_lens of
+    ``store``, the new tokens, and context_lens plus the accepted rows for ``pages_resize`` (None without
+    context_lens)."""
+    import torch
+    n, b, dev, vocab = r.total_rows, p.num_seqs, logits.get_device(), logits.shape[-1]
+    if accepted is None:
+        accepted = _new(torch.empty, n, torch.int32, logits, stream)
+    if accepted_cu is None:
+        accepted_cu = _new(torch.empty, b + 1, torch.int32, logits, stream)
+    if next_tokens is None:
+        next_tokens = _new(torch.empty, b, torch.int32, logits, stream)
+    if new_lens is None and context_lens is not None:
+        new_lens = _new(torch.empty, b, torch.int32, logits, stream)
+    _call("pa_verify", dev, stream, p, r, vocab, _logits(logits, p.q_dtype, n, vocab, r.q_stride, dev, "logits"),
+          None if draft_logits is None else _logits(draft_logits, p.q_dtype, n, vocab, r.k_stride, dev, "draft_logits"),
+          _ints(tokens, n, dev, "tokens"), _ints(parents, n, dev, "parents"), _ints(cu_lens, b + 1, dev, "cu_lens"),
+          _floats(temperature, b, dev, "temperature"), _floats(uniform, n, dev, "uniform"),
+          _floats(noise, b * vocab, dev, "noise"),
+          None if context_lens is None else _ints(context_lens, b, dev, "context_lens"),
+          _ints(accepted, n, dev, "accepted"), _ints(accepted_cu, b + 1, dev, "accepted_cu"),
+          _ints(next_tokens, b, dev, "next_tokens"), None if new_lens is None else _ints(new_lens, b, dev, "new_lens"),
+          _status(dev_status, dev))
+    return accepted, accepted_cu, next_tokens, new_lens
+
+
+def key_weights_workspace_size(p: Params, r: Rows) -> int:
+    return int(load().pa_key_weights_workspace_size(p, r))
+
+
+def key_weights(p: Params, r: Rows, q, cu_lens, k_cache, block_tables, context_lens, weights, decay=1.0,
+                workspace=None, dev_status=None, stream=None):
+    """Fades the weights [B][Hkv][slots of a table] and adds what each cached key gathers of the packed rows'
+    attention; weights change in place."""
+    n, d, hq, dev, b = r.total_rows, p.head_dim, p.num_q_heads, q.get_device(), p.num_seqs
+    if workspace is None:
+        workspace = _new_scratch(key_weights_workspace_size(p, r), q, stream)
+    _call("pa_key_weights", dev, stream, p, r, _packed(q, p.q_dtype, n, hq, d, r.q_stride, dev, "q"),
+          _ints(cu_lens, b + 1, dev, "cu_lens"), _pool(k_cache, p, dev, "k_cache"),
+          _table(block_tables, b, p.max_blocks_per_seq, dev, "block_tables"), _ints(context_lens, b, dev, "context_lens"),
+          decay, _key_table(weights, p, dev, "weights", 0), *_scratch(workspace, dev), _status(dev_status, dev))
+    return weights
+
+
+def _key_table(t, p, dev, what, code):
+    """Pointer of a float32 (code 0) or int32 (None) value of each slot of a table, for each sequence and kv head."""
+    slots = p.max_blocks_per_seq * p.page_size
+    dtype = _int32() if code is None else _dtypes()[code]
+    if (t.dtype is not dtype or t.get_device() != dev or t.dim() != 3 or t.shape[0] < p.num_seqs
+            or t.shape[1] != p.num_kv_heads or t.shape[2] != slots or not t.is_contiguous()):
+        raise ValueError(f"{what}: contiguous [{p.num_seqs}][{p.num_kv_heads}][{slots}] of {dtype} on cuda:{dev}")
+    return t.data_ptr()
+
+
+def evict(p: Params, k_cache, v_cache, block_tables, context_lens, weights, keep_lens, weights_out=None, kept=None,
+          new_lens=None, *, first=0, recent=0, refcounts=None, dev_status=None, stream=None):
+    """Takes sequences down to keep_lens keys a kv head: the first, the most recent, and of the others those with
+    the largest weights; k_cache and v_cache change in place.  Returns (weights_out, kept, new_lens); new_lens goes
+    to ``pages_resize`` after the last layer."""
+    import torch
+    dev, b = k_cache.get_device(), p.num_seqs
+    size = (b, p.num_kv_heads, p.max_blocks_per_seq * p.page_size)
+    if weights_out is None:
+        weights_out = _new(torch.zeros, size, torch.float32, weights, stream)
+    if kept is None:
+        kept = _new(torch.zeros, size, torch.int32, weights, stream)
+    if new_lens is None:
+        new_lens = _new(torch.empty, b, torch.int32, weights, stream)
+    _call("pa_evict", dev, stream, p, _pool(k_cache, p, dev, "k_cache"), _pool(v_cache, p, dev, "v_cache"),
+          _table(block_tables, b, p.max_blocks_per_seq, dev, "block_tables"), _ints(context_lens, b, dev, "context_lens"),
+          None if refcounts is None else _ints(refcounts, p.num_pages, dev, "refcounts"),
+          _key_table(weights, p, dev, "weights", 0), _ints(keep_lens, b, dev, "keep_lens"), first, recent,
+          _key_table(weights_out, p, dev, "weights_out", 0), _key_table(kept, p, dev, "kept", None),
+          _ints(new_lens, b, dev, "new_lens"), _status(dev_status, dev))
+    return weights_out, kept, new_lens
