@@ -7,8 +7,8 @@
 // so there are two passes over the scores.
 //
 // Few columns (decoding): K is read once.  The first kernel leaves the scores,
-// which are much smaller than K, and each chunk's largest scores and sums in
-// the workspace; the second joins the chunks' and turns scores into weights.
+// which are much smaller than K, and each part's largest scores and sums in
+// the workspace; the second joins the parts' and turns scores into weights.
 // Many columns: the second pass computes the scores again.
 #include "pa_device.h"
 #include "pa_ptx.cuh"
@@ -32,8 +32,9 @@ struct KwArgs {
     float* weights;
     float2* stats;  // [total_rows][Hq]: a column's largest score and the reciprocal of its sum
     float* scores;  // few columns: [num_seqs][Hkv][max_len][width]
-    float2* pieces; // few columns: [num_seqs][Hkv][ceil(max_len / 64)][width], largest score and sum of a chunk
+    float2* pieces; // few columns: [num_seqs][Hkv][max_pieces][width], largest score and sum of a warp's part
     int32_t width;  // of a key's scores, the columns rounded up to even
+    int64_t max_pieces;
     uint32_t* dev_status;
     int64_t q_stride, page_stride, token_stride, head_stride;
     int64_t slots;  // of a block table
@@ -67,48 +68,51 @@ __device__ inline void join(float& m, float& l, float m2, float l2) {
 }
 
 // ---- few columns ----------------------------------------------------------------
-// Chunks of 64 to 512 keys of a (sequence, kv head), numbered sequence by
-// sequence and head by head, are shared out in equal runs of consecutive ones.
-// A chunk's keys go in tiles of 16 (a page or half of one) to the CTA's four
-// warps.  A lane reads its part of a K row straight into the registers of the
-// product's fragments: the dims of a row may come in any order, as long as q's
-// come in the same, so that lane c of four takes 16 bytes out of each 64.
+// The keys of each (sequence, kv head) in tiles of 16 (a page or half of one),
+// numbered sequence by sequence and head by head, are shared out to warps in
+// equal runs of consecutive tiles.  A warp leaves its scores, and a piece for
+// each head in its run: the columns' largest scores and sums there.  A lane
+// takes its part of a K row to the registers of the product's fragments by way
+// of slots of shared memory that only it uses, kStages tiles ahead: the dims of
+// a row may come in any order, as long as q's come in the same, so that lane c
+// of four takes 16 bytes out of each 64.
 constexpr int kFewThr = 128;
 constexpr int kFewWarps = kFewThr / 32;
-constexpr int kFewCols = 32;   // columns of a (sequence, kv head) at most
-constexpr int kFewPerSm = 4;   // CTAs
-constexpr int kFoldKeys = kFewThr;
+constexpr int kFewCols = 32;  // columns of a (sequence, kv head) at most
+constexpr int kStages = 3;
+constexpr int kMinShare = 4;  // tiles of a warp at least
+constexpr int kFoldThr = 128;
+constexpr int kFoldPerSm = 8;
+constexpr int kFoldKeys = 128;  // the fold's own tile: a key to a thread
+constexpr int kFoldAhead = 4;
 
 struct Place {
-    int s, g, chunk;
-    int chunks;  // of each head of the sequence
+    int s, g, tile;
+    int tiles;  // of each head of the sequence
 };
 
-// Chunks of a head of sequence s.
-__device__ inline int chunks_of(const KwArgs& a, int s, int keys) {
+__device__ inline int tiles_of(const KwArgs& a, int s, int keys) {
     if (s >= a.num_seqs) return 0;
     const KwSeq q = seq_of(a, s);
     return q.T > 0 ? (q.L + keys - 1) / keys : 0;
 }
-// All chunks of the call (whole warp).
-__device__ inline int64_t all_chunks(const KwArgs& a, int keys, int lane) {
+// All tiles of the call (whole warp).
+__device__ inline int64_t all_tiles(const KwArgs& a, int keys, int lane) {
     int64_t n = 0;
-    for (int s = lane; s < a.num_seqs; s += 32) n += int64_t(chunks_of(a, s, keys)) * a.Hkv;
+    for (int s = lane; s < a.num_seqs; s += 32) n += int64_t(tiles_of(a, s, keys)) * a.Hkv;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
     return n;
 }
-// Keys of a chunk: 64, doubled while every CTA keeps two chunks.
-__device__ inline int chunk_keys(int64_t chunks64, int ctas) {
-    int k = 1;
-    while (k < 8 && chunks64 / (2 * k) >= 2 * ctas) k *= 2;
-    return 64 * k;
+__device__ inline int64_t share_of(int64_t tiles, int workers, int least) {
+    const int64_t n = (tiles + workers - 1) / workers;
+    return n < least ? least : n;
 }
-// The chunk with a number below all_chunks (whole warp).
+// The tile with a number below all_tiles (whole warp).
 __device__ inline Place place_of(const KwArgs& a, int64_t id, int keys, int lane) {
     Place p = {0, 0, 0, 0};
     for (int s0 = 0; s0 < a.num_seqs; s0 += 32) {
-        const int n = chunks_of(a, s0 + lane, keys);
+        const int n = tiles_of(a, s0 + lane, keys);
         int64_t v = int64_t(n) * a.Hkv;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -119,68 +123,60 @@ __device__ inline Place place_of(const KwArgs& a, int64_t id, int keys, int lane
         if (m) {
             const int l = __ffs(m) - 1;
             p.s = s0 + l;
-            p.chunks = __shfl_sync(0xffffffffu, n, l);
-            const int64_t in = id - (__shfl_sync(0xffffffffu, v, l) - int64_t(p.chunks) * a.Hkv);
-            p.g = int(in / p.chunks);
-            p.chunk = int(in - int64_t(p.g) * p.chunks);
+            p.tiles = __shfl_sync(0xffffffffu, n, l);
+            const int64_t in = id - (__shfl_sync(0xffffffffu, v, l) - int64_t(p.tiles) * a.Hkv);
+            p.g = int(in / p.tiles);
+            p.tile = int(in - int64_t(p.g) * p.tiles);
             return p;
         }
         id -= __shfl_sync(0xffffffffu, v, 31);
     }
     return p;
 }
-__device__ inline void next_place(const KwArgs& a, Place& p, int64_t id, int keys, int lane) {
-    if (++p.chunk < p.chunks) return;
-    p.chunk = 0;
-    if (++p.g < a.Hkv) return;
-    p = place_of(a, id, keys, lane);
-}
 
-// The lane's part of 16 rows: rows r and r + 8 (lane = 4 r + c), of each the
-// 16-byte units c, c + 4, c + 8, ...
-template <typename T, int D> struct RowPart {
-    static constexpr int kUnits = D / (4 * Elt<T>::kVec);
-    uint4 lo[kUnits], hi[kUnits];
+template <typename T, int D> struct Few {
+    static constexpr int kUnits = D / (4 * Elt<T>::kVec);  // 16-byte units of a lane in a row
+    static constexpr int kTileBytes = 16 * D * int(sizeof(T));
+    static constexpr size_t kSmem = size_t(kFewWarps) * kStages * kTileBytes;
+    static constexpr int kPerSm = kTileBytes <= 4096 ? 4 : 2;  // CTAs: 192 KB of slots an SM at most
 };
-template <typename T, int D>
-__device__ inline void load_part(RowPart<T, D>& p, const T* r0, const T* r8, int c) {
-#pragma unroll
-    for (int i = 0; i < RowPart<T, D>::kUnits; ++i) {
-        p.lo[i] = __ldg(reinterpret_cast<const uint4*>(r0) + 4 * i + c);
-        p.hi[i] = __ldg(reinterpret_cast<const uint4*>(r8) + 4 * i + c);
-    }
-}
 
-// Columns as the lane meets them in a product: column 8 n + 2 c and the next.
-// 16-bit types: q's fragments in registers; fp32: q in shared memory.
+__device__ inline void cp_async16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ inline void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ inline void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// q of the columns as the lane meets them in a product, column 8 n + 2 c and
+// the next: fragments in registers; fp32 reads q where it lies.
 template <typename T, int D, int NT> struct FewQ {
-    uint2 b[NT][2 * RowPart<T, D>::kUnits];
-    __device__ inline void load(const KwArgs& a, const KwSeq& q, int g, int lane, float*) {
-        const int c = lane & 3;
+    uint2 b[NT][2 * Few<T, D>::kUnits];
+    __device__ inline void load(const KwArgs& a, const KwSeq& q, int g, int lane) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int col = 8 * n + (lane >> 2), t = col / a.G;
             const bool real = t < q.T;
             const uint4* from = reinterpret_cast<const uint4*>(
-                static_cast<const T*>(a.q) + (real ? int64_t(q.row0 + t) * a.q_stride + int64_t(g * a.G + col - t * a.G) * D : 0));
+                static_cast<const T*>(a.q) +
+                (real ? int64_t(q.row0 + t) * a.q_stride + int64_t(g * a.G + col - t * a.G) * D : 0));
 #pragma unroll
-            for (int i = 0; i < RowPart<T, D>::kUnits; ++i) {
-                const uint4 v = real ? __ldg(from + 4 * i + c) : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < Few<T, D>::kUnits; ++i) {
+                const uint4 v = real ? __ldg(from + 4 * i + (lane & 3)) : make_uint4(0, 0, 0, 0);
                 b[n][2 * i] = make_uint2(v.x, v.y);
                 b[n][2 * i + 1] = make_uint2(v.z, v.w);
             }
         }
     }
     // x[n]: rows r and r + 8 of columns 8 n + 2 c, 8 n + 2 c + 1, as the MMA leaves them
-    __device__ inline void scores(const RowPart<T, D>& k, const float*, int, float (&x)[NT][4]) const {
+    __device__ inline void scores(const uint4* slot, int lane, float (&x)[NT][4]) const {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[n][i] = 0.f;
 #pragma unroll
-        for (int i = 0; i < RowPart<T, D>::kUnits; ++i) {
-            const uint32_t a0[4] = {k.lo[i].x, k.hi[i].x, k.lo[i].y, k.hi[i].y};
-            const uint32_t a1[4] = {k.lo[i].z, k.hi[i].z, k.lo[i].w, k.hi[i].w};
+        for (int i = 0; i < Few<T, D>::kUnits; ++i) {
+            const uint4 lo = slot[64 * i + lane], hi = slot[64 * i + 32 + lane];
+            const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 mma_16816<std::is_same<T, __nv_bfloat16>::value>(x[n], a0, b[n][2 * i].x, b[n][2 * i].y);
@@ -190,213 +186,286 @@ template <typename T, int D, int NT> struct FewQ {
     }
 };
 template <int D, int NT> struct FewQ<float, D, NT> {
-    __device__ inline void load(const KwArgs& a, const KwSeq& q, int g, int, float* sq) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < 8 * NT * (D / 4); i += kFewThr) {
-            const int col = i / (D / 4), u = i - col * (D / 4), t = col / a.G;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (t < q.T)
-                v = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + int64_t(q.row0 + t) * a.q_stride +
-                                                    int64_t(g * a.G + col - t * a.G) * D)[u];
-            reinterpret_cast<float4*>(sq)[i] = v;
-        }
-        __syncthreads();
+    const float* base;
+    int64_t stride;
+    int G, cols;
+    __device__ inline void load(const KwArgs& a, const KwSeq& q, int g, int) {
+        base = static_cast<const float*>(a.q) + int64_t(q.row0) * a.q_stride + int64_t(g) * a.G * D;
+        stride = a.q_stride;
+        G = a.G;
+        cols = q.T * a.G;
     }
-    __device__ inline void scores(const RowPart<float, D>& k, const float* sq, int lane, float (&x)[NT][4]) const {
+    __device__ inline void scores(const uint4* slot, int lane, float (&x)[NT][4]) const {
         const int c = lane & 3;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int col = 0; col < 8; ++col) {
+            for (int j = 0; j < 8; ++j) {
+                const int col = 8 * n + j;
                 float lo = 0.f, hi = 0.f;
+                if (col < cols) {
+                    const float4* y4 = reinterpret_cast<const float4*>(base + col / G * stride + col % G * D);
 #pragma unroll
-                for (int i = 0; i < RowPart<float, D>::kUnits; ++i) {
-                    const float4 y = reinterpret_cast<const float4*>(sq)[(8 * n + col) * (D / 4) + 4 * i + c];
-                    const float4 u = *reinterpret_cast<const float4*>(&k.lo[i]);
-                    const float4 v = *reinterpret_cast<const float4*>(&k.hi[i]);
-                    lo = fmaf(u.x, y.x, lo), lo = fmaf(u.y, y.y, lo), lo = fmaf(u.z, y.z, lo), lo = fmaf(u.w, y.w, lo);
-                    hi = fmaf(v.x, y.x, hi), hi = fmaf(v.y, y.y, hi), hi = fmaf(v.z, y.z, hi), hi = fmaf(v.w, y.w, hi);
-                }
+                    for (int i = 0; i < Few<float, D>::kUnits; ++i) {
+                        const float4 y = __ldg(y4 + 4 * i + c);
+                        const float4 u = reinterpret_cast<const float4*>(slot)[64 * i + lane];
+                        const float4 v = reinterpret_cast<const float4*>(slot)[64 * i + 32 + lane];
+                        lo = fmaf(u.x, y.x, lo), lo = fmaf(u.y, y.y, lo), lo = fmaf(u.z, y.z, lo), lo = fmaf(u.w, y.w, lo);
+                        hi = fmaf(v.x, y.x, hi), hi = fmaf(v.y, y.y, hi), hi = fmaf(v.z, y.z, hi), hi = fmaf(v.w, y.w, hi);
+                    }
 #pragma unroll
-                for (int o = 1; o < 4; o <<= 1) {
-                    lo += __shfl_xor_sync(0xffffffffu, lo, o);
-                    hi += __shfl_xor_sync(0xffffffffu, hi, o);
+                    for (int o = 1; o < 4; o <<= 1) {
+                        lo += __shfl_xor_sync(0xffffffffu, lo, o);
+                        hi += __shfl_xor_sync(0xffffffffu, hi, o);
+                    }
                 }
-                if (c == col / 2) {  // the lane that holds this column
-                    x[n][col % 2] = lo;
-                    x[n][2 + col % 2] = hi;
+                if (c == j / 2) {  // the lane that holds this column
+                    x[n][j % 2] = lo;
+                    x[n][2 + j % 2] = hi;
                 }
             }
     }
 };
 
-template <typename T, int D, int NT> __global__ void __launch_bounds__(kFewThr, kFewPerSm) few_scores(const KwArgs a) {
-    extern __shared__ float smem[];  // fp32: the columns' q
-    __shared__ float2 joined[kFewWarps][8 * NT];
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kFewThr, Few<T, D>::kPerSm) few_scores(const KwArgs a) {
+    extern __shared__ __align__(16) uint4 slots[];
     pdl_wait_primary();
     pdl_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & 3, r = lane >> 2;
     if (blockIdx.x == 0)
         for (int s = tid; s < a.num_seqs; s += kFewThr)
             if (seq_of(a, s).bad) flag(a.dev_status, PA_DEV_BAD_LEN);
-    const int64_t n64 = all_chunks(a, 64, lane);
-    const int keys = chunk_keys(n64, gridDim.x);
-    const int64_t total = keys == 64 ? n64 : all_chunks(a, keys, lane);
-    const int64_t share = (total + gridDim.x - 1) / gridDim.x;
-    const int64_t id0 = share * blockIdx.x, id1 = min(total, id0 + share);
-    if (id0 >= id1) return;
-    Place p = place_of(a, id0, keys, lane);
-    FewQ<T, D, NT> qf;
-    KwSeq q = {};
-    int at_s = -1, at_g = -1;
-    for (int64_t id = id0; id < id1; ++id) {
-        if (p.s != at_s) q = seq_of(a, p.s);
-        if (p.s != at_s || p.g != at_g) qf.load(a, q, p.g, lane, smem);
-        at_s = p.s, at_g = p.g;
-        const int j0 = p.chunk * keys, n_keys = min(keys, q.L - j0), before = q.L - q.T;
-        // the lane-th tile's page
-        const int tiles = (n_keys + 15) / 16;
-        int my_page = 0;
-        if (lane < tiles) {
-            my_page = a.block_tables[int64_t(p.s) * a.max_blocks + ((j0 + 16 * lane) >> a.page_shift)];
-            if (my_page < 0 || my_page >= a.num_pages) {
-                my_page = -1;
-                if (warp == 0) flag(a.dev_status, PA_DEV_BAD_PAGE);
-            }
-        }
+    const int workers = int(gridDim.x) * kFewWarps;
+    // the first CTAs' warps first, so that a small call's warps lie on different SMs
+    const int worker = warp * int(gridDim.x) + int(blockIdx.x);
+    const int64_t total = all_tiles(a, 16, lane), share = share_of(total, workers, kMinShare);
+    const int64_t id1 = min(total, share * (worker + 1));
+    int64_t id = share * worker;
+    uint4* mine = slots + warp * (kStages * Few<T, D>::kTileBytes / 16);
+    const uint32_t mine_u32 = smem_u32(mine);
+    const bool early = a.max_rows > 1;  // rows that do not see all keys
+    while (id < id1) {  // a head's part of the run
+        const Place p = place_of(a, id, 16, lane);
+        const KwSeq q = seq_of(a, p.s);
+        const int n = int(min(int64_t(p.tiles - p.tile), id1 - id));
         const int64_t unit = int64_t(p.s) * a.Hkv + p.g;
-        float* out = a.scores + (unit * a.max_len + j0) * a.width;
+        const int32_t* table = a.block_tables + int64_t(p.s) * a.max_blocks;
+        const T* head = static_cast<const T*>(a.k) + p.g * a.head_stride;
+        int my_page = 0, page_tile = -32;  // pages of tiles page_tile .. page_tile + 31 of the part, one a lane
+        auto page_at = [&](int i) {
+            if (i >= page_tile + 32) {
+                page_tile = i;
+                my_page = -1;
+                if (i + lane < n) {
+                    my_page = table[(16 * (p.tile + i + lane)) >> a.page_shift];
+                    if (my_page < 0 || my_page >= a.num_pages) {
+                        my_page = -1;
+                        flag(a.dev_status, PA_DEV_BAD_PAGE);
+                    }
+                }
+            }
+            return __shfl_sync(0xffffffffu, my_page, i - page_tile);
+        };
+        uint32_t bad = 0;  // a bit for each tile in flight, the next one lowest: its page is none
+        auto fetch = [&](int i) {
+            if (i < n) {
+                const int page = page_at(i);
+                if (page >= 0) {
+                    const T* row = head + page * a.page_stride + ((16 * (p.tile + i)) & (a.page_size - 1)) * a.token_stride;
+                    const uint4* lo = reinterpret_cast<const uint4*>(row + r * a.token_stride) + c;
+                    const uint4* hi = reinterpret_cast<const uint4*>(row + (r + 8) * a.token_stride) + c;
+                    const uint32_t to = mine_u32 + (i % kStages) * Few<T, D>::kTileBytes + 16 * lane;
+#pragma unroll
+                    for (int u = 0; u < Few<T, D>::kUnits; ++u) {
+                        cp_async16(to + 1024 * u, lo + 4 * u);
+                        cp_async16(to + 1024 * u + 512, hi + 4 * u);
+                    }
+                } else {
+                    bad |= 1u << (i % kStages);
+                }
+            }
+            cp_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) fetch(i);
+        FewQ<T, D, NT> qf;
+        qf.load(a, q, p.g, lane);
         float m[NT][2], l[NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = kLowest, l[n][0] = l[n][1] = 0.f;
-        for (int tile = warp; tile < tiles; tile += kFewWarps) {
-            const int page = __shfl_sync(0xffffffffu, my_page, tile);
-            if (page < 0) continue;  // nothing is read of its scores either
-            const T* row = static_cast<const T*>(a.k) + page * a.page_stride +
-                           ((j0 + 16 * tile) & (a.page_size - 1)) * a.token_stride + p.g * a.head_stride;
-            RowPart<T, D> k;
-            load_part<T, D>(k, row + r * a.token_stride, row + (r + 8) * a.token_stride, c);
+        for (int x = 0; x < NT; ++x) m[x][0] = m[x][1] = kLowest, l[x][0] = l[x][1] = 0.f;
+        const int before = q.L - q.T;
+        for (int i = 0; i < n; ++i) {
+            fetch(i + kStages - 1);
+            cp_wait<kStages - 1>();
+            const uint32_t bit = 1u << (i % kStages);
+            if (bad & bit) {  // nothing is read of its scores either
+                bad &= ~bit;
+                continue;
+            }
             float x[NT][4];
-            qf.scores(k, smem, lane, x);
-            const int j = j0 + 16 * tile + r;
-            const bool edge = j0 + 16 * tile + 15 > before;  // some column does not see all of the tile
+            qf.scores(mine + (i % kStages) * (Few<T, D>::kTileBytes / 16), lane, x);
+            const int j = 16 * (p.tile + i) + r;
+            const bool edge = 16 * (p.tile + i) + 15 > before;  // some column does not see all of the tile
+            float* to = a.scores + (unit * a.max_len + j) * a.width + 2 * c;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (8 * n + 2 * c >= a.width) continue;
+            for (int y = 0; y < NT; ++y) {
+                if (8 * y + 2 * c >= a.width) continue;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float s0 = x[n][i] * a.scale_log2, s1 = x[n][2 + i] * a.scale_log2;
+                for (int k = 0; k < 2; ++k) {
+                    float s0 = x[y][k] * a.scale_log2, s1 = x[y][2 + k] * a.scale_log2;
                     if (edge) {
-                        const int last = before + (8 * n + 2 * c + i) / a.G;
+                        const int last = before + (early ? (8 * y + 2 * c + k) / a.G : 0);
                         if (j > last) s0 = -INFINITY;
                         if (j + 8 > last) s1 = -INFINITY;
                     }
-                    const float top = fmaxf(m[n][i], fmaxf(s0, s1));
-                    l[n][i] = l[n][i] * ex2(m[n][i] - top) + ex2(s0 - top) + ex2(s1 - top);
-                    m[n][i] = top;
-                    x[n][i] = s0, x[n][2 + i] = s1;
+                    const float top = fmaxf(m[y][k], fmaxf(s0, s1));
+                    l[y][k] = l[y][k] * ex2(m[y][k] - top) + ex2(s0 - top) + ex2(s1 - top);
+                    m[y][k] = top;
+                    x[y][k] = s0, x[y][2 + k] = s1;
                 }
-                float* to = out + int64_t(16 * tile + r) * a.width + 8 * n + 2 * c;
-                if (j < q.L) *reinterpret_cast<float2*>(to) = make_float2(x[n][0], x[n][1]);
-                if (j + 8 < q.L) *reinterpret_cast<float2*>(to + 8 * a.width) = make_float2(x[n][2], x[n][3]);
+                if (j < q.L) *reinterpret_cast<float2*>(to + 8 * y) = make_float2(x[y][0], x[y][1]);
+                if (j + 8 < q.L) *reinterpret_cast<float2*>(to + 8 * (a.width + y)) = make_float2(x[y][2], x[y][3]);
             }
         }
+        cp_wait<0>();
+        // the piece's number in its head: the workers' that begin before it there
+        const int64_t first = id - p.tile;
+        const int64_t piece = worker - first / share;
+        float2* out = a.pieces + (unit * a.max_pieces + piece) * a.width + 2 * c;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int y = 0; y < NT; ++y)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int k = 0; k < 2; ++k) {
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1)
-                    join(m[n][i], l[n][i], __shfl_xor_sync(0xffffffffu, m[n][i], o),
-                         __shfl_xor_sync(0xffffffffu, l[n][i], o));
-                if (r == 0) joined[warp][8 * n + 2 * c + i] = make_float2(m[n][i], l[n][i]);
+                    join(m[y][k], l[y][k], __shfl_xor_sync(0xffffffffu, m[y][k], o),
+                         __shfl_xor_sync(0xffffffffu, l[y][k], o));
+                if (r == 0 && 8 * y + 2 * c < a.width) out[8 * y + k] = make_float2(m[y][k], l[y][k]);
             }
-        __syncthreads();
-        if (tid < a.width) {
-            float2 x = joined[0][tid];
-            for (int w = 1; w < kFewWarps; ++w) join(x.x, x.y, joined[w][tid].x, joined[w][tid].y);
-            a.pieces[(unit * ((a.max_len + 63) / 64) + p.chunk) * a.width + tid] = x;
-        }
-        __syncthreads();
-        if (id + 1 < id1) next_place(a, p, id + 1, keys, lane);
+        id += n;
     }
 }
 
-// Weights from scores: blocks of 128 keys in equal runs, a key to a thread.
-__global__ void __launch_bounds__(kFewThr) few_fold(const KwArgs a, const int ctas) {
-    __shared__ float2 joined[kFewWarps][kFewCols];
-    __shared__ float2 stats[kFewCols];
-    pdl_wait_primary();
-    pdl_launch_dependents();
+// Weights from scores: tiles of 128 keys in equal runs, a key to a thread and
+// kFoldAhead tiles at a time.  NP pairs of columns.
+template <int NP> __global__ void __launch_bounds__(kFoldThr) few_fold(const KwArgs a, const int workers) {
+    __shared__ float2 joined[kFoldThr / 32][kFewCols];
+    __shared__ float2 stats[2 * NP];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int keys = chunk_keys(all_chunks(a, 64, lane), ctas);
-    const int64_t total = all_chunks(a, kFoldKeys, lane);
-    const int64_t share = (total + gridDim.x - 1) / gridDim.x;
-    const int64_t id0 = share * blockIdx.x, id1 = min(total, id0 + share);
-    if (id0 >= id1) return;
-    Place p = place_of(a, id0, kFoldKeys, lane);
-    KwSeq q = {};
-    int at_s = -1, at_g = -1;
-    for (int64_t id = id0; id < id1; ++id) {
-        if (p.s != at_s) q = seq_of(a, p.s);
+    // the lengths were there before the scores' kernel let this one start
+    const int64_t fine = all_tiles(a, 16, lane), fine_share = share_of(fine, workers, kMinShare);
+    const int64_t total = all_tiles(a, kFoldKeys, lane), share = share_of(total, gridDim.x, 1);
+    const int64_t id1 = min(total, share * (blockIdx.x + 1));
+    bool waited = false;
+    for (int64_t id = share * blockIdx.x; id < id1;) {
+        const Place p = place_of(a, id, kFoldKeys, lane);
+        const KwSeq q = seq_of(a, p.s);
+        const int n = int(min(int64_t(p.tiles - p.tile), id1 - id));
         const int64_t unit = int64_t(p.s) * a.Hkv + p.g;
-        const int cols = q.T * a.G;
-        if (p.s != at_s || p.g != at_g) {
-            const int n = (q.L + keys - 1) / keys;
-            const float2* from = a.pieces + unit * ((a.max_len + 63) / 64) * a.width;
-            float m = kLowest, l = 0.f;
-            if (lane < cols)
-                for (int i = warp; i < n; i += kFewWarps) {
-                    const float2 x = from[int64_t(i) * a.width + lane];
-                    join(m, l, x.x, x.y);
-                }
-            __syncthreads();
-            if (lane < cols) joined[warp][lane] = make_float2(m, l);
-            __syncthreads();
-            if (tid < cols) {
-                float2 x = joined[0][tid];
-                for (int w = 1; w < kFewWarps; ++w) join(x.x, x.y, joined[w][tid].x, joined[w][tid].y);
-                stats[tid] = make_float2(x.x, reciprocal(x.y));
-            }
-            __syncthreads();
+        const int cols = q.T * a.G, before = q.L - q.T;
+        // the head's pieces: of the workers that its first and its last tile belong to, and those between
+        int64_t first = 0;
+        {
+            int64_t sum = 0;
+            for (int s = lane; s < p.s; s += 32) sum += int64_t(tiles_of(a, s, 16)) * a.Hkv;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            first = sum + int64_t(p.g) * ((q.L + 15) / 16);
         }
-        at_s = p.s, at_g = p.g;
-        const int j = p.chunk * kFoldKeys + tid, before = q.L - q.T;
-        if (j < q.L) {
-            float* to = a.weights + unit * a.slots + j;
-            const int pg = a.block_tables[int64_t(p.s) * a.max_blocks + (j >> a.page_shift)];
-            float w = 0.f;
-            if (pg >= 0 && pg < a.num_pages) {
-                const float* x = a.scores + (unit * a.max_len + j) * a.width;
-                for (int col = 0; col < cols; col += 2) {
-                    const float2 y = *reinterpret_cast<const float2*>(x + col);
-                    if (j <= before + col / a.G) w += ex2(y.x - stats[col].x) * stats[col].y;
-                    if (col + 1 < cols && j <= before + (col + 1) / a.G)
-                        w += ex2(y.y - stats[col + 1].x) * stats[col + 1].y;
-                }
-            }
-            if (a.decay > 0.f && j < before) w += a.decay * *to;
-            *to = w;
+        const int pieces = int((first + (q.L + 15) / 16 - 1) / fine_share - first / fine_share) + 1;
+        if (!waited) {
+            pdl_wait_primary();
+            pdl_launch_dependents();
+            waited = true;
         }
-        if (id + 1 < id1) next_place(a, p, id + 1, kFoldKeys, lane);
+        const float2* from = a.pieces + unit * a.max_pieces * a.width;
+        float m = kLowest, l = 0.f;
+        if (lane < cols)
+            for (int i = warp; i < pieces; i += kFoldThr / 32) {
+                const float2 x = from[int64_t(i) * a.width + lane];
+                join(m, l, x.x, x.y);
+            }
+        __syncthreads();
+        if (lane < cols) joined[warp][lane] = make_float2(m, l);
+        __syncthreads();
+        if (tid < 2 * NP) {
+            float2 x = tid < cols ? joined[0][tid] : make_float2(0.f, 0.f);
+            if (tid < cols)
+                for (int w = 1; w < kFoldThr / 32; ++w) join(x.x, x.y, joined[w][tid].x, joined[w][tid].y);
+            stats[tid] = make_float2(x.x, reciprocal(x.y));
+        }
+        __syncthreads();
+        float2 st[2 * NP];
+#pragma unroll
+        for (int i = 0; i < 2 * NP; ++i) st[i] = stats[i];
+        const float* x0 = a.scores + unit * a.max_len * a.width;
+        float* w0 = a.weights + unit * a.slots;
+        const int32_t* table = a.block_tables + int64_t(p.s) * a.max_blocks;
+        for (int i = 0; i < n; i += kFoldAhead) {
+            float2 x[kFoldAhead][NP];
+            float old[kFoldAhead];
+            int page[kFoldAhead];
+#pragma unroll
+            for (int u = 0; u < kFoldAhead; ++u) {
+                const int j = (p.tile + i + u) * kFoldKeys + tid;
+                const bool in = i + u < n && j < q.L;
+                page[u] = in ? table[j >> a.page_shift] : -1;
+                old[u] = in && a.decay > 0.f && j < before ? w0[j] : 0.f;
+#pragma unroll
+                for (int k = 0; k < NP; ++k)
+                    x[u][k] = in && 2 * k < a.width
+                                  ? *reinterpret_cast<const float2*>(x0 + int64_t(j) * a.width + 2 * k)
+                                  : make_float2(0.f, 0.f);
+            }
+#pragma unroll
+            for (int u = 0; u < kFoldAhead; ++u) {
+                const int j = (p.tile + i + u) * kFoldKeys + tid;
+                if (i + u >= n || j >= q.L) continue;
+                float w = 0.f;
+                if (page[u] >= 0 && page[u] < a.num_pages) {
+                    const int sees = (j - before) * a.G;  // the columns from this one on see the key
+#pragma unroll
+                    for (int k = 0; k < NP; ++k) {
+                        if (2 * k < cols && 2 * k >= sees) w += ex2(x[u][k].x - st[2 * k].x) * st[2 * k].y;
+                        if (2 * k + 1 < cols && 2 * k + 1 >= sees) w += ex2(x[u][k].y - st[2 * k + 1].x) * st[2 * k + 1].y;
+                    }
+                }
+                w0[j] = w + a.decay * old[u];
+            }
+        }
+        id += n;
+    }
+    if (!waited) pdl_wait_primary();  // nor may the kernel behind this one start early
+}
+
+template <typename T, int D, int NT> cudaError_t launch_few(const KwArgs& a, int sms, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e =
+        allow_shared_memory(reinterpret_cast<const void*>(few_scores<T, D, NT>), Few<T, D>::kSmem, done);
+    if (e != cudaSuccess) return e;
+    const int ctas = sms * Few<T, D>::kPerSm, workers = ctas * kFewWarps;
+    e = launch_pdl(few_scores<T, D, NT>, dim3(ctas), dim3(kFewThr), Few<T, D>::kSmem, st, a);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(sms * kFoldPerSm), block(kFoldThr);
+    switch (a.width / 2) {
+        case 1: return launch_pdl(few_fold<1>, grid, block, 0, st, a, workers);
+        case 2: return launch_pdl(few_fold<2>, grid, block, 0, st, a, workers);
+        case 3: return launch_pdl(few_fold<3>, grid, block, 0, st, a, workers);
+        case 4: return launch_pdl(few_fold<4>, grid, block, 0, st, a, workers);
+        default: return a.width <= 16 ? launch_pdl(few_fold<8>, grid, block, 0, st, a, workers)
+                                      : launch_pdl(few_fold<16>, grid, block, 0, st, a, workers);
     }
 }
 
-template <typename T, int D, int NT> cudaError_t launch_few(const KwArgs& a, int ctas, cudaStream_t st) {
-    const size_t smem = std::is_same<T, float>::value ? 8 * NT * D * sizeof(float) : 0;  // 16 KB at most
-    const cudaError_t e = launch_pdl(few_scores<T, D, NT>, dim3(ctas), dim3(kFewThr), smem, st, a);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(few_fold, dim3(ctas), dim3(kFewThr), 0, st, a, ctas);
-}
-
-template <typename T> cudaError_t launch_few_of(const KwArgs& a, int D, int ctas, cudaStream_t st) {
+template <typename T> cudaError_t launch_few_of(const KwArgs& a, int D, int sms, cudaStream_t st) {
     if (D == 64)
-        return a.width <= 8    ? launch_few<T, 64, 1>(a, ctas, st)
-               : a.width <= 16 ? launch_few<T, 64, 2>(a, ctas, st)
-                               : launch_few<T, 64, 4>(a, ctas, st);
-    return a.width <= 8    ? launch_few<T, 128, 1>(a, ctas, st)
-           : a.width <= 16 ? launch_few<T, 128, 2>(a, ctas, st)
-                           : launch_few<T, 128, 4>(a, ctas, st);
+        return a.width <= 8    ? launch_few<T, 64, 1>(a, sms, st)
+               : a.width <= 16 ? launch_few<T, 64, 2>(a, sms, st)
+                               : launch_few<T, 64, 4>(a, sms, st);
+    return a.width <= 8    ? launch_few<T, 128, 1>(a, sms, st)
+           : a.width <= 16 ? launch_few<T, 128, 2>(a, sms, st)
+                           : launch_few<T, 128, 4>(a, sms, st);
 }
 
 // ---- CUDA cores: 64 columns x 64 keys to a tile ---------------------------------
@@ -592,6 +661,8 @@ size_t rounded(size_t n) { return (n + 255) & ~size_t(255); }
 int64_t columns(const KeyWeightsCall& c) { return int64_t(c.r.max_rows) * (c.Hq / c.Hkv); }
 int few_width(const KeyWeightsCall& c) { return int(columns(c) + 1) / 2 * 2; }
 size_t few_units(const KeyWeightsCall& c) { return size_t(c.r.num_seqs) * c.Hkv; }
+// Parts of a head: of kMinShare tiles at least, but for the first and the last.
+size_t few_pieces(const KeyWeightsCall& c) { return size_t((c.max_len + 15) / 16) / kMinShare + 2; }
 size_t few_scores_bytes(const KeyWeightsCall& c) {
     return rounded(few_units(c) * c.max_len * few_width(c) * sizeof(float));
 }
@@ -600,7 +671,7 @@ size_t few_scores_bytes(const KeyWeightsCall& c) {
 
 size_t key_weights_workspace_bytes(const KeyWeightsCall& c) {
     if (columns(c) <= kFewCols)
-        return few_scores_bytes(c) + rounded(few_units(c) * ((c.max_len + 63) / 64) * few_width(c) * sizeof(float2));
+        return few_scores_bytes(c) + rounded(few_units(c) * few_pieces(c) * few_width(c) * sizeof(float2));
     return rounded(size_t(c.r.total_rows) * c.Hq * sizeof(float2));
 }
 
@@ -616,6 +687,7 @@ cudaError_t launch_key_weights(const KeyWeightsCall& c, cudaStream_t st) {
     a.scores = static_cast<float*>(c.workspace);
     a.pieces = reinterpret_cast<float2*>(static_cast<char*>(c.workspace) + (columns(c) <= kFewCols ? few_scores_bytes(c) : 0));
     a.width = columns(c) <= kFewCols ? few_width(c) : 0;
+    a.max_pieces = int64_t(few_pieces(c));
     a.dev_status = c.dev_status;
     a.q_stride = c.r.q_stride;
     a.page_stride = c.c.page_stride;
@@ -636,10 +708,9 @@ cudaError_t launch_key_weights(const KeyWeightsCall& c, cudaStream_t st) {
     a.scale_log2 = c.scale_log2;
     a.decay = c.decay;
     if (columns(c) <= kFewCols) {
-        const int ctas = c.n_ctas * kFewPerSm;
-        if (c.dtype == PA_F32) return launch_few_of<float>(a, c.D, ctas, st);
-        return c.dtype == PA_F16 ? launch_few_of<__half>(a, c.D, ctas, st)
-                                 : launch_few_of<__nv_bfloat16>(a, c.D, ctas, st);
+        if (c.dtype == PA_F32) return launch_few_of<float>(a, c.D, c.n_ctas, st);
+        return c.dtype == PA_F16 ? launch_few_of<__half>(a, c.D, c.n_ctas, st)
+                                 : launch_few_of<__nv_bfloat16>(a, c.D, c.n_ctas, st);
     }
     if (c.dtype == PA_F32) return c.D == 64 ? launch_tiles<float, 64>(a, st) : launch_tiles<float, 128>(a, st);
     if (c.dtype == PA_F16) return c.D == 64 ? launch_tiles<__half, 64>(a, st) : launch_tiles<__half, 128>(a, st);
