@@ -141,8 +141,10 @@ template <typename T, int D> struct Few {
     static constexpr int kPerSm = kTileBytes <= 4096 ? 4 : 2;  // CTAs: 192 KB of slots an SM at most
 };
 
-__device__ inline void cp_async16(uint32_t to, const void* from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+// K passes through L2 as the first to leave it: the scores are to be there still.
+__device__ inline void cp_async16(uint32_t to, const void* from, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "l"(policy)
+                 : "memory");
 }
 __device__ inline void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ inline void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -244,6 +246,7 @@ __global__ void __launch_bounds__(kFewThr, Few<T, D>::kPerSm) few_scores(const K
     int64_t id = share * worker;
     uint4* mine = slots + warp * (kStages * Few<T, D>::kTileBytes / 16);
     const uint32_t mine_u32 = smem_u32(mine);
+    const uint64_t policy = l2_policy_evict_first();
     const bool early = a.max_rows > 1;  // rows that do not see all keys
     while (id < id1) {  // a head's part of the run
         const Place p = place_of(a, id, 16, lane);
@@ -278,8 +281,8 @@ __global__ void __launch_bounds__(kFewThr, Few<T, D>::kPerSm) few_scores(const K
                     const uint32_t to = mine_u32 + (i % kStages) * Few<T, D>::kTileBytes + 16 * lane;
 #pragma unroll
                     for (int u = 0; u < Few<T, D>::kUnits; ++u) {
-                        cp_async16(to + 1024 * u, lo + 4 * u);
-                        cp_async16(to + 1024 * u + 512, hi + 4 * u);
+                        cp_async16(to + 1024 * u, lo + 4 * u, policy);
+                        cp_async16(to + 1024 * u + 512, hi + 4 * u, policy);
                     }
                 } else {
                     bad |= 1u << (i % kStages);
