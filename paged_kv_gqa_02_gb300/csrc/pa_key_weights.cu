@@ -12,60 +12,13 @@
 // Many columns: the second pass computes the scores again.
 #include "pa_device.h"
 #include "pa_ptx.cuh"
-#include "pa_rows.cuh"
-#include "pa_serving.h"
+#include "pa_key_weights.h"
 
 #include <type_traits>
 
 namespace pa {
 
 namespace {
-
-constexpr float kLowest = -3.402823466e38f;  // the running maximum before the first score
-
-struct KwArgs {
-    const void* q;
-    const void* k;
-    const int32_t* cu_lens;
-    const int32_t* block_tables;
-    const int32_t* context_lens;
-    float* weights;
-    float2* stats;  // [total_rows][Hq]: a column's largest score and the reciprocal of its sum
-    float* scores;  // few columns: [num_seqs][Hkv][max_len][width]
-    float2* pieces; // few columns: [num_seqs][Hkv][max_pieces][width], largest score and sum of a warp's part
-    int32_t width;  // of a key's scores, the columns rounded up to even
-    int64_t max_pieces;
-    uint32_t* dev_status;
-    int64_t q_stride, page_stride, token_stride, head_stride;
-    int64_t slots;  // of a block table
-    int32_t num_seqs, total_rows, max_rows, num_pages, max_blocks, page_size, page_shift;
-    int32_t Hq, Hkv, G, max_len;
-    float scale_log2, decay;
-};
-
-struct KwSeq {
-    int row0, T, L;
-    bool bad;
-};
-__device__ inline KwSeq seq_of(const KwArgs& a, int s) {
-    KwSeq q;
-    q.row0 = a.cu_lens[s];
-    const int r1 = a.cu_lens[s + 1];
-    q.L = a.context_lens[s];
-    q.T = r1 - q.row0;
-    q.bad = bad_rows(q.row0, r1, a.total_rows, a.max_rows) || q.L < q.T || q.L > a.max_len;
-    if (q.bad) q.T = 0;
-    return q;
-}
-
-// 1 / l, and 0 for a column that saw nothing (a NaN stays one).
-__device__ inline float reciprocal(float l) { return l == 0.f ? 0.f : 1.f / l; }
-
-__device__ inline void join(float& m, float& l, float m2, float l2) {
-    const float top = fmaxf(m, m2);
-    l = l * ex2(m - top) + l2 * ex2(m2 - top);
-    m = top;
-}
 
 // ---- few columns ----------------------------------------------------------------
 // The keys of each (sequence, kv head) in tiles of 16 (a page or half of one),
@@ -93,7 +46,7 @@ struct Place {
 
 __device__ inline int tiles_of(const KwArgs& a, int s, int keys) {
     if (s >= a.num_seqs) return 0;
-    const KwSeq q = seq_of(a, s);
+    const KwSeq q = kw_seq(a, s);
     return q.T > 0 ? (q.L + keys - 1) / keys : 0;
 }
 // All tiles of the call (whole warp).
@@ -237,7 +190,7 @@ __global__ void __launch_bounds__(kFewThr, Few<T, D>::kPerSm) few_scores(const K
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & 3, r = lane >> 2;
     if (blockIdx.x == 0)
         for (int s = tid; s < a.num_seqs; s += kFewThr)
-            if (seq_of(a, s).bad) flag(a.dev_status, PA_DEV_BAD_LEN);
+            if (kw_seq(a, s).bad) flag(a.dev_status, PA_DEV_BAD_LEN);
     const int workers = int(gridDim.x) * kFewWarps;
     // the first CTAs' warps first, so that a small call's warps lie on different SMs
     const int worker = warp * int(gridDim.x) + int(blockIdx.x);
@@ -250,7 +203,7 @@ __global__ void __launch_bounds__(kFewThr, Few<T, D>::kPerSm) few_scores(const K
     const bool early = a.max_rows > 1;  // rows that do not see all keys
     while (id < id1) {  // a head's part of the run
         const Place p = place_of(a, id, 16, lane);
-        const KwSeq q = seq_of(a, p.s);
+        const KwSeq q = kw_seq(a, p.s);
         const int n = int(min(int64_t(p.tiles - p.tile), id1 - id));
         const int64_t unit = int64_t(p.s) * a.Hkv + p.g;
         const int32_t* table = a.block_tables + int64_t(p.s) * a.max_blocks;
@@ -296,7 +249,7 @@ __global__ void __launch_bounds__(kFewThr, Few<T, D>::kPerSm) few_scores(const K
         qf.load(a, q, p.g, lane);
         float m[NT][2], l[NT][2];
 #pragma unroll
-        for (int x = 0; x < NT; ++x) m[x][0] = m[x][1] = kLowest, l[x][0] = l[x][1] = 0.f;
+        for (int x = 0; x < NT; ++x) m[x][0] = m[x][1] = kLowestScore, l[x][0] = l[x][1] = 0.f;
         const int before = q.L - q.T;
         for (int i = 0; i < n; ++i) {
             fetch(i + kStages - 1);
@@ -342,7 +295,7 @@ __global__ void __launch_bounds__(kFewThr, Few<T, D>::kPerSm) few_scores(const K
             for (int k = 0; k < 2; ++k) {
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1)
-                    join(m[y][k], l[y][k], __shfl_xor_sync(0xffffffffu, m[y][k], o),
+                    kw_join(m[y][k], l[y][k], __shfl_xor_sync(0xffffffffu, m[y][k], o),
                          __shfl_xor_sync(0xffffffffu, l[y][k], o));
                 if (r == 0 && 8 * y + 2 * c < a.width) out[8 * y + k] = make_float2(m[y][k], l[y][k]);
             }
@@ -363,7 +316,7 @@ template <int NP> __global__ void __launch_bounds__(kFoldThr) few_fold(const KwA
     bool waited = false;
     for (int64_t id = share * blockIdx.x; id < id1;) {
         const Place p = place_of(a, id, kFoldKeys, lane);
-        const KwSeq q = seq_of(a, p.s);
+        const KwSeq q = kw_seq(a, p.s);
         const int n = int(min(int64_t(p.tiles - p.tile), id1 - id));
         const int64_t unit = int64_t(p.s) * a.Hkv + p.g;
         const int cols = q.T * a.G, before = q.L - q.T;
@@ -383,11 +336,11 @@ template <int NP> __global__ void __launch_bounds__(kFoldThr) few_fold(const KwA
             waited = true;
         }
         const float2* from = a.pieces + unit * a.max_pieces * a.width;
-        float m = kLowest, l = 0.f;
+        float m = kLowestScore, l = 0.f;
         if (lane < cols)
             for (int i = warp; i < pieces; i += kFoldThr / 32) {
                 const float2 x = from[int64_t(i) * a.width + lane];
-                join(m, l, x.x, x.y);
+                kw_join(m, l, x.x, x.y);
             }
         __syncthreads();
         if (lane < cols) joined[warp][lane] = make_float2(m, l);
@@ -395,8 +348,8 @@ template <int NP> __global__ void __launch_bounds__(kFoldThr) few_fold(const KwA
         if (tid < 2 * NP) {
             float2 x = tid < cols ? joined[0][tid] : make_float2(0.f, 0.f);
             if (tid < cols)
-                for (int w = 1; w < kFoldThr / 32; ++w) join(x.x, x.y, joined[w][tid].x, joined[w][tid].y);
-            stats[tid] = make_float2(x.x, reciprocal(x.y));
+                for (int w = 1; w < kFoldThr / 32; ++w) kw_join(x.x, x.y, joined[w][tid].x, joined[w][tid].y);
+            stats[tid] = make_float2(x.x, kw_reciprocal(x.y));
         }
         __syncthreads();
         float2 st[2 * NP];
@@ -471,7 +424,7 @@ template <typename T> cudaError_t launch_few_of(const KwArgs& a, int D, int sms,
                            : launch_few<T, 128, 4>(a, sms, st);
 }
 
-// ---- CUDA cores: 64 columns x 64 keys to a tile ---------------------------------
+// ---- many columns, fp32: CUDA cores, 64 columns x 64 keys to a tile ---------------------------------
 constexpr int kThr = 256;
 constexpr int kTile = 64;
 
@@ -534,7 +487,7 @@ template <typename T, int D> __global__ void __launch_bounds__(kThr) kw_stats(co
     pdl_wait_primary();
     pdl_launch_dependents();
     const int s = blockIdx.z, g = blockIdx.y, c0 = int(blockIdx.x) * kTile;
-    const KwSeq q = seq_of(a, s);
+    const KwSeq q = kw_seq(a, s);
     if (q.bad && g == 0 && blockIdx.x == 0 && threadIdx.x == 0) flag(a.dev_status, PA_DEV_BAD_LEN);
     const int cols = q.T * a.G;
     if (c0 >= cols) return;
@@ -550,7 +503,7 @@ template <typename T, int D> __global__ void __launch_bounds__(kThr) kw_stats(co
     for (int i = 0; i < 4; ++i) {
         const int c = c0 + ty + 16 * i;
         last[i] = c < cols ? q.L - q.T + c / a.G : -1;
-        m[i] = kLowest;
+        m[i] = kLowestScore;
         l[i] = 0.f;
     }
     const int end = q.L - q.T + min(cols - 1, c0 + kTile - 1) / a.G + 1;
@@ -587,7 +540,7 @@ template <typename T, int D> __global__ void __launch_bounds__(kThr) kw_stats(co
         }
         const int c = c0 + ty + 16 * i, t = c / a.G;
         if (tx == 0 && c < cols)
-            a.stats[int64_t(q.row0 + t) * a.Hq + g * a.G + c - t * a.G] = make_float2(m[i], reciprocal(l[i]));
+            a.stats[int64_t(q.row0 + t) * a.Hq + g * a.G + c - t * a.G] = make_float2(m[i], kw_reciprocal(l[i]));
     }
 }
 
@@ -601,7 +554,7 @@ template <typename T, int D> __global__ void __launch_bounds__(kThr) kw_gather(c
     pdl_wait_primary();
     pdl_launch_dependents();
     const int s = blockIdx.z, g = blockIdx.y, j0 = int(blockIdx.x) * kTile;
-    const KwSeq q = seq_of(a, s);
+    const KwSeq q = kw_seq(a, s);
     if (q.T == 0 || j0 >= q.L) return;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int cols = q.T * a.G, before = q.L - q.T;
@@ -666,6 +619,7 @@ int few_width(const KeyWeightsCall& c) { return int(columns(c) + 1) / 2 * 2; }
 size_t few_units(const KeyWeightsCall& c) { return size_t(c.r.num_seqs) * c.Hkv; }
 // Parts of a head: of kMinShare tiles at least, but for the first and the last.
 size_t few_pieces(const KeyWeightsCall& c) { return size_t((c.max_len + 15) / 16) / kMinShare + 2; }
+size_t stats_bytes(const KeyWeightsCall& c) { return rounded(size_t(c.r.total_rows) * c.Hq * sizeof(float2)); }
 size_t few_scores_bytes(const KeyWeightsCall& c) {
     return rounded(few_units(c) * c.max_len * few_width(c) * sizeof(float));
 }
@@ -675,7 +629,7 @@ size_t few_scores_bytes(const KeyWeightsCall& c) {
 size_t key_weights_workspace_bytes(const KeyWeightsCall& c) {
     if (columns(c) <= kFewCols)
         return few_scores_bytes(c) + rounded(few_units(c) * few_pieces(c) * few_width(c) * sizeof(float2));
-    return rounded(size_t(c.r.total_rows) * c.Hq * sizeof(float2));
+    return stats_bytes(c) + (c.dtype == PA_F32 ? 0 : rounded(key_weights_tc_parts(c.n_ctas)));
 }
 
 cudaError_t launch_key_weights(const KeyWeightsCall& c, cudaStream_t st) {
@@ -710,14 +664,14 @@ cudaError_t launch_key_weights(const KeyWeightsCall& c, cudaStream_t st) {
     a.max_len = c.max_len;
     a.scale_log2 = c.scale_log2;
     a.decay = c.decay;
+    a.debug_timeout = c.debug_timeout;
     if (columns(c) <= kFewCols) {
         if (c.dtype == PA_F32) return launch_few_of<float>(a, c.D, c.n_ctas, st);
         return c.dtype == PA_F16 ? launch_few_of<__half>(a, c.D, c.n_ctas, st)
                                  : launch_few_of<__nv_bfloat16>(a, c.D, c.n_ctas, st);
     }
     if (c.dtype == PA_F32) return c.D == 64 ? launch_tiles<float, 64>(a, st) : launch_tiles<float, 128>(a, st);
-    if (c.dtype == PA_F16) return c.D == 64 ? launch_tiles<__half, 64>(a, st) : launch_tiles<__half, 128>(a, st);
-    return c.D == 64 ? launch_tiles<__nv_bfloat16, 64>(a, st) : launch_tiles<__nv_bfloat16, 128>(a, st);
+    return launch_key_weights_tc(a, c.dtype, c.D, c.n_ctas, static_cast<char*>(c.workspace) + stats_bytes(c), st);
 }
 
 }  // namespace pa

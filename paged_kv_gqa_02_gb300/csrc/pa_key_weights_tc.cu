@@ -1,0 +1,638 @@
+// pa_key_weights_tc.cu -- key weights of many columns (rows x heads) of a
+// 16-bit type, on the tensor cores.
+//
+// Both passes multiply a tile A of 128 rows, which stays, with tiles B of 128
+// rows that stream past it, and reduce along B.  A is on the accumulator's 128
+// lanes, so a thread reduces its own lane's columns and nothing crosses lanes:
+//   statistics: A = 128 columns (128 / G rows of q, all G heads of the kv
+//               head), B = the keys; a running maximum and sum a lane
+//   gathering:  A = 128 keys, B = the columns; sum of 2^(s - m) / l a lane
+// So Q K^T is computed twice, and no score leaves the SM.
+//
+// Two CTAs an SM, each with four warps for the scores, one that loads (TMA) and
+// one that multiplies (two accumulators of 128 columns of tensor memory): while
+// one CTA begins or ends a unit, the other computes.  Exponentials bound the
+// kernel: a score takes a multiply-add, an exponential and an addition in each
+// pass, and 128 x 128 of them take longer than their product.
+//
+// Units (an A tile with all its B tiles) are laid on a line, sequence by
+// sequence and kv head by kv head, each as long as it costs, and the line is cut
+// into equal shares, one a CTA.  Causal units get longer or shorter along the
+// sequence; the i-th is followed by the i-th from the end, so that a pair's
+// length is the same for all of them and a place on the line is found by
+// division.  A unit inside one share is finished there; the pieces of others
+// are joined in ascending order by a kernel of its own.
+#include <type_traits>
+
+#include "pa_device.h"
+#include "pa_key_weights.h"
+#include "pa_tc.cuh"
+#include "pa_tmap.h"
+
+namespace pa {
+
+namespace {
+
+constexpr int kTile = 128;
+constexpr int kThr = 192;
+constexpr int kLoadWarp = 4, kMmaWarp = 5;
+constexpr int kPerSm = 2;          // CTAs
+constexpr int kStart = 2;          // what beginning and ending a unit costs, in B tiles
+constexpr int kMinShare = 4;
+constexpr uint32_t kHalf = kTile * 128;  // bytes of 64 dims of a tile
+constexpr uint32_t kNegInf = 0xff800000u;
+constexpr uint64_t kWaitNs = 2000000000ull;  // a role gives up after 2 s on one barrier
+constexpr uint32_t kSleepNs = 20000;
+
+template <int D> struct Smem {
+    static constexpr int kStages = D == 128 ? 2 : 4;
+    static constexpr uint32_t kTileBytes = kTile * D * 2;
+    static constexpr uint32_t kB = kTileBytes;
+    static constexpr uint32_t kStats = kB + kStages * kTileBytes;  // [2][64] of (-m, -m', 1/l, 1/l')
+    static constexpr uint32_t kLimits = kStats + 2 * 64 * 16;      // [2][128] last key that a column sees
+    static constexpr uint32_t kChunks = kLimits + 2 * 128 * 4;     // [2][4][2] lowest and highest of 32 columns'
+    static constexpr uint32_t kBars = kChunks + 2 * 4 * 2 * 4;
+    static constexpr int kNumBars = 2 + 2 * kStages + 6 + 1;
+    static constexpr uint32_t kBytes = 1024 + kBars + kNumBars * 8 + 16;
+};
+
+struct WideArgs {
+    KwArgs a;
+    int32_t tq, workers, head_first;
+    float2* parts_stats;  // [2 workers][128]
+    float* parts_sums;    // [2 workers][128]
+};
+
+// ---- the line of units ------------------------------------------------------------
+struct Line {
+    int T, L, before, row0;
+    int flat, tri;      // units of equal length, then units in pairs
+    int flat_cost;
+    int64_t pair, len;  // positions of a pair, of a kv head
+};
+
+// Length of unit u.
+template <int kPass> __device__ inline int tiles_of(const WideArgs& w, const Line& q, int u) {
+    if (kPass == 0) return (q.before + min(q.T, (u + 1) * w.tq) + kTile - 1) / kTile;
+    return (q.T + w.tq - 1) / w.tq - max(0, kTile * u - q.before) / w.tq;
+}
+// The first B tile of unit u.
+template <int kPass> __device__ inline int first_of(const WideArgs& w, const Line& q, int u) {
+    return kPass == 0 ? 0 : max(0, kTile * u - q.before) / w.tq;
+}
+
+template <int kPass> __device__ inline Line line_of(const WideArgs& w, int s) {
+    Line q = {};
+    if (s >= w.a.num_seqs) return q;
+    const KwSeq k = kw_seq(w.a, s);
+    q.T = k.T;
+    q.L = k.L;
+    q.row0 = k.row0;
+    q.before = k.L - k.T;
+    if (k.T == 0) return q;
+    const int nq = (k.T + w.tq - 1) / w.tq, nk = (k.L + kTile - 1) / kTile;
+    if (kPass == 0) {
+        q.tri = nq;
+        // the sum of two floors is at most the floor of the sum
+        q.pair = 2 * kStart + (2 * int64_t(q.before) + int64_t(nq + 1) * w.tq + 2 * (kTile - 1)) / kTile;
+    } else {
+        q.flat = int(min(int64_t(nk), (int64_t(q.before) + w.tq - 1) / kTile + 1));
+        q.flat_cost = kStart + nq;
+        q.tri = nk - q.flat;
+        q.pair = 2 * kStart + 2 * int64_t(nq) + 1 -
+                 (int64_t(kTile) * (2 * int64_t(q.flat) + q.tri - 1) - 2 * int64_t(q.before)) / w.tq;
+    }
+    q.len = int64_t(q.flat) * q.flat_cost + int64_t((q.tri + 1) / 2) * q.pair;
+    return q;
+}
+template <int kPass> __device__ inline int64_t line_total(const WideArgs& w, int lane) {
+    int64_t n = 0;
+    for (int s = lane; s < w.a.num_seqs; s += 32) n += line_of<kPass>(w, s).len * w.a.Hkv;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    return n;
+}
+
+// A unit, or its part in a share: B tiles [b0, b1).
+struct Part {
+    Line q;
+    int s, g, unit;
+    int64_t begin, end;  // the unit on the line
+    int b0, b1;
+    bool begins, whole;
+};
+
+// The part of the share's end [x, x1) that lies in the unit at x (whole warp);
+// moves x behind it.  False where there is no tile in it.
+template <int kPass>
+__device__ inline bool next_part(const WideArgs& w, int64_t& x, int64_t x1, int lane, Part& p) {
+    // the sequence and the place in it
+    int64_t in = x;
+    int s = 0;
+    for (int s0 = 0;; s0 += 32) {
+        const int64_t n = line_of<kPass>(w, s0 + lane).len * w.a.Hkv;
+        int64_t v = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        const unsigned m = __ballot_sync(0xffffffffu, in < v);
+        if (m) {
+            const int l = __ffs(m) - 1;
+            s = s0 + l;
+            in -= __shfl_sync(0xffffffffu, v - n, l);
+            break;
+        }
+        in -= __shfl_sync(0xffffffffu, v, 31);
+        if (s0 + 32 >= w.a.num_seqs) {  // x is below the total, so this is not reached
+            x = x1;
+            return false;
+        }
+    }
+    p.q = line_of<kPass>(w, s);
+    p.s = s;
+    p.g = int(in / p.q.len);
+    int64_t off = in - int64_t(p.g) * p.q.len;
+    const int64_t flat_len = int64_t(p.q.flat) * p.q.flat_cost;
+    int tiles;
+    if (off < flat_len) {
+        p.unit = int(off / p.q.flat_cost);
+        off -= int64_t(p.unit) * p.q.flat_cost;
+        tiles = p.q.flat_cost - kStart;
+    } else {
+        off -= flat_len;
+        const int i = int(off / p.q.pair), j = p.q.tri - 1 - i;
+        off -= int64_t(i) * p.q.pair;
+        // the longer one first
+        const int u0 = p.q.flat + (kPass == 0 ? j : i), u1 = p.q.flat + (kPass == 0 ? i : j);
+        p.unit = u0;
+        tiles = tiles_of<kPass>(w, p.q, u0);
+        if (off >= kStart + tiles) {
+            off -= kStart + tiles;
+            p.unit = u1;
+            tiles = i == j ? -kStart : tiles_of<kPass>(w, p.q, u1);
+            if (off >= kStart + tiles) {  // behind the pair's units
+                x += p.q.pair - (off + (kStart + tiles_of<kPass>(w, p.q, u0)));
+                return false;
+            }
+        }
+    }
+    p.begin = x - off;
+    p.end = p.begin + kStart + tiles;
+    p.begins = off == 0;
+    const int64_t stop = min(p.end, x1);
+    p.whole = p.begins && stop == p.end;
+    const int first = first_of<kPass>(w, p.q, p.unit);
+    p.b0 = first + int(max(int64_t(0), off - kStart));
+    p.b1 = first + int(max(int64_t(0), stop - p.begin - kStart));
+    x = stop;
+    return p.b1 > p.b0;
+}
+
+// ---- waits ------------------------------------------------------------------------
+__device__ inline bool wait_bar(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        if (mbar_try_wait_sleep(bar, parity, kSleepNs)) return true;
+        if (*abort_flag || globaltimer_ns() - t0 > kWaitNs) return false;
+    }
+}
+__device__ inline bool wait_warp(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag));
+}
+__device__ inline void raise_abort(volatile uint32_t* abort_flag, uint32_t* dev_status) {
+    *abort_flag = 1u;
+    flag(dev_status, PA_DEV_TIMEOUT);
+}
+
+__device__ inline float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ inline uint64_t f2_pack(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ inline uint64_t f2_pack(uint32_t lo, uint32_t hi) {
+    return f2_pack(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ inline float2 f2_unpack(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ inline uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ inline uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// 32 scores of a lane: the running maximum (base 2, scaled) and sum.
+__device__ inline void take(float& m, uint64_t& l, const uint32_t (&r)[32], float scale) {
+    float top = __uint_as_float(r[0]);
+#pragma unroll
+    for (int i = 1; i < 31; i += 2) top = max3(top, __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+    top = fmaxf(top, __uint_as_float(r[31])) * scale;
+    if (top > m) {
+        const float down = ex2(m - top);
+        const float2 old = f2_unpack(l);
+        l = f2_pack(old.x * down, old.y * down);
+        m = top;
+    }
+    const uint64_t k = f2_pack(scale, scale), minus = f2_pack(-m, -m);
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        const float2 x = f2_unpack(f2_fma(f2_pack(r[i], r[i + 1]), k, minus));
+        l = f2_add(l, f2_pack(ex2(x.x), ex2(x.y)));
+    }
+}
+
+template <int kPass, typename T, int D>
+__global__ void __launch_bounds__(kThr, kPerSm)
+    wide_pass(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+              const __grid_constant__ WideArgs w) {
+    using S = Smem<D>;
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr int kStages = S::kStages, kHalves = D / 64;
+    const KwArgs& a = w.a;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(base + S::kBars);
+    uint64_t* a_full = bars;
+    uint64_t* a_empty = bars + 1;
+    uint64_t* b_full = bars + 2;
+    uint64_t* b_empty = b_full + kStages;
+    uint64_t* s_full = b_empty + kStages;
+    uint64_t* s_empty = s_full + 2;
+    uint64_t* st_full = s_empty + 2;  // gathering: the columns' statistics written
+    uint64_t* never = st_full + 2;  // never arrived on: the debug_timeout wait
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + S::kNumBars);
+    volatile uint32_t* abort_flag = tslot + 1;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        mbar_init(a_full, 1);
+        mbar_init(a_empty, 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&b_full[i], 1);
+            mbar_init(&b_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_empty[i], 4);
+            mbar_init(&st_full[i], 4);
+        }
+        mbar_init(never, 1);
+        *abort_flag = 0u;
+        mbar_fence_init();
+    }
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    if (kPass == 0 && blockIdx.x == 0)
+        for (int s = tid; s < a.num_seqs; s += kThr)
+            if (kw_seq(a, s).bad) flag(a.dev_status, PA_DEV_BAD_LEN);
+    const int64_t total = line_total<kPass>(w, lane);
+    int64_t share = (total + w.workers - 1) / w.workers;
+    if (share < kMinShare) share = kMinShare;
+    const int64_t x0 = share * blockIdx.x, x1 = min(total, x0 + share);
+    if (x0 >= x1) return;  // the whole CTA, before any barrier
+    if (warp == kMmaWarp) {
+        tc::tmem_alloc(tslot, 256);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tm = *tslot;
+    if (a.debug_timeout) {
+        // Testing: a wait that runs out before any copy is issued aborts every role.
+        if (tid == 0 && !mbar_wait_ns(never, 0, 0)) raise_abort(abort_flag, a.dev_status);
+        __syncthreads();
+    }
+    bool ok = !*abort_flag;
+    const int P = a.page_size, PT = kTile / P;
+
+    if (warp == kLoadWarp) {
+        const uint32_t q_bytes = uint32_t(kHalves) * 128u * uint32_t(a.G * w.tq);
+        auto load_q = [&](uint8_t* dst, uint64_t* bar, const Part& p, int i) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, q_bytes);
+                for (int h = 0; h < kHalves; ++h)
+                    tma_load_3d(dst + h * kHalf, &tmQ, bar, 64 * h, p.g * a.G, p.q.row0 + i * w.tq);
+            }
+            __syncwarp();
+        };
+        auto load_k = [&](uint8_t* dst, uint64_t* bar, const Part& p, int j) {
+            // lane l: page l of the tile; none: beyond the tensor, so that the box reads as zeros
+            int pg = a.num_pages;
+            const int at = j * PT + lane;
+            if (lane < PT && at * P < p.q.L) {
+                const int e = a.block_tables[int64_t(p.s) * a.max_blocks + at];
+                if (e >= 0 && e < a.num_pages)
+                    pg = e;
+                else if (kPass == 0)
+                    flag(a.dev_status, PA_DEV_BAD_PAGE);
+            }
+            if (lane == 0) mbar_arrive_expect_tx(bar, S::kTileBytes);
+            __syncwarp();
+            if (lane < PT)
+                for (int h = 0; h < kHalves; ++h)
+                    tma_load_4d(dst + h * kHalf + lane * P * 128, &tmK, bar, 64 * h, w.head_first ? p.g : 0,
+                                w.head_first ? 0 : p.g, pg);
+        };
+        int n = 0, parts = 0;
+        Part p;
+        for (int64_t x = x0; ok && x < x1;) {
+            if (!next_part<kPass>(w, x, x1, lane, p)) continue;
+            if (parts) ok = wait_warp(a_empty, (parts - 1) & 1, abort_flag);
+            if (!ok) break;
+            if (kPass == 0)
+                load_q(base, a_full, p, p.unit);
+            else
+                load_k(base, a_full, p, p.unit);
+            ++parts;
+            for (int b = p.b0; b < p.b1; ++b, ++n) {
+                const int st = n % kStages;
+                if (n >= kStages) ok = wait_warp(&b_empty[st], ((n / kStages) - 1) & 1, abort_flag);
+                if (!ok) break;
+                uint8_t* dst = base + S::kB + st * S::kTileBytes;
+                if (kPass == 0)
+                    load_k(dst, &b_full[st], p, b);
+                else
+                    load_q(dst, &b_full[st], p, b);
+            }
+        }
+        if (lane == 0) {
+            if (!ok) raise_abort(abort_flag, a.dev_status);
+            // never leave the CTA with copies in flight
+            for (int i = max(0, n - kStages); i < n; ++i) mbar_wait_ns(&b_full[i % kStages], (i / kStages) & 1, kWaitNs);
+            if (parts) mbar_wait_ns(a_full, (parts - 1) & 1, kWaitNs);
+        }
+    } else if (warp == kMmaWarp) {
+        const uint32_t idesc = tc::idesc_f16(kTile, kTile, kBf16, false), hi = tc::desc_hi_sw128(1024);
+        const uint32_t a_lo = tc::desc_lo(smem_u32(base), 16), b_lo = tc::desc_lo(smem_u32(base + S::kB), 16);
+        int n = 0, parts = 0;
+        Part p;
+        for (int64_t x = x0; ok && x < x1;) {
+            if (!next_part<kPass>(w, x, x1, lane, p)) continue;
+            ok = wait_warp(a_full, parts & 1, abort_flag);
+            ++parts;
+            for (int b = p.b0; ok && b < p.b1; ++b, ++n) {
+                const int st = n % kStages, buf = n & 1;
+                ok = wait_warp(&b_full[st], (n / kStages) & 1, abort_flag);
+                if (ok && n >= 2) ok = wait_warp(&s_empty[buf], ((n >> 1) - 1) & 1, abort_flag);
+                if (!ok) break;
+                tc::fence_after_sync();
+                const uint32_t bx = b_lo + st * (S::kTileBytes >> 4);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+                    tc::mma_ss_elect(tm + 128 * buf, tc::make_desc(a_lo + off, hi), tc::make_desc(bx + off, hi), idesc,
+                                     ks > 0);
+                }
+                tc::commit_elect(&b_empty[st]);
+                if (b + 1 == p.b1) tc::commit_elect(a_empty);
+                tc::commit_elect(&s_full[buf]);
+            }
+        }
+        if (!ok && lane == 0) raise_abort(abort_flag, a.dev_status);
+    } else {
+        float4* sm_stats = reinterpret_cast<float4*>(base + S::kStats);
+        int* sm_limits = reinterpret_cast<int*>(base + S::kLimits);
+        int* sm_chunks = reinterpret_cast<int*>(base + S::kChunks);
+        const uint32_t lanes = uint32_t(warp) << 21;  // tensor-memory lanes 32 warp ..
+        const int cols = w.tq * a.G;
+        const int my_t = tid / a.G, my_h = tid - my_t * a.G;
+        int n = 0;
+        Part p;
+        for (int64_t x = x0; ok && x < x1;) {
+            if (!next_part<kPass>(w, x, x1, lane, p)) continue;
+            float m = kLowestScore, sum = 0.f;
+            uint64_t acc = 0;  // two sums
+            const int32_t* table = a.block_tables + int64_t(p.s) * a.max_blocks;
+            // statistics: the lane's column; gathering: the lane's key
+            const int t = p.unit * w.tq + my_t;
+            const bool real = kPass == 0 && tid < cols && t < p.q.T;
+            const int last = p.q.before + t;
+            const int key = kTile * p.unit + tid;
+            bool there = false;
+            if (kPass == 1 && key < p.q.L) {
+                const int pg = table[key >> a.page_shift];
+                there = pg >= 0 && pg < a.num_pages;
+            }
+            auto column = [&](int b) {  // the statistics of the thread's column of Q tile b
+                const int tt = b * w.tq + my_t;
+                float2 st = make_float2(0.f, 0.f);
+                if (tid < cols && tt < p.q.T) st = a.stats[int64_t(p.q.row0 + tt) * a.Hq + p.g * a.G + my_h];
+                return st;
+            };
+            auto pages = [&](int b) {  // a lane of PT: whether the tile's page is in the pool
+                const int at = b * PT + lane;
+                int pg = -1;
+                if (lane < PT && at * P < p.q.L) pg = table[at];
+                return pg;
+            };
+            float2 ahead = make_float2(0.f, 0.f);
+            int page_ahead = -1;
+            if (kPass == 1)
+                ahead = column(p.b0);
+            else
+                page_ahead = pages(p.b0);
+            for (int b = p.b0; b < p.b1; ++b, ++n) {
+                const int buf = n & 1;
+                uint32_t page_bits = 0;
+                if (kPass == 1) {
+                    const int tt = b * w.tq + my_t;
+                    const int lim = ahead.y != 0.f ? p.q.before + tt : -1;  // a NaN counts as seen
+                    float* st = reinterpret_cast<float*>(sm_stats + 64 * buf + tid / 2);
+                    st[tid & 1] = -ahead.x;
+                    st[2 + (tid & 1)] = ahead.y;
+                    sm_limits[128 * buf + tid] = lim;
+                    const int low = __reduce_min_sync(0xffffffffu, lim), high = __reduce_max_sync(0xffffffffu, lim);
+                    if (lane == 0) {
+                        sm_chunks[8 * buf + 2 * warp] = low;
+                        sm_chunks[8 * buf + 2 * warp + 1] = high;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&st_full[buf]);
+                    if (b + 1 < p.b1) ahead = column(b + 1);
+                    ok = wait_warp(&st_full[buf], (n >> 1) & 1, abort_flag);
+                    if (!ok) break;
+                } else {
+                    page_bits = __ballot_sync(0xffffffffu, page_ahead >= 0 && page_ahead < a.num_pages);
+                    if (b + 1 < p.b1) page_ahead = pages(b + 1);
+                }
+                ok = wait_warp(&s_full[buf], (n >> 1) & 1, abort_flag);
+                if (!ok) break;
+                tc::fence_after_sync();
+                uint32_t r[2][32];
+                tc::ld_32x32b_x32(tm + 128 * buf + lanes, r[0]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tc::wait_ld();
+                    tc::reg_fence(r[c & 1]);
+                    if (c < 3)
+                        tc::ld_32x32b_x32(tm + 128 * buf + 32 * (c + 1) + lanes, r[(c + 1) & 1]);
+                    else {
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s_empty[buf]);
+                    }
+                    uint32_t(&v)[32] = r[c & 1];
+                    if (kPass == 0) {
+                        // keys 32 c .. 32 c + 31 of the tile: seen by all lanes, or a bit for each
+                        const int k0 = kTile * b + 32 * c;
+                        const uint32_t mine = P == 32 ? (page_bits >> c) & 1u : (page_bits >> (2 * c)) & 3u;
+                        const bool all = mine == (P == 32 ? 1u : 3u) && k0 + 31 <= p.q.before + p.unit * w.tq;
+                        if (!all) {
+                            const int seen = last - k0 + 1;
+                            uint32_t bits = seen >= 32 ? 0xffffffffu : seen <= 0 ? 0u : (1u << seen) - 1u;
+                            bits &= P == 32 ? (mine ? 0xffffffffu : 0u)
+                                            : ((mine & 1u) ? 0xffffu : 0u) | ((mine & 2u) ? 0xffff0000u : 0u);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = (bits >> i) & 1u ? v[i] : kNegInf;
+                        }
+                        take(m, acc, v, a.scale_log2);
+                    } else {
+                        const int low = sm_chunks[8 * buf + 2 * c], high = sm_chunks[8 * buf + 2 * c + 1];
+                        if (high < kTile * p.unit) continue;  // no column sees a key of the tile
+                        const float4* st = sm_stats + 64 * buf + 16 * c;
+                        const uint64_t k = f2_pack(a.scale_log2, a.scale_log2);
+                        if (low >= kTile * p.unit + kTile - 1) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                const float4 y = st[i / 2];
+                                const float2 e = f2_unpack(f2_fma(f2_pack(v[i], v[i + 1]), k, f2_pack(y.x, y.y)));
+                                acc = f2_fma(f2_pack(ex2(e.x), ex2(e.y)), f2_pack(y.z, y.w), acc);
+                            }
+                        } else {
+                            const int* lim = sm_limits + 128 * buf + 32 * c;
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                const float4 y = st[i / 2];
+                                const float2 e = f2_unpack(f2_fma(f2_pack(v[i], v[i + 1]), k, f2_pack(y.x, y.y)));
+                                if (key <= lim[i]) sum += ex2(e.x) * y.z;
+                                if (key <= lim[i + 1]) sum += ex2(e.y) * y.w;
+                            }
+                        }
+                    }
+                }
+            }
+            if (!ok) break;
+            const float2 two = f2_unpack(acc);
+            if (kPass == 0) {
+                const float l = two.x + two.y;
+                if (p.whole) {
+                    if (real)
+                        a.stats[int64_t(p.q.row0 + t) * a.Hq + p.g * a.G + my_h] = make_float2(m, kw_reciprocal(l));
+                } else {
+                    w.parts_stats[(2 * int64_t(blockIdx.x) + p.begins) * kTile + tid] = make_float2(m, l);
+                }
+            } else {
+                sum += two.x + two.y;
+                if (!there) sum = 0.f;
+                if (!p.whole) {
+                    w.parts_sums[(2 * int64_t(blockIdx.x) + p.begins) * kTile + tid] = sum;
+                } else if (key < p.q.L) {
+                    float* to = a.weights + (int64_t(p.s) * a.Hkv + p.g) * a.slots + key;
+                    if (a.decay > 0.f && key < p.q.before) sum += a.decay * *to;
+                    *to = sum;
+                }
+            }
+        }
+        if (!ok && lane == 0) raise_abort(abort_flag, a.dev_status);
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tm, 256);
+    }
+}
+
+// A CTA for each share: the unit that begins in it and ends behind it.
+template <int kPass> __global__ void __launch_bounds__(kTile) wide_join(const __grid_constant__ WideArgs w) {
+    const KwArgs& a = w.a;
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int64_t total = line_total<kPass>(w, lane);
+    int64_t share = (total + w.workers - 1) / w.workers;
+    if (share < kMinShare) share = kMinShare;
+    const int64_t x0 = share * blockIdx.x, x1 = min(total, x0 + share);
+    if (x1 >= total) return;
+    // the unit at the share's last place
+    int64_t x = x1 - 1;
+    Part p;
+    p.end = 0;
+    next_part<kPass>(w, x, x1, lane, p);
+    if (p.end <= x1 || p.begin < x0) return;  // none, whole, or another CTA's
+    float m = kLowestScore, l = 0.f;
+    for (int64_t i = blockIdx.x; i * share < p.end; ++i) {
+        if (min(p.end, (i + 1) * share) <= p.begin + kStart) continue;  // no tile in this share
+        const int64_t slot = (2 * i + (i == blockIdx.x)) * kTile + tid;
+        if (kPass == 0)
+            kw_join(m, l, w.parts_stats[slot].x, w.parts_stats[slot].y);
+        else
+            l += w.parts_sums[slot];
+    }
+    if (kPass == 0) {
+        const int t = p.unit * w.tq + tid / a.G;
+        if (tid < w.tq * a.G && t < p.q.T)
+            a.stats[int64_t(p.q.row0 + t) * a.Hq + p.g * a.G + tid % a.G] = make_float2(m, kw_reciprocal(l));
+    } else {
+        const int key = kTile * p.unit + tid;
+        if (key < p.q.L) {
+            float* to = a.weights + (int64_t(p.s) * a.Hkv + p.g) * a.slots + key;
+            if (a.decay > 0.f && key < p.q.before) l += a.decay * *to;
+            *to = l;
+        }
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_wide(const CUtensorMap& mq, const CUtensorMap& mk, const WideArgs& w, cudaStream_t st) {
+    static std::atomic<uint64_t> done0{0}, done1{0};
+    constexpr size_t smem = Smem<D>::kBytes;
+    cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(wide_pass<0, T, D>), smem, done0);
+    if (e == cudaSuccess) e = allow_shared_memory(reinterpret_cast<const void*>(wide_pass<1, T, D>), smem, done1);
+    if (e == cudaSuccess) e = launch_pdl(wide_pass<0, T, D>, dim3(w.workers), dim3(kThr), smem, st, mq, mk, w);
+    if (e == cudaSuccess) e = launch_pdl(wide_join<0>, dim3(w.workers), dim3(kTile), 0, st, w);
+    if (e == cudaSuccess) e = launch_pdl(wide_pass<1, T, D>, dim3(w.workers), dim3(kThr), smem, st, mq, mk, w);
+    if (e == cudaSuccess) e = launch_pdl(wide_join<1>, dim3(w.workers), dim3(kTile), 0, st, w);
+    return e;
+}
+
+}  // namespace
+
+size_t key_weights_tc_parts(int n_ctas) {
+    return size_t(2 * kPerSm) * n_ctas * kTile * (sizeof(float2) + sizeof(float));
+}
+
+cudaError_t launch_key_weights_tc(const KwArgs& a, pa_dtype dt, int D, int n_ctas, void* parts, cudaStream_t st) {
+    WideArgs w = {};
+    w.a = a;
+    w.tq = kTile / a.G;
+    w.workers = kPerSm * n_ctas;
+    w.head_first = a.head_stride <= a.token_stride;
+    w.parts_stats = static_cast<float2*>(parts);
+    w.parts_sums = reinterpret_cast<float*>(w.parts_stats + size_t(2) * w.workers * kTile);
+    CUtensorMap mq, mk;
+    if (!tmap_rows(&mq, dt, a.q, D, a.Hq, a.total_rows, a.q_stride, a.G, w.tq) ||
+        !tmap_pages(&mk, dt, a.k, D, a.Hkv, a.page_size, a.num_pages, a.head_stride, a.token_stride, a.page_stride,
+                    w.head_first))
+        return cudaErrorInvalidValue;
+    if (dt == PA_BF16)
+        return D == 64 ? launch_wide<__nv_bfloat16, 64>(mq, mk, w, st) : launch_wide<__nv_bfloat16, 128>(mq, mk, w, st);
+    return D == 64 ? launch_wide<__half, 64>(mq, mk, w, st) : launch_wide<__half, 128>(mq, mk, w, st);
+}
+
+}  // namespace pa
