@@ -26,6 +26,7 @@
 
 #include "pa_device.h"
 #include "pa_key_weights.h"
+#include "pa_pairs.cuh"
 #include "pa_tc.cuh"
 #include "pa_tmap.h"
 
@@ -212,28 +213,8 @@ __device__ inline float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-__device__ inline uint64_t f2_pack(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ inline uint64_t f2_pack(uint32_t lo, uint32_t hi) {
-    return f2_pack(__uint_as_float(lo), __uint_as_float(hi));
-}
-__device__ inline float2 f2_unpack(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ inline uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ inline uint64_t f2_add(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
+__device__ inline uint64_t pair_of(uint32_t lo, uint32_t hi) {
+    return pairs::pack(__uint_as_float(lo), __uint_as_float(hi));
 }
 
 // 32 scores of a lane: the running maximum (base 2, scaled) and sum.
@@ -244,15 +225,15 @@ __device__ inline void take(float& m, uint64_t& l, const uint32_t (&r)[32], floa
     top = fmaxf(top, __uint_as_float(r[31])) * scale;
     if (top > m) {
         const float down = ex2(m - top);
-        const float2 old = f2_unpack(l);
-        l = f2_pack(old.x * down, old.y * down);
+        const float2 old = pairs::unpack(l);
+        l = pairs::pack(old.x * down, old.y * down);
         m = top;
     }
-    const uint64_t k = f2_pack(scale, scale), minus = f2_pack(-m, -m);
+    const uint64_t k = pairs::pack(scale, scale), minus = pairs::pack(-m, -m);
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
-        const float2 x = f2_unpack(f2_fma(f2_pack(r[i], r[i + 1]), k, minus));
-        l = f2_add(l, f2_pack(ex2(x.x), ex2(x.y)));
+        const float2 x = pairs::unpack(pairs::fma(pair_of(r[i], r[i + 1]), k, minus));
+        l = pairs::add(l, pairs::pack(ex2(x.x), ex2(x.y)));
     }
 }
 
@@ -505,20 +486,20 @@ __global__ void __launch_bounds__(kThr, kPerSm)
                         const int low = sm_chunks[8 * buf + 2 * c], high = sm_chunks[8 * buf + 2 * c + 1];
                         if (high < kTile * p.unit) continue;  // no column sees a key of the tile
                         const float4* st = sm_stats + 64 * buf + 16 * c;
-                        const uint64_t k = f2_pack(a.scale_log2, a.scale_log2);
+                        const uint64_t k = pairs::pack(a.scale_log2, a.scale_log2);
                         if (low >= kTile * p.unit + kTile - 1) {
 #pragma unroll
                             for (int i = 0; i < 32; i += 2) {
                                 const float4 y = st[i / 2];
-                                const float2 e = f2_unpack(f2_fma(f2_pack(v[i], v[i + 1]), k, f2_pack(y.x, y.y)));
-                                acc = f2_fma(f2_pack(ex2(e.x), ex2(e.y)), f2_pack(y.z, y.w), acc);
+                                const float2 e = pairs::unpack(pairs::fma(pair_of(v[i], v[i + 1]), k, pairs::pack(y.x, y.y)));
+                                acc = pairs::fma(pairs::pack(ex2(e.x), ex2(e.y)), pairs::pack(y.z, y.w), acc);
                             }
                         } else {
                             const int* lim = sm_limits + 128 * buf + 32 * c;
 #pragma unroll
                             for (int i = 0; i < 32; i += 2) {
                                 const float4 y = st[i / 2];
-                                const float2 e = f2_unpack(f2_fma(f2_pack(v[i], v[i + 1]), k, f2_pack(y.x, y.y)));
+                                const float2 e = pairs::unpack(pairs::fma(pair_of(v[i], v[i + 1]), k, pairs::pack(y.x, y.y)));
                                 if (key <= lim[i]) sum += ex2(e.x) * y.z;
                                 if (key <= lim[i + 1]) sum += ex2(e.y) * y.w;
                             }
@@ -527,7 +508,7 @@ __global__ void __launch_bounds__(kThr, kPerSm)
                 }
             }
             if (!ok) break;
-            const float2 two = f2_unpack(acc);
+            const float2 two = pairs::unpack(acc);
             if (kPass == 0) {
                 const float l = two.x + two.y;
                 if (p.whole) {

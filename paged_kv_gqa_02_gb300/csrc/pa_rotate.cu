@@ -8,8 +8,10 @@
 // chosen so that both dims of a pair are its own (the runs lie rotary_dim / 2
 // apart, or beside one another where neighbours turn together): the rotation
 // needs no exchange, and a call may write over its input.  Only the norm's sum
-// crosses the D / 16 lanes of a head.  A warp has the loads of kAhead groups of
-// heads in flight.  Rows of V pass through the same loop untouched.
+// crosses the D / 16 lanes of a head.  Heads go in groups as wide as a warp, q's
+// first, then k's and v's; the next groups' loads are in flight while a group is
+// turned, in paired fp32 arithmetic.
+#include "pa_pairs.cuh"
 #include "pa_ptx.cuh"
 #include "pa_rows.cuh"
 #include "pa_serving.h"
@@ -19,7 +21,6 @@ namespace pa {
 namespace {
 
 constexpr int kThr = 256;
-constexpr int kAhead = 2;  // groups of heads whose loads a warp has in flight
 
 struct RotateArgs {
     const uint4* q;
@@ -40,7 +41,7 @@ struct RotateArgs {
     int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;  // 16-byte units
     int64_t page_stride, token_stride, head_stride;
     int32_t num_seqs, total_rows, max_rows, num_pages, max_blocks, page_size;
-    int32_t Hq, Hkv, heads;  // heads: Hq + Hkv, and Hkv of V with a store
+    int32_t Hq, Hkv;
     int32_t rot, table_rows, axes, end0, end1;  // pairs below end0 follow axis 0, below end1 axis 1
     int32_t parts;  // warps of a row
     float eps;
@@ -83,6 +84,7 @@ template <typename T, int D, bool kMixed> __global__ void __launch_bounds__(kThr
     constexpr int kLanes = D / 16;         // lanes of a head
     constexpr int kHeads = 32 / kLanes;    // heads of a warp at a time
     constexpr int kHeadUnits = D / kVec;   // 16-byte units of a head
+    constexpr int kAhead = kVec / 4;       // groups whose loads are in flight: 64 bytes a lane
     pdl_wait_primary();
     pdl_launch_dependents();
     if (blockIdx.x == 0) flag_bad_rows(a.cu_lens, a.num_seqs, a.total_rows, a.max_rows, a.dev_status);
@@ -109,7 +111,7 @@ template <typename T, int D, bool kMixed> __global__ void __launch_bounds__(kThr
     // cosines and sines of the lane's eight pairs, the same for every head
     const int sub = lane & (kLanes - 1), half = a.rot / 2;
     const bool turns = sub < a.rot / 16;
-    float cs[8], sn[8];
+    uint64_t cs[4], sn[4];  // of pairs 2 i and 2 i + 1
     int pos[3];
     bool off = false;
 #pragma unroll
@@ -125,25 +127,28 @@ template <typename T, int D, bool kMixed> __global__ void __launch_bounds__(kThr
         if (a.axes == 1) {
             const float* t = a.table + int64_t(pos[0]) * a.rot + 8 * sub;
 #pragma unroll
-            for (int i = 0; i < 8; i += 4) {
-                const float4 c = *reinterpret_cast<const float4*>(t + i);
-                const float4 w = *reinterpret_cast<const float4*>(t + half + i);
-                cs[i] = c.x, cs[i + 1] = c.y, cs[i + 2] = c.z, cs[i + 3] = c.w;
-                sn[i] = w.x, sn[i + 1] = w.y, sn[i + 2] = w.z, sn[i + 3] = w.w;
+            for (int i = 0; i < 2; ++i) {
+                const float4 c = *reinterpret_cast<const float4*>(t + 4 * i);
+                const float4 z = *reinterpret_cast<const float4*>(t + half + 4 * i);
+                cs[2 * i] = pairs::pack(c.x, c.y), cs[2 * i + 1] = pairs::pack(c.z, c.w);
+                sn[2 * i] = pairs::pack(z.x, z.y), sn[2 * i + 1] = pairs::pack(z.z, z.w);
             }
         } else {
+            float c[8], z[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int pair = 8 * sub + i;
                 const int where = pair < a.end0 ? pos[0] : pair < a.end1 ? pos[1] : pos[2];
                 const float* t = a.table + int64_t(where) * a.rot + pair;
-                cs[i] = t[0];
-                sn[i] = t[half];
+                c[i] = t[0];
+                z[i] = t[half];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                cs[i] = pairs::pack(c[2 * i], c[2 * i + 1]);
+                sn[i] = pairs::pack(z[2 * i], z[2 * i + 1]);
             }
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
     }
     // the lane's two runs of eight dims, in 16-byte units
     const int turning = a.rot / 16;
@@ -158,91 +163,119 @@ template <typename T, int D, bool kMixed> __global__ void __launch_bounds__(kThr
         else if (lane == 0)
             flag(a.dev_status, PA_DEV_BAD_PAGE);
     }
+    // groups of heads: q's, k's and, with a store, v's
+    const int nq = (a.Hq + kHeads - 1) / kHeads, nk = (a.Hkv + kHeads - 1) / kHeads;
+    const int groups = nq + nk + (a.k_cache ? nk : 0), mine = lane / kLanes;
+    const int g0 = int(int64_t(groups) * part / a.parts), g1 = int(int64_t(groups) * (part + 1) / a.parts);
     const uint4* qr = a.q + row * a.q_stride;
     const uint4* kr = a.k + row * a.k_stride;
     const uint4* vr = a.v + row * a.v_stride;
-    const int groups = (a.heads + kHeads - 1) / kHeads;
-    const int g0 = int(int64_t(groups) * part / a.parts), g1 = int(int64_t(groups) * (part + 1) / a.parts);
-    for (int g = g0; g < g1; g += kAhead) {
-        uint4 raw[kAhead][kUnits];
+    auto fetch = [&](int g, uint4 (&raw)[kUnits]) {
+        const int h = (g < nq ? g : g < nq + nk ? g - nq : g - nq - nk) * kHeads + mine;
+        if (g < g1 && h < (g < nq ? a.Hq : a.Hkv)) {
+            const uint4* from = (g < nq ? qr : g < nq + nk ? kr : vr) + h * kHeadUnits;
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int h = (g + u) * kHeads + lane / kLanes;
-            if (g + u < g1 && h < a.heads) {
-                const uint4* from = h < a.Hq ? qr + h * kHeadUnits
-                                    : h < a.Hq + a.Hkv ? kr + (h - a.Hq) * kHeadUnits
-                                                       : vr + (h - a.Hq - a.Hkv) * kHeadUnits;
-#pragma unroll
-                for (int i = 0; i < kRun; ++i) {
-                    raw[u][i] = from[run0 + i];
-                    raw[u][kRun + i] = from[run1 + i];
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < kUnits; ++i) raw[u][i] = make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < kRun; ++i) {
+                raw[i] = __ldcs(from + run0 + i);
+                raw[kRun + i] = __ldcs(from + run1 + i);
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) raw[i] = make_uint4(0, 0, 0, 0);
         }
+    };
+    uint4 next[kAhead][kUnits];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) fetch(g0 + u, next[u]);
+    uint64_t w[8];  // the norm's weights of the kind at hand
+    const uint4* held = nullptr;
+    for (int base = g0; base < g1; base += kAhead) {
+        uint4 now[kAhead][kUnits];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) now[u][i] = next[u][i];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) fetch(base + kAhead + u, next[u]);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int h = (g + u) * kHeads + lane / kLanes;
-            const bool real = g + u < g1 && h < a.heads;
-            const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
+            const int g = base + u;
+            if (g >= g1) break;
+            const bool is_q = g < nq, is_k = !is_q && g < nq + nk;
+            const int h = (is_q ? g : is_k ? g - nq : g - nq - nk) * kHeads + mine;
+            const bool real = h < (is_q ? a.Hq : a.Hkv);
             const uint4* weight = is_q ? a.q_weight : is_k ? a.k_weight : nullptr;
-            float x[16];
-            to_f32<T>(raw[u], x);
-            float sum = 0.f;
+            if (weight != nullptr || (is_q || is_k ? half > 0 : false)) {
+                float x[16];
+                to_f32<T>(now[u], x);
+                uint64_t y[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sum = fmaf(x[i], x[i], sum);
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (!real) continue;
-            if (is_q || is_k) {
+                for (int i = 0; i < 8; ++i) y[i] = pairs::pack(x[2 * i], x[2 * i + 1]);
                 if (weight) {
-                    const float inv = 1.f / sqrtf(sum * (1.f / D) + a.eps);
-                    uint4 wr[kUnits];
-                    float w[16];
+                    uint64_t sums = pairs::mul(y[0], y[0]);
 #pragma unroll
-                    for (int i = 0; i < kRun; ++i) {
-                        wr[i] = weight[run0 + i];
-                        wr[kRun + i] = weight[run1 + i];
+                    for (int i = 1; i < 8; ++i) sums = pairs::fma(y[i], y[i], sums);
+                    const float2 two = pairs::unpack(sums);
+                    float sum = two.x + two.y;
+#pragma unroll
+                    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (weight != held) {
+                        uint4 wr[kUnits];
+                        float wf[16];
+#pragma unroll
+                        for (int i = 0; i < kRun; ++i) {
+                            wr[i] = weight[run0 + i];
+                            wr[kRun + i] = weight[run1 + i];
+                        }
+                        to_f32<T>(wr, wf);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) w[i] = pairs::pack(wf[2 * i], wf[2 * i + 1]);
+                        held = weight;
                     }
-                    to_f32<T>(wr, w);
+                    const float inv = 1.f / sqrtf(sum * (1.f / D) + a.eps);
+                    const uint64_t inv2 = pairs::pack(inv, inv);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = x[i] * inv * w[i];
+                    for (int i = 0; i < 8; ++i) y[i] = pairs::mul(pairs::mul(y[i], inv2), w[i]);
                 }
                 if (turns) {
+                    if (kMixed) {  // dims 2 i and 2 i + 1 lie in one pair
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int ia = kMixed ? 2 * i : i, ib = kMixed ? 2 * i + 1 : 8 + i;
-                        const float ya = x[ia], yb = x[ib];
-                        x[ia] = ya * cs[i] - yb * sn[i];
-                        x[ib] = ya * sn[i] + yb * cs[i];
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 v = pairs::unpack(y[i]);
+                            const float2 c = pairs::unpack(cs[i / 2]), z = pairs::unpack(sn[i / 2]);
+                            const float cc = i & 1 ? c.y : c.x, ss = i & 1 ? z.y : z.x;
+                            y[i] = pairs::pack(v.x * cc - v.y * ss, v.x * ss + v.y * cc);
+                        }
+                    } else {  // dims 2 i, 2 i + 1 of both runs
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint64_t ya = y[i], yb = y[4 + i];
+                            y[i] = pairs::fma(ya, cs[i], pairs::mul(yb, pairs::mul(sn[i], pairs::pack(-1.f, -1.f))));
+                            y[4 + i] = pairs::fma(ya, sn[i], pairs::mul(yb, cs[i]));
+                        }
                     }
                 }
-                if (weight || turns) {
 #pragma unroll
-                    for (int i = 0; i < kUnits; ++i) raw[u][i] = pack_vec<T>(x + i * kVec);
+                for (int i = 0; i < 8; ++i) {
+                    const float2 v = pairs::unpack(y[i]);
+                    x[2 * i] = v.x, x[2 * i + 1] = v.y;
                 }
-                uint4* to = is_q ? a.q_out + row * a.q_out_stride + h * kHeadUnits
-                            : a.k_out ? a.k_out + row * a.k_out_stride + (h - a.Hq) * kHeadUnits
-                                      : nullptr;
-                if (to) {
+                if (weight || turns) {  // otherwise the dims are as they were
 #pragma unroll
-                    for (int i = 0; i < kRun; ++i) {
-                        to[run0 + i] = raw[u][i];
-                        to[run1 + i] = raw[u][kRun + i];
-                    }
+                    for (int i = 0; i < kUnits; ++i) now[u][i] = pack_vec<T>(x + i * kVec);
                 }
             }
-            if (!is_q && slot >= 0) {
-                uint4* to = is_k ? a.k_cache + slot + (h - a.Hq) * a.head_stride
-                                 : a.v_cache + slot + (h - a.Hq - a.Hkv) * a.head_stride;
+            if (!real) continue;
+            auto put = [&](uint4* to) {
 #pragma unroll
                 for (int i = 0; i < kRun; ++i) {
-                    to[run0 + i] = raw[u][i];
-                    to[run1 + i] = raw[u][kRun + i];
+                    to[run0 + i] = now[u][i];
+                    to[run1 + i] = now[u][kRun + i];
                 }
-            }
+            };
+            if (is_q) put(a.q_out + row * a.q_out_stride + h * kHeadUnits);
+            if (is_k && a.k_out) put(a.k_out + row * a.k_out_stride + h * kHeadUnits);
+            if (!is_q && slot >= 0) put((is_k ? a.k_cache : a.v_cache) + slot + h * a.head_stride);
         }
     }
 }
@@ -293,7 +326,6 @@ cudaError_t launch_rotate(const RotateCall& c, cudaStream_t st) {
     a.page_size = c.c.page_size;
     a.Hq = c.Hq;
     a.Hkv = c.Hkv;
-    a.heads = c.Hq + c.Hkv + (a.k_cache ? c.Hkv : 0);
     a.rot = c.t.rotary_dim;
     a.table_rows = c.t.table_rows;
     a.axes = c.t.axes;
@@ -301,7 +333,8 @@ cudaError_t launch_rotate(const RotateCall& c, cudaStream_t st) {
     a.end1 = a.end0 + c.t.sections[1];
     a.eps = c.t.eps;
     // a row to a warp, or to several while the warps are fewer than eight an SM
-    const int groups = (a.heads + 512 / c.D - 1) / (512 / c.D);
+    const int wide = 512 / c.D;  // heads of a group
+    const int groups = (c.Hq + wide - 1) / wide + (c.Hkv + wide - 1) / wide * (a.k_cache ? 2 : 1);
     const int want = (152 * 8 + a.total_rows - 1) / a.total_rows;
     a.parts = want < 1 ? 1 : want > groups ? groups : want;
     return c.dtype == PA_F32   ? launch_dim<float>(a, c.D, c.t.interleaved, st)
