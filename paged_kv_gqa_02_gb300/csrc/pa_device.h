@@ -24,4 +24,16 @@ inline cudaError_t allow_shared_memory(const void* kern, size_t bytes, std::atom
     return e;
 }
 
+// Lets `kern` run in clusters of up to 16 CTAs on the current device; `done` as above.
+inline cudaError_t allow_wide_clusters(const void* kern, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
 }  // namespace pa
