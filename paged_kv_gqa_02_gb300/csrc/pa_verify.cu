@@ -17,13 +17,14 @@
 // The walk's time is a chain of passes, each bound by latency: a read of the row
 // (from L2: the first child's row and the random numbers are prefetched while
 // earlier passes run), the exponentials, and one exchange.  For that, every warp
-// leaves its result in the shared memory of every CTA of the cluster; behind one
-// cluster barrier each warp joins all of them in the same order and takes the
-// decisions itself.  Only rank 0 writes.  A second kernel joins the sequences'
+// sends its result to the shared memory of every CTA of the cluster, counted by
+// an mbarrier there; each warp then joins all of them in the same order and takes
+// the decisions itself.  Only rank 0 writes.  A second kernel joins the sequences'
 // lists.
 #include <cooperative_groups.h>
 
 #include "pa_device.h"
+#include "pa_pairs.cuh"
 #include "pa_ptx.cuh"
 #include "pa_rows.cuh"
 #include "pa_serving.h"
@@ -39,6 +40,7 @@ constexpr int kWarps = kThr / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxDrafts = 1024;  // rows of a sequence
 constexpr int kPackThr = 1024;
+constexpr uint64_t kWaitNs = 2000000000ull;  // an exchange gives up after 2 s
 
 // The largest logit and the sum of 2^((x - largest) c); with a NaN or an
 // infinite largest one the sum is not finite.
@@ -46,10 +48,16 @@ struct Stat {
     float top, sum;
 };
 // What a warp found in a pass.
-struct Slot {
+struct __align__(16) Slot {
     Stat p, q;
     float key;  // of the best candidate for the next token, or a sum
     int at;     // where the largest logit (greedy) or the best candidate is
+    int pad[2];
+};
+// A thread's running Stat, the sum in two parts.
+struct Run {
+    float top;
+    uint64_t sum;
 };
 
 // A row of the vocabulary as the threads read it: single elements up to the
@@ -87,31 +95,68 @@ template <typename T> struct Eight {
 
 __device__ inline void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-template <int N> __device__ inline void take(Stat& s, const float (&x)[N], float c) {
-    float top = x[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) top = fmaxf(top, x[i]);
+// 16 bytes to the same place of another CTA's shared memory, counted by its mbarrier.
+__device__ inline void send16(uint32_t to, uint32_t bar, const uint4& v) {
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+        "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar)
+        : "memory");
+}
+__device__ inline uint32_t in_cta(uint32_t addr, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ inline void raise(Run& s, float top, float c) {
     if (top > s.top) {
-        s.sum *= ex2((s.top - top) * c);
+        const float down = ex2((s.top - top) * c);
+        s.sum = pairs::mul(s.sum, pairs::pack(down, down));
         s.top = top;
     }
+}
+__device__ inline void take8(Run& s, const float (&x)[8], float c) {
+    float top = x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top = fmaxf(top, x[i]);
+    raise(s, top, c);
     if (s.top > -INFINITY) {
+        const uint64_t minus = pairs::pack(-s.top, -s.top), c2 = pairs::pack(c, c);
 #pragma unroll
-        for (int i = 0; i < N; ++i) s.sum += ex2((x[i] - s.top) * c);
-    } else {
+        for (int i = 0; i < 8; i += 2) {
+            const float2 e = pairs::unpack(pairs::mul(pairs::add(pairs::pack(x[i], x[i + 1]), minus), c2));
+            s.sum = pairs::add(s.sum, pairs::pack(ex2(e.x), ex2(e.y)));
+        }
+    } else {  // a NaN is not lost
 #pragma unroll
-        for (int i = 0; i < N; ++i) s.sum += x[i] != x[i] ? x[i] : 0.f;
+        for (int i = 0; i < 8; ++i)
+            if (x[i] != x[i]) s.sum = pairs::pack(x[i], x[i]);
     }
 }
-// s over the warp's lanes.
-__device__ inline Stat over_warp(Stat s, float c) {
-    float top = s.top;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // a lane that saw nothing, or only -infinity, adds what it has: 0, or a NaN
-    s.sum = warp_sum(s.top > -INFINITY ? s.sum * ex2((s.top - top) * c) : s.sum);
-    s.top = top;
-    return s;
+__device__ inline void take1(Run& s, float x, float c) {
+    raise(s, x, c);
+    const float e = s.top > -INFINITY ? ex2((x - s.top) * c) : x != x ? x : 0.f;
+    s.sum = pairs::add(s.sum, pairs::pack(e, 0.f));
+}
+
+// The largest of the warp's values, none of them a NaN.
+__device__ inline float max_over_warp(float v) {
+    const int b = __float_as_int(v);
+    const int m = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));  // the order of floats
+    return __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
+}
+// A Stat's sum for another largest value.  One that saw nothing, or -infinity
+// alone, has what it has: 0, or a NaN.
+__device__ inline float sum_at(const Stat& s, float top, float c) {
+    return s.top > -INFINITY ? s.sum * ex2((s.top - top) * c) : s.sum;
+}
+__device__ inline Stat over_warp(const Stat& s, float c) {
+    const float top = max_over_warp(s.top);
+    return Stat{top, warp_sum(sum_at(s, top, c))};
+}
+__device__ inline Stat over_warp(const Run& s, float c) {
+    const float2 two = pairs::unpack(s.sum);
+    return over_warp(Stat{s.top, two.x + two.y}, c);
 }
 __device__ inline bool usable(const Stat& s) {
     return s.top > -INFINITY && s.top < INFINITY && s.sum < INFINITY;  // false for a NaN
@@ -123,14 +168,20 @@ __device__ inline void better(float& key, int& at, float key2, int at2) {
     }
 }
 __device__ inline void better_over_warp(float& key, int& at) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        better(key, at, __shfl_xor_sync(0xffffffffu, key, o), __shfl_xor_sync(0xffffffffu, at, o));
+    const float top = max_over_warp(key);
+    at = __reduce_min_sync(0xffffffffu, key == top ? at : 0x7fffffff);
+    key = top;
+}
+__device__ inline float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(const VerifyCall a) {
     constexpr int kAhead = Elt<T>::kVec / 2;  // units of eight logits whose loads a thread has in flight
     __shared__ Slot inbox[2][kMaxCluster * kWarps];
+    __shared__ uint64_t arrived[2];
     __shared__ int parents[kMaxDrafts], tokens[kMaxDrafts], removed[kMaxDrafts];
     cg::cluster_group cluster = cg::this_cluster();
     const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
@@ -167,20 +218,36 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
         tokens[t] = token;
     }
     if (!greedy) prefetch(reinterpret_cast<const char*>(noise), int64_t(V) * sizeof(float));
-    __syncthreads();
+    const uint32_t bytes = uint32_t(C) * kWarps * sizeof(Slot);  // of an exchange
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&arrived[i], 1);
+            mbar_fence_init();
+            mbar_arrive_expect_tx(&arrived[i], bytes);
+        }
+    }
+    cluster.sync();  // the barriers are there before anyone sends
 
-    int phase = 0;
-    // Leaves the warp's result with every CTA of the cluster; `meanwhile` runs
-    // before the others' have come.  Returns all of them, a slot to be read again
-    // only before the next exchange but one.
+    int turn = 0;
+    bool lost = false;  // an exchange gave up
+    // Sends the warp's result to every CTA of the cluster and waits for all of
+    // theirs; `meanwhile` runs in between.  A place is written again by the
+    // exchange after the next, which nobody begins before all have sent for the
+    // next, and so have read this one.
     auto exchange = [&](const Slot& mine, auto&& meanwhile) -> const Slot* {
-        if (lane < C) *cluster.map_shared_rank(&inbox[phase][rank * kWarps + warp], lane) = mine;
-        asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+        const int at = turn & 1;
+        if (lane < C) {
+            const uint32_t to = in_cta(smem_u32(&inbox[at][rank * kWarps + warp]), lane);
+            const uint32_t bar = in_cta(smem_u32(&arrived[at]), lane);
+            const uint4* v = reinterpret_cast<const uint4*>(&mine);
+            send16(to, bar, v[0]);
+            send16(to + 16, bar, v[1]);
+        }
         meanwhile();
-        asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-        const Slot* all = inbox[phase];
-        phase ^= 1;
-        return all;
+        if (!__all_sync(0xffffffffu, mbar_wait_ns(&arrived[at], (turn >> 1) & 1, kWaitNs))) lost = true;
+        if (tid == 0) mbar_arrive_expect_tx(&arrived[at], bytes);  // for the exchange after the next
+        ++turn;
+        return inbox[at];
     };
     // f(index of eight) and g(index of one) over the row, the cluster's threads in turn
     auto over = [&](const Span& sp, auto&& f, auto&& g) {
@@ -205,11 +272,12 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
         int base = here + 1;
         unsigned children = window(here, base);
         const T* const q_row = draft && children ? draft + int64_t(r0 + here) * a.draft_stride : nullptr;
-        // the lane's child: its logits
-        float x_mine = 0.f, y_mine = 0.f;
+        // the lane's child: its logits and its random number
+        float x_mine = 0.f, y_mine = 0.f, u_mine = 0.f;
         auto look = [&] {
             if ((children >> lane) & 1u) {
                 const int token = tokens[base + lane];
+                u_mine = a.uniform[r0 + base + lane];
                 x_mine = Elt<T>::f(row[token]);
                 if (q_row) y_mine = Elt<T>::f(q_row[token]);
             }
@@ -217,7 +285,8 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
         look();
         const Span sp = span_of(row, V);
         const bool q_wide = q_row && wide_at(q_row + sp.head);
-        Slot mine = {{-INFINITY, 0.f}, {-INFINITY, 0.f}, -INFINITY, V};
+        Slot mine = {{-INFINITY, 0.f}, {-INFINITY, 0.f}, -INFINITY, V, {0, 0}};
+        Run run_p = {-INFINITY, 0}, run_q = {-INFINITY, 0};
         auto first_place = [&](float x, int at) {  // greedy: a thread meets indices in ascending order but for the ends
             if (x > mine.key || (x == mine.key && at < mine.at)) mine.key = x, mine.at = at;
         };
@@ -237,7 +306,7 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
                     if (i + k * workers < sp.units) {
                         float x[8];
                         u[k].get(x);
-                        take<8>(mine.p, x, c);
+                        take8(run_p, x, c);
                         if (greedy) {
                             const int at = sp.head + 8 * (i + k * workers);
 #pragma unroll
@@ -245,21 +314,18 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
                         }
                         if (q_row) {
                             v[k].get(x);
-                            take<8>(mine.q, x, c);
+                            take8(run_q, x, c);
                         }
                     }
             },
             [&](int at) {
-                float x[1] = {Elt<T>::f(row[at])};
-                take<1>(mine.p, x, c);
-                if (greedy) first_place(x[0], at);
-                if (q_row) {
-                    x[0] = Elt<T>::f(q_row[at]);
-                    take<1>(mine.q, x, c);
-                }
+                const float x = Elt<T>::f(row[at]);
+                take1(run_p, x, c);
+                if (greedy) first_place(x, at);
+                if (q_row) take1(run_q, Elt<T>::f(q_row[at]), c);
             });
-        mine.p = over_warp(mine.p, c);
-        if (q_row) mine.q = over_warp(mine.q, c);
+        mine.p = over_warp(run_p, c);
+        if (q_row) mine.q = over_warp(run_q, c);
         if (greedy) better_over_warp(mine.key, mine.at);
         const Slot* all = exchange(mine, [&] {  // the row that the walk most likely goes on to
             if (!children) return;
@@ -268,24 +334,25 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
             if (draft && t + 1 < rows && parents[t + 1] == t)
                 prefetch(reinterpret_cast<const char*>(draft + int64_t(r0 + t) * a.draft_stride), int64_t(V) * sizeof(T));
         });
+        if (lost) break;
+        // the cluster's: the largest values first, then every sum once
         Stat P = {-INFINITY, 0.f}, Q = {-INFINITY, 0.f};
         float top_key = -INFINITY;
         int top_at = V;
         for (int i = lane; i < C * kWarps; i += 32) {
-            const Slot o = all[i];
-            auto join = [&](Stat& x, const Stat& y) {
-                const float top = fmaxf(x.top, y.top);
-                x.sum = (x.top > -INFINITY ? x.sum * ex2((x.top - top) * c) : x.sum) +
-                        (y.top > -INFINITY ? y.sum * ex2((y.top - top) * c) : y.sum);
-                x.top = top;
-            };
-            join(P, o.p);
-            if (q_row) join(Q, o.q);
-            if (greedy) better(top_key, top_at, o.key, o.at);
+            P.top = fmaxf(P.top, all[i].p.top);
+            if (q_row) Q.top = fmaxf(Q.top, all[i].q.top);
+            if (greedy) better(top_key, top_at, all[i].key, all[i].at);
         }
-        P = over_warp(P, c);
-        if (q_row) Q = over_warp(Q, c);
+        P.top = max_over_warp(P.top);
+        if (q_row) Q.top = max_over_warp(Q.top);
         if (greedy) better_over_warp(top_key, top_at);
+        for (int i = lane; i < C * kWarps; i += 32) {
+            P.sum += sum_at(all[i].p, P.top, c);
+            if (q_row) Q.sum += sum_at(all[i].q, Q.top, c);
+        }
+        P.sum = warp_sum(P.sum);
+        if (q_row) Q.sum = warp_sum(Q.sum);
         if (!usable(P) || (q_row && !usable(Q))) {
             if (rank == 0 && tid == 0) flag(a.dev_status, PA_DEV_BAD_VALUE);
             break;
@@ -298,6 +365,7 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
         while (children) {
             const int l = __ffs(children) - 1, t = base + l;
             const float x = __shfl_sync(0xffffffffu, x_mine, l), y = __shfl_sync(0xffffffffu, y_mine, l);
+            const float u = __shfl_sync(0xffffffffu, u_mine, l);
             const int token = tokens[t];
             bool again = false;
             float p = 0.f;
@@ -314,7 +382,7 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
                     again = __any_sync(0xffffffffu, again);
                     p = again ? 0.f : p / mass;
                 }
-                if (p > 0.f && a.uniform[r0 + t] * q < p) went = t;
+                if (p > 0.f && u * q < p) went = t;
             }
             if (went) break;
             children &= children - 1;
@@ -365,6 +433,7 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
                     [&](int at) { rest(Elt<T>::f(row[at]), Elt<T>::f(q_row[at])); });
                 mine.key = warp_sum(sum);
                 const Slot* sums = exchange(mine, [] {});
+                if (lost) break;
                 sum = 0.f;
                 for (int i = lane; i < C * kWarps; i += 32) sum += sums[i].key;
                 sum = warp_sum(sum);
@@ -374,6 +443,7 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
                 }
             }
         }
+        if (lost) break;
         if (went) {
             here = went;
             continue;
@@ -384,22 +454,29 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
         }
         const bool e_wide = wide_at(noise + sp.head);
         for (;;) {
-            const float q_s = used * q_of;
+            // what is left of p times P.sum, and by how much the draft's exponentials count in it
+            const float q_s = used * q_of * P.sum;
             float best = 0.f;
             int best_at = V;
-            // p / e against the best one so far: a division only where a product says that it may be better
-            auto weigh = [&](float p, float e, int at) {
-                if (!(p > best * e * 0.999999f)) return;
-                const float key = p / e;
-                if (!(key > best || (key == best && at < best_at))) return;
-                for (int k = 0; k < dropped; ++k)
-                    if (removed[k] == at) return;
-                best = key;
-                best_at = at;
-            };
             auto left = [&](float x, float y) {
-                const float p = ex2((x - P.top) * c) * p_of;
+                const float p = ex2((x - P.top) * c);
                 return q_s > 0.f ? fmaxf(p - ex2((y - Q.top) * c) * q_s, 0.f) : p;
+            };
+            // rejected certain drafts among the n places from `at`, a bit each
+            auto out_of = [&](int at, unsigned n) {
+                unsigned bits = 0;
+                for (int k = 0; k < dropped; ++k) {
+                    const unsigned d = unsigned(removed[k] - at);
+                    if (d < n) bits |= 1u << d;
+                }
+                return bits;
+            };
+            auto weigh = [&](float p, float e, int at, bool out) {
+                const float key = p * rcp(e);  // a NaN is never better, nor a number below 0
+                if (!out && (key > best || (key == best && key > 0.f && at < best_at))) {
+                    best = key;
+                    best_at = at;
+                }
             };
             over(
                 sp,
@@ -422,15 +499,20 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
                             if (q_s > 0.f) v[k].get(y8);
                             z[k].get(e8);
                             const int at = sp.head + 8 * (i + k * workers);
+                            const unsigned out = out_of(at, 8);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) weigh(left(x8[e], q_s > 0.f ? y8[e] : 0.f), e8[e], at + e);
+                            for (int e = 0; e < 8; ++e)
+                                weigh(left(x8[e], q_s > 0.f ? y8[e] : 0.f), e8[e], at + e, (out >> e) & 1u);
                         }
                 },
-                [&](int at) { weigh(left(Elt<T>::f(row[at]), q_s > 0.f ? Elt<T>::f(q_row[at]) : 0.f), noise[at], at); });
+                [&](int at) {
+                    weigh(left(Elt<T>::f(row[at]), q_s > 0.f ? Elt<T>::f(q_row[at]) : 0.f), noise[at], at, out_of(at, 1));
+                });
             better_over_warp(best, best_at);
             mine.key = best;
             mine.at = best_at;
             const Slot* picks = exchange(mine, [] {});
+            if (lost) break;
             best = 0.f;
             best_at = V;
             for (int i = lane; i < C * kWarps; i += 32) better(best, best_at, picks[i].key, picks[i].at);
@@ -449,6 +531,7 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
         break;
     }
     if (rank == 0 && tid == 0) {
+        if (lost) flag(a.dev_status, PA_DEV_TIMEOUT);
         a.accepted_cu[s + 1] = count;
         a.next_tokens[s] = next;
     }
