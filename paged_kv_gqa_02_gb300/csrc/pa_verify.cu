@@ -14,13 +14,14 @@
 // other, while a search in running sums would meet a border every few 2^-24 in a
 // vocabulary's tail.  M does not matter to it.
 //
-// The walk's time is a chain of passes, each bound by latency: a read of the row
-// (from L2: the first child's row and the random numbers are prefetched while
-// earlier passes run), the exponentials, and one exchange.  For that, every warp
-// sends its result to the shared memory of every CTA of the cluster, counted by
-// an mbarrier there; each warp then joins all of them in the same order and takes
-// the decisions itself.  Only rank 0 writes.  A second kernel joins the sequences'
-// lists.
+// The walk's time is a chain of passes, each bound by latency: the exponentials
+// of a row and one exchange.  A thread's part of the rows waits in slots of
+// shared memory that only it uses: the row at hand, for all of its passes, and
+// the first child's, on its way while the parent's passes run; the random numbers
+// from the start.  For an exchange every warp sends its result to the shared
+// memory of every CTA of the cluster, counted by an mbarrier there; each warp then
+// joins all of them in the same order and takes the decisions itself.  Only rank 0
+// writes.  A second kernel joins the sequences' lists.
 #include <cooperative_groups.h>
 
 #include "pa_device.h"
@@ -47,9 +48,11 @@ constexpr uint64_t kWaitNs = 2000000000ull;  // an exchange gives up after 2 s
 struct Stat {
     float top, sum;
 };
-// What a warp found in a pass.
-struct __align__(16) Slot {
+// What a warp found in a pass, in two parts of 16 bytes.
+struct __align__(16) Stats {
     Stat p, q;
+};
+struct __align__(16) Pick {
     float key;  // of the best candidate for the next token, or a sum
     int at;     // where the largest logit (greedy) or the best candidate is
     int pad[2];
@@ -74,7 +77,22 @@ template <typename T> __device__ inline Span span_of(const T* row, int vocab) {
 }
 template <typename T> __device__ inline bool wide_at(const T* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Eight elements from p, by 16-byte loads where p is aligned.
+__device__ inline void cp_async16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ inline void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ inline void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Slots of shared memory for units of eight elements: a thread's k-th unit of a
+// row, its 16-byte parts kThr apart.
+template <typename T> struct Stage {
+    static constexpr int kParts = 8 / Elt<T>::kVec;
+    static constexpr int kSlots = 4 / kParts;                    // a thread's units of a row
+    static constexpr int kRow = kSlots * kParts * kThr;          // 16-byte parts of a row
+    static constexpr int kNoise = kSlots * 2 * kThr;
+    static constexpr size_t kBytes = size_t(4 * kRow + kNoise) * 16;  // two rows and their drafts', random numbers
+};
+// Eight elements.
 template <typename T> struct Eight {
     uint4 v[8 / Elt<T>::kVec];
     __device__ inline void load(const T* p, bool wide) {
@@ -91,9 +109,24 @@ template <typename T> struct Eight {
 #pragma unroll
         for (int i = 0; i < 8 / Elt<T>::kVec; ++i) vec_to_f32<T>(v[i], x + i * Elt<T>::kVec);
     }
+    // from the thread's slot and to it: copies that arrive later where p is aligned
+    __device__ inline void take(const uint4* slot) {
+#pragma unroll
+        for (int i = 0; i < 8 / Elt<T>::kVec; ++i) v[i] = slot[i * kThr];
+    }
+    __device__ static inline void stage(uint4* slot, const T* p, bool wide) {
+        if (wide) {
+#pragma unroll
+            for (int i = 0; i < 8 / Elt<T>::kVec; ++i)
+                cp_async16(smem_u32(slot + i * kThr), reinterpret_cast<const uint4*>(p) + i);
+        } else {
+            Eight e;
+            e.load(p, false);
+#pragma unroll
+            for (int i = 0; i < 8 / Elt<T>::kVec; ++i) slot[i * kThr] = e.v[i];
+        }
+    }
 };
-
-__device__ inline void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // 16 bytes to the same place of another CTA's shared memory, counted by its mbarrier.
 __device__ inline void send16(uint32_t to, uint32_t bar, const uint4& v) {
@@ -108,35 +141,30 @@ __device__ inline uint32_t in_cta(uint32_t addr, int rank) {
     return r;
 }
 
-__device__ inline void raise(Run& s, float top, float c) {
-    if (top > s.top) {
-        const float down = ex2((s.top - top) * c);
-        s.sum = pairs::mul(s.sum, pairs::pack(down, down));
-        s.top = top;
-    }
+// Without branches: a largest value of -infinity stands for 0, so that
+// -infinity adds nothing and a NaN is not lost.
+__device__ inline float raise(Run& s, float top, float c) {
+    const float now = fmaxf(s.top, top), ref = now > -INFINITY ? now : 0.f;
+    const float down = ex2((s.top - ref) * c);
+    s.sum = pairs::mul(s.sum, pairs::pack(down, down));
+    s.top = now;
+    return ref;
 }
 __device__ inline void take8(Run& s, const float (&x)[8], float c) {
-    float top = x[0];
+    const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+    const float ref = raise(s, top, c);
+    const uint64_t minus = pairs::pack(-ref, -ref), c2 = pairs::pack(c, c);
+    uint64_t e[4];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) top = fmaxf(top, x[i]);
-    raise(s, top, c);
-    if (s.top > -INFINITY) {
-        const uint64_t minus = pairs::pack(-s.top, -s.top), c2 = pairs::pack(c, c);
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            const float2 e = pairs::unpack(pairs::mul(pairs::add(pairs::pack(x[i], x[i + 1]), minus), c2));
-            s.sum = pairs::add(s.sum, pairs::pack(ex2(e.x), ex2(e.y)));
-        }
-    } else {  // a NaN is not lost
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (x[i] != x[i]) s.sum = pairs::pack(x[i], x[i]);
+    for (int i = 0; i < 4; ++i) {
+        const float2 d = pairs::unpack(pairs::mul(pairs::add(pairs::pack(x[2 * i], x[2 * i + 1]), minus), c2));
+        e[i] = pairs::pack(ex2(d.x), ex2(d.y));
     }
+    s.sum = pairs::add(s.sum, pairs::add(pairs::add(e[0], e[1]), pairs::add(e[2], e[3])));
 }
 __device__ inline void take1(Run& s, float x, float c) {
-    raise(s, x, c);
-    const float e = s.top > -INFINITY ? ex2((x - s.top) * c) : x != x ? x : 0.f;
-    s.sum = pairs::add(s.sum, pairs::pack(e, 0.f));
+    const float ref = raise(s, x, c);
+    s.sum = pairs::add(s.sum, pairs::pack(ex2((x - ref) * c), 0.f));
 }
 
 // The largest of the warp's values, none of them a NaN.
@@ -179,10 +207,15 @@ __device__ inline float rcp(float x) {
 }
 
 template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(const VerifyCall a) {
-    constexpr int kAhead = Elt<T>::kVec / 2;  // units of eight logits whose loads a thread has in flight
-    __shared__ Slot inbox[2][kMaxCluster * kWarps];
+    extern __shared__ uint4 slots[];
+    __shared__ Stats in_stats[2][kMaxCluster * kWarps];
+    __shared__ Pick in_picks[2][kMaxCluster * kWarps];
     __shared__ uint64_t arrived[2];
+    __shared__ Stats all_stats[2];
+    __shared__ Pick all_picks[2];
+    __shared__ int all_lost;
     __shared__ int parents[kMaxDrafts], tokens[kMaxDrafts], removed[kMaxDrafts];
+    using St = Stage<T>;
     cg::cluster_group cluster = cg::this_cluster();
     const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -202,14 +235,64 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
     const int V = a.vocab;
     const bool greedy = !(heat > 0.f);
     const float c = greedy ? kLog2e : fminf(kLog2e / heat, 3.402823466e38f);
-    const T* const logits = static_cast<const T*>(a.logits);
-    const T* const draft = greedy ? nullptr : static_cast<const T*>(a.draft);
     const float* const noise = a.noise + int64_t(s) * V;
     const int worker = rank * kThr + tid, workers = C * kThr;
-    // a line of 128 bytes to a thread
-    auto prefetch = [&](const char* p, int64_t bytes) {
-        for (int64_t i = int64_t(worker) * 128; i < bytes; i += int64_t(workers) * 128) prefetch_l2(p + i);
+
+    // A row as the thread reads it.
+    struct Row {
+        const T* p;
+        const T* q;  // the draft's, or nullptr
+        Span sp;
+        bool q_wide;
+        int single;  // the thread's single element, or -1
+        T one_p, one_q;
     };
+    auto row_at = [&](int t, bool with_q) {
+        Row r;
+        r.p = static_cast<const T*>(a.logits) + int64_t(r0 + t) * a.logits_stride;
+        r.q = with_q && !greedy && a.draft ? static_cast<const T*>(a.draft) + int64_t(r0 + t) * a.draft_stride : nullptr;
+        r.sp = span_of(r.p, V);
+        r.q_wide = r.q && wide_at(r.q + r.sp.head);
+        const int behind = r.sp.head + 8 * r.sp.units;
+        r.single = rank == C - 1 && tid < r.sp.head + V - behind ? (tid < r.sp.head ? tid : behind + tid - r.sp.head) : -1;
+        return r;
+    };
+    uint4* const noise_slots = slots + 4 * St::kRow + tid;
+    auto slot_of = [&](int held, int draft, int k) { return slots + (2 * held + draft) * St::kRow + k * St::kParts * kThr + tid; };
+    // the first units of a row, of its draft's, on their way to the slots of `held`
+    auto fetch_p = [&](Row& r, int held) {
+#pragma unroll
+        for (int k = 0; k < St::kSlots; ++k) {
+            const int i = worker + k * workers;
+            if (i < r.sp.units) Eight<T>::stage(slot_of(held, 0, k), r.p + r.sp.head + 8 * i, true);
+        }
+        if (r.single >= 0) r.one_p = r.p[r.single];
+    };
+    auto fetch_q = [&](Row& r, int held) {
+        if (!r.q) return;
+#pragma unroll
+        for (int k = 0; k < St::kSlots; ++k) {
+            const int i = worker + k * workers;
+            if (i < r.sp.units) Eight<T>::stage(slot_of(held, 1, k), r.q + r.sp.head + 8 * i, r.q_wide);
+        }
+        if (r.single >= 0) r.one_q = r.q[r.single];
+    };
+    auto fetch = [&](Row& r, int held) {
+        fetch_p(r, held);
+        fetch_q(r, held);
+        cp_commit();
+    };
+    auto fetch_noise = [&](const Span& sp) {
+        const bool wide = wide_at(noise + sp.head);
+#pragma unroll
+        for (int k = 0; k < St::kSlots; ++k) {
+            const int i = worker + k * workers;
+            if (i < sp.units) Eight<float>::stage(noise_slots + 2 * k * kThr, noise + sp.head + 8 * i, wide);
+        }
+    };
+    Row row = row_at(0, rows > 1);
+    int held = 0;
+    fetch(row, held);
     for (int t = tid; t < rows; t += kThr) {
         const int p = t ? a.parents[r0 + t] : -1, token = t ? a.tokens[r0 + t] : -1;
         const bool good = t && p >= 0 && p < t && token >= 0 && token < V;
@@ -217,8 +300,7 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
         parents[t] = good ? p : -1;  // nobody's child
         tokens[t] = token;
     }
-    if (!greedy) prefetch(reinterpret_cast<const char*>(noise), int64_t(V) * sizeof(float));
-    const uint32_t bytes = uint32_t(C) * kWarps * sizeof(Slot);  // of an exchange
+    const uint32_t bytes = uint32_t(C) * kWarps * (sizeof(Stats) + sizeof(Pick));  // of an exchange
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&arrived[i], 1);
@@ -230,30 +312,100 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
 
     int turn = 0;
     bool lost = false;  // an exchange gave up
-    // Sends the warp's result to every CTA of the cluster and waits for all of
-    // theirs; `meanwhile` runs in between.  A place is written again by the
-    // exchange after the next, which nobody begins before all have sent for the
-    // next, and so have read this one.
-    auto exchange = [&](const Slot& mine, auto&& meanwhile) -> const Slot* {
+    // Sends the warp's result to every CTA of the cluster; warp 0 waits for all
+    // of theirs and joins them, largest values first, then every sum once.  A
+    // place is written again by the exchange after the next, which nobody begins
+    // before all have sent for the next, and so have read this one.
+    enum { kStats, kSum, kPick };
+    auto exchange = [&](int what, const Stats& stats, const Pick& pick) {
         const int at = turn & 1;
         if (lane < C) {
-            const uint32_t to = in_cta(smem_u32(&inbox[at][rank * kWarps + warp]), lane);
             const uint32_t bar = in_cta(smem_u32(&arrived[at]), lane);
-            const uint4* v = reinterpret_cast<const uint4*>(&mine);
-            send16(to, bar, v[0]);
-            send16(to + 16, bar, v[1]);
+            send16(in_cta(smem_u32(&in_stats[at][rank * kWarps + warp]), lane), bar, *reinterpret_cast<const uint4*>(&stats));
+            send16(in_cta(smem_u32(&in_picks[at][rank * kWarps + warp]), lane), bar, *reinterpret_cast<const uint4*>(&pick));
         }
-        meanwhile();
-        if (!__all_sync(0xffffffffu, mbar_wait_ns(&arrived[at], (turn >> 1) & 1, kWaitNs))) lost = true;
-        if (tid == 0) mbar_arrive_expect_tx(&arrived[at], bytes);  // for the exchange after the next
+        if (warp == 0) {
+            const bool fine = __all_sync(0xffffffffu, mbar_wait_ns(&arrived[at], (turn >> 1) & 1, kWaitNs));
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&arrived[at], bytes);  // for the exchange after the next
+                all_lost = !fine;
+            }
+            const int n = C * kWarps;
+            constexpr int kMine = kMaxCluster * kWarps / 32;
+            if (what == kStats) {
+                Stats o[kMine], r = {{-INFINITY, 0.f}, {-INFINITY, 0.f}};
+#pragma unroll
+                for (int j = 0; j < kMine; ++j)
+                    if (lane + 32 * j < n) o[j] = in_stats[at][lane + 32 * j];
+#pragma unroll
+                for (int j = 0; j < kMine; ++j)
+                    if (lane + 32 * j < n) r.p.top = fmaxf(r.p.top, o[j].p.top), r.q.top = fmaxf(r.q.top, o[j].q.top);
+                r.p.top = max_over_warp(r.p.top);
+                r.q.top = max_over_warp(r.q.top);
+#pragma unroll
+                for (int j = 0; j < kMine; ++j)
+                    if (lane + 32 * j < n) {
+                        r.p.sum += sum_at(o[j].p, r.p.top, c);
+                        r.q.sum += sum_at(o[j].q, r.q.top, c);
+                    }
+                r.p.sum = warp_sum(r.p.sum);
+                r.q.sum = warp_sum(r.q.sum);
+                if (lane == 0) all_stats[at] = r;
+            }
+            if (what == kPick || (what == kStats && greedy)) {
+                float key = -INFINITY;
+                int where = V;
+                for (int i = lane; i < n; i += 32) better(key, where, in_picks[at][i].key, in_picks[at][i].at);
+                better_over_warp(key, where);
+                if (lane == 0) all_picks[at] = Pick{key, where, {0, 0}};
+            } else if (what == kSum) {
+                float sum = 0.f;
+                for (int i = lane; i < n; i += 32) sum += in_picks[at][i].key;
+                sum = warp_sum(sum);
+                if (lane == 0) all_picks[at] = Pick{sum, 0, {0, 0}};
+            }
+        }
+        __syncthreads();
+        lost = all_lost != 0;
         ++turn;
-        return inbox[at];
+        return at;
     };
-    // f(index of eight) and g(index of one) over the row, the cluster's threads in turn
-    auto over = [&](const Span& sp, auto&& f, auto&& g) {
-        for (int i = worker; i < sp.units; i += kAhead * workers) f(i);
-        const int behind = sp.head + 8 * sp.units, single = sp.head + (V - behind);
-        if (rank == C - 1 && tid < single) g(tid < sp.head ? tid : behind + tid - sp.head);
+    // f(eight of p, eight of q, first index, k) over the thread's units of the row
+    // at hand.  Units that have no slot of their own come to one that is done with,
+    // and the first ones back to theirs before the next pass over the row.
+    const Span* noise_at = nullptr;  // where the pass reads random numbers too
+    bool again_from_start = false;
+    auto stage_unit = [&](int k, int i) {
+        const int at = row.sp.head + 8 * i, slot = k % St::kSlots;
+        Eight<T>::stage(slot_of(held, 0, slot), row.p + at, true);
+        if (row.q) Eight<T>::stage(slot_of(held, 1, slot), row.q + at, row.q_wide);
+        if (noise_at) Eight<float>::stage(noise_slots + 2 * slot * kThr, noise + at, wide_at(noise + noise_at->head));
+    };
+    auto over = [&](auto&& f) {
+        const bool more = worker + St::kSlots * workers < row.sp.units;
+        if (more && again_from_start) {
+            cp_wait<0>();
+            for (int k = 0; k < St::kSlots; ++k) stage_unit(k, worker + k * workers);
+            cp_commit();
+            cp_wait<0>();
+        }
+#pragma unroll 1
+        for (int k = 0, i = worker; i < row.sp.units; ++k, i += workers) {
+            if (k >= St::kSlots) cp_wait<St::kSlots - 1>();
+            const int slot = k % St::kSlots;
+            Eight<T> u, v;
+            u.take(slot_of(held, 0, slot));
+            if (row.q) v.take(slot_of(held, 1, slot));
+            float x[8], y[8];
+            u.get(x);
+            if (row.q) v.get(y);
+            f(x, y, row.sp.head + 8 * i, slot);
+            if (more) {
+                if (i + St::kSlots * workers < row.sp.units) stage_unit(k, i + St::kSlots * workers);
+                cp_commit();
+            }
+        }
+        again_from_start = true;
     };
     // children of `here` among rows base .. base + 31, or the next such run that has some
     auto window = [&](int here, int& base) -> unsigned {
@@ -265,106 +417,91 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
     };
 
     int here = 0, count = 0, next = -1;
+    {
+        int base = 1;
+        if (!window(0, base)) row.q = nullptr;  // nothing is used of a row without children
+    }
+    Span noise_span = row.sp;
+    bool first = true;
     for (;;) {
         if (rank == 0 && tid == 0) a.accepted[r0 + count] = r0 + here;
         ++count;
-        const T* const row = logits + int64_t(r0 + here) * a.logits_stride;
         int base = here + 1;
         unsigned children = window(here, base);
-        const T* const q_row = draft && children ? draft + int64_t(r0 + here) * a.draft_stride : nullptr;
         // the lane's child: its logits and its random number
-        float x_mine = 0.f, y_mine = 0.f, u_mine = 0.f;
+        T x_mine = T(0.f), y_mine = T(0.f);
+        float u_mine = 0.f;
         auto look = [&] {
             if ((children >> lane) & 1u) {
                 const int token = tokens[base + lane];
                 u_mine = a.uniform[r0 + base + lane];
-                x_mine = Elt<T>::f(row[token]);
-                if (q_row) y_mine = Elt<T>::f(q_row[token]);
+                x_mine = row.p[token];
+                if (row.q) y_mine = row.q[token];
             }
         };
         look();
-        const Span sp = span_of(row, V);
-        const bool q_wide = q_row && wide_at(q_row + sp.head);
-        Slot mine = {{-INFINITY, 0.f}, {-INFINITY, 0.f}, -INFINITY, V, {0, 0}};
+        // the row that the walk most likely goes on to
+        const int guess = children ? base + __ffs(children) - 1 : -1;
+        Row ahead = {};
+        if (guess >= 0) {
+            int after = guess + 1;
+            ahead = row_at(guess, window(guess, after) != 0);
+            fetch(ahead, held ^ 1);
+        } else {
+            cp_commit();
+        }
+        if (first && !greedy) fetch_noise(noise_span);
+        if (first) cp_commit();
+        if (first)
+            cp_wait<2>();  // all but the row ahead and the random numbers
+        else
+            cp_wait<1>();
+        first = false;
+        again_from_start = false;
+
         Run run_p = {-INFINITY, 0}, run_q = {-INFINITY, 0};
+        Pick pick = {-INFINITY, V, {0, 0}};
         auto first_place = [&](float x, int at) {  // greedy: a thread meets indices in ascending order but for the ends
-            if (x > mine.key || (x == mine.key && at < mine.at)) mine.key = x, mine.at = at;
+            if (x > pick.key || (x == pick.key && at < pick.at)) pick.key = x, pick.at = at;
         };
-        over(
-            sp,
-            [&](int i) {
-                Eight<T> u[kAhead], v[kAhead];
+        over([&](const float(&x)[8], const float(&y)[8], int at, int) {
+            take8(run_p, x, c);
+            if (row.q) take8(run_q, y, c);
+            if (greedy) {
 #pragma unroll
-                for (int k = 0; k < kAhead; ++k)
-                    if (i + k * workers < sp.units) {
-                        const int at = sp.head + 8 * (i + k * workers);
-                        u[k].load(row + at, true);
-                        if (q_row) v[k].load(q_row + at, q_wide);
-                    }
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k)
-                    if (i + k * workers < sp.units) {
-                        float x[8];
-                        u[k].get(x);
-                        take8(run_p, x, c);
-                        if (greedy) {
-                            const int at = sp.head + 8 * (i + k * workers);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) first_place(x[e], at + e);
-                        }
-                        if (q_row) {
-                            v[k].get(x);
-                            take8(run_q, x, c);
-                        }
-                    }
-            },
-            [&](int at) {
-                const float x = Elt<T>::f(row[at]);
-                take1(run_p, x, c);
-                if (greedy) first_place(x, at);
-                if (q_row) take1(run_q, Elt<T>::f(q_row[at]), c);
-            });
-        mine.p = over_warp(run_p, c);
-        if (q_row) mine.q = over_warp(run_q, c);
-        if (greedy) better_over_warp(mine.key, mine.at);
-        const Slot* all = exchange(mine, [&] {  // the row that the walk most likely goes on to
-            if (!children) return;
-            const int t = base + __ffs(children) - 1;
-            prefetch(reinterpret_cast<const char*>(logits + int64_t(r0 + t) * a.logits_stride), int64_t(V) * sizeof(T));
-            if (draft && t + 1 < rows && parents[t + 1] == t)
-                prefetch(reinterpret_cast<const char*>(draft + int64_t(r0 + t) * a.draft_stride), int64_t(V) * sizeof(T));
+                for (int e = 0; e < 8; ++e) first_place(x[e], at + e);
+            }
         });
+        if (row.single >= 0) {
+            take1(run_p, Elt<T>::f(row.one_p), c);
+            if (row.q) take1(run_q, Elt<T>::f(row.one_q), c);
+            if (greedy) first_place(Elt<T>::f(row.one_p), row.single);
+        }
+        Stats stats = {over_warp(run_p, c), {-INFINITY, 0.f}};
+        if (row.q) stats.q = over_warp(run_q, c);
+        if (greedy) better_over_warp(pick.key, pick.at);
+        const int got = exchange(kStats, stats, pick);
         if (lost) break;
-        // the cluster's: the largest values first, then every sum once
-        Stat P = {-INFINITY, 0.f}, Q = {-INFINITY, 0.f};
-        float top_key = -INFINITY;
-        int top_at = V;
-        for (int i = lane; i < C * kWarps; i += 32) {
-            P.top = fmaxf(P.top, all[i].p.top);
-            if (q_row) Q.top = fmaxf(Q.top, all[i].q.top);
-            if (greedy) better(top_key, top_at, all[i].key, all[i].at);
-        }
-        P.top = max_over_warp(P.top);
-        if (q_row) Q.top = max_over_warp(Q.top);
-        if (greedy) better_over_warp(top_key, top_at);
-        for (int i = lane; i < C * kWarps; i += 32) {
-            P.sum += sum_at(all[i].p, P.top, c);
-            if (q_row) Q.sum += sum_at(all[i].q, Q.top, c);
-        }
-        P.sum = warp_sum(P.sum);
-        if (q_row) Q.sum = warp_sum(Q.sum);
-        if (!usable(P) || (q_row && !usable(Q))) {
+        const Stat P = all_stats[got].p, Q = all_stats[got].q;
+        const int top_at = all_picks[got].at;  // greedy
+        if (!usable(P) || (row.q && !usable(Q))) {
             if (rank == 0 && tid == 0) flag(a.dev_status, PA_DEV_BAD_VALUE);
             break;
         }
         // what is left of p is max(p - used q, 0) / mass
-        const float p_of = 1.f / P.sum, q_of = q_row ? 1.f / Q.sum : 0.f;
+        const float p_of = rcp(P.sum), q_of = row.q ? rcp(Q.sum) : 0.f;
         float used = 0.f, mass = 1.f, kept = -1.f;  // kept: what `used` was before the last child's rejection
         int dropped = 0;                            // certain drafts rejected here
         int went = 0;
+        // what is left of p times P.sum, of which a draft's exponential takes `less`
+        auto left = [&](float x, float y, float less) {
+            const float p = ex2((x - P.top) * c);
+            return less > 0.f ? fmaxf(p - ex2((y - Q.top) * c) * less, 0.f) : p;
+        };
         while (children) {
             const int l = __ffs(children) - 1, t = base + l;
-            const float x = __shfl_sync(0xffffffffu, x_mine, l), y = __shfl_sync(0xffffffffu, y_mine, l);
+            const float x = __shfl_sync(0xffffffffu, Elt<T>::f(x_mine), l);
+            const float y = __shfl_sync(0xffffffffu, Elt<T>::f(y_mine), l);
             const float u = __shfl_sync(0xffffffffu, u_mine, l);
             const int token = tokens[t];
             bool again = false;
@@ -374,13 +511,13 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
             } else {
                 p = ex2((x - P.top) * c) * p_of;
                 float q = 1.f;
-                if (q_row) {
+                if (row.q) {
                     q = ex2((y - Q.top) * c) * q_of;
-                    p = fmaxf(p - used * q, 0.f) / mass;
+                    p = fmaxf(p - used * q, 0.f) * rcp(mass);
                 } else {
                     for (int i = lane; i < dropped; i += 32) again |= removed[i] == token;
                     again = __any_sync(0xffffffffu, again);
-                    p = again ? 0.f : p / mass;
+                    p = again ? 0.f : p * rcp(mass);
                 }
                 if (p > 0.f && u * q < p) went = t;
             }
@@ -392,7 +529,7 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
                 if (children) look();
             }
             if (greedy) continue;
-            if (!q_row) {
+            if (!row.q) {
                 if (!again && mass - p * mass > 0.f) {
                     mass -= p * mass;
                     __syncthreads();  // all warps have looked through the list
@@ -404,39 +541,17 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
                 kept = used;
                 used += mass;
             } else {
-                const float more = used + mass, q_s = more * q_of;
+                const float more = used + mass, less = more * q_of * P.sum;
                 float sum = 0.f;
-                auto rest = [&](float x, float y) {
-                    sum += fmaxf(ex2((x - P.top) * c) * p_of - ex2((y - Q.top) * c) * q_s, 0.f);
-                };
-                over(
-                    sp,
-                    [&](int i) {
-                        Eight<T> u[kAhead], v[kAhead];
+                over([&](const float(&x8)[8], const float(&y8)[8], int, int) {
 #pragma unroll
-                        for (int k = 0; k < kAhead; ++k)
-                            if (i + k * workers < sp.units) {
-                                const int at = sp.head + 8 * (i + k * workers);
-                                u[k].load(row + at, true);
-                                v[k].load(q_row + at, q_wide);
-                            }
-#pragma unroll
-                        for (int k = 0; k < kAhead; ++k)
-                            if (i + k * workers < sp.units) {
-                                float x8[8], y8[8];
-                                u[k].get(x8);
-                                v[k].get(y8);
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) rest(x8[e], y8[e]);
-                            }
-                    },
-                    [&](int at) { rest(Elt<T>::f(row[at]), Elt<T>::f(q_row[at])); });
-                mine.key = warp_sum(sum);
-                const Slot* sums = exchange(mine, [] {});
+                    for (int e = 0; e < 8; ++e) sum += left(x8[e], y8[e], less);
+                });
+                if (row.single >= 0) sum += left(Elt<T>::f(row.one_p), Elt<T>::f(row.one_q), less);
+                pick.key = warp_sum(sum);
+                const int from = exchange(kSum, stats, pick);
                 if (lost) break;
-                sum = 0.f;
-                for (int i = lane; i < C * kWarps; i += 32) sum += sums[i].key;
-                sum = warp_sum(sum);
+                sum = all_picks[from].key * p_of;
                 if (sum > 0.f) {
                     used = more;
                     mass = sum;
@@ -446,22 +561,33 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
         if (lost) break;
         if (went) {
             here = went;
+            if (went == guess) {
+                row = ahead;
+            } else {
+                row = row_at(went, false);
+                int after = went + 1;
+                if (window(went, after)) row = row_at(went, true);
+                cp_wait<0>();  // the guess is still on its way there
+                fetch(row, held ^ 1);
+            }
+            held ^= 1;
             continue;
         }
         if (greedy) {
             next = top_at;
             break;
         }
-        const bool e_wide = wide_at(noise + sp.head);
+        if (noise_span.head != row.sp.head) {  // another alignment than the first row's
+            cp_wait<0>();
+            fetch_noise(row.sp);
+            cp_commit();
+        }
+        cp_wait<0>();
+        noise_at = &row.sp;
         for (;;) {
-            // what is left of p times P.sum, and by how much the draft's exponentials count in it
-            const float q_s = used * q_of * P.sum;
+            const float less = used * q_of * P.sum;
             float best = 0.f;
             int best_at = V;
-            auto left = [&](float x, float y) {
-                const float p = ex2((x - P.top) * c);
-                return q_s > 0.f ? fmaxf(p - ex2((y - Q.top) * c) * q_s, 0.f) : p;
-            };
             // rejected certain drafts among the n places from `at`, a bit each
             auto out_of = [&](int at, unsigned n) {
                 unsigned bits = 0;
@@ -478,47 +604,25 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
                     best_at = at;
                 }
             };
-            over(
-                sp,
-                [&](int i) {
-                    Eight<T> u[kAhead], v[kAhead];
-                    Eight<float> z[kAhead];
+            over([&](const float(&x8)[8], const float(&y8)[8], int at, int slot) {
+                Eight<float> z;
+                z.take(noise_slots + 2 * slot * kThr);
+                float e8[8];
+                z.get(e8);
+                const unsigned out = out_of(at, 8);
 #pragma unroll
-                    for (int k = 0; k < kAhead; ++k)
-                        if (i + k * workers < sp.units) {
-                            const int at = sp.head + 8 * (i + k * workers);
-                            u[k].load(row + at, true);
-                            if (q_s > 0.f) v[k].load(q_row + at, q_wide);
-                            z[k].load(noise + at, e_wide);
-                        }
-#pragma unroll
-                    for (int k = 0; k < kAhead; ++k)
-                        if (i + k * workers < sp.units) {
-                            float x8[8], y8[8], e8[8];
-                            u[k].get(x8);
-                            if (q_s > 0.f) v[k].get(y8);
-                            z[k].get(e8);
-                            const int at = sp.head + 8 * (i + k * workers);
-                            const unsigned out = out_of(at, 8);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                weigh(left(x8[e], q_s > 0.f ? y8[e] : 0.f), e8[e], at + e, (out >> e) & 1u);
-                        }
-                },
-                [&](int at) {
-                    weigh(left(Elt<T>::f(row[at]), q_s > 0.f ? Elt<T>::f(q_row[at]) : 0.f), noise[at], at, out_of(at, 1));
-                });
+                for (int e = 0; e < 8; ++e) weigh(left(x8[e], y8[e], less), e8[e], at + e, (out >> e) & 1u);
+            });
+            if (row.single >= 0)
+                weigh(left(Elt<T>::f(row.one_p), Elt<T>::f(row.one_q), less), noise[row.single], row.single,
+                      out_of(row.single, 1));
             better_over_warp(best, best_at);
-            mine.key = best;
-            mine.at = best_at;
-            const Slot* picks = exchange(mine, [] {});
+            pick.key = best;
+            pick.at = best_at;
+            const int from = exchange(kPick, stats, pick);
             if (lost) break;
-            best = 0.f;
-            best_at = V;
-            for (int i = lane; i < C * kWarps; i += 32) better(best, best_at, picks[i].key, picks[i].at);
-            better_over_warp(best, best_at);
-            if (best > 0.f) {
-                next = best_at;
+            if (all_picks[from].key > 0.f) {
+                next = all_picks[from].at;
                 break;
             }
             if (kept < 0.f) {
@@ -530,6 +634,7 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
         }
         break;
     }
+    cp_wait<0>();  // nobody leaves with copies under way
     if (rank == 0 && tid == 0) {
         if (lost) flag(a.dev_status, PA_DEV_TIMEOUT);
         a.accepted_cu[s + 1] = count;
@@ -600,8 +705,10 @@ __global__ void __launch_bounds__(kPackThr) verify_pack(const VerifyCall a) {
 }
 
 template <typename T> cudaError_t launch_walk(const VerifyCall& c, cudaStream_t st) {
-    static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_wide_clusters(reinterpret_cast<const void*>(verify_walk<T>), done);
+    static std::atomic<uint64_t> wide{0}, allowed{0};
+    const void* kern = reinterpret_cast<const void*>(verify_walk<T>);
+    cudaError_t e = allow_wide_clusters(kern, wide);
+    if (e == cudaSuccess) e = allow_shared_memory(kern, Stage<T>::kBytes, allowed);
     if (e != cudaSuccess) return e;
     // as many CTAs as the GPU holds at once, each with a unit for every thread
     int size = kMaxCluster;
@@ -609,6 +716,7 @@ template <typename T> cudaError_t launch_walk(const VerifyCall& c, cudaStream_t 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(c.num_seqs) * size);
     cfg.blockDim = dim3(kThr);
+    cfg.dynamicSmemBytes = Stage<T>::kBytes;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
