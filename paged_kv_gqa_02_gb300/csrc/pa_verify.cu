@@ -17,11 +17,13 @@
 // The walk's time is a chain of passes, each bound by latency: the exponentials
 // of a row and one exchange.  A thread's part of the rows waits in slots of
 // shared memory that only it uses: the row at hand, for all of its passes, and
-// the first child's, on its way while the parent's passes run; the random numbers
+// the first child's, on its way while the parent's is decided; the random numbers
 // from the start.  For an exchange every warp sends its result to the shared
-// memory of every CTA of the cluster, counted by an mbarrier there; each warp then
-// joins all of them in the same order and takes the decisions itself.  Only rank 0
-// writes.  A second kernel joins the sequences' lists.
+// memory of every CTA of the cluster, counted by an mbarrier there.  A warp of
+// its own, the leader, reads what it needs of the children meanwhile, joins the
+// results and orders the next pass; leaders of a cluster join the same in the same
+// order and so decide the same.  Only rank 0 writes.  A second kernel joins the
+// sequences' lists.
 #include <cooperative_groups.h>
 
 #include "pa_device.h"
@@ -36,10 +38,11 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThr = 512;
+constexpr int kThr = 512;          // of the passes; the leader's warp comes behind them
 constexpr int kWarps = kThr / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxDrafts = 1024;  // rows of a sequence
+constexpr int kSingles = 16;      // elements of a row outside its units of eight at most, and two
 constexpr int kPackThr = 1024;
 constexpr uint64_t kWaitNs = 2000000000ull;  // an exchange gives up after 2 s
 
@@ -57,24 +60,21 @@ struct __align__(16) Pick {
     int at;     // where the largest logit (greedy) or the best candidate is
     int pad[2];
 };
+// What the leader wants next: the walk to go on to a row, the sum of what is left
+// of p, the best candidate for the next token, or nothing more.
+enum { kGo, kMass, kPick, kStop };
+struct Order {
+    int what, went;
+    int dropped;              // certain drafts rejected
+    float p_top, q_top, less; // what is left: 2^((x - p_top) c) - less 2^((y - q_top) c), not below 0
+};
 // A thread's running Stat, the sum in two parts.
 struct Run {
     float top;
     uint64_t sum;
 };
 
-// A row of the vocabulary as the threads read it: single elements up to the
-// first 16-byte boundary, units of eight, single elements.
-struct Span {
-    int head, units;
-};
-template <typename T> __device__ inline Span span_of(const T* row, int vocab) {
-    Span s;
-    const int off = int((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
-    s.head = min(vocab, off ? int(16 / sizeof(T)) - off : 0);
-    s.units = (vocab - s.head) / 8;
-    return s;
-}
+// Whether p lies on a 16-byte boundary.
 template <typename T> __device__ inline bool wide_at(const T* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 __device__ inline void cp_async16(uint32_t to, const void* from) {
@@ -92,41 +92,32 @@ template <typename T> struct Stage {
     static constexpr int kNoise = kSlots * 2 * kThr;
     static constexpr size_t kBytes = size_t(4 * kRow + kNoise) * 16;  // two rows and their drafts', random numbers
 };
-// Eight elements.
-template <typename T> struct Eight {
-    uint4 v[8 / Elt<T>::kVec];
-    __device__ inline void load(const T* p, bool wide) {
-        if (wide) {
+__device__ inline void cp_async4(uint32_t to, const void* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+
+// Eight elements to the thread's slot and from it.  Copies that arrive later,
+// but for 16-bit elements off the 16-byte boundaries.
+template <typename T> __device__ inline void stage8(uint4* slot, const T* p) {
+    if (wide_at(p)) {
 #pragma unroll
-            for (int i = 0; i < 8 / Elt<T>::kVec; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-        } else {
-            T* e = reinterpret_cast<T*>(v);
+        for (int i = 0; i < 8 / Elt<T>::kVec; ++i)
+            cp_async16(smem_u32(slot + i * kThr), reinterpret_cast<const uint4*>(p) + i);
+    } else if (sizeof(T) == 4) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] = __ldg(p + i);
-        }
+        for (int i = 0; i < 8; ++i) cp_async4(smem_u32(slot + i / 4 * kThr) + 4 * (i % 4), p + i);
+    } else {
+        const unsigned short* e = reinterpret_cast<const unsigned short*>(p);
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = uint32_t(__ldg(e + 2 * i)) | uint32_t(__ldg(e + 2 * i + 1)) << 16;
+        *slot = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    __device__ inline void get(float (&x)[8]) const {
+}
+template <typename T> __device__ inline void take_slot(const uint4* slot, float (&x)[8]) {
 #pragma unroll
-        for (int i = 0; i < 8 / Elt<T>::kVec; ++i) vec_to_f32<T>(v[i], x + i * Elt<T>::kVec);
-    }
-    // from the thread's slot and to it: copies that arrive later where p is aligned
-    __device__ inline void take(const uint4* slot) {
-#pragma unroll
-        for (int i = 0; i < 8 / Elt<T>::kVec; ++i) v[i] = slot[i * kThr];
-    }
-    __device__ static inline void stage(uint4* slot, const T* p, bool wide) {
-        if (wide) {
-#pragma unroll
-            for (int i = 0; i < 8 / Elt<T>::kVec; ++i)
-                cp_async16(smem_u32(slot + i * kThr), reinterpret_cast<const uint4*>(p) + i);
-        } else {
-            Eight e;
-            e.load(p, false);
-#pragma unroll
-            for (int i = 0; i < 8 / Elt<T>::kVec; ++i) slot[i * kThr] = e.v[i];
-        }
-    }
-};
+    for (int i = 0; i < 8 / Elt<T>::kVec; ++i) vec_to_f32<T>(slot[i * kThr], x + i * Elt<T>::kVec);
+}
 
 // 16 bytes to the same place of another CTA's shared memory, counted by its mbarrier.
 __device__ inline void send16(uint32_t to, uint32_t bar, const uint4& v) {
@@ -206,14 +197,13 @@ __device__ inline float rcp(float x) {
     return y;
 }
 
-template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(const VerifyCall a) {
+template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_walk(const VerifyCall a) {
     extern __shared__ uint4 slots[];
     __shared__ Stats in_stats[2][kMaxCluster * kWarps];
     __shared__ Pick in_picks[2][kMaxCluster * kWarps];
     __shared__ uint64_t arrived[2];
-    __shared__ Stats all_stats[2];
-    __shared__ Pick all_picks[2];
-    __shared__ int all_lost;
+    __shared__ Order orders[2];
+    __shared__ float singles[2][2][kSingles];
     __shared__ int parents[kMaxDrafts], tokens[kMaxDrafts], removed[kMaxDrafts];
     using St = Stage<T>;
     cg::cluster_group cluster = cg::this_cluster();
@@ -238,62 +228,57 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
     const float* const noise = a.noise + int64_t(s) * V;
     const int worker = rank * kThr + tid, workers = C * kThr;
 
-    // A row as the thread reads it.
+    // A row as the threads read it: single elements up to the first 16-byte
+    // boundary, units of eight, the cluster's threads in turn, single elements.
     struct Row {
         const T* p;
         const T* q;  // the draft's, or nullptr
-        Span sp;
-        bool q_wide;
-        int single;  // the thread's single element, or -1
-        T one_p, one_q;
+        int head;    // single elements before the units
     };
     auto row_at = [&](int t, bool with_q) {
         Row r;
         r.p = static_cast<const T*>(a.logits) + int64_t(r0 + t) * a.logits_stride;
         r.q = with_q && !greedy && a.draft ? static_cast<const T*>(a.draft) + int64_t(r0 + t) * a.draft_stride : nullptr;
-        r.sp = span_of(r.p, V);
-        r.q_wide = r.q && wide_at(r.q + r.sp.head);
-        const int behind = r.sp.head + 8 * r.sp.units;
-        r.single = rank == C - 1 && tid < r.sp.head + V - behind ? (tid < r.sp.head ? tid : behind + tid - r.sp.head) : -1;
+        r.head = min(V, int((16 - (reinterpret_cast<uintptr_t>(r.p) & 15)) & 15) / int(sizeof(T)));
         return r;
+    };
+    auto units_of = [&](int head) { return (V - head) >> 3; };
+    // the thread's single element, or -1
+    auto single_of = [&](int head) {
+        const int behind = head + 8 * units_of(head);
+        return rank == C - 1 && tid < head + V - behind ? (tid < head ? tid : behind + tid - head) : -1;
     };
     uint4* const noise_slots = slots + 4 * St::kRow + tid;
     auto slot_of = [&](int held, int draft, int k) { return slots + (2 * held + draft) * St::kRow + k * St::kParts * kThr + tid; };
-    // the first units of a row, of its draft's, on their way to the slots of `held`
-    auto fetch_p = [&](Row& r, int held) {
+    // the first units of a row and of its draft's on their way to the slots of `held`
+    auto fetch = [&](const Row& r, int held) {
+        const int units = units_of(r.head), single = single_of(r.head);
 #pragma unroll
         for (int k = 0; k < St::kSlots; ++k) {
             const int i = worker + k * workers;
-            if (i < r.sp.units) Eight<T>::stage(slot_of(held, 0, k), r.p + r.sp.head + 8 * i, true);
+            if (i < units) {
+                stage8<T>(slot_of(held, 0, k), r.p + r.head + 8 * i);
+                if (r.q) stage8<T>(slot_of(held, 1, k), r.q + r.head + 8 * i);
+            }
         }
-        if (r.single >= 0) r.one_p = r.p[r.single];
-    };
-    auto fetch_q = [&](Row& r, int held) {
-        if (!r.q) return;
-#pragma unroll
-        for (int k = 0; k < St::kSlots; ++k) {
-            const int i = worker + k * workers;
-            if (i < r.sp.units) Eight<T>::stage(slot_of(held, 1, k), r.q + r.sp.head + 8 * i, r.q_wide);
+        if (single >= 0) {
+            singles[held][0][tid] = Elt<T>::f(r.p[single]);
+            if (r.q) singles[held][1][tid] = Elt<T>::f(r.q[single]);
         }
-        if (r.single >= 0) r.one_q = r.q[r.single];
-    };
-    auto fetch = [&](Row& r, int held) {
-        fetch_p(r, held);
-        fetch_q(r, held);
         cp_commit();
     };
-    auto fetch_noise = [&](const Span& sp) {
-        const bool wide = wide_at(noise + sp.head);
+    auto fetch_noise = [&](int head) {
+        const int units = units_of(head);
 #pragma unroll
         for (int k = 0; k < St::kSlots; ++k) {
             const int i = worker + k * workers;
-            if (i < sp.units) Eight<float>::stage(noise_slots + 2 * k * kThr, noise + sp.head + 8 * i, wide);
+            if (i < units) stage8<float>(noise_slots + 2 * k * kThr, noise + head + 8 * i);
         }
     };
     Row row = row_at(0, rows > 1);
     int held = 0;
-    fetch(row, held);
-    for (int t = tid; t < rows; t += kThr) {
+    if (warp < kWarps) fetch(row, held);
+    for (int t = tid; t < rows; t += kThr + 32) {
         const int p = t ? a.parents[r0 + t] : -1, token = t ? a.tokens[r0 + t] : -1;
         const bool good = t && p >= 0 && p < t && token >= 0 && token < V;
         if (t && !good && rank == 0) flag(a.dev_status, PA_DEV_BAD_INDEX);
@@ -310,103 +295,6 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
     }
     cluster.sync();  // the barriers are there before anyone sends
 
-    int turn = 0;
-    bool lost = false;  // an exchange gave up
-    // Sends the warp's result to every CTA of the cluster; warp 0 waits for all
-    // of theirs and joins them, largest values first, then every sum once.  A
-    // place is written again by the exchange after the next, which nobody begins
-    // before all have sent for the next, and so have read this one.
-    enum { kStats, kSum, kPick };
-    auto exchange = [&](int what, const Stats& stats, const Pick& pick) {
-        const int at = turn & 1;
-        if (lane < C) {
-            const uint32_t bar = in_cta(smem_u32(&arrived[at]), lane);
-            send16(in_cta(smem_u32(&in_stats[at][rank * kWarps + warp]), lane), bar, *reinterpret_cast<const uint4*>(&stats));
-            send16(in_cta(smem_u32(&in_picks[at][rank * kWarps + warp]), lane), bar, *reinterpret_cast<const uint4*>(&pick));
-        }
-        if (warp == 0) {
-            const bool fine = __all_sync(0xffffffffu, mbar_wait_ns(&arrived[at], (turn >> 1) & 1, kWaitNs));
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&arrived[at], bytes);  // for the exchange after the next
-                all_lost = !fine;
-            }
-            const int n = C * kWarps;
-            constexpr int kMine = kMaxCluster * kWarps / 32;
-            if (what == kStats) {
-                Stats o[kMine], r = {{-INFINITY, 0.f}, {-INFINITY, 0.f}};
-#pragma unroll
-                for (int j = 0; j < kMine; ++j)
-                    if (lane + 32 * j < n) o[j] = in_stats[at][lane + 32 * j];
-#pragma unroll
-                for (int j = 0; j < kMine; ++j)
-                    if (lane + 32 * j < n) r.p.top = fmaxf(r.p.top, o[j].p.top), r.q.top = fmaxf(r.q.top, o[j].q.top);
-                r.p.top = max_over_warp(r.p.top);
-                r.q.top = max_over_warp(r.q.top);
-#pragma unroll
-                for (int j = 0; j < kMine; ++j)
-                    if (lane + 32 * j < n) {
-                        r.p.sum += sum_at(o[j].p, r.p.top, c);
-                        r.q.sum += sum_at(o[j].q, r.q.top, c);
-                    }
-                r.p.sum = warp_sum(r.p.sum);
-                r.q.sum = warp_sum(r.q.sum);
-                if (lane == 0) all_stats[at] = r;
-            }
-            if (what == kPick || (what == kStats && greedy)) {
-                float key = -INFINITY;
-                int where = V;
-                for (int i = lane; i < n; i += 32) better(key, where, in_picks[at][i].key, in_picks[at][i].at);
-                better_over_warp(key, where);
-                if (lane == 0) all_picks[at] = Pick{key, where, {0, 0}};
-            } else if (what == kSum) {
-                float sum = 0.f;
-                for (int i = lane; i < n; i += 32) sum += in_picks[at][i].key;
-                sum = warp_sum(sum);
-                if (lane == 0) all_picks[at] = Pick{sum, 0, {0, 0}};
-            }
-        }
-        __syncthreads();
-        lost = all_lost != 0;
-        ++turn;
-        return at;
-    };
-    // f(eight of p, eight of q, first index, k) over the thread's units of the row
-    // at hand.  Units that have no slot of their own come to one that is done with,
-    // and the first ones back to theirs before the next pass over the row.
-    const Span* noise_at = nullptr;  // where the pass reads random numbers too
-    bool again_from_start = false;
-    auto stage_unit = [&](int k, int i) {
-        const int at = row.sp.head + 8 * i, slot = k % St::kSlots;
-        Eight<T>::stage(slot_of(held, 0, slot), row.p + at, true);
-        if (row.q) Eight<T>::stage(slot_of(held, 1, slot), row.q + at, row.q_wide);
-        if (noise_at) Eight<float>::stage(noise_slots + 2 * slot * kThr, noise + at, wide_at(noise + noise_at->head));
-    };
-    auto over = [&](auto&& f) {
-        const bool more = worker + St::kSlots * workers < row.sp.units;
-        if (more && again_from_start) {
-            cp_wait<0>();
-            for (int k = 0; k < St::kSlots; ++k) stage_unit(k, worker + k * workers);
-            cp_commit();
-            cp_wait<0>();
-        }
-#pragma unroll 1
-        for (int k = 0, i = worker; i < row.sp.units; ++k, i += workers) {
-            if (k >= St::kSlots) cp_wait<St::kSlots - 1>();
-            const int slot = k % St::kSlots;
-            Eight<T> u, v;
-            u.take(slot_of(held, 0, slot));
-            if (row.q) v.take(slot_of(held, 1, slot));
-            float x[8], y[8];
-            u.get(x);
-            if (row.q) v.get(y);
-            f(x, y, row.sp.head + 8 * i, slot);
-            if (more) {
-                if (i + St::kSlots * workers < row.sp.units) stage_unit(k, i + St::kSlots * workers);
-                cp_commit();
-            }
-        }
-        again_from_start = true;
-    };
     // children of `here` among rows base .. base + 31, or the next such run that has some
     auto window = [&](int here, int& base) -> unsigned {
         for (; base < rows; base += 32) {
@@ -416,49 +304,243 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
         return 0u;
     };
 
-    int here = 0, count = 0, next = -1;
+    int turn = 0;  // exchanges so far
+
+    if (warp == kWarps) {
+        // ================================ leader ================================
+        bool lost = false;  // an exchange gave up
+        // the cluster's results of an exchange
+        auto wait = [&] {
+            const int at = turn & 1;
+            if (!__all_sync(0xffffffffu, mbar_wait_ns(&arrived[at], (turn >> 1) & 1, kWaitNs))) lost = true;
+            if (lane == 0) mbar_arrive_expect_tx(&arrived[at], bytes);  // for the exchange after the next
+            ++turn;
+            return at;
+        };
+        int ordered = 0;
+        auto order = [&](const Order& o) {
+            if (lane == 0) orders[ordered & 1] = o;
+            ++ordered;
+            __syncthreads();
+        };
+        const int n = C * kWarps;
+        int here = 0, count = 0, next = -1;
+        for (;;) {
+            if (rank == 0 && lane == 0) a.accepted[r0 + count] = r0 + here;
+            ++count;
+            int base = here + 1;
+            unsigned children = window(here, base);
+            row = row_at(here, children != 0);
+            // the lane's child: its logits and its random number
+            T x_mine = T(0.f), y_mine = T(0.f);
+            float u_mine = 0.f;
+            auto look = [&] {
+                if ((children >> lane) & 1u) {
+                    const int token = tokens[base + lane];
+                    u_mine = a.uniform[r0 + base + lane];
+                    x_mine = row.p[token];
+                    if (row.q) y_mine = row.q[token];
+                }
+            };
+            look();
+            // the row's largest logit and sum, the draft's: the largest values first, then every sum once
+            const int at = wait();
+            if (lost) break;
+            constexpr int kMine = kMaxCluster * kWarps / 32;
+            Stats o[kMine];
+            Stat P = {-INFINITY, 0.f}, Q = {-INFINITY, 0.f};
+#pragma unroll
+            for (int j = 0; j < kMine; ++j)
+                if (lane + 32 * j < n) o[j] = in_stats[at][lane + 32 * j];
+#pragma unroll
+            for (int j = 0; j < kMine; ++j)
+                if (lane + 32 * j < n) P.top = fmaxf(P.top, o[j].p.top), Q.top = fmaxf(Q.top, o[j].q.top);
+            P.top = max_over_warp(P.top);
+            Q.top = max_over_warp(Q.top);
+#pragma unroll
+            for (int j = 0; j < kMine; ++j)
+                if (lane + 32 * j < n) P.sum += sum_at(o[j].p, P.top, c), Q.sum += sum_at(o[j].q, Q.top, c);
+            P.sum = warp_sum(P.sum);
+            Q.sum = warp_sum(Q.sum);
+            int top_at = V;
+            if (greedy) {
+                float key = -INFINITY;
+                for (int i = lane; i < n; i += 32) better(key, top_at, in_picks[at][i].key, in_picks[at][i].at);
+                better_over_warp(key, top_at);
+            }
+            if (!usable(P) || (row.q && !usable(Q))) {
+                if (rank == 0 && lane == 0) flag(a.dev_status, PA_DEV_BAD_VALUE);
+                break;
+            }
+            // what is left of p is max(p - used q, 0) / mass
+            const float p_of = rcp(P.sum), q_of = row.q ? rcp(Q.sum) : 0.f;
+            float used = 0.f, mass = 1.f, kept = -1.f;  // kept: what `used` was before the last child's rejection
+            int dropped = 0;                            // certain drafts rejected here
+            int went = 0;
+            while (children) {
+                const int l = __ffs(children) - 1, t = base + l;
+                const float x = __shfl_sync(0xffffffffu, Elt<T>::f(x_mine), l);
+                const float y = __shfl_sync(0xffffffffu, Elt<T>::f(y_mine), l);
+                const float u = __shfl_sync(0xffffffffu, u_mine, l);
+                const int token = tokens[t];
+                bool again = false;
+                float p = 0.f;
+                if (greedy) {
+                    if (token == top_at) went = t;
+                } else {
+                    p = ex2((x - P.top) * c) * p_of;
+                    float q = 1.f;
+                    if (row.q) {
+                        q = ex2((y - Q.top) * c) * q_of;
+                        p = fmaxf(p - used * q, 0.f) * rcp(mass);
+                    } else {
+                        for (int i = lane; i < dropped; i += 32) again |= removed[i] == token;
+                        again = __any_sync(0xffffffffu, again);
+                        p = again ? 0.f : p * rcp(mass);
+                    }
+                    if (p > 0.f && u * q < p) went = t;
+                }
+                if (went) break;
+                children &= children - 1;
+                if (!children) {
+                    base += 32;
+                    children = window(here, base);
+                    if (children) look();
+                }
+                if (greedy) continue;
+                if (!row.q) {
+                    if (!again && mass - p * mass > 0.f) {
+                        mass -= p * mass;
+                        if (lane == 0) removed[dropped] = token;
+                        __syncwarp();
+                        ++dropped;
+                    }
+                } else if (!children) {
+                    kept = used;
+                    used += mass;
+                } else {
+                    const float more = used + mass;
+                    order(Order{kMass, 0, 0, P.top, Q.top, more * q_of * P.sum});
+                    const int from = wait();
+                    if (lost) break;
+                    float sum = 0.f;
+                    for (int i = lane; i < n; i += 32) sum += in_picks[from][i].key;
+                    sum = warp_sum(sum) * p_of;
+                    if (sum > 0.f) {
+                        used = more;
+                        mass = sum;
+                    }
+                }
+            }
+            if (lost) break;
+            if (went) {
+                order(Order{kGo, went, 0, 0.f, 0.f, 0.f});
+                here = went;
+                continue;
+            }
+            if (greedy) {
+                next = top_at;
+                break;
+            }
+            for (;;) {
+                order(Order{kPick, 0, dropped, P.top, Q.top, used * q_of * P.sum});
+                const int from = wait();
+                if (lost) break;
+                float key = 0.f;
+                int where = V;
+                for (int i = lane; i < n; i += 32) better(key, where, in_picks[from][i].key, in_picks[from][i].at);
+                better_over_warp(key, where);
+                if (key > 0.f) {
+                    next = where;
+                    break;
+                }
+                if (kept < 0.f) {
+                    if (rank == 0 && lane == 0) flag(a.dev_status, PA_DEV_BAD_VALUE);
+                    break;
+                }
+                used = kept;  // nothing was left behind the last rejection: p is as it was
+                kept = -1.f;
+            }
+            break;
+        }
+        order(Order{kStop, 0, 0, 0.f, 0.f, 0.f});
+        if (rank == 0 && lane == 0) {
+            if (lost) flag(a.dev_status, PA_DEV_TIMEOUT);
+            a.accepted_cu[s + 1] = count;
+            a.next_tokens[s] = next;
+        }
+        return;
+    }
+
+    // ================================== passes ==================================
+    // Sends the warp's result to every CTA of the cluster.  A place is written
+    // again by the exchange after the next, which nobody begins before its leader
+    // has read the next, for which all have sent.
+    auto send = [&](const Stats& stats, const Pick& pick) {
+        const int at = turn++ & 1;
+        if (lane < C) {
+            const uint32_t bar = in_cta(smem_u32(&arrived[at]), lane);
+            send16(in_cta(smem_u32(&in_stats[at][rank * kWarps + warp]), lane), bar, *reinterpret_cast<const uint4*>(&stats));
+            send16(in_cta(smem_u32(&in_picks[at][rank * kWarps + warp]), lane), bar, *reinterpret_cast<const uint4*>(&pick));
+        }
+    };
+    int taken = 0;
+    auto next_order = [&] {
+        __syncthreads();
+        return orders[taken++ & 1];
+    };
+    // f(eight of p, eight of q, first index, slot) over the thread's units of the row
+    // at hand.  Units that have no slot of their own come to one that is done with,
+    // and the first ones back to theirs before the next pass over the row.
+    bool with_noise = false;  // the pass reads random numbers too
+    bool again_from_start = false;
+    auto over = [&](auto&& f) {
+        const int units = units_of(row.head);
+        const bool more = worker + St::kSlots * workers < units;
+        auto stage_unit = [&](int slot, int i) {
+            stage8<T>(slot_of(held, 0, slot), row.p + row.head + 8 * i);
+            if (row.q) stage8<T>(slot_of(held, 1, slot), row.q + row.head + 8 * i);
+            if (with_noise) stage8<float>(noise_slots + 2 * slot * kThr, noise + row.head + 8 * i);
+        };
+        if (more && again_from_start) {
+            cp_wait<0>();
+#pragma unroll 1
+            for (int k = 0; k < St::kSlots; ++k) stage_unit(k, worker + k * workers);
+            cp_commit();
+            cp_wait<0>();
+        }
+        int slot = 0;
+#pragma unroll 1
+        for (int i = worker; i < units; i += workers) {
+            if (i >= St::kSlots * workers) cp_wait<St::kSlots - 1>();
+            float x[8], y[8];
+            take_slot<T>(slot_of(held, 0, slot), x);
+            if (row.q) take_slot<T>(slot_of(held, 1, slot), y);
+            f(x, y, row.head + 8 * i, slot);
+            if (more) {
+                if (i + St::kSlots * workers < units) stage_unit(slot, i + St::kSlots * workers);
+                cp_commit();
+            }
+            slot = slot + 1 == St::kSlots ? 0 : slot + 1;
+        }
+        again_from_start = true;
+    };
+    int here = 0;
     {
         int base = 1;
         if (!window(0, base)) row.q = nullptr;  // nothing is used of a row without children
     }
-    Span noise_span = row.sp;
+    const int noise_head = row.head;
+    if (!greedy) fetch_noise(row.head);
+    cp_commit();
     bool first = true;
     for (;;) {
-        if (rank == 0 && tid == 0) a.accepted[r0 + count] = r0 + here;
-        ++count;
-        int base = here + 1;
-        unsigned children = window(here, base);
-        // the lane's child: its logits and its random number
-        T x_mine = T(0.f), y_mine = T(0.f);
-        float u_mine = 0.f;
-        auto look = [&] {
-            if ((children >> lane) & 1u) {
-                const int token = tokens[base + lane];
-                u_mine = a.uniform[r0 + base + lane];
-                x_mine = row.p[token];
-                if (row.q) y_mine = row.q[token];
-            }
-        };
-        look();
-        // the row that the walk most likely goes on to
-        const int guess = children ? base + __ffs(children) - 1 : -1;
-        Row ahead = {};
-        if (guess >= 0) {
-            int after = guess + 1;
-            ahead = row_at(guess, window(guess, after) != 0);
-            fetch(ahead, held ^ 1);
-        } else {
-            cp_commit();
-        }
-        if (first && !greedy) fetch_noise(noise_span);
-        if (first) cp_commit();
         if (first)
-            cp_wait<2>();  // all but the row ahead and the random numbers
+            cp_wait<1>();  // all but the random numbers
         else
-            cp_wait<1>();
+            cp_wait<0>();
         first = false;
         again_from_start = false;
-
         Run run_p = {-INFINITY, 0}, run_q = {-INFINITY, 0};
         Pick pick = {-INFINITY, V, {0, 0}};
         auto first_place = [&](float x, int at) {  // greedy: a thread meets indices in ascending order but for the ends
@@ -472,174 +554,96 @@ template <typename T> __global__ void __launch_bounds__(kThr, 1) verify_walk(con
                 for (int e = 0; e < 8; ++e) first_place(x[e], at + e);
             }
         });
-        if (row.single >= 0) {
-            take1(run_p, Elt<T>::f(row.one_p), c);
-            if (row.q) take1(run_q, Elt<T>::f(row.one_q), c);
-            if (greedy) first_place(Elt<T>::f(row.one_p), row.single);
+        const int single = single_of(row.head);
+        if (single >= 0) {
+            take1(run_p, singles[held][0][tid], c);
+            if (row.q) take1(run_q, singles[held][1][tid], c);
+            if (greedy) first_place(singles[held][0][tid], single);
         }
         Stats stats = {over_warp(run_p, c), {-INFINITY, 0.f}};
         if (row.q) stats.q = over_warp(run_q, c);
         if (greedy) better_over_warp(pick.key, pick.at);
-        const int got = exchange(kStats, stats, pick);
-        if (lost) break;
-        const Stat P = all_stats[got].p, Q = all_stats[got].q;
-        const int top_at = all_picks[got].at;  // greedy
-        if (!usable(P) || (row.q && !usable(Q))) {
-            if (rank == 0 && tid == 0) flag(a.dev_status, PA_DEV_BAD_VALUE);
-            break;
+        send(stats, pick);
+        // the row that the walk most likely goes on to
+        int base = here + 1;
+        const unsigned children = window(here, base);
+        const int guess = children ? base + __ffs(children) - 1 : -1;
+        Row ahead = {};
+        if (guess >= 0) {
+            int after = guess + 1;
+            ahead = row_at(guess, window(guess, after) != 0);
+            fetch(ahead, held ^ 1);
         }
-        // what is left of p is max(p - used q, 0) / mass
-        const float p_of = rcp(P.sum), q_of = row.q ? rcp(Q.sum) : 0.f;
-        float used = 0.f, mass = 1.f, kept = -1.f;  // kept: what `used` was before the last child's rejection
-        int dropped = 0;                            // certain drafts rejected here
-        int went = 0;
-        // what is left of p times P.sum, of which a draft's exponential takes `less`
-        auto left = [&](float x, float y, float less) {
-            const float p = ex2((x - P.top) * c);
-            return less > 0.f ? fmaxf(p - ex2((y - Q.top) * c) * less, 0.f) : p;
-        };
-        while (children) {
-            const int l = __ffs(children) - 1, t = base + l;
-            const float x = __shfl_sync(0xffffffffu, Elt<T>::f(x_mine), l);
-            const float y = __shfl_sync(0xffffffffu, Elt<T>::f(y_mine), l);
-            const float u = __shfl_sync(0xffffffffu, u_mine, l);
-            const int token = tokens[t];
-            bool again = false;
-            float p = 0.f;
-            if (greedy) {
-                if (token == top_at) went = t;
-            } else {
-                p = ex2((x - P.top) * c) * p_of;
-                float q = 1.f;
-                if (row.q) {
-                    q = ex2((y - Q.top) * c) * q_of;
-                    p = fmaxf(p - used * q, 0.f) * rcp(mass);
-                } else {
-                    for (int i = lane; i < dropped; i += 32) again |= removed[i] == token;
-                    again = __any_sync(0xffffffffu, again);
-                    p = again ? 0.f : p * rcp(mass);
-                }
-                if (p > 0.f && u * q < p) went = t;
-            }
-            if (went) break;
-            children &= children - 1;
-            if (!children) {
-                base += 32;
-                children = window(here, base);
-                if (children) look();
-            }
-            if (greedy) continue;
-            if (!row.q) {
-                if (!again && mass - p * mass > 0.f) {
-                    mass -= p * mass;
-                    __syncthreads();  // all warps have looked through the list
-                    if (tid == 0) removed[dropped] = token;
-                    ++dropped;
-                    __syncthreads();
-                }
-            } else if (!children) {
-                kept = used;
-                used += mass;
-            } else {
-                const float more = used + mass, less = more * q_of * P.sum;
+        Order o = next_order();
+        while (o.what == kMass || o.what == kPick) {
+            // what is left of p times P.sum, of which a draft's exponential takes `less`
+            auto left = [&](float x, float y) {
+                const float p = ex2((x - o.p_top) * c);
+                return o.less > 0.f ? fmaxf(p - ex2((y - o.q_top) * c) * o.less, 0.f) : p;
+            };
+            if (o.what == kMass) {
                 float sum = 0.f;
                 over([&](const float(&x8)[8], const float(&y8)[8], int, int) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) sum += left(x8[e], y8[e], less);
+                    for (int e = 0; e < 8; ++e) sum += left(x8[e], y8[e]);
                 });
-                if (row.single >= 0) sum += left(Elt<T>::f(row.one_p), Elt<T>::f(row.one_q), less);
+                if (single >= 0) sum += left(singles[held][0][tid], singles[held][1][tid]);
                 pick.key = warp_sum(sum);
-                const int from = exchange(kSum, stats, pick);
-                if (lost) break;
-                sum = all_picks[from].key * p_of;
-                if (sum > 0.f) {
-                    used = more;
-                    mass = sum;
-                }
-            }
-        }
-        if (lost) break;
-        if (went) {
-            here = went;
-            if (went == guess) {
-                row = ahead;
             } else {
-                row = row_at(went, false);
-                int after = went + 1;
-                if (window(went, after)) row = row_at(went, true);
-                cp_wait<0>();  // the guess is still on its way there
-                fetch(row, held ^ 1);
-            }
-            held ^= 1;
-            continue;
-        }
-        if (greedy) {
-            next = top_at;
-            break;
-        }
-        if (noise_span.head != row.sp.head) {  // another alignment than the first row's
-            cp_wait<0>();
-            fetch_noise(row.sp);
-            cp_commit();
-        }
-        cp_wait<0>();
-        noise_at = &row.sp;
-        for (;;) {
-            const float less = used * q_of * P.sum;
-            float best = 0.f;
-            int best_at = V;
-            // rejected certain drafts among the n places from `at`, a bit each
-            auto out_of = [&](int at, unsigned n) {
-                unsigned bits = 0;
-                for (int k = 0; k < dropped; ++k) {
-                    const unsigned d = unsigned(removed[k] - at);
-                    if (d < n) bits |= 1u << d;
+                cp_wait<0>();
+                if (!with_noise && noise_head != row.head) {  // another alignment than the first row's
+                    fetch_noise(row.head);
+                    cp_commit();
+                    cp_wait<0>();
                 }
-                return bits;
-            };
-            auto weigh = [&](float p, float e, int at, bool out) {
-                const float key = p * rcp(e);  // a NaN is never better, nor a number below 0
-                if (!out && (key > best || (key == best && key > 0.f && at < best_at))) {
-                    best = key;
-                    best_at = at;
-                }
-            };
-            over([&](const float(&x8)[8], const float(&y8)[8], int at, int slot) {
-                Eight<float> z;
-                z.take(noise_slots + 2 * slot * kThr);
-                float e8[8];
-                z.get(e8);
-                const unsigned out = out_of(at, 8);
+                with_noise = true;
+                float best = 0.f;
+                int best_at = V;
+                // rejected certain drafts among the n places from `at`, a bit each
+                auto out_of = [&](int at, unsigned n) {
+                    unsigned bits = 0;
+                    for (int k = 0; k < o.dropped; ++k) {
+                        const unsigned d = unsigned(removed[k] - at);
+                        if (d < n) bits |= 1u << d;
+                    }
+                    return bits;
+                };
+                auto weigh = [&](float p, float e, int at, bool out) {
+                    const float key = p * rcp(e);  // a NaN is never better, nor a number below 0
+                    if (!out && (key > best || (key == best && key > 0.f && at < best_at))) {
+                        best = key;
+                        best_at = at;
+                    }
+                };
+                over([&](const float(&x8)[8], const float(&y8)[8], int at, int slot) {
+                    float e8[8];
+                    take_slot<float>(noise_slots + 2 * slot * kThr, e8);
+                    const unsigned out = out_of(at, 8);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) weigh(left(x8[e], y8[e], less), e8[e], at + e, (out >> e) & 1u);
-            });
-            if (row.single >= 0)
-                weigh(left(Elt<T>::f(row.one_p), Elt<T>::f(row.one_q), less), noise[row.single], row.single,
-                      out_of(row.single, 1));
-            better_over_warp(best, best_at);
-            pick.key = best;
-            pick.at = best_at;
-            const int from = exchange(kPick, stats, pick);
-            if (lost) break;
-            if (all_picks[from].key > 0.f) {
-                next = all_picks[from].at;
-                break;
+                    for (int e = 0; e < 8; ++e) weigh(left(x8[e], y8[e]), e8[e], at + e, (out >> e) & 1u);
+                });
+                if (single >= 0)
+                    weigh(left(singles[held][0][tid], singles[held][1][tid]), noise[single], single, out_of(single, 1));
+                better_over_warp(best, best_at);
+                pick.key = best;
+                pick.at = best_at;
             }
-            if (kept < 0.f) {
-                if (rank == 0 && tid == 0) flag(a.dev_status, PA_DEV_BAD_VALUE);
-                break;
-            }
-            used = kept;  // nothing was left behind the last rejection: p is as it was
-            kept = -1.f;
+            send(stats, pick);
+            o = next_order();
         }
-        break;
+        if (o.what == kStop) break;
+        here = o.went;
+        if (here == guess) {
+            row = ahead;
+        } else {
+            int after = here + 1;
+            row = row_at(here, window(here, after) != 0);
+            cp_wait<0>();  // the guess is still on its way there
+            fetch(row, held ^ 1);
+        }
+        held ^= 1;
     }
     cp_wait<0>();  // nobody leaves with copies under way
-    if (rank == 0 && tid == 0) {
-        if (lost) flag(a.dev_status, PA_DEV_TIMEOUT);
-        a.accepted_cu[s + 1] = count;
-        a.next_tokens[s] = next;
-    }
 }
 
 // Joins the sequences' lists: the walk left counts in accepted_cu and each
@@ -715,7 +719,7 @@ template <typename T> cudaError_t launch_walk(const VerifyCall& c, cudaStream_t 
     while (size > 1 && (int64_t(c.num_seqs) * size > 152 || c.vocab / 8 < size * kThr / 2)) size /= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(c.num_seqs) * size);
-    cfg.blockDim = dim3(kThr);
+    cfg.blockDim = dim3(kThr + 32);
     cfg.dynamicSmemBytes = Stage<T>::kBytes;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
