@@ -114,6 +114,22 @@ template <typename T> __device__ inline void stage8(uint4* slot, const T* p) {
         *slot = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
+// Eight numbers off the 16-byte boundaries, out of the three units of four that
+// hold them where those lie inside [first, end).
+__device__ inline void read8(const float* p, const float* first, const float* end, float (&x)[8]) {
+    const int off = int(reinterpret_cast<uintptr_t>(p) & 15) / 4;
+    const float* q = p - off;
+    if (q < first || q + 12 > end) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __ldg(p + i);
+        return;
+    }
+    const float4 a = __ldg(reinterpret_cast<const float4*>(q)), b = __ldg(reinterpret_cast<const float4*>(q) + 1);
+    const float4 c = __ldg(reinterpret_cast<const float4*>(q) + 2);
+    const float y[11] = {a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = off == 1 ? y[i] : off == 2 ? y[i + 1] : y[i + 2];
+}
 template <typename T> __device__ inline void take_slot(const uint4* slot, float (&x)[8]) {
 #pragma unroll
     for (int i = 0; i < 8 / Elt<T>::kVec; ++i) vec_to_f32<T>(slot[i * kThr], x + i * Elt<T>::kVec);
@@ -267,8 +283,11 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
         }
         cp_commit();
     };
+    // random numbers off the 16-byte boundaries are read where they lie
+    auto noise_wide = [&](int head) { return wide_at(noise + head); };
     auto fetch_noise = [&](int head) {
         const int units = units_of(head);
+        if (!noise_wide(head)) return;
 #pragma unroll
         for (int k = 0; k < St::kSlots; ++k) {
             const int i = worker + k * workers;
@@ -500,7 +519,7 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
         auto stage_unit = [&](int slot, int i) {
             stage8<T>(slot_of(held, 0, slot), row.p + row.head + 8 * i);
             if (row.q) stage8<T>(slot_of(held, 1, slot), row.q + row.head + 8 * i);
-            if (with_noise) stage8<float>(noise_slots + 2 * slot * kThr, noise + row.head + 8 * i);
+            if (with_noise && noise_wide(row.head)) stage8<float>(noise_slots + 2 * slot * kThr, noise + row.head + 8 * i);
         };
         if (more && again_from_start) {
             cp_wait<0>();
@@ -617,7 +636,10 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
                 };
                 over([&](const float(&x8)[8], const float(&y8)[8], int at, int slot) {
                     float e8[8];
-                    take_slot<float>(noise_slots + 2 * slot * kThr, e8);
+                    if (noise_wide(row.head))
+                        take_slot<float>(noise_slots + 2 * slot * kThr, e8);
+                    else
+                        read8(noise + at, a.noise, a.noise + int64_t(a.num_seqs) * V, e8);
                     const unsigned out = out_of(at, 8);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) weigh(left(x8[e], y8[e]), e8[e], at + e, (out >> e) & 1u);
