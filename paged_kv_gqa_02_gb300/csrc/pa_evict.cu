@@ -1,16 +1,20 @@
 // pa_evict.cu -- eviction of the keys that gathered the least attention.
 //
-// Selection: a cluster of CTAs for each (sequence, kv head).  The weights are
-// taken as ordered 32-bit keys; four passes of eight bits find the key of the
-// last one that stays, from histograms that the cluster's CTAs add up, and how
-// many of its equals stay with it.  Then each CTA numbers the keys of its run
-// that stay, in order, and writes where they came from and what they weigh.
+// Selection: a CTA for each (sequence, kv head), a cluster of them where a
+// block table holds more than a CTA's registers.  A warp holds a run of up to 512
+// consecutive weights.  Taken as ordered 32-bit keys, four passes of eight bits
+// find the key of the last one that stays, from histograms in shared memory (the
+// cluster's added up), and how many of its equals stay with it.  Then ballots
+// number the keys that stay, in order; they leave where they came from and what
+// they weigh.  The passes are bound by latency: no weight is read twice.
 //
 // Move: key j comes from slot kept[j] >= j, so a CTA that takes a column of
 // the rows (some 16-byte units of K or of V of one kv head) can work its way up
 // tile by tile, reading a tile before it writes it: what a tile overwrites
-// belongs to keys that it or an earlier tile has read.  Columns do not meet, so
-// they are what the work is split over, and no second copy is needed.
+// belongs to keys that it or an earlier tile has read.  For the same reason the
+// next tile may be read before this one is written, so that its rows are on their
+// way meanwhile.  Columns do not meet, so they are what the work is split over, and
+// no second copy is needed.
 #include <cooperative_groups.h>
 
 #include "pa_ptx.cuh"
@@ -22,12 +26,14 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSelThr = 512;
+constexpr int kSelThr = 1024;
 constexpr int kSelWarps = kSelThr / 32;
+constexpr int kHeld = 16;                  // weights of a thread
+constexpr int kRun = kHeld * kSelThr;      // of a CTA
 constexpr int kSelMaxCluster = 8;
 constexpr int kBins = 256;
 constexpr int kMoveThr = 256;
-constexpr int kMovePer = 4;  // rows that a thread has in flight
+constexpr int kMovePer = 8;                // rows of a tile that a thread moves
 
 // What happens to a sequence.
 struct Cut {
@@ -55,44 +61,44 @@ __device__ inline uint32_t ordered(float w) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThr) evict_select(const EvictCall a) {
+template <bool kCluster> __global__ void __launch_bounds__(kSelThr) evict_select(const EvictCall a) {
     __shared__ int hist[kBins];
     __shared__ int totals[kBins];
     __shared__ int sums[2][kSelWarps];
-    __shared__ int mine[2];      // keys of the CTA's run that equal the last one; that stay for certain
-    __shared__ int found[2];     // a digit, and how many keys are still to be chosen among its own
-    __shared__ int shared_page;
+    __shared__ int mine[2];  // keys of the CTA's run that equal the last one; that stay for certain
+    __shared__ int found[2]; // a digit, and how many keys are still to be chosen among its own
     cg::cluster_group cluster = cg::this_cluster();
-    const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
+    const int C = kCluster ? int(cluster.num_blocks()) : 1, rank = kCluster ? int(cluster.block_rank()) : 0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto sync = [&] {
+        if (kCluster)
+            cluster.sync();
+        else
+            __syncthreads();
+    };
     pdl_wait_primary();
     pdl_launch_dependents();
     const int unit = int(blockIdx.x) / C;
     const int s = unit / a.Hkv, g = unit - s * a.Hkv;
     Cut c = cut_of(a, s);
-    if (tid == 0) shared_page = 0;
-    __syncthreads();
-    if (c.cut && a.refcounts) {  // pages that would be written
-        bool held = false;
+    bool held = false;  // a page that would be written has another holder
+    if (c.cut && a.refcounts)
         for (int b = c.first / a.c.page_size + tid; b < (c.n + a.c.page_size - 1) / a.c.page_size; b += kSelThr) {
             const int pg = a.c.block_tables[int64_t(s) * a.c.max_blocks + b];
             held |= pg >= 0 && pg < a.c.num_pages && a.refcounts[pg] > 1;
         }
-        if (held) shared_page = 1;
-    }
-    __syncthreads();
-    const bool kept_whole = shared_page != 0;
-    if (kept_whole) c.cut = false, c.n = c.L;
+    const bool whole = __syncthreads_or(held) != 0;
+    if (whole) c.cut = false, c.n = c.L;
     if (g == 0 && rank == 0 && tid == 0) {
         a.new_lens[s] = c.cut ? c.n : -1;
         if (c.bad) flag(a.dev_status, PA_DEV_BAD_LEN);
-        if (kept_whole) flag(a.dev_status, PA_DEV_SHARED_PAGE);
+        if (whole) flag(a.dev_status, PA_DEV_SHARED_PAGE);
     }
     const int64_t slots = int64_t(a.c.max_blocks) * a.c.page_size;
     const float* w = a.weights + unit * slots;
     float* w_out = a.weights_out + unit * slots;
     int32_t* kept = a.kept + unit * slots;
-    if (!c.cut) {
+    if (!c.cut) {  // the whole cluster
         for (int j = rank * kSelThr + tid; j < c.L; j += C * kSelThr) {
             kept[j] = j;
             w_out[j] = w[j];
@@ -102,38 +108,54 @@ __global__ void __launch_bounds__(kSelThr) evict_select(const EvictCall a) {
     // the middle: keys that stay by weight, `want` of them
     const int m0 = c.first, m1 = c.L - c.recent;
     int want = c.n - c.first - c.recent;
-    // the CTA's run of all slots
-    const int run = ((c.L + C - 1) / C + kSelThr - 1) / kSelThr * kSelThr;
-    const int lo = min(c.L, rank * run), hi = min(c.L, lo + run);
+    const bool any = want > 0;
+    // the CTA's run, the warp's in it: rows of 32 keys, the first kHeld of them held
+    const int run = (c.L + C - 1) / C, lo = min(c.L, rank * run), hi = min(c.L, lo + run);
+    const int rows = ((hi - lo + kSelWarps - 1) / kSelWarps + 31) / 32;
+    const int j0 = lo + warp * rows * 32 + lane;
+    float x[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) x[i] = i < rows && j0 + 32 * i < hi ? w[j0 + 32 * i] : 0.f;
+    // f(j, weight, in the run) for the warp's rows, whole warp
+    auto each = [&](auto&& f) {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            if (i < rows) f(j0 + 32 * i, x[i], j0 + 32 * i < hi);
+        for (int i = kHeld; i < rows; ++i) f(j0 + 32 * i, j0 + 32 * i < hi ? w[j0 + 32 * i] : 0.f, j0 + 32 * i < hi);
+    };
     uint32_t prefix = 0;  // the leading digits of the last key that stays
     for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int b = tid; b < kBins; b += kSelThr) hist[b] = 0;
+        if (tid < kBins) hist[tid] = 0;
         __syncthreads();
-        for (int j = max(lo, m0) + tid; j < min(hi, m1); j += kSelThr) {
-            const uint32_t k = ordered(w[j]);
-            if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255], 1);
+        each([&](int j, float v, bool in) {
+            const uint32_t k = ordered(v);
+            if (in && j >= m0 && j < m1 && (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))))
+                atomicAdd(&hist[(k >> shift) & 255], 1);
+        });
+        sync();
+        if (kCluster) {
+            if (tid < kBins) {
+                int n = 0;
+                for (int r = 0; r < C; ++r) n += cluster.map_shared_rank(hist, r)[tid];
+                totals[tid] = n;
+            }
+            __syncthreads();
         }
-        cluster.sync();
-        if (tid < kBins) {
-            int n = 0;
-            for (int r = 0; r < C; ++r) n += cluster.map_shared_rank(hist, r)[tid];
-            totals[tid] = n;
-        }
-        __syncthreads();
         if (warp == 0) {  // from the largest digit down: where the count reaches `want`
-            int above = 0, part[kBins / 32], sum = 0;
+            const int* all = kCluster ? totals : hist;
+            int part[kBins / 32], sum = 0;
 #pragma unroll
             for (int i = 0; i < kBins / 32; ++i) {
-                part[i] = totals[kBins - 1 - (lane * (kBins / 32) + i)];
+                part[i] = all[kBins - 1 - (lane * (kBins / 32) + i)];
                 sum += part[i];
             }
             int v = sum;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += x;
+                const int y = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += y;
             }
-            above = v - sum;
+            int above = v - sum;
             if (lane == 0) found[0] = 0, found[1] = 0;
             __syncwarp();
 #pragma unroll
@@ -145,64 +167,48 @@ __global__ void __launch_bounds__(kSelThr) evict_select(const EvictCall a) {
                 above += part[i];
             }
         }
-        cluster.sync();  // the others have read this histogram, the CTA its digit
+        sync();  // the others have read this histogram, the CTA its digit
         prefix |= uint32_t(found[0]) << shift;
         want = found[1];
-        __syncthreads();
     }
     // keys above the last one stay, and the first `want` equal to it; none where none is wanted
-    const bool any = c.n - c.first - c.recent > 0;
     auto sure = [&](int j, uint32_t k) { return j < m0 || j >= m1 || (any && k > prefix); };
     auto equal = [&](int j, uint32_t k) { return any && j >= m0 && j < m1 && k == prefix; };
-    int eq = 0, st = 0;
-    for (int j = lo + tid; j < hi; j += kSelThr) {
-        const uint32_t k = ordered(w[j]);
-        eq += equal(j, k);
-        st += sure(j, k);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        eq += __shfl_xor_sync(0xffffffffu, eq, o);
-        st += __shfl_xor_sync(0xffffffffu, st, o);
-    }
+    int eq = 0, st = 0;  // of the warp
+    each([&](int j, float v, bool in) {
+        const uint32_t k = ordered(v);
+        eq += __popc(__ballot_sync(0xffffffffu, in && equal(j, k)));
+        st += __popc(__ballot_sync(0xffffffffu, in && sure(j, k)));
+    });
     if (lane == 0) sums[0][warp] = eq, sums[1][warp] = st;
     __syncthreads();
-    if (tid < 2) {
-        int n = 0;
-        for (int i = 0; i < kSelWarps; ++i) n += sums[tid][i];
-        mine[tid] = n;
-    }
-    cluster.sync();
-    int eq_at = 0, st_at = 0;  // equals and certain ones before the tile
-    for (int r = 0; r < rank; ++r) {
-        eq_at += cluster.map_shared_rank(mine, r)[0];
-        st_at += cluster.map_shared_rank(mine, r)[1];
-    }
-    for (int j0 = lo; j0 < hi; j0 += kSelThr) {
-        const int j = j0 + tid;
-        const float x = j < hi ? w[j] : 0.f;
-        const uint32_t k = ordered(x);
-        const bool e = j < hi && equal(j, k), su = j < hi && sure(j, k);
-        const unsigned em = __ballot_sync(0xffffffffu, e), sm = __ballot_sync(0xffffffffu, su);
-        __syncthreads();
-        if (lane == 0) sums[0][warp] = __popc(em), sums[1][warp] = __popc(sm);
-        __syncthreads();
-        int eb = eq_at, sb = st_at;
-        for (int i = 0; i < kSelWarps; ++i) {
-            if (i < warp) eb += sums[0][i], sb += sums[1][i];
-            eq_at += sums[0][i];
-            st_at += sums[1][i];
+    // before the warp's run, in the CTA: each warp adds up for itself
+    int eq_at = lane < warp ? sums[0][lane] : 0, st_at = lane < warp ? sums[1][lane] : 0;
+    eq_at = __reduce_add_sync(0xffffffffu, eq_at);
+    st_at = __reduce_add_sync(0xffffffffu, st_at);
+    if (kCluster) {
+        if (tid == kSelThr - 1) mine[0] = eq_at + eq, mine[1] = st_at + st;
+        cluster.sync();
+        for (int r = 0; r < rank; ++r) {
+            eq_at += cluster.map_shared_rank(mine, r)[0];
+            st_at += cluster.map_shared_rank(mine, r)[1];
         }
-        const unsigned below = (1u << lane) - 1u;
-        eb += __popc(em & below);
-        sb += __popc(sm & below);
+    }
+    const unsigned below = (1u << lane) - 1u;
+    each([&](int j, float v, bool in) {
+        const uint32_t k = ordered(v);
+        const bool e = in && equal(j, k), su = in && sure(j, k);
+        const unsigned em = __ballot_sync(0xffffffffu, e), sm = __ballot_sync(0xffffffffu, su);
+        const int eb = eq_at + __popc(em & below), sb = st_at + __popc(sm & below);
         if (su || (e && eb < want)) {
             const int to = sb + min(eb, want);
             kept[to] = j;
-            w_out[to] = x;
+            w_out[to] = v;
         }
-    }
-    cluster.sync();  // nobody leaves while another may read its counts
+        eq_at += __popc(em);
+        st_at += __popc(sm);
+    });
+    if (kCluster) cluster.sync();  // nobody leaves while another may read its counts
 }
 
 struct MoveArgs {
@@ -237,31 +243,54 @@ __global__ void __launch_bounds__(kMoveThr) evict_move(const MoveArgs a) {
         if (pg < 0 || pg >= a.num_pages) return -1;
         return pg * a.page_stride + (slot & (a.page_size - 1)) * a.token_stride + off;
     };
-    for (int j0 = 0; j0 < n; j0 += per * kMovePer) {
-        uint4 x[kMovePer];
-        int64_t to[kMovePer];
+    // Three tiles under way: of the one after the next, where its rows come from;
+    // of the next, the rows; and the one that is written.
+    const int tile = per * kMovePer;
+    int from[kMovePer];
+    auto look = [&](int j0) {
 #pragma unroll
         for (int i = 0; i < kMovePer; ++i) {
             const int j = j0 + i * per + mine;
-            to[i] = -1;
-            if (j < n) {
-                const int from = kept[j];
-                if (from != j) {
-                    const int64_t src = place(from);
-                    to[i] = place(j);
-                    if (src < 0 || to[i] < 0) {
-                        flag(a.dev_status, PA_DEV_BAD_PAGE);
-                        to[i] = -1;
-                    } else {
-                        x[i] = pool[src];
-                    }
-                }
+            from[i] = j < n ? kept[j] : -1;
+        }
+    };
+    uint4 x[kMovePer];
+    bool moves[kMovePer];
+    auto read = [&](int j0) {
+#pragma unroll
+        for (int i = 0; i < kMovePer; ++i) {
+            const int j = j0 + i * per + mine;
+            moves[i] = from[i] >= 0 && from[i] != j;
+            if (moves[i]) {
+                const int64_t src = place(from[i]);
+                moves[i] = src >= 0;
+                if (src >= 0)
+                    x[i] = pool[src];
+                else
+                    flag(a.dev_status, PA_DEV_BAD_PAGE);
             }
         }
-        __syncthreads();  // the tile is read
+    };
+    look(0);
+    read(0);
+    look(tile);
+    for (int j0 = 0; j0 < n; j0 += tile) {
+        uint4 y[kMovePer];
+        bool due[kMovePer];
+#pragma unroll
+        for (int i = 0; i < kMovePer; ++i) y[i] = x[i], due[i] = moves[i];
+        read(j0 + tile);
+        look(j0 + 2 * tile);
+        __syncthreads();  // this tile is read, by all threads
 #pragma unroll
         for (int i = 0; i < kMovePer; ++i)
-            if (to[i] >= 0) pool[to[i]] = x[i];
+            if (due[i]) {
+                const int64_t to = place(j0 + i * per + mine);
+                if (to >= 0)
+                    pool[to] = y[i];
+                else
+                    flag(a.dev_status, PA_DEV_BAD_PAGE);
+            }
     }
 }
 
@@ -269,21 +298,27 @@ __global__ void __launch_bounds__(kMoveThr) evict_move(const MoveArgs a) {
 
 cudaError_t launch_evict(const EvictCall& c, cudaStream_t st) {
     const int units = c.num_seqs * c.Hkv;
-    int size = kSelMaxCluster;
-    while (size > 1 && int64_t(units) * size > 2 * 152) size /= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(units) * size);
-    cfg.blockDim = dim3(kSelThr);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = size;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select, c);
+    int size = 1;
+    const int64_t slots = int64_t(c.c.max_blocks) * c.c.page_size;
+    while (size < kSelMaxCluster && int64_t(size) * kRun < slots) size *= 2;
+    cudaError_t e;
+    if (size == 1) {
+        e = launch_pdl(evict_select<false>, dim3(unsigned(units)), dim3(kSelThr), 0, st, c);
+    } else {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(unsigned(units) * size);
+        cfg.blockDim = dim3(kSelThr);
+        cfg.stream = st;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = size;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        e = cudaLaunchKernelEx(&cfg, evict_select<true>, c);
+    }
     if (e != cudaSuccess) return e;
     MoveArgs a;
     a.k = static_cast<uint4*>(const_cast<void*>(c.c.k));
