@@ -8,13 +8,13 @@
 // number the keys that stay, in order; they leave where they came from and what
 // they weigh.  The passes are bound by latency: no weight is read twice.
 //
-// Move: key j comes from slot kept[j] >= j, so a CTA that takes a column of
-// the rows (some 16-byte units of K or of V of one kv head) can work its way up
-// tile by tile, reading a tile before it writes it: what a tile overwrites
-// belongs to keys that it or an earlier tile has read.  For the same reason the
-// next tile may be read before this one is written, so that its rows are on their
-// way meanwhile.  Columns do not meet, so they are what the work is split over, and
-// no second copy is needed.
+// Move: key j comes from slot kept[j] >= j, so a cluster of CTAs that has the
+// keys of one kv head, of K or of V, can work its way up tile by tile, reading a
+// tile before it writes it: what a tile overwrites belongs to keys that it or an
+// earlier tile has read.  A tile is 8 CTAs wide, so that a long sequence takes
+// few of them, and rows are read whole: columns of 32 or 64 bytes of them, which
+// need no cluster, were slower (86 and 100 us for eight long prompts, kernels
+// of both operations) as HBM reads scattered short pieces badly.
 #include <cooperative_groups.h>
 
 #include "pa_ptx.cuh"
@@ -34,6 +34,7 @@ constexpr int kSelMaxCluster = 8;
 constexpr int kBins = 256;
 constexpr int kMoveThr = 256;
 constexpr int kMovePer = 8;                // rows of a tile that a thread moves
+constexpr int kMoveCluster = 8;
 
 // What happens to a sequence.
 struct Cut {
@@ -220,77 +221,60 @@ struct MoveArgs {
     const int32_t* new_lens;
     uint32_t* dev_status;
     int32_t Hkv, max_blocks, page_size, page_shift, num_pages;
-    int32_t parts, width;  // columns of a row, and their 16-byte units
+    int32_t width;  // 16-byte units of a row
 };
 
-__global__ void __launch_bounds__(kMoveThr) evict_move(const MoveArgs a) {
+__global__ void __cluster_dims__(kMoveCluster, 1, 1) __launch_bounds__(kMoveThr) evict_move(const MoveArgs a) {
+    cg::cluster_group cluster = cg::this_cluster();
     pdl_wait_primary();
     pdl_launch_dependents();
-    int id = int(blockIdx.x);
-    const int part = id % a.parts;
-    id /= a.parts;
+    const int rank = int(cluster.block_rank()), id = int(blockIdx.x) / kMoveCluster;
     uint4* pool = id & 1 ? a.v : a.k;
     const int unit = id >> 1, s = unit / a.Hkv, g = unit - s * a.Hkv;
     const int n = a.new_lens[s];
-    if (n <= 0) return;
+    if (n <= 0) return;  // the whole cluster
     const int32_t* table = a.block_tables + int64_t(s) * a.max_blocks;
     const int32_t* kept = a.kept + unit * (int64_t(a.max_blocks) * a.page_size);
-    const int per = kMoveThr / a.width;  // rows of a step; a tile has kMovePer steps
-    const int sub = threadIdx.x % a.width, mine = threadIdx.x / a.width;
-    const int64_t off = g * a.head_stride + part * a.width + sub;
+    const int per = kMoveThr / a.width, tile = per * kMovePer * kMoveCluster;
+    const int mine = rank * kMovePer * per + int(threadIdx.x) / a.width;  // the thread's first row of a tile
+    const int64_t off = g * a.head_stride + int(threadIdx.x) % a.width;
     auto place = [&](int slot) -> int64_t {
         const int pg = table[slot >> a.page_shift];
         if (pg < 0 || pg >= a.num_pages) return -1;
         return pg * a.page_stride + (slot & (a.page_size - 1)) * a.token_stride + off;
     };
-    // Three tiles under way: of the one after the next, where its rows come from;
-    // of the next, the rows; and the one that is written.
-    const int tile = per * kMovePer;
-    int from[kMovePer];
+    int from[kMovePer];  // where the rows of the next tile come from
     auto look = [&](int j0) {
 #pragma unroll
         for (int i = 0; i < kMovePer; ++i) {
-            const int j = j0 + i * per + mine;
+            const int j = j0 + mine + i * per;
             from[i] = j < n ? kept[j] : -1;
         }
     };
-    uint4 x[kMovePer];
-    bool moves[kMovePer];
-    auto read = [&](int j0) {
+    look(0);
+    for (int j0 = 0; j0 < n; j0 += tile) {
+        uint4 x[kMovePer];
+        int64_t to[kMovePer];
 #pragma unroll
         for (int i = 0; i < kMovePer; ++i) {
-            const int j = j0 + i * per + mine;
-            moves[i] = from[i] >= 0 && from[i] != j;
-            if (moves[i]) {
+            const int j = j0 + mine + i * per;
+            to[i] = -1;
+            if (from[i] >= 0 && from[i] != j) {
                 const int64_t src = place(from[i]);
-                moves[i] = src >= 0;
-                if (src >= 0)
-                    x[i] = pool[src];
-                else
+                to[i] = place(j);
+                if (src < 0 || to[i] < 0) {
                     flag(a.dev_status, PA_DEV_BAD_PAGE);
+                    to[i] = -1;
+                } else {
+                    x[i] = pool[src];
+                }
             }
         }
-    };
-    look(0);
-    read(0);
-    look(tile);
-    for (int j0 = 0; j0 < n; j0 += tile) {
-        uint4 y[kMovePer];
-        bool due[kMovePer];
-#pragma unroll
-        for (int i = 0; i < kMovePer; ++i) y[i] = x[i], due[i] = moves[i];
-        read(j0 + tile);
-        look(j0 + 2 * tile);
-        __syncthreads();  // this tile is read, by all threads
+        look(j0 + tile);
+        cluster.sync();  // the tile is read
 #pragma unroll
         for (int i = 0; i < kMovePer; ++i)
-            if (due[i]) {
-                const int64_t to = place(j0 + i * per + mine);
-                if (to >= 0)
-                    pool[to] = y[i];
-                else
-                    flag(a.dev_status, PA_DEV_BAD_PAGE);
-            }
+            if (to[i] >= 0) pool[to[i]] = x[i];
     }
 }
 
@@ -335,11 +319,8 @@ cudaError_t launch_evict(const EvictCall& c, cudaStream_t st) {
     a.page_size = c.c.page_size;
     a.page_shift = c.c.page_size == 16 ? 4 : 5;
     a.num_pages = c.c.num_pages;
-    const int row = c.D * c.elt_bytes / 16;  // 16-byte units, a power of two from 8 to 64
-    a.width = row;
-    while (a.width > 4 && int64_t(units) * 2 * (row / a.width) < 2 * 152) a.width /= 2;  // a column is 64 bytes at least
-    a.parts = row / a.width;
-    return launch_pdl(evict_move, dim3(unsigned(units) * 2 * a.parts), dim3(kMoveThr), 0, st, a);
+    a.width = c.D * c.elt_bytes / 16;  // a power of two from 8 to 64
+    return launch_pdl(evict_move, dim3(unsigned(units) * 2 * kMoveCluster), dim3(kMoveThr), 0, st, a);
 }
 
 }  // namespace pa
