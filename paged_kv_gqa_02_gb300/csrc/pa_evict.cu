@@ -2,8 +2,8 @@
 //
 // Selection: a CTA for each (sequence, kv head), a cluster of them where a
 // block table holds more than a CTA's registers.  A warp holds a run of up to 512
-// consecutive weights.  Taken as ordered 32-bit keys, four passes of eight bits
-// find the key of the last one that stays, from histograms in shared memory (the
+// consecutive weights.  Taken as ordered 32-bit keys, three passes of eleven
+// bits find the key of the last one that stays, from histograms in shared memory (the
 // cluster's added up), and how many of its equals stay with it.  Then ballots
 // number the keys that stay, in order; they leave where they came from and what
 // they weigh.  The passes are bound by latency: no weight is read twice.
@@ -31,10 +31,12 @@ constexpr int kSelWarps = kSelThr / 32;
 constexpr int kHeld = 16;                  // weights of a thread
 constexpr int kRun = kHeld * kSelThr;      // of a CTA
 constexpr int kSelMaxCluster = 8;
-constexpr int kBins = 256;
+constexpr int kDigit = 11;                 // bits of a pass, the last one's fewer
+constexpr int kBins = 1 << kDigit;
 constexpr int kMoveThr = 256;
-constexpr int kMovePer = 8;                // rows of a tile that a thread moves
+constexpr int kMovePer = 4;                // rows of a tile that a thread moves
 constexpr int kMoveCluster = 8;
+constexpr int kMoveWidth = 8;              // 16-byte units of a row that a cluster moves
 
 // What happens to a sequence.
 struct Cut {
@@ -64,7 +66,6 @@ __device__ inline uint32_t ordered(float w) {
 
 template <bool kCluster> __global__ void __launch_bounds__(kSelThr) evict_select(const EvictCall a) {
     __shared__ int hist[kBins];
-    __shared__ int totals[kBins];
     __shared__ int sums[2][kSelWarps];
     __shared__ int mine[2];  // keys of the CTA's run that equal the last one; that stay for certain
     __shared__ int found[2]; // a digit, and how many keys are still to be chosen among its own
@@ -82,6 +83,17 @@ template <bool kCluster> __global__ void __launch_bounds__(kSelThr) evict_select
     const int unit = int(blockIdx.x) / C;
     const int s = unit / a.Hkv, g = unit - s * a.Hkv;
     Cut c = cut_of(a, s);
+    const int64_t slots = int64_t(a.c.max_blocks) * a.c.page_size;
+    const float* w = a.weights + unit * slots;
+    float* w_out = a.weights_out + unit * slots;
+    int32_t* kept = a.kept + unit * slots;
+    // the CTA's run, the warp's in it: rows of 32 keys, the first kHeld of them held
+    const int run = (c.L + C - 1) / C, lo = min(c.L, rank * run), hi = min(c.L, lo + run);
+    const int rows = ((hi - lo + kSelWarps - 1) / kSelWarps + 31) / 32;
+    const int j0 = lo + warp * rows * 32 + lane;
+    float x[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) x[i] = c.cut && i < rows && j0 + 32 * i < hi ? w[j0 + 32 * i] : 0.f;
     bool held = false;  // a page that would be written has another holder
     if (c.cut && a.refcounts)
         for (int b = c.first / a.c.page_size + tid; b < (c.n + a.c.page_size - 1) / a.c.page_size; b += kSelThr) {
@@ -95,10 +107,6 @@ template <bool kCluster> __global__ void __launch_bounds__(kSelThr) evict_select
         if (c.bad) flag(a.dev_status, PA_DEV_BAD_LEN);
         if (whole) flag(a.dev_status, PA_DEV_SHARED_PAGE);
     }
-    const int64_t slots = int64_t(a.c.max_blocks) * a.c.page_size;
-    const float* w = a.weights + unit * slots;
-    float* w_out = a.weights_out + unit * slots;
-    int32_t* kept = a.kept + unit * slots;
     if (!c.cut) {  // the whole cluster
         for (int j = rank * kSelThr + tid; j < c.L; j += C * kSelThr) {
             kept[j] = j;
@@ -110,13 +118,6 @@ template <bool kCluster> __global__ void __launch_bounds__(kSelThr) evict_select
     const int m0 = c.first, m1 = c.L - c.recent;
     int want = c.n - c.first - c.recent;
     const bool any = want > 0;
-    // the CTA's run, the warp's in it: rows of 32 keys, the first kHeld of them held
-    const int run = (c.L + C - 1) / C, lo = min(c.L, rank * run), hi = min(c.L, lo + run);
-    const int rows = ((hi - lo + kSelWarps - 1) / kSelWarps + 31) / 32;
-    const int j0 = lo + warp * rows * 32 + lane;
-    float x[kHeld];
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) x[i] = i < rows && j0 + 32 * i < hi ? w[j0 + 32 * i] : 0.f;
     // f(j, weight, in the run) for the warp's rows, whole warp
     auto each = [&](auto&& f) {
 #pragma unroll
@@ -125,48 +126,47 @@ template <bool kCluster> __global__ void __launch_bounds__(kSelThr) evict_select
         for (int i = kHeld; i < rows; ++i) f(j0 + 32 * i, j0 + 32 * i < hi ? w[j0 + 32 * i] : 0.f, j0 + 32 * i < hi);
     };
     uint32_t prefix = 0;  // the leading digits of the last key that stays
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < kBins) hist[tid] = 0;
+    for (int top = 32; top > 0; top -= kDigit) {  // bits top - kDigit .. top - 1
+        const int shift = max(0, top - kDigit);
+        const uint32_t mask = (1u << (top - shift)) - 1u;
+        for (int b = tid; b < kBins; b += kSelThr) hist[b] = 0;
         __syncthreads();
         each([&](int j, float v, bool in) {
             const uint32_t k = ordered(v);
-            if (in && j >= m0 && j < m1 && (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))))
-                atomicAdd(&hist[(k >> shift) & 255], 1);
+            if (in && j >= m0 && j < m1 && (top == 32 || (k >> top) == (prefix >> top)))
+                atomicAdd(&hist[(k >> shift) & mask], 1);
         });
         sync();
-        if (kCluster) {
-            if (tid < kBins) {
-                int n = 0;
-                for (int r = 0; r < C; ++r) n += cluster.map_shared_rank(hist, r)[tid];
-                totals[tid] = n;
+        // from the largest digit down: where the count reaches `want`; a thread has two digits
+        constexpr int kMine = kBins / kSelThr;
+        int part[kMine], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int bin = kBins - 1 - (kMine * tid + i);
+            part[i] = hist[bin];
+            if (kCluster) {
+                part[i] = 0;
+                for (int r = 0; r < C; ++r) part[i] += cluster.map_shared_rank(hist, r)[bin];
             }
-            __syncthreads();
+            sum += part[i];
         }
-        if (warp == 0) {  // from the largest digit down: where the count reaches `want`
-            const int* all = kCluster ? totals : hist;
-            int part[kBins / 32], sum = 0;
+        int v = sum;
 #pragma unroll
-            for (int i = 0; i < kBins / 32; ++i) {
-                part[i] = all[kBins - 1 - (lane * (kBins / 32) + i)];
-                sum += part[i];
-            }
-            int v = sum;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        if (lane == 31) sums[0][warp] = v;
+        if (tid == 0) found[0] = 0, found[1] = 0;
+        __syncthreads();
+        int above = v - sum + __reduce_add_sync(0xffffffffu, lane < warp ? sums[0][lane] : 0);
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += y;
+        for (int i = 0; i < kMine; ++i) {
+            if (above < want && want <= above + part[i]) {
+                found[0] = kBins - 1 - (kMine * tid + i);
+                found[1] = want - above;
             }
-            int above = v - sum;
-            if (lane == 0) found[0] = 0, found[1] = 0;
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < kBins / 32; ++i) {
-                if (above < want && want <= above + part[i]) {
-                    found[0] = kBins - 1 - (lane * (kBins / 32) + i);
-                    found[1] = want - above;
-                }
-                above += part[i];
-            }
+            above += part[i];
         }
         sync();  // the others have read this histogram, the CTA its digit
         prefix |= uint32_t(found[0]) << shift;
@@ -221,14 +221,17 @@ struct MoveArgs {
     const int32_t* new_lens;
     uint32_t* dev_status;
     int32_t Hkv, max_blocks, page_size, page_shift, num_pages;
-    int32_t width;  // 16-byte units of a row
+    int32_t parts, width;  // columns of a row, and their 16-byte units
 };
 
 __global__ void __cluster_dims__(kMoveCluster, 1, 1) __launch_bounds__(kMoveThr) evict_move(const MoveArgs a) {
     cg::cluster_group cluster = cg::this_cluster();
     pdl_wait_primary();
     pdl_launch_dependents();
-    const int rank = int(cluster.block_rank()), id = int(blockIdx.x) / kMoveCluster;
+    const int rank = int(cluster.block_rank());
+    int id = int(blockIdx.x) / kMoveCluster;
+    const int part = id % a.parts;
+    id /= a.parts;
     uint4* pool = id & 1 ? a.v : a.k;
     const int unit = id >> 1, s = unit / a.Hkv, g = unit - s * a.Hkv;
     const int n = a.new_lens[s];
@@ -237,7 +240,7 @@ __global__ void __cluster_dims__(kMoveCluster, 1, 1) __launch_bounds__(kMoveThr)
     const int32_t* kept = a.kept + unit * (int64_t(a.max_blocks) * a.page_size);
     const int per = kMoveThr / a.width, tile = per * kMovePer * kMoveCluster;
     const int mine = rank * kMovePer * per + int(threadIdx.x) / a.width;  // the thread's first row of a tile
-    const int64_t off = g * a.head_stride + int(threadIdx.x) % a.width;
+    const int64_t off = g * a.head_stride + part * a.width + int(threadIdx.x) % a.width;
     auto place = [&](int slot) -> int64_t {
         const int pg = table[slot >> a.page_shift];
         if (pg < 0 || pg >= a.num_pages) return -1;
@@ -319,8 +322,10 @@ cudaError_t launch_evict(const EvictCall& c, cudaStream_t st) {
     a.page_size = c.c.page_size;
     a.page_shift = c.c.page_size == 16 ? 4 : 5;
     a.num_pages = c.c.num_pages;
-    a.width = c.D * c.elt_bytes / 16;  // a power of two from 8 to 64
-    return launch_pdl(evict_move, dim3(unsigned(units) * 2 * kMoveCluster), dim3(kMoveThr), 0, st, a);
+    const int row = c.D * c.elt_bytes / 16;  // 16-byte units, a power of two from 8 to 64
+    a.width = row < kMoveWidth ? row : kMoveWidth;
+    a.parts = row / a.width;
+    return launch_pdl(evict_move, dim3(unsigned(units) * 2 * a.parts * kMoveCluster), dim3(kMoveThr), 0, st, a);
 }
 
 }  // namespace pa
