@@ -68,7 +68,7 @@ template <bool kCluster> __global__ void __launch_bounds__(kSelThr) evict_select
     __shared__ int hist[kBins];
     __shared__ int sums[2][kSelWarps];
     __shared__ int mine[2];  // keys of the CTA's run that equal the last one; that stay for certain
-    __shared__ int found[2]; // a digit, and how many keys are still to be chosen among its own
+    __shared__ int found[3]; // a digit, how many keys are still to be chosen among its own, how many it has
     cg::cluster_group cluster = cg::this_cluster();
     const int C = kCluster ? int(cluster.num_blocks()) : 1, rank = kCluster ? int(cluster.block_rank()) : 0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -92,8 +92,9 @@ template <bool kCluster> __global__ void __launch_bounds__(kSelThr) evict_select
     const int rows = ((hi - lo + kSelWarps - 1) / kSelWarps + 31) / 32;
     const int j0 = lo + warp * rows * 32 + lane;
     float x[kHeld];
+    auto weight_of = [&](int i) { return c.cut && i < rows && j0 + 32 * i < hi ? w[j0 + 32 * i] : 0.f; };
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) x[i] = c.cut && i < rows && j0 + 32 * i < hi ? w[j0 + 32 * i] : 0.f;
+    for (int i = 0; i < kHeld; ++i) x[i] = weight_of(i);
     bool held = false;  // a page that would be written has another holder
     if (c.cut && a.refcounts)
         for (int b = c.first / a.c.page_size + tid; b < (c.n + a.c.page_size - 1) / a.c.page_size; b += kSelThr) {
@@ -118,12 +119,20 @@ template <bool kCluster> __global__ void __launch_bounds__(kSelThr) evict_select
     const int m0 = c.first, m1 = c.L - c.recent;
     int want = c.n - c.first - c.recent;
     const bool any = want > 0;
-    // f(j, weight, in the run) for the warp's rows, whole warp
+    // ordered weights; more than any of them for keys that stay anyway, 0 outside the run
+    auto key_of = [&](int i, float v) {
+        const int j = j0 + 32 * i;
+        return i >= rows || j >= hi ? 0u : j < m0 || j >= m1 ? 0xffffffffu : ordered(v);
+    };
+    uint32_t keys[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) keys[i] = key_of(i, x[i]);
+    // f(row, key) for the warp's rows, whole warp
     auto each = [&](auto&& f) {
 #pragma unroll
         for (int i = 0; i < kHeld; ++i)
-            if (i < rows) f(j0 + 32 * i, x[i], j0 + 32 * i < hi);
-        for (int i = kHeld; i < rows; ++i) f(j0 + 32 * i, j0 + 32 * i < hi ? w[j0 + 32 * i] : 0.f, j0 + 32 * i < hi);
+            if (i < rows) f(i, keys[i]);
+        for (int i = kHeld; i < rows; ++i) f(i, key_of(i, weight_of(i)));
     };
     uint32_t prefix = 0;  // the leading digits of the last key that stays
     for (int top = 32; top > 0; top -= kDigit) {  // bits top - kDigit .. top - 1
@@ -131,11 +140,14 @@ template <bool kCluster> __global__ void __launch_bounds__(kSelThr) evict_select
         const uint32_t mask = (1u << (top - shift)) - 1u;
         for (int b = tid; b < kBins; b += kSelThr) hist[b] = 0;
         __syncthreads();
-        each([&](int j, float v, bool in) {
-            const uint32_t k = ordered(v);
-            if (in && j >= m0 && j < m1 && (top == 32 || (k >> top) == (prefix >> top)))
-                atomicAdd(&hist[(k >> shift) & mask], 1);
-        });
+        if (top == 32)
+            each([&](int, uint32_t k) {
+                if (k + 1u > 1u) atomicAdd(&hist[k >> shift], 1);  // neither 0 nor the largest number
+            });
+        else
+            each([&](int, uint32_t k) {
+                if ((k ^ prefix) >> top == 0u) atomicAdd(&hist[(k >> shift) & mask], 1);
+            });
         sync();
         // from the largest digit down: where the count reaches `want`; a thread has two digits
         constexpr int kMine = kBins / kSelThr;
@@ -165,6 +177,7 @@ template <bool kCluster> __global__ void __launch_bounds__(kSelThr) evict_select
             if (above < want && want <= above + part[i]) {
                 found[0] = kBins - 1 - (kMine * tid + i);
                 found[1] = want - above;
+                found[2] = part[i];
             }
             above += part[i];
         }
@@ -173,14 +186,15 @@ template <bool kCluster> __global__ void __launch_bounds__(kSelThr) evict_select
         want = found[1];
     }
     // keys above the last one stay, and the first `want` equal to it; none where none is wanted
-    auto sure = [&](int j, uint32_t k) { return j < m0 || j >= m1 || (any && k > prefix); };
-    auto equal = [&](int j, uint32_t k) { return any && j >= m0 && j < m1 && k == prefix; };
+    const bool all_equal = any && want == found[2];  // all of its equals stay
+    if (!any) prefix = 0xfffffffeu;
     int eq = 0, st = 0;  // of the warp
-    each([&](int j, float v, bool in) {
-        const uint32_t k = ordered(v);
-        eq += __popc(__ballot_sync(0xffffffffu, in && equal(j, k)));
-        st += __popc(__ballot_sync(0xffffffffu, in && sure(j, k)));
+    each([&](int, uint32_t k) {
+        eq += k == prefix;
+        st += k > prefix;
     });
+    eq = __reduce_add_sync(0xffffffffu, eq);
+    st = __reduce_add_sync(0xffffffffu, st);
     if (lane == 0) sums[0][warp] = eq, sums[1][warp] = st;
     __syncthreads();
     // before the warp's run, in the CTA: each warp adds up for itself
@@ -196,19 +210,30 @@ template <bool kCluster> __global__ void __launch_bounds__(kSelThr) evict_select
         }
     }
     const unsigned below = (1u << lane) - 1u;
-    each([&](int j, float v, bool in) {
-        const uint32_t k = ordered(v);
-        const bool e = in && equal(j, k), su = in && sure(j, k);
-        const unsigned em = __ballot_sync(0xffffffffu, e), sm = __ballot_sync(0xffffffffu, su);
-        const int eb = eq_at + __popc(em & below), sb = st_at + __popc(sm & below);
-        if (su || (e && eb < want)) {
-            const int to = sb + min(eb, want);
-            kept[to] = j;
-            w_out[to] = v;
-        }
-        eq_at += __popc(em);
-        st_at += __popc(sm);
-    });
+    if (all_equal) {
+        int at = st_at + eq_at;
+        each([&](int i, uint32_t k) {
+            const unsigned m = __ballot_sync(0xffffffffu, k >= prefix);
+            if (k >= prefix) {
+                const int to = at + __popc(m & below);
+                kept[to] = j0 + 32 * i;
+                w_out[to] = w[j0 + 32 * i];
+            }
+            at += __popc(m);
+        });
+    } else {
+        each([&](int i, uint32_t k) {
+            const unsigned em = __ballot_sync(0xffffffffu, k == prefix), sm = __ballot_sync(0xffffffffu, k > prefix);
+            const int eb = eq_at + __popc(em & below), sb = st_at + __popc(sm & below);
+            if (k > prefix || (k == prefix && eb < want)) {
+                const int to = sb + min(eb, want);
+                kept[to] = j0 + 32 * i;
+                w_out[to] = w[j0 + 32 * i];
+            }
+            eq_at += __popc(em);
+            st_at += __popc(sm);
+        });
+    }
     if (kCluster) cluster.sync();  // nobody leaves while another may read its counts
 }
 
