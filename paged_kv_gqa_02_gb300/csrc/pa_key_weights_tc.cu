@@ -6,14 +6,18 @@
 // lanes, so a thread reduces its own lane's columns and nothing crosses lanes:
 //   statistics: A = 128 columns (128 / G rows of q, all G heads of the kv
 //               head), B = the keys; a running maximum and sum a lane
-//   gathering:  A = 128 keys, B = the columns; sum of 2^(s - m) / l a lane
+//   gathering:  A = 128 keys, B = the columns; sum of 2^(s - m - log2 l) a lane
 // So Q K^T is computed twice, and no score leaves the SM.
 //
 // Two CTAs an SM, each with four warps for the scores, one that loads (TMA) and
 // one that multiplies (two accumulators of 128 columns of tensor memory): while
 // one CTA begins or ends a unit, the other computes.  Exponentials bound the
 // kernel: a score takes a multiply-add, an exponential and an addition in each
-// pass, and 128 x 128 of them take longer than their product.
+// pass, and 128 x 128 of them take longer than their product.  A column's m and l
+// go into one number, m + log2 l, which all lanes read from shared memory: with
+// two, 16 bytes for two scores, those reads bounded the second pass (92 us against
+// the first's 59, four prompts of 2560 rows and less); its rounding is half a step
+// of a number near the scores, as theirs is.
 //
 // Units (an A tile with all its B tiles) are laid on a line, sequence by
 // sequence and kv head by kv head, each as long as it costs, and the line is cut
@@ -49,8 +53,8 @@ template <int D> struct Smem {
     static constexpr int kStages = D == 128 ? 2 : 4;
     static constexpr uint32_t kTileBytes = kTile * D * 2;
     static constexpr uint32_t kB = kTileBytes;
-    static constexpr uint32_t kStats = kB + kStages * kTileBytes;  // [2][64] of (-m, -m', 1/l, 1/l')
-    static constexpr uint32_t kLimits = kStats + 2 * 64 * 16;      // [2][128] last key that a column sees
+    static constexpr uint32_t kStats = kB + kStages * kTileBytes;  // [2][128] of -(m + log2 l)
+    static constexpr uint32_t kLimits = kStats + 2 * 128 * 4;      // [2][128] last key that a column sees
     static constexpr uint32_t kChunks = kLimits + 2 * 128 * 4;     // [2][4][2] lowest and highest of 32 columns'
     static constexpr uint32_t kBars = kChunks + 2 * 4 * 2 * 4;
     static constexpr int kNumBars = 2 + 2 * kStages + 6 + 1;
@@ -60,6 +64,7 @@ template <int D> struct Smem {
 struct WideArgs {
     KwArgs a;
     int32_t tq, workers, head_first;
+    float* logs;          // [total_rows][Hq] of m + log2 l, -infinity where a column saw nothing
     float2* parts_stats;  // [2 workers][128]
     float* parts_sums;    // [2 workers][128]
 };
@@ -216,6 +221,9 @@ __device__ inline float max3(float a, float b, float c) {
 __device__ inline uint64_t pair_of(uint32_t lo, uint32_t hi) {
     return pairs::pack(__uint_as_float(lo), __uint_as_float(hi));
 }
+
+// m + log2 l; -infinity for a column that saw nothing.
+__device__ inline float log_of(float m, float l) { return l == 0.f ? -INFINITY : m + log2f(l); }
 
 // 32 scores of a lane: the running maximum (base 2, scaled) and sum.
 __device__ inline void take(float& m, uint64_t& l, const uint32_t (&r)[32], float scale) {
@@ -386,7 +394,7 @@ __global__ void __launch_bounds__(kThr, kPerSm)
         }
         if (!ok && lane == 0) raise_abort(abort_flag, a.dev_status);
     } else {
-        float4* sm_stats = reinterpret_cast<float4*>(base + S::kStats);
+        float* sm_stats = reinterpret_cast<float*>(base + S::kStats);
         int* sm_limits = reinterpret_cast<int*>(base + S::kLimits);
         int* sm_chunks = reinterpret_cast<int*>(base + S::kChunks);
         const uint32_t lanes = uint32_t(warp) << 21;  // tensor-memory lanes 32 warp ..
@@ -397,7 +405,7 @@ __global__ void __launch_bounds__(kThr, kPerSm)
         for (int64_t x = x0; ok && x < x1;) {
             if (!next_part<kPass>(w, x, x1, lane, p)) continue;
             float m = kLowestScore, sum = 0.f;
-            uint64_t acc = 0;  // two sums
+            uint64_t acc = 0, acc2 = 0;  // two sums each
             const int32_t* table = a.block_tables + int64_t(p.s) * a.max_blocks;
             // statistics: the lane's column; gathering: the lane's key
             const int t = p.unit * w.tq + my_t;
@@ -411,9 +419,7 @@ __global__ void __launch_bounds__(kThr, kPerSm)
             }
             auto column = [&](int b) {  // the statistics of the thread's column of Q tile b
                 const int tt = b * w.tq + my_t;
-                float2 st = make_float2(0.f, 0.f);
-                if (tid < cols && tt < p.q.T) st = a.stats[int64_t(p.q.row0 + tt) * a.Hq + p.g * a.G + my_h];
-                return st;
+                return tid < cols && tt < p.q.T ? w.logs[int64_t(p.q.row0 + tt) * a.Hq + p.g * a.G + my_h] : -INFINITY;
             };
             auto pages = [&](int b) {  // a lane of PT: whether the tile's page is in the pool
                 const int at = b * PT + lane;
@@ -421,7 +427,7 @@ __global__ void __launch_bounds__(kThr, kPerSm)
                 if (lane < PT && at * P < p.q.L) pg = table[at];
                 return pg;
             };
-            float2 ahead = make_float2(0.f, 0.f);
+            float ahead = -INFINITY;
             int page_ahead = -1;
             if (kPass == 1)
                 ahead = column(p.b0);
@@ -432,10 +438,8 @@ __global__ void __launch_bounds__(kThr, kPerSm)
                 uint32_t page_bits = 0;
                 if (kPass == 1) {
                     const int tt = b * w.tq + my_t;
-                    const int lim = ahead.y != 0.f ? p.q.before + tt : -1;  // a NaN counts as seen
-                    float* st = reinterpret_cast<float*>(sm_stats + 64 * buf + tid / 2);
-                    st[tid & 1] = -ahead.x;
-                    st[2 + (tid & 1)] = ahead.y;
+                    const int lim = ahead == -INFINITY ? -1 : p.q.before + tt;  // a NaN counts as seen
+                    sm_stats[128 * buf + tid] = -ahead;
                     sm_limits[128 * buf + tid] = lim;
                     const int low = __reduce_min_sync(0xffffffffu, lim), high = __reduce_max_sync(0xffffffffu, lim);
                     if (lane == 0) {
@@ -485,35 +489,41 @@ __global__ void __launch_bounds__(kThr, kPerSm)
                     } else {
                         const int low = sm_chunks[8 * buf + 2 * c], high = sm_chunks[8 * buf + 2 * c + 1];
                         if (high < kTile * p.unit) continue;  // no column sees a key of the tile
-                        const float4* st = sm_stats + 64 * buf + 16 * c;
+                        const float4* st = reinterpret_cast<const float4*>(sm_stats + 128 * buf + 32 * c);
                         const uint64_t k = pairs::pack(a.scale_log2, a.scale_log2);
                         if (low >= kTile * p.unit + kTile - 1) {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                const float4 y = st[i / 2];
+                            for (int i = 0; i < 32; i += 4) {
+                                const float4 y = st[i / 4];
                                 const float2 e = pairs::unpack(pairs::fma(pair_of(v[i], v[i + 1]), k, pairs::pack(y.x, y.y)));
-                                acc = pairs::fma(pairs::pack(ex2(e.x), ex2(e.y)), pairs::pack(y.z, y.w), acc);
+                                const float2 f = pairs::unpack(pairs::fma(pair_of(v[i + 2], v[i + 3]), k, pairs::pack(y.z, y.w)));
+                                acc = pairs::add(acc, pairs::pack(ex2(e.x), ex2(e.y)));
+                                acc2 = pairs::add(acc2, pairs::pack(ex2(f.x), ex2(f.y)));
                             }
                         } else {
                             const int* lim = sm_limits + 128 * buf + 32 * c;
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                const float4 y = st[i / 2];
-                                const float2 e = pairs::unpack(pairs::fma(pair_of(v[i], v[i + 1]), k, pairs::pack(y.x, y.y)));
-                                if (key <= lim[i]) sum += ex2(e.x) * y.z;
-                                if (key <= lim[i + 1]) sum += ex2(e.y) * y.w;
+                            for (int i = 0; i < 32; i += 4) {
+                                const float4 y = st[i / 4];
+                                const int4 last4 = *reinterpret_cast<const int4*>(lim + i);
+                                const float e0 = ex2(fmaf(__uint_as_float(v[i]), a.scale_log2, y.x));
+                                const float e1 = ex2(fmaf(__uint_as_float(v[i + 1]), a.scale_log2, y.y));
+                                const float e2 = ex2(fmaf(__uint_as_float(v[i + 2]), a.scale_log2, y.z));
+                                const float e3 = ex2(fmaf(__uint_as_float(v[i + 3]), a.scale_log2, y.w));
+                                sum += (key <= last4.x ? e0 : 0.f) + (key <= last4.y ? e1 : 0.f);
+                                sum += (key <= last4.z ? e2 : 0.f) + (key <= last4.w ? e3 : 0.f);
                             }
                         }
                     }
                 }
             }
             if (!ok) break;
-            const float2 two = pairs::unpack(acc);
+            const float2 two = pairs::unpack(kPass == 0 ? acc : pairs::add(acc, acc2));
             if (kPass == 0) {
                 const float l = two.x + two.y;
                 if (p.whole) {
                     if (real)
-                        a.stats[int64_t(p.q.row0 + t) * a.Hq + p.g * a.G + my_h] = make_float2(m, kw_reciprocal(l));
+                        w.logs[int64_t(p.q.row0 + t) * a.Hq + p.g * a.G + my_h] = log_of(m, l);
                 } else {
                     w.parts_stats[(2 * int64_t(blockIdx.x) + p.begins) * kTile + tid] = make_float2(m, l);
                 }
@@ -568,7 +578,7 @@ template <int kPass> __global__ void __launch_bounds__(kTile) wide_join(const __
     if (kPass == 0) {
         const int t = p.unit * w.tq + tid / a.G;
         if (tid < w.tq * a.G && t < p.q.T)
-            a.stats[int64_t(p.q.row0 + t) * a.Hq + p.g * a.G + tid % a.G] = make_float2(m, kw_reciprocal(l));
+            w.logs[int64_t(p.q.row0 + t) * a.Hq + p.g * a.G + tid % a.G] = log_of(m, l);
     } else {
         const int key = kTile * p.unit + tid;
         if (key < p.q.L) {
@@ -604,6 +614,7 @@ cudaError_t launch_key_weights_tc(const KwArgs& a, pa_dtype dt, int D, int n_cta
     w.tq = kTile / a.G;
     w.workers = kPerSm * n_ctas;
     w.head_first = a.head_stride <= a.token_stride;
+    w.logs = reinterpret_cast<float*>(a.stats);
     w.parts_stats = static_cast<float2*>(parts);
     w.parts_sums = reinterpret_cast<float*>(w.parts_stats + size_t(2) * w.workers * kTile);
     CUtensorMap mq, mk;
