@@ -9,9 +9,12 @@
 //   gathering:  A = 128 keys, B = the columns; sum of 2^(s - m - log2 l) a lane
 // So Q K^T is computed twice, and no score leaves the SM.
 //
-// Two CTAs an SM, each with four warps for the scores, one that loads (TMA) and
-// one that multiplies (two accumulators of 128 columns of tensor memory): while
-// one CTA begins or ends a unit, the other computes.  Exponentials bound the
+// Two CTAs an SM, each with two groups of four warps for the scores, which take
+// the B tiles in turn, one warp that loads (TMA) and one that multiplies (two
+// accumulators of 128 columns of tensor memory, one a group): while one CTA
+// begins or ends a unit, the other computes, and four warps to a scheduler hide
+// one another's latencies (one group: 58 and 69 us for the passes of four prompts
+// of 2560 rows and less).  Exponentials bound the
 // kernel: a score takes a multiply-add, an exponential and an addition in each
 // pass, and 128 x 128 of them take longer than their product.  A column's m and l
 // go into one number, m + log2 l, which all lanes read from shared memory: with
@@ -39,8 +42,8 @@ namespace pa {
 namespace {
 
 constexpr int kTile = 128;
-constexpr int kThr = 192;
-constexpr int kLoadWarp = 4, kMmaWarp = 5;
+constexpr int kThr = 320;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr int kPerSm = 2;          // CTAs
 constexpr int kStart = 2;          // what beginning and ending a unit costs, in B tiles
 constexpr int kMinShare = 4;
@@ -53,11 +56,12 @@ template <int D> struct Smem {
     static constexpr int kStages = D == 128 ? 2 : 4;
     static constexpr uint32_t kTileBytes = kTile * D * 2;
     static constexpr uint32_t kB = kTileBytes;
-    static constexpr uint32_t kStats = kB + kStages * kTileBytes;  // [2][128] of -(m + log2 l)
-    static constexpr uint32_t kLimits = kStats + 2 * 128 * 4;      // [2][128] last key that a column sees
-    static constexpr uint32_t kChunks = kLimits + 2 * 128 * 4;     // [2][4][2] lowest and highest of 32 columns'
-    static constexpr uint32_t kBars = kChunks + 2 * 4 * 2 * 4;
-    static constexpr int kNumBars = 2 + 2 * kStages + 6 + 1;
+    static constexpr uint32_t kStats = kB + kStages * kTileBytes;  // [group][2][128] of -(m + log2 l)
+    static constexpr uint32_t kLimits = kStats + 4 * 128 * 4;      // [2][2][128] last key that a column sees
+    static constexpr uint32_t kChunks = kLimits + 4 * 128 * 4;     // [2][2][4][2] lowest and highest of 32 columns'
+    static constexpr uint32_t kHelp = kChunks + 4 * 4 * 2 * 4;     // [2][128] what a group leaves for the other
+    static constexpr uint32_t kBars = kHelp + 2 * 128 * 8;
+    static constexpr int kNumBars = 2 + 2 * kStages + 4 + 4 + 4 + 1;
     static constexpr uint32_t kBytes = 1024 + kBars + kNumBars * 8 + 16;
 };
 
@@ -74,7 +78,7 @@ struct Line {
     int T, L, before, row0;
     int flat, tri;      // units of equal length, then units in pairs
     int flat_cost;
-    int64_t pair, len;  // positions of a pair, of a kv head
+    int pair, len;      // positions of a pair, of a kv head (below 2^30: the host sees to that)
 };
 
 // Length of unit u.
@@ -97,101 +101,162 @@ template <int kPass> __device__ inline Line line_of(const WideArgs& w, int s) {
     q.before = k.L - k.T;
     if (k.T == 0) return q;
     const int nq = (k.T + w.tq - 1) / w.tq, nk = (k.L + kTile - 1) / kTile;
+    // (sums of twice 2^30 and a few tiles fit in 32 bits without a sign)
     if (kPass == 0) {
         q.tri = nq;
         // the sum of two floors is at most the floor of the sum
-        q.pair = 2 * kStart + (2 * int64_t(q.before) + int64_t(nq + 1) * w.tq + 2 * (kTile - 1)) / kTile;
+        q.pair = 2 * kStart + int((2u * unsigned(q.before) + unsigned(nq + 1) * w.tq + 2u * (kTile - 1)) / kTile);
     } else {
-        q.flat = int(min(int64_t(nk), (int64_t(q.before) + w.tq - 1) / kTile + 1));
+        q.flat = min(nk, (q.before + w.tq - 1) / kTile + 1);
         q.flat_cost = kStart + nq;
         q.tri = nk - q.flat;
-        q.pair = 2 * kStart + 2 * int64_t(nq) + 1 -
-                 (int64_t(kTile) * (2 * int64_t(q.flat) + q.tri - 1) - 2 * int64_t(q.before)) / w.tq;
+        if (q.tri)
+            q.pair = 2 * kStart + 2 * nq + 1 -
+                     int((unsigned(kTile) * (2u * q.flat + q.tri - 1u) - 2u * unsigned(q.before)) / w.tq);
     }
-    q.len = int64_t(q.flat) * q.flat_cost + int64_t((q.tri + 1) / 2) * q.pair;
+    q.len = q.flat * q.flat_cost + (q.tri + 1) / 2 * q.pair;
     return q;
 }
-template <int kPass> __device__ inline int64_t line_total(const WideArgs& w, int lane) {
-    int64_t n = 0;
-    for (int s = lane; s < w.a.num_seqs; s += 32) n += line_of<kPass>(w, s).len * w.a.Hkv;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    return n;
-}
-
-// A unit, or its part in a share: B tiles [b0, b1).
+// A unit, or its part in a share: B tiles [b0, b1).  Walks along the line: the
+// units of a kv head, head by head, sequence by sequence.
 struct Part {
     Line q;
     int s, g, unit;
     int64_t begin, end;  // the unit on the line
     int b0, b1;
     bool begins, whole;
+    // the place of the unit: its number among those of equal length, or its pair and which of it
+    int pair, second;
+    int64_t pair_end;
 };
 
-// The part of the share's end [x, x1) that lies in the unit at x (whole warp);
-// moves x behind it.  False where there is no tile in it.
+template <int kPass> __device__ inline void set_unit(const WideArgs& w, Part& p) {
+    if (p.pair < 0) {
+        p.end = p.begin + p.q.flat_cost;
+        return;
+    }
+    const int far = p.q.tri - 1 - p.pair;  // the longer one first
+    p.unit = p.q.flat + ((kPass == 0) == (p.second == 0) ? far : p.pair);
+    p.end = p.begin + kStart + tiles_of<kPass>(w, p.q, p.unit);
+}
+// The first unit of the kv head that begins at p.begin.
+template <int kPass> __device__ inline void first_unit(const WideArgs& w, Part& p) {
+    p.unit = 0;
+    p.pair = p.q.flat ? -1 : 0;
+    p.second = 0;
+    p.pair_end = p.begin + p.q.pair;
+    set_unit<kPass>(w, p);
+}
+// The unit behind p's; the line's end lies behind every share, so there is one
+// wherever a share goes on.
+template <int kPass> __device__ inline void next_unit(const WideArgs& w, Part& p) {
+    if (p.pair < 0 && p.unit + 1 < p.q.flat) {
+        p.begin = p.end;
+        ++p.unit;
+    } else if (p.pair >= 0 && !p.second && p.pair != p.q.tri - 1 - p.pair) {
+        p.begin = p.end;
+        p.second = 1;
+    } else if (p.pair + 1 < (p.q.tri + 1) / 2) {  // the first or the next pair
+        p.begin = p.pair < 0 ? p.end : p.pair_end;
+        ++p.pair;
+        p.second = 0;
+        p.pair_end = p.begin + p.q.pair;
+    } else {
+        p.begin = p.pair < 0 ? p.end : p.pair_end;
+        if (++p.g == w.a.Hkv) {
+            p.g = 0;
+            do p.q = line_of<kPass>(w, ++p.s);
+            while (p.q.len == 0 && p.s < w.a.num_seqs);
+        }
+        first_unit<kPass>(w, p);
+        return;
+    }
+    set_unit<kPass>(w, p);
+}
+
+// The share of worker i of a line (whole warp): its first place and, behind it,
+// its last; the unit at its first place.  False where the share is empty.
 template <int kPass>
-__device__ inline bool next_part(const WideArgs& w, int64_t& x, int64_t x1, int lane, Part& p) {
-    // the sequence and the place in it
-    int64_t in = x;
-    int s = 0;
-    for (int s0 = 0;; s0 += 32) {
-        const int64_t n = line_of<kPass>(w, s0 + lane).len * w.a.Hkv;
-        int64_t v = n;
+__device__ inline bool share_of(const WideArgs& w, int i, int lane, int64_t& share, int64_t& x0, int64_t& x1,
+                                int64_t& total, Part& p, bool at_end = false) {
+    // lengths of 32 sequences at a time, kept for the search where there are no more
+    int64_t v = 0, n = 0;
+    total = 0;
+    auto scan = [&](int s0) {
+        n = int64_t(line_of<kPass>(w, s0 + lane).len) * w.a.Hkv;
+        v = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
             if (lane >= o) v += y;
         }
+    };
+    for (int s0 = 0; s0 < w.a.num_seqs; s0 += 32) {
+        scan(s0);
+        total += __shfl_sync(0xffffffffu, v, 31);
+    }
+    const int64_t even = total + w.workers - 1;
+    share = (even >> 31) == 0 ? int64_t(unsigned(even) / unsigned(w.workers)) : even / w.workers;
+    if (share < kMinShare) share = kMinShare;
+    x0 = share * i;
+    x1 = min(total, x0 + share);
+    if (x0 >= x1) return false;
+    const int64_t x = at_end ? x1 - 1 : x0;
+    int64_t in = x;
+    p.s = 0;
+    for (int s0 = 0; s0 < w.a.num_seqs; s0 += 32) {
+        if (w.a.num_seqs > 32) scan(s0);
         const unsigned m = __ballot_sync(0xffffffffu, in < v);
         if (m) {
             const int l = __ffs(m) - 1;
-            s = s0 + l;
+            p.s = s0 + l;
             in -= __shfl_sync(0xffffffffu, v - n, l);
             break;
         }
         in -= __shfl_sync(0xffffffffu, v, 31);
-        if (s0 + 32 >= w.a.num_seqs) {  // x is below the total, so this is not reached
-            x = x1;
-            return false;
-        }
     }
-    p.q = line_of<kPass>(w, s);
-    p.s = s;
-    p.g = int(in / p.q.len);
-    int64_t off = in - int64_t(p.g) * p.q.len;
-    const int64_t flat_len = int64_t(p.q.flat) * p.q.flat_cost;
-    int tiles;
+    p.q = line_of<kPass>(w, p.s);
+    p.g = (in >> 31) == 0 ? int(unsigned(in) / unsigned(p.q.len)) : int(in / p.q.len);
+    int off = int(in - int64_t(p.g) * p.q.len);
+    const int flat_len = p.q.flat * p.q.flat_cost;
+    p.unit = 0;
+    p.second = 0;
     if (off < flat_len) {
-        p.unit = int(off / p.q.flat_cost);
-        off -= int64_t(p.unit) * p.q.flat_cost;
-        tiles = p.q.flat_cost - kStart;
+        p.pair = -1;
+        p.unit = off / p.q.flat_cost;
+        p.begin = x - (off - p.unit * p.q.flat_cost);
+        p.pair_end = 0;
+        set_unit<kPass>(w, p);
     } else {
         off -= flat_len;
-        const int i = int(off / p.q.pair), j = p.q.tri - 1 - i;
-        off -= int64_t(i) * p.q.pair;
-        // the longer one first
-        const int u0 = p.q.flat + (kPass == 0 ? j : i), u1 = p.q.flat + (kPass == 0 ? i : j);
-        p.unit = u0;
-        tiles = tiles_of<kPass>(w, p.q, u0);
-        if (off >= kStart + tiles) {
-            off -= kStart + tiles;
-            p.unit = u1;
-            tiles = i == j ? -kStart : tiles_of<kPass>(w, p.q, u1);
-            if (off >= kStart + tiles) {  // behind the pair's units
-                x += p.q.pair - (off + (kStart + tiles_of<kPass>(w, p.q, u0)));
-                return false;
-            }
+        p.pair = off / p.q.pair;
+        p.begin = x - (off - p.pair * p.q.pair);
+        p.pair_end = p.begin + p.q.pair;
+        set_unit<kPass>(w, p);
+        if (x >= p.end && p.pair != p.q.tri - 1 - p.pair) {
+            p.begin = p.end;
+            p.second = 1;
+            set_unit<kPass>(w, p);
         }
     }
-    p.begin = x - off;
-    p.end = p.begin + kStart + tiles;
-    p.begins = off == 0;
+    return true;
+}
+// The part of the share's end [x, x1) that lies in p's unit, or in the next one
+// where x is behind it; x moves behind the part.  False where there is no tile in it.
+template <int kPass>
+__device__ inline bool next_part(const WideArgs& w, int64_t& x, int64_t x1, Part& p) {
+    if (x >= p.end) {
+        next_unit<kPass>(w, p);
+        if (x < p.begin) x = p.begin;
+        if (x >= x1) return false;
+    }
     const int64_t stop = min(p.end, x1);
+    const int off = int(x - p.begin);
+    p.begins = off == 0;
     p.whole = p.begins && stop == p.end;
     const int first = first_of<kPass>(w, p.q, p.unit);
-    p.b0 = first + int(max(int64_t(0), off - kStart));
-    p.b1 = first + int(max(int64_t(0), stop - p.begin - kStart));
+    p.b0 = first + max(0, off - kStart);
+    p.b1 = first + max(0, int(stop - p.begin) - kStart);
     x = stop;
     return p.b1 > p.b0;
 }
@@ -226,22 +291,25 @@ __device__ inline uint64_t pair_of(uint32_t lo, uint32_t hi) {
 __device__ inline float log_of(float m, float l) { return l == 0.f ? -INFINITY : m + log2f(l); }
 
 // 32 scores of a lane: the running maximum (base 2, scaled) and sum.
-__device__ inline void take(float& m, uint64_t& l, const uint32_t (&r)[32], float scale) {
+__device__ inline void take(float& m, uint64_t& l, uint64_t& l2, const uint32_t (&r)[32], float scale) {
     float top = __uint_as_float(r[0]);
 #pragma unroll
     for (int i = 1; i < 31; i += 2) top = max3(top, __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
     top = fmaxf(top, __uint_as_float(r[31])) * scale;
     if (top > m) {
         const float down = ex2(m - top);
-        const float2 old = pairs::unpack(l);
-        l = pairs::pack(old.x * down, old.y * down);
+        const uint64_t down2 = pairs::pack(down, down);
+        l = pairs::mul(l, down2);
+        l2 = pairs::mul(l2, down2);
         m = top;
     }
     const uint64_t k = pairs::pack(scale, scale), minus = pairs::pack(-m, -m);
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
+    for (int i = 0; i < 32; i += 4) {
         const float2 x = pairs::unpack(pairs::fma(pair_of(r[i], r[i + 1]), k, minus));
+        const float2 y = pairs::unpack(pairs::fma(pair_of(r[i + 2], r[i + 3]), k, minus));
         l = pairs::add(l, pairs::pack(ex2(x.x), ex2(x.y)));
+        l2 = pairs::add(l2, pairs::pack(ex2(y.x), ex2(y.y)));
     }
 }
 
@@ -262,8 +330,10 @@ __global__ void __launch_bounds__(kThr, kPerSm)
     uint64_t* b_empty = b_full + kStages;
     uint64_t* s_full = b_empty + kStages;
     uint64_t* s_empty = s_full + 2;
-    uint64_t* st_full = s_empty + 2;  // gathering: the columns' statistics written
-    uint64_t* never = st_full + 2;  // never arrived on: the debug_timeout wait
+    uint64_t* st_full = s_empty + 2;  // [group][2], gathering: the columns' statistics written
+    uint64_t* help_full = st_full + 4;
+    uint64_t* help_empty = help_full + 2;
+    uint64_t* never = help_empty + 2;  // never arrived on: the debug_timeout wait
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + S::kNumBars);
     volatile uint32_t* abort_flag = tslot + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -277,22 +347,30 @@ __global__ void __launch_bounds__(kThr, kPerSm)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&s_empty[i], 4);
-            mbar_init(&st_full[i], 4);
+            mbar_init(&st_full[2 * i], 4);
+            mbar_init(&st_full[2 * i + 1], 4);
+            mbar_init(&help_full[i], 4);
+            mbar_init(&help_empty[i], 4);
         }
         mbar_init(never, 1);
         *abort_flag = 0u;
         mbar_fence_init();
     }
-    pdl_wait_primary();
-    pdl_launch_dependents();
-    if (kPass == 0 && blockIdx.x == 0)
-        for (int s = tid; s < a.num_seqs; s += kThr)
-            if (kw_seq(a, s).bad) flag(a.dev_status, PA_DEV_BAD_LEN);
-    const int64_t total = line_total<kPass>(w, lane);
-    int64_t share = (total + w.workers - 1) / w.workers;
-    if (share < kMinShare) share = kMinShare;
-    const int64_t x0 = share * blockIdx.x, x1 = min(total, x0 + share);
-    if (x0 >= x1) return;  // the whole CTA, before any barrier
+    if (kPass == 0) {
+        pdl_wait_primary();
+        pdl_launch_dependents();
+        if (blockIdx.x == 0)
+            for (int s = tid; s < a.num_seqs; s += kThr)
+                if (kw_seq(a, s).bad) flag(a.dev_status, PA_DEV_BAD_LEN);
+    }
+    int64_t share, x0, x1, total;
+    Part p;
+    const bool any = share_of<kPass>(w, blockIdx.x, lane, share, x0, x1, total, p);
+    if (kPass == 1) {  // the lengths were there before the first kernel let others start
+        pdl_wait_primary();
+        pdl_launch_dependents();
+    }
+    if (!any) return;  // the whole CTA, before any barrier
     if (warp == kMmaWarp) {
         tc::tmem_alloc(tslot, 256);
         tc::tmem_relinquish();
@@ -338,9 +416,8 @@ __global__ void __launch_bounds__(kThr, kPerSm)
                                 w.head_first ? 0 : p.g, pg);
         };
         int n = 0, parts = 0;
-        Part p;
         for (int64_t x = x0; ok && x < x1;) {
-            if (!next_part<kPass>(w, x, x1, lane, p)) continue;
+            if (!next_part<kPass>(w, x, x1, p)) continue;
             if (parts) ok = wait_warp(a_empty, (parts - 1) & 1, abort_flag);
             if (!ok) break;
             if (kPass == 0)
@@ -369,9 +446,8 @@ __global__ void __launch_bounds__(kThr, kPerSm)
         const uint32_t idesc = tc::idesc_f16(kTile, kTile, kBf16, false), hi = tc::desc_hi_sw128(1024);
         const uint32_t a_lo = tc::desc_lo(smem_u32(base), 16), b_lo = tc::desc_lo(smem_u32(base + S::kB), 16);
         int n = 0, parts = 0;
-        Part p;
         for (int64_t x = x0; ok && x < x1;) {
-            if (!next_part<kPass>(w, x, x1, lane, p)) continue;
+            if (!next_part<kPass>(w, x, x1, p)) continue;
             ok = wait_warp(a_full, parts & 1, abort_flag);
             ++parts;
             for (int b = p.b0; ok && b < p.b1; ++b, ++n) {
@@ -394,98 +470,92 @@ __global__ void __launch_bounds__(kThr, kPerSm)
         }
         if (!ok && lane == 0) raise_abort(abort_flag, a.dev_status);
     } else {
-        float* sm_stats = reinterpret_cast<float*>(base + S::kStats);
-        int* sm_limits = reinterpret_cast<int*>(base + S::kLimits);
-        int* sm_chunks = reinterpret_cast<int*>(base + S::kChunks);
-        const uint32_t lanes = uint32_t(warp) << 21;  // tensor-memory lanes 32 warp ..
+        const int group = warp >> 2, row = tid & 127;  // the group's accumulator and buffers, the thread's lane of A
+        float* sm_stats = reinterpret_cast<float*>(base + S::kStats) + 256 * group;
+        int* sm_limits = reinterpret_cast<int*>(base + S::kLimits) + 256 * group;
+        int* sm_chunks = reinterpret_cast<int*>(base + S::kChunks) + 16 * group;
+        float2* sm_help = reinterpret_cast<float2*>(base + S::kHelp);
+        const uint32_t acc_at = tm + 128 * group + (uint32_t(warp & 3) << 21);
         const int cols = w.tq * a.G;
-        const int my_t = tid / a.G, my_h = tid - my_t * a.G;
-        int n = 0;
-        Part p;
+        const int my_t = row / a.G, my_h = row - my_t * a.G;
+        int n = 0, seen = 0;           // tiles of the CTA before the part, of the group so far
+        int helped = 0, was_helped = 0;  // parts that the group left to the other, and the other to it
         for (int64_t x = x0; ok && x < x1;) {
-            if (!next_part<kPass>(w, x, x1, lane, p)) continue;
+            if (!next_part<kPass>(w, x, x1, p)) continue;
+            const int tiles = p.b1 - p.b0, first = (group + n) & 1;  // the group's first tile of the part
+            const bool ends = first == 0;  // it has the part's first tile and writes its result
+            n += tiles;
+            if (first >= tiles) continue;
             float m = kLowestScore, sum = 0.f;
             uint64_t acc = 0, acc2 = 0;  // two sums each
             const int32_t* table = a.block_tables + int64_t(p.s) * a.max_blocks;
             // statistics: the lane's column; gathering: the lane's key
             const int t = p.unit * w.tq + my_t;
-            const bool real = kPass == 0 && tid < cols && t < p.q.T;
-            const int last = p.q.before + t;
-            const int key = kTile * p.unit + tid;
-            bool there = false;
-            if (kPass == 1 && key < p.q.L) {
-                const int pg = table[key >> a.page_shift];
-                there = pg >= 0 && pg < a.num_pages;
-            }
-            auto column = [&](int b) {  // the statistics of the thread's column of Q tile b
+            const int key = kTile * p.unit + row;
+            auto column = [&](int b) {  // m + log2 l of the thread's column of Q tile b
                 const int tt = b * w.tq + my_t;
-                return tid < cols && tt < p.q.T ? w.logs[int64_t(p.q.row0 + tt) * a.Hq + p.g * a.G + my_h] : -INFINITY;
+                return row < cols && tt < p.q.T ? w.logs[int64_t(p.q.row0 + tt) * a.Hq + p.g * a.G + my_h] : -INFINITY;
             };
-            auto pages = [&](int b) {  // a lane of PT: whether the tile's page is in the pool
+            auto pages = [&](int b) {  // a lane of PT: the tile's page
                 const int at = b * PT + lane;
-                int pg = -1;
-                if (lane < PT && at * P < p.q.L) pg = table[at];
-                return pg;
+                return lane < PT && at * P < p.q.L ? table[at] : -1;
             };
             float ahead = -INFINITY;
             int page_ahead = -1;
             if (kPass == 1)
-                ahead = column(p.b0);
+                ahead = column(p.b0 + first);
             else
-                page_ahead = pages(p.b0);
-            for (int b = p.b0; b < p.b1; ++b, ++n) {
-                const int buf = n & 1;
+                page_ahead = pages(p.b0 + first);
+            for (int b = p.b0 + first; b < p.b1; b += 2, ++seen) {
+                const int buf = seen & 1;
                 uint32_t page_bits = 0;
                 if (kPass == 1) {
                     const int tt = b * w.tq + my_t;
                     const int lim = ahead == -INFINITY ? -1 : p.q.before + tt;  // a NaN counts as seen
-                    sm_stats[128 * buf + tid] = -ahead;
-                    sm_limits[128 * buf + tid] = lim;
+                    sm_stats[128 * buf + row] = -ahead;
+                    sm_limits[128 * buf + row] = lim;
                     const int low = __reduce_min_sync(0xffffffffu, lim), high = __reduce_max_sync(0xffffffffu, lim);
                     if (lane == 0) {
-                        sm_chunks[8 * buf + 2 * warp] = low;
-                        sm_chunks[8 * buf + 2 * warp + 1] = high;
+                        sm_chunks[8 * buf + 2 * (warp & 3)] = low;
+                        sm_chunks[8 * buf + 2 * (warp & 3) + 1] = high;
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&st_full[buf]);
-                    if (b + 1 < p.b1) ahead = column(b + 1);
-                    ok = wait_warp(&st_full[buf], (n >> 1) & 1, abort_flag);
+                    if (lane == 0) mbar_arrive(&st_full[2 * group + buf]);
+                    if (b + 2 < p.b1) ahead = column(b + 2);
+                    ok = wait_warp(&st_full[2 * group + buf], (seen >> 1) & 1, abort_flag);
                     if (!ok) break;
                 } else {
                     page_bits = __ballot_sync(0xffffffffu, page_ahead >= 0 && page_ahead < a.num_pages);
-                    if (b + 1 < p.b1) page_ahead = pages(b + 1);
+                    if (b + 2 < p.b1) page_ahead = pages(b + 2);
                 }
-                ok = wait_warp(&s_full[buf], (n >> 1) & 1, abort_flag);
+                ok = wait_warp(&s_full[group], seen & 1, abort_flag);
                 if (!ok) break;
                 tc::fence_after_sync();
-                uint32_t r[2][32];
-                tc::ld_32x32b_x32(tm + 128 * buf + lanes, r[0]);
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
+                    uint32_t v[32];
+                    tc::ld_32x32b_x32(acc_at + 32 * c, v);
                     tc::wait_ld();
-                    tc::reg_fence(r[c & 1]);
-                    if (c < 3)
-                        tc::ld_32x32b_x32(tm + 128 * buf + 32 * (c + 1) + lanes, r[(c + 1) & 1]);
-                    else {
+                    tc::reg_fence(v);
+                    if (c == 3) {
                         tc::fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&s_empty[buf]);
+                        if (lane == 0) mbar_arrive(&s_empty[group]);
                     }
-                    uint32_t(&v)[32] = r[c & 1];
                     if (kPass == 0) {
                         // keys 32 c .. 32 c + 31 of the tile: seen by all lanes, or a bit for each
                         const int k0 = kTile * b + 32 * c;
                         const uint32_t mine = P == 32 ? (page_bits >> c) & 1u : (page_bits >> (2 * c)) & 3u;
                         const bool all = mine == (P == 32 ? 1u : 3u) && k0 + 31 <= p.q.before + p.unit * w.tq;
                         if (!all) {
-                            const int seen = last - k0 + 1;
-                            uint32_t bits = seen >= 32 ? 0xffffffffu : seen <= 0 ? 0u : (1u << seen) - 1u;
+                            const int upto = p.q.before + t - k0 + 1;
+                            uint32_t bits = upto >= 32 ? 0xffffffffu : upto <= 0 ? 0u : (1u << upto) - 1u;
                             bits &= P == 32 ? (mine ? 0xffffffffu : 0u)
                                             : ((mine & 1u) ? 0xffffu : 0u) | ((mine & 2u) ? 0xffff0000u : 0u);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] = (bits >> i) & 1u ? v[i] : kNegInf;
                         }
-                        take(m, acc, v, a.scale_log2);
+                        take(m, acc, acc2, v, a.scale_log2);
                     } else {
                         const int low = sm_chunks[8 * buf + 2 * c], high = sm_chunks[8 * buf + 2 * c + 1];
                         if (high < kTile * p.unit) continue;  // no column sees a key of the tile
@@ -518,20 +588,43 @@ __global__ void __launch_bounds__(kThr, kPerSm)
                 }
             }
             if (!ok) break;
-            const float2 two = pairs::unpack(kPass == 0 ? acc : pairs::add(acc, acc2));
+            const float2 two = pairs::unpack(pairs::add(acc, acc2));
+            sum += two.x + two.y;
+            if (!ends) {  // leave it to the group that has the first tile
+                if (helped) ok = wait_warp(&help_empty[group], (helped - 1) & 1, abort_flag);
+                if (!ok) break;
+                ++helped;
+                sm_help[128 * group + row] = make_float2(m, sum);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&help_full[group]);
+                continue;
+            }
+            if (tiles > 1) {
+                ok = wait_warp(&help_full[group ^ 1], was_helped & 1, abort_flag);
+                if (!ok) break;
+                ++was_helped;
+                const float2 other = sm_help[128 * (group ^ 1) + row];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&help_empty[group ^ 1]);
+                if (kPass == 0)
+                    kw_join(m, sum, other.x, other.y);
+                else
+                    sum += other.y;
+            }
             if (kPass == 0) {
-                const float l = two.x + two.y;
-                if (p.whole) {
-                    if (real)
-                        w.logs[int64_t(p.q.row0 + t) * a.Hq + p.g * a.G + my_h] = log_of(m, l);
-                } else {
-                    w.parts_stats[(2 * int64_t(blockIdx.x) + p.begins) * kTile + tid] = make_float2(m, l);
-                }
+                if (!p.whole)
+                    w.parts_stats[(2 * int64_t(blockIdx.x) + p.begins) * kTile + row] = make_float2(m, sum);
+                else if (row < cols && t < p.q.T)
+                    w.logs[int64_t(p.q.row0 + t) * a.Hq + p.g * a.G + my_h] = log_of(m, sum);
             } else {
-                sum += two.x + two.y;
+                bool there = false;
+                if (key < p.q.L) {
+                    const int pg = table[key >> a.page_shift];
+                    there = pg >= 0 && pg < a.num_pages;
+                }
                 if (!there) sum = 0.f;
                 if (!p.whole) {
-                    w.parts_sums[(2 * int64_t(blockIdx.x) + p.begins) * kTile + tid] = sum;
+                    w.parts_sums[(2 * int64_t(blockIdx.x) + p.begins) * kTile + row] = sum;
                 } else if (key < p.q.L) {
                     float* to = a.weights + (int64_t(p.s) * a.Hkv + p.g) * a.slots + key;
                     if (a.decay > 0.f && key < p.q.before) sum += a.decay * *to;
@@ -552,24 +645,18 @@ __global__ void __launch_bounds__(kThr, kPerSm)
 // A CTA for each share: the unit that begins in it and ends behind it.
 template <int kPass> __global__ void __launch_bounds__(kTile) wide_join(const __grid_constant__ WideArgs w) {
     const KwArgs& a = w.a;
+    const int tid = threadIdx.x, lane = tid & 31;
+    int64_t share, x0, x1, total;
+    Part p;
+    // the unit at the share's last place; the lengths were there before the first kernel let others start
+    const bool any = share_of<kPass>(w, blockIdx.x, lane, share, x0, x1, total, p, true);
     pdl_wait_primary();
     pdl_launch_dependents();
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int64_t total = line_total<kPass>(w, lane);
-    int64_t share = (total + w.workers - 1) / w.workers;
-    if (share < kMinShare) share = kMinShare;
-    const int64_t x0 = share * blockIdx.x, x1 = min(total, x0 + share);
-    if (x1 >= total) return;
-    // the unit at the share's last place
-    int64_t x = x1 - 1;
-    Part p;
-    p.end = 0;
-    next_part<kPass>(w, x, x1, lane, p);
-    if (p.end <= x1 || p.begin < x0) return;  // none, whole, or another CTA's
+    if (!any || x1 >= total || p.end <= x1 || p.begin < x0) return;  // none, whole, or another CTA's
     float m = kLowestScore, l = 0.f;
-    for (int64_t i = blockIdx.x; i * share < p.end; ++i) {
+    for (int i = blockIdx.x; i < w.workers && i * share < p.end; ++i) {
         if (min(p.end, (i + 1) * share) <= p.begin + kStart) continue;  // no tile in this share
-        const int64_t slot = (2 * i + (i == blockIdx.x)) * kTile + tid;
+        const int slot = (2 * i + (i == int(blockIdx.x))) * kTile + tid;
         if (kPass == 0)
             kw_join(m, l, w.parts_stats[slot].x, w.parts_stats[slot].y);
         else

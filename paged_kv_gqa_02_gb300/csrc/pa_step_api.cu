@@ -29,6 +29,9 @@ pa_status check_key_weights(const pa_params* p, const pa_rows* r, pa::KeyWeights
     if (len > kMaxHistory) len = kMaxHistory;
     if (p->max_context_len && p->max_context_len < len) len = p->max_context_len;
     c->max_len = int(len);
+    // products of a kv head are numbered in tiles of at least 65 x 128, in 32 bits
+    if ((int64_t(c->r.max_rows) * (p->num_q_heads / p->num_kv_heads) / 64 + 8) * (len / 128 + 8) > (1 << 30))
+        return PA_ERR_UNSUPPORTED;
     c->dtype = p->q_dtype;
     c->Hq = p->num_q_heads;
     c->Hkv = p->num_kv_heads;
