@@ -56,12 +56,12 @@ template <int D> struct Smem {
     static constexpr int kStages = D == 128 ? 2 : 4;
     static constexpr uint32_t kTileBytes = kTile * D * 2;
     static constexpr uint32_t kB = kTileBytes;
-    static constexpr uint32_t kStats = kB + kStages * kTileBytes;  // [group][2][128] of -(m + log2 l)
-    static constexpr uint32_t kLimits = kStats + 4 * 128 * 4;      // [2][2][128] last key that a column sees
-    static constexpr uint32_t kChunks = kLimits + 4 * 128 * 4;     // [2][2][4][2] lowest and highest of 32 columns'
-    static constexpr uint32_t kHelp = kChunks + 4 * 4 * 2 * 4;     // [2][128] what a group leaves for the other
+    static constexpr uint32_t kStats = kB + kStages * kTileBytes;  // [group][3][128] of -(m + log2 l)
+    static constexpr uint32_t kLimits = kStats + 6 * 128 * 4;      // [2][3][128] last key that a column sees
+    static constexpr uint32_t kChunks = kLimits + 6 * 128 * 4;     // [2][3][4][2] lowest and highest of 32 columns'
+    static constexpr uint32_t kHelp = kChunks + 6 * 4 * 2 * 4;     // [2][128] what a group leaves for the other
     static constexpr uint32_t kBars = kHelp + 2 * 128 * 8;
-    static constexpr int kNumBars = 2 + 2 * kStages + 4 + 4 + 4 + 1;
+    static constexpr int kNumBars = 2 + 2 * kStages + 4 + 6 + 4 + 1;
     static constexpr uint32_t kBytes = 1024 + kBars + kNumBars * 8 + 16;
 };
 
@@ -330,8 +330,8 @@ __global__ void __launch_bounds__(kThr, kPerSm)
     uint64_t* b_empty = b_full + kStages;
     uint64_t* s_full = b_empty + kStages;
     uint64_t* s_empty = s_full + 2;
-    uint64_t* st_full = s_empty + 2;  // [group][2], gathering: the columns' statistics written
-    uint64_t* help_full = st_full + 4;
+    uint64_t* st_full = s_empty + 2;  // [group][3], gathering: the columns' statistics written
+    uint64_t* help_full = st_full + 6;
     uint64_t* help_empty = help_full + 2;
     uint64_t* never = help_empty + 2;  // never arrived on: the debug_timeout wait
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + S::kNumBars);
@@ -347,8 +347,7 @@ __global__ void __launch_bounds__(kThr, kPerSm)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&s_empty[i], 4);
-            mbar_init(&st_full[2 * i], 4);
-            mbar_init(&st_full[2 * i + 1], 4);
+            for (int j = 0; j < 3; ++j) mbar_init(&st_full[3 * i + j], 4);
             mbar_init(&help_full[i], 4);
             mbar_init(&help_empty[i], 4);
         }
@@ -471,14 +470,15 @@ __global__ void __launch_bounds__(kThr, kPerSm)
         if (!ok && lane == 0) raise_abort(abort_flag, a.dev_status);
     } else {
         const int group = warp >> 2, row = tid & 127;  // the group's accumulator and buffers, the thread's lane of A
-        float* sm_stats = reinterpret_cast<float*>(base + S::kStats) + 256 * group;
-        int* sm_limits = reinterpret_cast<int*>(base + S::kLimits) + 256 * group;
-        int* sm_chunks = reinterpret_cast<int*>(base + S::kChunks) + 16 * group;
+        float* sm_stats = reinterpret_cast<float*>(base + S::kStats) + 384 * group;
+        int* sm_limits = reinterpret_cast<int*>(base + S::kLimits) + 384 * group;
+        int* sm_chunks = reinterpret_cast<int*>(base + S::kChunks) + 24 * group;
         float2* sm_help = reinterpret_cast<float2*>(base + S::kHelp);
         const uint32_t acc_at = tm + 128 * group + (uint32_t(warp & 3) << 21);
         const int cols = w.tq * a.G;
         const int my_t = row / a.G, my_h = row - my_t * a.G;
         int n = 0, seen = 0;           // tiles of the CTA before the part, of the group so far
+        int buf = 0, turn = 0;         // seen % 3 and the parity of seen / 3
         int helped = 0, was_helped = 0;  // parts that the group left to the other, and the other to it
         for (int64_t x = x0; ok && x < x1;) {
             if (!next_part<kPass>(w, x, x1, p)) continue;
@@ -500,29 +500,38 @@ __global__ void __launch_bounds__(kThr, kPerSm)
                 const int at = b * PT + lane;
                 return lane < PT && at * P < p.q.L ? table[at] : -1;
             };
+            // The statistics of a tile's columns, to be read by the whole group: written
+            // a tile ahead.  Whoever writes a buffer has seen all warps begin the tile
+            // but one before, so nobody reads what stood in it three tiles ago.
+            auto show = [&](int b, float log, int to) {
+                const int lim = log == -INFINITY ? -1 : p.q.before + b * w.tq + my_t;  // a NaN counts as seen
+                sm_stats[128 * to + row] = -log;
+                sm_limits[128 * to + row] = lim;
+                const int low = __reduce_min_sync(0xffffffffu, lim), high = __reduce_max_sync(0xffffffffu, lim);
+                if (lane == 0) {
+                    sm_chunks[8 * to + 2 * (warp & 3)] = low;
+                    sm_chunks[8 * to + 2 * (warp & 3) + 1] = high;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&st_full[3 * group + to]);
+            };
             float ahead = -INFINITY;
             int page_ahead = -1;
-            if (kPass == 1)
-                ahead = column(p.b0 + first);
-            else
+            if (kPass == 1) {
+                const float log = column(p.b0 + first);
+                if (p.b0 + first + 2 < p.b1) ahead = column(p.b0 + first + 2);
+                show(p.b0 + first, log, buf);
+            } else {
                 page_ahead = pages(p.b0 + first);
+            }
             for (int b = p.b0 + first; b < p.b1; b += 2, ++seen) {
-                const int buf = seen & 1;
                 uint32_t page_bits = 0;
                 if (kPass == 1) {
-                    const int tt = b * w.tq + my_t;
-                    const int lim = ahead == -INFINITY ? -1 : p.q.before + tt;  // a NaN counts as seen
-                    sm_stats[128 * buf + row] = -ahead;
-                    sm_limits[128 * buf + row] = lim;
-                    const int low = __reduce_min_sync(0xffffffffu, lim), high = __reduce_max_sync(0xffffffffu, lim);
-                    if (lane == 0) {
-                        sm_chunks[8 * buf + 2 * (warp & 3)] = low;
-                        sm_chunks[8 * buf + 2 * (warp & 3) + 1] = high;
+                    if (b + 2 < p.b1) {
+                        show(b + 2, ahead, buf == 2 ? 0 : buf + 1);
+                        if (b + 4 < p.b1) ahead = column(b + 4);
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&st_full[2 * group + buf]);
-                    if (b + 2 < p.b1) ahead = column(b + 2);
-                    ok = wait_warp(&st_full[2 * group + buf], (seen >> 1) & 1, abort_flag);
+                    ok = wait_warp(&st_full[3 * group + buf], turn, abort_flag);
                     if (!ok) break;
                 } else {
                     page_bits = __ballot_sync(0xffffffffu, page_ahead >= 0 && page_ahead < a.num_pages);
@@ -585,6 +594,10 @@ __global__ void __launch_bounds__(kThr, kPerSm)
                             }
                         }
                     }
+                }
+                if (++buf == 3) {
+                    buf = 0;
+                    turn ^= 1;
                 }
             }
             if (!ok) break;
@@ -649,9 +662,10 @@ template <int kPass> __global__ void __launch_bounds__(kTile) wide_join(const __
     int64_t share, x0, x1, total;
     Part p;
     // the unit at the share's last place; the lengths were there before the first kernel let others start
+    if (kPass == 0) pdl_launch_dependents();  // the second pass reads nothing else before this kernel's end
     const bool any = share_of<kPass>(w, blockIdx.x, lane, share, x0, x1, total, p, true);
     pdl_wait_primary();
-    pdl_launch_dependents();
+    if (kPass == 1) pdl_launch_dependents();
     if (!any || x1 >= total || p.end <= x1 || p.begin < x0) return;  // none, whole, or another CTA's
     float m = kLowestScore, l = 0.f;
     for (int i = blockIdx.x; i < w.workers && i * share < p.end; ++i) {
