@@ -20,7 +20,7 @@ namespace pa {
 
 namespace {
 
-constexpr int kThr = 256;
+constexpr int kThr = 128;
 
 struct RotateArgs {
     const uint4* q;
@@ -43,6 +43,7 @@ struct RotateArgs {
     int32_t num_seqs, total_rows, max_rows, num_pages, max_blocks, page_size;
     int32_t Hq, Hkv;
     int32_t rot, table_rows, axes, end0, end1;  // pairs below end0 follow axis 0, below end1 axis 1
+    int32_t whole;  // both are multiples of eight
     int32_t parts;  // warps of a row
     float eps;
 };
@@ -124,8 +125,9 @@ template <typename T, int D, bool kMixed> __global__ void __launch_bounds__(kThr
         return;
     }
     if (turns) {
-        if (a.axes == 1) {
-            const float* t = a.table + int64_t(pos[0]) * a.rot + 8 * sub;
+        if (a.whole) {  // the lane's eight pairs follow one axis
+            const int where = 8 * sub < a.end0 ? pos[0] : 8 * sub < a.end1 ? pos[1] : pos[2];
+            const float* t = a.table + int64_t(where) * a.rot + 8 * sub;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float4 c = *reinterpret_cast<const float4*>(t + 4 * i);
@@ -329,8 +331,9 @@ cudaError_t launch_rotate(const RotateCall& c, cudaStream_t st) {
     a.rot = c.t.rotary_dim;
     a.table_rows = c.t.table_rows;
     a.axes = c.t.axes;
-    a.end0 = c.t.sections[0];
+    a.end0 = c.t.axes == 1 ? c.t.rotary_dim / 2 : c.t.sections[0];
     a.end1 = a.end0 + c.t.sections[1];
+    a.whole = a.end0 % 8 == 0 && a.end1 % 8 == 0;
     a.eps = c.t.eps;
     // a row to a warp, or to several while the warps are fewer than eight an SM
     const int wide = 512 / c.D;  // heads of a group
