@@ -154,3 +154,49 @@ def test_captured_and_replayed():
             for g in range(2):
                 want = stays(w[s, g].tolist(), lens[s], n[s], 2, 3) if cut else list(range(lens[s]))
                 assert kept[s, g, :len(want)].tolist() == want
+
+
+def test_pages_far_apart():
+    """Pages whose offsets, in elements, pass 32 bits."""
+    gen = torch.Generator().manual_seed(4)
+    pages, page, hkv, d, stride = 36, 16, 2, 64, 1 << 26
+    pools = [torch.zeros(pages * stride, dtype=torch.bfloat16, device="cuda").as_strided((pages, page, hkv, d), (stride, hkv * d, d, 1)) for _ in range(2)]
+    for x in pools:
+        x.copy_(torch.randn(pages, page, hkv, d, generator=gen))
+    old = [x.clone() for x in pools]
+    table = torch.randperm(pages, generator=gen).to(torch.int32).cuda().reshape(1, pages)
+    p = ops.make_params(num_seqs=1, num_q_heads=2, num_kv_heads=hkv, head_dim=d, page_size=page, num_pages=pages, max_blocks_per_seq=pages,
+                        max_context_len=pages * page, dtype="bf16", strides=(stride, 0, 0))
+    w = torch.rand(1, hkv, pages * page, generator=gen).cuda()
+    _, kept, new = ops.evict(p, pools[0], pools[1], table, torch.tensor([570], dtype=torch.int32, device="cuda"), w,
+                             torch.tensor([300], dtype=torch.int32, device="cuda"), first=3, recent=10)
+    assert new.tolist() == [300]
+    to = torch.arange(300, device="cuda")
+    t = table[0].long()
+    for g in range(hkv):
+        src = torch.tensor(stays(w[0, g].tolist(), 570, 300, 3, 10), device="cuda")
+        assert torch.equal(kept[0, g, :300].long(), src)
+        for x, y in zip(pools, old):
+            assert torch.equal(x[t[to // page], to % page, g], y[t[src // page], src % page, g])
+
+
+@pytest.mark.parametrize("blocks,L", [(2048, 30000), (20000, 300000)])
+def test_tables_longer_than_a_cta_holds(blocks, L):
+    """Clusters of two and eight CTAs, the latter with more weights than their registers hold."""
+    page, pages = 16, -(-L // 16)
+    p = ops.make_params(num_seqs=1, num_q_heads=1, num_kv_heads=1, head_dim=64, page_size=page, num_pages=pages, max_blocks_per_seq=blocks,
+                        max_context_len=blocks * page, dtype="bf16")
+    gen = torch.Generator().manual_seed(5)
+    pool = [torch.randn(pages, page, 1, 64, generator=gen).to(torch.bfloat16).cuda() for _ in range(2)]
+    old = [x.clone() for x in pool]
+    table = torch.full((1, blocks), -1, dtype=torch.int32, device="cuda")
+    table[0, :pages] = torch.randperm(pages, generator=gen).to(torch.int32).cuda()
+    w = (torch.rand(1, 1, blocks * page, generator=gen) * 1000).round().cuda()  # many equal ones
+    n = L // 3
+    _, kept, new = ops.evict(p, pool[0], pool[1], table, torch.tensor([L], dtype=torch.int32, device="cuda"), w,
+                             torch.tensor([n], dtype=torch.int32, device="cuda"), first=5, recent=77)
+    src = torch.tensor(stays(w[0, 0].tolist(), L, n, 5, 77), device="cuda")
+    assert new.tolist() == [n] and torch.equal(kept[0, 0, :n].long(), src)
+    to, t = torch.arange(n, device="cuda"), table[0].long()
+    for x, y in zip(pool, old):
+        assert torch.equal(x[t[to // page], to % page], y[t[src // page], src % page])

@@ -196,3 +196,66 @@ def test_two_streams_and_repeats_are_bit_equal():
 def _on(st, p, r, q, starts, pool, w):
     st.wait_stream(torch.cuda.current_stream())
     return ops.key_weights(p, r, q, starts, pool.k, pool.tables, pool.context, w, stream=st)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_many_sequences(rows, dtype):
+    """More sequences than a warp has lanes, some without rows, one longer than the host's bound."""
+    gen = torch.Generator().manual_seed(11)
+    counts = [0 if i % 7 == 3 else 1 + (i * 5) % rows for i in range(75)]
+    lens = [n + (i * 37) % 400 for i, n in enumerate(counts)]
+    pool = Pool(lens, 16, 2, 64, dtype, gen)
+    q = torch.randn(sum(counts), 6, 64, generator=gen).to(DT[dtype]).cuda()
+    weights = fresh(pool, gen)
+    clean = weights.clone()
+    p, r = pool.params(6), ops.make_rows(sum(counts), rows)
+    want, tol = reference(q, counts, pool, clean, 0.5, p.scale)
+    got = ops.key_weights(p, r, q, cu(counts), pool.k, pool.tables, pool.context, weights.clone(), decay=0.5)
+    for s, (n, L) in enumerate(zip(counts, lens)):
+        assert_close(got[s, :, :L], (want if n else clean.double())[s, :, :L], tol[s, :, :L], f"sequence {s}") if L else None
+    p.max_context_len = 250
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    bounded = ops.key_weights(p, r, q, cu(counts), pool.k, pool.tables, pool.context, weights.clone(), decay=0.5, dev_status=status)
+    assert int(status) == ops.PA_DEV_BAD_LEN
+    for s, L in enumerate(lens):
+        assert_close(bounded[s, :, :L], (clean.double() if L > 250 else want)[s, :, :L], tol[s, :, :L], f"bounded {s}") if L else None
+
+
+@pytest.mark.parametrize("rows", [1, 100])
+def test_pages_far_apart(rows):
+    """Pages whose offsets, in elements, pass 32 bits."""
+    gen = torch.Generator().manual_seed(12)
+    pages, page, hkv, d, stride = 36, 32, 2, 128, 1 << 26
+    store = torch.zeros(pages * stride, dtype=torch.bfloat16, device="cuda")
+    L = 300
+    table = (pages - 1 - torch.arange(10, dtype=torch.int32)).cuda().reshape(1, 10)
+    k = torch.randn(L, hkv, d, generator=gen).to(torch.bfloat16).cuda()
+    view = store.as_strided((pages, page, hkv, d), (stride, hkv * d, d, 1))
+    spot = torch.arange(L, device="cuda")
+    view[table[0].long()[spot // page], spot % page] = k
+    p = ops.make_params(num_seqs=1, num_q_heads=8, num_kv_heads=hkv, head_dim=d, page_size=page, num_pages=pages, max_blocks_per_seq=10,
+                        max_context_len=320, dtype="bf16", strides=(stride, 0, 0))
+    q = torch.randn(rows, 8, d, generator=gen).to(torch.bfloat16).cuda()
+    w = torch.zeros(1, hkv, 320, device="cuda")
+    ops.key_weights(p, ops.make_rows(rows, rows), q, cu([rows]), store, table, torch.tensor([L], dtype=torch.int32, device="cuda"), w, decay=0.0)
+    pool = Pool([L], page, hkv, d, "bf16", gen)
+    pool.tables, pool.pages, pool.kv, pool.lens = table, pages, [view], [L]
+    want, tol = reference(q, [rows], pool, w * 0, 0.0, p.scale)
+    assert_close(w[0, :, :L], want[0, :, :L], tol[0, :, :L])
+
+
+def test_a_wait_that_runs_out_leaves_the_context_usable():
+    gen = torch.Generator().manual_seed(13)
+    pool = Pool([500], 16, 2, 128, "f16", gen)
+    q = torch.randn(200, 8, 128, generator=gen).to(torch.float16).cuda()
+    w = torch.zeros(1, 2, pool.blocks * 16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    p, r = pool.params(8, debug_timeout=1), ops.make_rows(200, 200)
+    ops.key_weights(p, r, q, cu([200]), pool.k, pool.tables, pool.context, w, decay=0.0, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status) == ops.PA_DEV_TIMEOUT
+    p, w = pool.params(8), torch.zeros_like(w)
+    ops.key_weights(p, r, q, cu([200]), pool.k, pool.tables, pool.context, w, decay=0.0)
+    want, tol = reference(q, [200], pool, torch.zeros_like(w), 0.0, p.scale)
+    assert_close(w[0, :, :500], want[0, :, :500], tol[0, :, :500])

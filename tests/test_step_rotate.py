@@ -151,3 +151,46 @@ def test_refused_rows_are_left_out():
     assert left == [1, 2, 3, 4, 5] and [int(i) for i in ((k_out == 7).flatten(1).all(1)).nonzero()] == left
     changed = (pool.k.nan_to_num(5.0) != old.nan_to_num(5.0)).flatten(2).any(2)
     assert int(changed.sum()) == 1 and bool(changed[pool.tables[0, 2].long(), 38 - 32])
+
+
+def test_captured_and_replayed_with_far_pages():
+    """One captured call for other rows, lengths and tables; pages whose offsets, in elements, pass 32 bits."""
+    gen = torch.Generator().manual_seed(8)
+    pages, page, hq, hkv, d, stride = 36, 16, 4, 2, 64, 1 << 26
+    k_cache, v_cache = (torch.zeros(pages * stride, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    p = ops.make_params(num_seqs=40, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, page_size=page, num_pages=pages, max_blocks_per_seq=2,
+                        max_context_len=32, dtype="bf16", strides=(stride, 0, 0))
+    rope, table = ops.make_rope(d, table_rows=32, eps=EPS), table_of(32, d)
+    total = 60
+    q, k, v = (torch.randn(total, h, d, generator=gen).to(torch.bfloat16).cuda() for h in (hq, hkv, hkv))
+    r = ops.make_rows(total, 20)
+    starts, lens, tables = cu([1] * 40), torch.zeros(40, dtype=torch.int32, device="cuda"), torch.full((40, 2), -1, dtype=torch.int32, device="cuda")
+    q_out = torch.zeros_like(q)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            ops.rotate(p, r, rope, q, k, starts, table, v=v, context_lens=lens, q_out=q_out, k_cache=k_cache, v_cache=v_cache, block_tables=tables)
+    views = [x.as_strided((pages, page, hkv, d), (stride, hkv * d, d, 1)) for x in (k_cache, v_cache)]
+    for counts in ([1] * 30 + [0] * 10, [0] * 35 + [20, 0, 3, 1, 2]):
+        held = [n + (i % 9 if n else 0) for i, n in enumerate(counts)]
+        starts.copy_(cu(counts))
+        lens.copy_(torch.tensor(held, dtype=torch.int32))
+        order = torch.randperm(pages, generator=gen).tolist()
+        rows = [[order.pop() if b * page < L else -1 for b in range(2)] for L in held]
+        tables.copy_(torch.tensor(rows, dtype=torch.int32))
+        q_out.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        at = 0
+        for s, (n, L) in enumerate(zip(counts, held)):
+            if n:
+                spot = torch.arange(L - n, L, device="cuda")
+                pos = spot[:, None].expand(-1, d // 2)
+                pg = tables[s].long()[spot // page]
+                assert_close(q_out[at:at + n], *turned(q[at:at + n], None, d, False, table, pos), "q")
+                assert_close(views[0][pg, spot % page], *turned(k[at:at + n], None, d, False, table, pos), "k")
+                assert torch.equal(views[1][pg, spot % page], v[at:at + n])
+            at += n
+        assert (q_out[at:] == 7).all()

@@ -136,6 +136,70 @@ def test_strided_rows_and_odd_bases(dtype):
     check(x)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("which", ["logits", "draft", "noise"])
+@pytest.mark.parametrize("vocab", [1000, 40003])
+def test_each_base_on_its_own_boundary(which, vocab, dtype):
+    x = problem((4, 6, 2), vocab, dtype, True, False, 19)
+    flat = torch.zeros(x[which].numel() + 1, dtype=x[which].dtype, device="cuda")
+    flat[1:] = x[which].reshape(-1)
+    x[which] = flat[1:].view(x[which].shape)
+    check(x)
+
+
+@pytest.mark.parametrize("dtype,vocab", [("bf16", 300007), ("f32", 150001), ("f16", 8)])
+def test_vocabularies_beyond_the_slots(dtype, vocab):
+    check(problem((3, 1, 5), vocab, dtype, True, False, 21), near=1)
+    check(problem((2,) * 160, vocab // 40 + 1, dtype, True, True, 22), near=2)  # one CTA a sequence
+
+
+def test_captured_and_replayed():
+    """A captured call takes the rows, lengths and numbers that it finds; two graphs replayed in turn do not disturb one another."""
+    graphs = []
+    for seed in (30, 31):
+        x = problem((5, 9, 1, 30), 5003, "bf16", True, False, seed)
+        rows = cu(x["rows"])
+        p, r = ops.verify_params(num_seqs=4, dtype="bf16"), ops.make_rows(x["logits"].shape[0], 30)
+        out = [torch.zeros(n, dtype=torch.int32, device="cuda") for n in (x["logits"].shape[0], 5, 4)]
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=stream):
+                ops.verify(p, r, x["logits"], x["draft"], x["tokens"], x["parents"], rows, x["heat"], x["uniform"], x["noise"],
+                           accepted=out[0], accepted_cu=out[1], next_tokens=out[2])
+        graphs.append((graph, x, rows, out))
+    torch.cuda.synchronize()
+    for counts in ((5, 9, 1, 30), (1, 0, 4, 2)):
+        for graph, x, rows, out in graphs:
+            rows.copy_(cu(counts))
+            graph.replay()
+            graph.replay()
+        torch.cuda.synchronize()
+        for graph, x, rows, out in graphs:
+            ends, at = out[1].tolist(), 0
+            for s, n in enumerate(counts):
+                mine = slice(at, at + n)
+                if n:
+                    parents = [p if 0 <= p < t else -1 for t, p in enumerate(x["parents"][mine].tolist())]
+                    path, token, margin = walk(x["logits"][mine], x["draft"][mine], x["tokens"][mine].tolist(), parents, float(x["heat"][s]),
+                                               x["uniform"][mine], x["noise"][s])
+                    if margin > 2.0 ** -16:
+                        assert out[0][ends[s]:ends[s + 1]].tolist() == [at + t for t in path] and int(out[2][s]) == token
+                else:
+                    assert ends[s] == ends[s + 1] and int(out[2][s]) == -1
+                at += n
+
+
+def test_hot_and_cold_temperatures():
+    x = problem((4, 4, 4), 700, "f32", True, True, 23)
+    x["heat"][0], x["heat"][1], x["heat"][2] = 1e-30, 1e30, 50.0
+    check(x, near=1)
+    x["logits"][:] = -3.4028234e38  # masked everywhere: uniform
+    x["heat"][:] = 1.0
+    check(x, near=1)
+
+
 def test_greedy_and_ties():
     x = problem((6, 9, 30), 333, "bf16", True, False, 3)
     x["heat"][0], x["heat"][1] = 0.0, -1.0
