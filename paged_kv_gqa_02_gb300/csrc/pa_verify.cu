@@ -15,15 +15,15 @@
 // vocabulary's tail.  M does not matter to it.
 //
 // The walk's time is a chain of passes, each bound by latency: the exponentials
-// of a row and one exchange.  A thread's part of the rows waits in slots of
-// shared memory that only it uses: the row at hand, for all of its passes, and
-// the first child's, on its way while the parent's is decided; the random numbers
-// from the start.  For an exchange every warp sends its result to the shared
-// memory of every CTA of the cluster, counted by an mbarrier there.  A warp of
-// its own, the leader, reads what it needs of the children meanwhile, joins the
-// results and orders the next pass; leaders of a cluster join the same in the same
-// order and so decide the same.  Only rank 0 writes.  A second kernel joins the
-// sequences' lists.
+// of a row and one exchange.  A CTA has a run of the vocabulary, and its part of
+// the rows waits in shared memory: the row at hand, for all of its passes, and the
+// first child's, on its way (bulk copies) while the parent's is summed and decided;
+// the random numbers from the start.  For an exchange every warp sends its result
+// to the shared memory of every CTA of the cluster, counted by an mbarrier there.  A
+// warp of its own, the leader, orders the copies, reads what it needs of the
+// children meanwhile, joins the results and orders the next pass; leaders of a
+// cluster join the same in the same order and so decide the same.  Only rank 0
+// writes.  A second kernel joins the sequences' lists.
 #include <cooperative_groups.h>
 
 #include "pa_device.h"
@@ -42,7 +42,6 @@ constexpr int kThr = 512;          // of the passes; the leader's warp comes beh
 constexpr int kWarps = kThr / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxDrafts = 1024;  // rows of a sequence
-constexpr int kSingles = 16;      // elements of a row outside its units of eight at most, and two
 constexpr int kPackThr = 1024;
 constexpr uint64_t kWaitNs = 2000000000ull;  // an exchange gives up after 2 s
 
@@ -64,7 +63,7 @@ struct __align__(16) Pick {
 // of p, the best candidate for the next token, or nothing more.
 enum { kGo, kMass, kPick, kStop };
 struct Order {
-    int what, went;
+    int what, went, phase;    // phase: of the copies to the row's slots
     int dropped;              // certain drafts rejected
     float p_top, q_top, less; // what is left: 2^((x - p_top) c) - less 2^((y - q_top) c), not below 0
 };
@@ -83,29 +82,37 @@ __device__ inline void cp_async16(uint32_t to, const void* from) {
 __device__ inline void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ inline void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Slots of shared memory for units of eight elements: a thread's k-th unit of a
-// row, its 16-byte parts kThr apart.
-template <typename T> struct Stage {
-    static constexpr int kParts = 8 / Elt<T>::kVec;
-    static constexpr int kSlots = 4 / kParts;                    // a thread's units of a row
-    static constexpr int kRow = kSlots * kParts * kThr;          // 16-byte parts of a row
-    static constexpr int kNoise = kSlots * 2 * kThr;
-    static constexpr size_t kBytes = size_t(4 * kRow + kNoise) * 16;  // two rows and their drafts', random numbers
-};
+// Shared memory for a CTA's part of two rows and their drafts', and of the
+// random numbers where they fit beside them: units of eight elements, in order.
+// Units beyond the room come to the slots of units that are done with.
+constexpr size_t kRoom = 203648;  // with what is laid out by the compiler, all that a CTA may have
+template <typename T> constexpr int kParts = 8 / Elt<T>::kVec;  // 16-byte parts of a unit
+
 __device__ inline void cp_async4(uint32_t to, const void* from) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
 }
+// A whole number of 16 bytes between 16-byte boundaries, counted by the mbarrier.
+__device__ inline void copy_bulk(void* to, const void* from, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(to)),
+                 "l"(from), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
 
-// Eight elements to the thread's slot and from it.  Copies that arrive later,
-// but for 16-bit elements off the 16-byte boundaries.
+__device__ inline void prefetch_bulk(const void* from, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
+}
+
+// Eight elements to a unit's slot.  Copies that arrive later, but for 16-bit
+// elements off the 16-byte boundaries.
 template <typename T> __device__ inline void stage8(uint4* slot, const T* p) {
     if (wide_at(p)) {
 #pragma unroll
         for (int i = 0; i < 8 / Elt<T>::kVec; ++i)
-            cp_async16(smem_u32(slot + i * kThr), reinterpret_cast<const uint4*>(p) + i);
+            cp_async16(smem_u32(slot + i), reinterpret_cast<const uint4*>(p) + i);
     } else if (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) cp_async4(smem_u32(slot + i / 4 * kThr) + 4 * (i % 4), p + i);
+        for (int i = 0; i < 8; ++i) cp_async4(smem_u32(slot) + 4 * i, p + i);
     } else {
         const unsigned short* e = reinterpret_cast<const unsigned short*>(p);
         uint32_t w[4];
@@ -132,7 +139,26 @@ __device__ inline void read8(const float* p, const float* first, const float* en
 }
 template <typename T> __device__ inline void take_slot(const uint4* slot, float (&x)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8 / Elt<T>::kVec; ++i) vec_to_f32<T>(slot[i * kThr], x + i * Elt<T>::kVec);
+    for (int i = 0; i < 8 / Elt<T>::kVec; ++i) vec_to_f32<T>(slot[i], x + i * Elt<T>::kVec);
+}
+// The largest of a slot's eight; NaNs are passed over.  16-bit types two at a time.
+template <typename T> __device__ inline float max_slot(const uint4* slot);
+template <> __device__ inline float max_slot<float>(const uint4* slot) {
+    float x[8];
+    take_slot<float>(slot, x);
+    return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+}
+template <> __device__ inline float max_slot<__half>(const uint4* slot) {
+    const uint4 v = *slot;
+    const __half2* h = reinterpret_cast<const __half2*>(&v);
+    const float2 m = __half22float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
+    return fmaxf(m.x, m.y);
+}
+template <> __device__ inline float max_slot<__nv_bfloat16>(const uint4* slot) {
+    const uint4 v = *slot;
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+    const float2 m = __bfloat1622float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
+    return fmaxf(m.x, m.y);
 }
 
 // 16 bytes to the same place of another CTA's shared memory, counted by its mbarrier.
@@ -157,9 +183,7 @@ __device__ inline float raise(Run& s, float top, float c) {
     s.top = now;
     return ref;
 }
-__device__ inline void take8(Run& s, const float (&x)[8], float c) {
-    const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-    const float ref = raise(s, top, c);
+__device__ inline void add8(Run& s, const float (&x)[8], float ref, float c) {
     const uint64_t minus = pairs::pack(-ref, -ref), c2 = pairs::pack(c, c);
     uint64_t e[4];
 #pragma unroll
@@ -217,11 +241,9 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
     extern __shared__ uint4 slots[];
     __shared__ Stats in_stats[2][kMaxCluster * kWarps];
     __shared__ Pick in_picks[2][kMaxCluster * kWarps];
-    __shared__ uint64_t arrived[2];
+    __shared__ uint64_t arrived[2], row_full[2], noise_full;
     __shared__ Order orders[2];
-    __shared__ float singles[2][2][kSingles];
     __shared__ int parents[kMaxDrafts], tokens[kMaxDrafts], removed[kMaxDrafts];
-    using St = Stage<T>;
     cg::cluster_group cluster = cg::this_cluster();
     const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -241,11 +263,11 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
     const int V = a.vocab;
     const bool greedy = !(heat > 0.f);
     const float c = greedy ? kLog2e : fminf(kLog2e / heat, 3.402823466e38f);
+    const bool draft = !greedy && a.draft;
     const float* const noise = a.noise + int64_t(s) * V;
-    const int worker = rank * kThr + tid, workers = C * kThr;
 
-    // A row as the threads read it: single elements up to the first 16-byte
-    // boundary, units of eight, the cluster's threads in turn, single elements.
+    // A row: single elements up to the first 16-byte boundary, units of eight, a
+    // run of them to a CTA, single elements.
     struct Row {
         const T* p;
         const T* q;  // the draft's, or nullptr
@@ -254,49 +276,26 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
     auto row_at = [&](int t, bool with_q) {
         Row r;
         r.p = static_cast<const T*>(a.logits) + int64_t(r0 + t) * a.logits_stride;
-        r.q = with_q && !greedy && a.draft ? static_cast<const T*>(a.draft) + int64_t(r0 + t) * a.draft_stride : nullptr;
+        r.q = with_q && draft ? static_cast<const T*>(a.draft) + int64_t(r0 + t) * a.draft_stride : nullptr;
         r.head = min(V, int((16 - (reinterpret_cast<uintptr_t>(r.p) & 15)) & 15) / int(sizeof(T)));
         return r;
     };
-    auto units_of = [&](int head) { return (V - head) >> 3; };
-    // the thread's single element, or -1
-    auto single_of = [&](int head) {
-        const int behind = head + 8 * units_of(head);
-        return rank == C - 1 && tid < head + V - behind ? (tid < head ? tid : behind + tid - head) : -1;
+    // the CTA's first unit and the number of its units
+    struct Span {
+        int first, count;
     };
-    uint4* const noise_slots = slots + 4 * St::kRow + tid;
-    auto slot_of = [&](int held, int draft, int k) { return slots + (2 * held + draft) * St::kRow + k * St::kParts * kThr + tid; };
-    // the first units of a row and of its draft's on their way to the slots of `held`
-    auto fetch = [&](const Row& r, int held) {
-        const int units = units_of(r.head), single = single_of(r.head);
-#pragma unroll
-        for (int k = 0; k < St::kSlots; ++k) {
-            const int i = worker + k * workers;
-            if (i < units) {
-                stage8<T>(slot_of(held, 0, k), r.p + r.head + 8 * i);
-                if (r.q) stage8<T>(slot_of(held, 1, k), r.q + r.head + 8 * i);
-            }
-        }
-        if (single >= 0) {
-            singles[held][0][tid] = Elt<T>::f(r.p[single]);
-            if (r.q) singles[held][1][tid] = Elt<T>::f(r.q[single]);
-        }
-        cp_commit();
+    auto run_of = [&](int head) {
+        const int64_t units = (V - head) >> 3;
+        const int first = int(units * rank / C);
+        return Span{first, int(units * (rank + 1) / C) - first};
     };
-    // random numbers off the 16-byte boundaries are read where they lie
-    auto noise_wide = [&](int head) { return wide_at(noise + head); };
-    auto fetch_noise = [&](int head) {
-        const int units = units_of(head);
-        if (!noise_wide(head)) return;
-#pragma unroll
-        for (int k = 0; k < St::kSlots; ++k) {
-            const int i = worker + k * workers;
-            if (i < units) stage8<float>(noise_slots + 2 * k * kThr, noise + head + 8 * i);
-        }
-    };
-    Row row = row_at(0, rows > 1);
-    int held = 0;
-    if (warp < kWarps) fetch(row, held);
+    const int noise_head = row_at(0, false).head;
+    const int most = ((V >> 3) + C - 1) / C + 1;  // units of a CTA at most
+    constexpr int kAll = int(kRoom / 16), kFour = 4 * kParts<T>;
+    const bool noise_staged = !greedy && wide_at(noise + noise_head) && most <= kAll / (kFour + 2);
+    const int room = kAll / (noise_staged ? kFour + 2 : kFour);  // units of a row
+    auto slot_of = [&](int held, int which, int unit) { return slots + ((2 * held + which) * room + unit) * kParts<T>; };
+    uint4* const noise_slots = slots + room * kFour;
     for (int t = tid; t < rows; t += kThr + 32) {
         const int p = t ? a.parents[r0 + t] : -1, token = t ? a.tokens[r0 + t] : -1;
         const bool good = t && p >= 0 && p < t && token >= 0 && token < V;
@@ -305,11 +304,37 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
         tokens[t] = token;
     }
     const uint32_t bytes = uint32_t(C) * kWarps * (sizeof(Stats) + sizeof(Pick));  // of an exchange
-    if (tid == 0) {
+    // a row's first units, its draft's, to the slots of `held`, what is beyond them to L2 (one thread)
+    auto copy_row = [&](int t, bool with_q, int held) {
+        const Row r = row_at(t, with_q);
+        const Span run = run_of(r.head);
+        const uint32_t n = uint32_t(min(run.count, room)) * (8 * sizeof(T)), beyond = uint32_t(run.count) * (8 * sizeof(T)) - n;
+        const T* p = r.p + r.head + 8 * run.first;
+        const T* q = r.q && wide_at(r.q + r.head) ? r.q + r.head + 8 * run.first : nullptr;
+        mbar_arrive_expect_tx(&row_full[held], q ? 2 * n : n);
+        if (n) copy_bulk(slot_of(held, 0, 0), p, n, &row_full[held]);
+        if (n && q) copy_bulk(slot_of(held, 1, 0), q, n, &row_full[held]);
+        if (beyond) prefetch_bulk(p + 8 * room, beyond);
+        if (beyond && q) prefetch_bulk(q + 8 * room, beyond);
+    };
+    if (tid == kThr) {  // the leader's first lane
         for (int i = 0; i < 2; ++i) {
             mbar_init(&arrived[i], 1);
-            mbar_fence_init();
-            mbar_arrive_expect_tx(&arrived[i], bytes);
+            mbar_init(&row_full[i], 1);
+        }
+        mbar_init(&noise_full, 1);
+        mbar_fence_init();
+        for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&arrived[i], bytes);
+        fence_proxy_async_smem();
+        copy_row(0, rows > 1, 0);  // the draft's before it is known whether the row has children
+        const Span run = run_of(noise_head);
+        const uint32_t n = noise_staged ? uint32_t(run.count) * 32u : 0u;
+        mbar_arrive_expect_tx(&noise_full, n);
+        const float* from = noise + noise_head + 8 * run.first;
+        if (n) copy_bulk(noise_slots, from, n, &noise_full);
+        if (!greedy && !noise_staged && run.count > 1) {  // to L2, between the boundaries in it
+            const char* p = reinterpret_cast<const char*>((reinterpret_cast<uintptr_t>(from) + 15) & ~uintptr_t(15));
+            prefetch_bulk(p, uint32_t(reinterpret_cast<const char*>(from + 8 * run.count) - p) & ~15u);
         }
     }
     cluster.sync();  // the barriers are there before anyone sends
@@ -344,12 +369,26 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
         };
         const int n = C * kWarps;
         int here = 0, count = 0, next = -1;
+        int held = 0, fills[2] = {1, 0};  // the row at hand; copies to the slots so far
+        auto fill = [&](int t, bool with_q, int to) {
+            if (lane == 0) {
+                fence_proxy_async_smem();  // behind what the passes did there, by way of the last order
+                copy_row(t, with_q, to);
+            }
+            ++fills[to];
+        };
         for (;;) {
             if (rank == 0 && lane == 0) a.accepted[r0 + count] = r0 + here;
             ++count;
             int base = here + 1;
             unsigned children = window(here, base);
-            row = row_at(here, children != 0);
+            const Row row = row_at(here, children != 0);
+            // the row that the walk most likely goes on to
+            const int guess = children ? base + __ffs(children) - 1 : -1;
+            if (guess >= 0) {
+                int after = guess + 1;
+                fill(guess, window(guess, after) != 0, held ^ 1);
+            }
             // the lane's child: its logits and its random number
             T x_mine = T(0.f), y_mine = T(0.f);
             float u_mine = 0.f;
@@ -439,7 +478,7 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
                     used += mass;
                 } else {
                     const float more = used + mass;
-                    order(Order{kMass, 0, 0, P.top, Q.top, more * q_of * P.sum});
+                    order(Order{kMass, 0, 0, 0, P.top, Q.top, more * q_of * P.sum});
                     const int from = wait();
                     if (lost) break;
                     float sum = 0.f;
@@ -453,7 +492,16 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
             }
             if (lost) break;
             if (went) {
-                order(Order{kGo, went, 0, 0.f, 0.f, 0.f});
+                held ^= 1;
+                if (went != guess) {  // behind the guess's copies to the same slots
+                    if (!__all_sync(0xffffffffu, mbar_wait_ns(&row_full[held], (fills[held] - 1) & 1, kWaitNs))) {
+                        lost = true;
+                        break;
+                    }
+                    int after = went + 1;
+                    fill(went, window(went, after) != 0, held);
+                }
+                order(Order{kGo, went, (fills[held] - 1) & 1, 0, 0.f, 0.f, 0.f});
                 here = went;
                 continue;
             }
@@ -462,7 +510,7 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
                 break;
             }
             for (;;) {
-                order(Order{kPick, 0, dropped, P.top, Q.top, used * q_of * P.sum});
+                order(Order{kPick, 0, 0, dropped, P.top, Q.top, used * q_of * P.sum});
                 const int from = wait();
                 if (lost) break;
                 float key = 0.f;
@@ -482,7 +530,11 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
             }
             break;
         }
-        order(Order{kStop, 0, 0, 0.f, 0.f, 0.f});
+        order(Order{kStop, 0, 0, 0, 0.f, 0.f, 0.f});
+        // nobody leaves with copies under way
+        for (int i = 0; i < 2; ++i)
+            if (fills[i]) mbar_wait_ns(&row_full[i], (fills[i] - 1) & 1, kWaitNs);
+        mbar_wait_ns(&noise_full, 0, kWaitNs);
         if (rank == 0 && lane == 0) {
             if (lost) flag(a.dev_status, PA_DEV_TIMEOUT);
             a.accepted_cu[s + 1] = count;
@@ -504,124 +556,130 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
         }
     };
     int taken = 0;
-    auto next_order = [&] {
+    auto next_order = [&]() -> const Order* {
         __syncthreads();
-        return orders[taken++ & 1];
+        return &orders[taken++ & 1];
     };
-    // f(eight of p, eight of q, first index, slot) over the thread's units of the row
-    // at hand.  Units that have no slot of their own come to one that is done with,
-    // and the first ones back to theirs before the next pass over the row.
-    bool with_noise = false;  // the pass reads random numbers too
+    int here = 0, held = 0, phase = 0;  // the row at hand, its slots and the phase of the copies to them
     bool again_from_start = false;
-    auto over = [&](auto&& f) {
-        const int units = units_of(row.head);
-        const bool more = worker + St::kSlots * workers < units;
-        auto stage_unit = [&](int slot, int i) {
-            stage8<T>(slot_of(held, 0, slot), row.p + row.head + 8 * i);
-            if (row.q) stage8<T>(slot_of(held, 1, slot), row.q + row.head + 8 * i);
-            if (with_noise && noise_wide(row.head)) stage8<float>(noise_slots + 2 * slot * kThr, noise + row.head + 8 * i);
-        };
-        if (more && again_from_start) {
-            cp_wait<0>();
-#pragma unroll 1
-            for (int k = 0; k < St::kSlots; ++k) stage_unit(k, worker + k * workers);
-            cp_commit();
-            cp_wait<0>();
-        }
-        int slot = 0;
-#pragma unroll 1
-        for (int i = worker; i < units; i += workers) {
-            if (i >= St::kSlots * workers) cp_wait<St::kSlots - 1>();
-            float x[8], y[8];
-            take_slot<T>(slot_of(held, 0, slot), x);
-            if (row.q) take_slot<T>(slot_of(held, 1, slot), y);
-            f(x, y, row.head + 8 * i, slot);
-            if (more) {
-                if (i + St::kSlots * workers < units) stage_unit(slot, i + St::kSlots * workers);
-                cp_commit();
+    // body(first index of a round, units, row) for rounds of `room` of the CTA's
+    // units.  The next round's come to the slots when one is done with, and the
+    // first one's back before the next pass over the row.
+    auto rounds = [&](const Row& row, auto&& body) {
+        const Span run = run_of(row.head);
+        const bool more = run.count > room;
+        auto stage_round = [&](int c0) {
+            for (int u = tid; u < room && c0 + u < run.count; u += kThr) {
+                const int at = row.head + 8 * (run.first + c0 + u);
+                stage8<T>(slot_of(held, 0, u), row.p + at);
+                if (row.q) stage8<T>(slot_of(held, 1, u), row.q + at);
             }
-            slot = slot + 1 == St::kSlots ? 0 : slot + 1;
+            cp_commit();
+        };
+        if (more && again_from_start) stage_round(0);
+        for (int c0 = 0; c0 < run.count; c0 += room) {
+            cp_wait<0>();
+            body(row.head + 8 * (run.first + c0), min(room, run.count - c0));
+            if (more) stage_round(c0 + room);
         }
         again_from_start = true;
     };
-    int here = 0;
+    // the thread's element outside the units, or -1
+    auto single_of = [&](int head) {
+        const int behind = head + ((V - head) >> 3 << 3);
+        return rank == C - 1 && tid < head + V - behind ? (tid < head ? tid : behind + tid - head) : -1;
+    };
+    bool with_draft;
     {
         int base = 1;
-        if (!window(0, base)) row.q = nullptr;  // nothing is used of a row without children
+        with_draft = draft && window(0, base);  // nothing is used of a row without children
     }
-    const int noise_head = row.head;
-    if (!greedy) fetch_noise(row.head);
-    cp_commit();
-    bool first = true;
+    bool fine = true;
     for (;;) {
-        if (first)
-            cp_wait<1>();  // all but the random numbers
-        else
-            cp_wait<0>();
-        first = false;
+        const Row row = row_at(here, with_draft);
+        const int single = single_of(row.head);
+        float one_p = 0.f, one_q = 0.f;
+        if (single >= 0) {
+            one_p = Elt<T>::f(row.p[single]);
+            if (row.q) one_q = Elt<T>::f(row.q[single]);
+        }
+        if (row.q && !wide_at(row.q + row.head)) {  // no bulk copy takes it
+            const Span run = run_of(row.head);
+            for (int u = tid; u < room && u < run.count; u += kThr)
+                stage8<T>(slot_of(held, 1, u), row.q + row.head + 8 * (run.first + u));
+            cp_commit();
+        }
+        fine &= __all_sync(0xffffffffu, mbar_wait_ns(&row_full[held], phase, kWaitNs));
         again_from_start = false;
         Run run_p = {-INFINITY, 0}, run_q = {-INFINITY, 0};
         Pick pick = {-INFINITY, V, {0, 0}};
         auto first_place = [&](float x, int at) {  // greedy: a thread meets indices in ascending order but for the ends
             if (x > pick.key || (x == pick.key && at < pick.at)) pick.key = x, pick.at = at;
         };
-        over([&](const float(&x)[8], const float(&y)[8], int at, int) {
-            take8(run_p, x, c);
-            if (row.q) take8(run_q, y, c);
-            if (greedy) {
+        rounds(row, [&](int at, int units) {
+            // the largest values first, then all exponentials against them
+            float top_p = -INFINITY, top_q = -INFINITY;
+#pragma unroll 4
+            for (int u = tid; u < units; u += kThr) {
+                top_p = fmaxf(top_p, max_slot<T>(slot_of(held, 0, u)));
+                if (with_draft) top_q = fmaxf(top_q, max_slot<T>(slot_of(held, 1, u)));
+            }
+            const float ref_p = raise(run_p, top_p, c), ref_q = raise(run_q, top_q, c);
+#pragma unroll 2
+            for (int u = tid; u < units; u += kThr) {
+                float x[8];
+                take_slot<T>(slot_of(held, 0, u), x);
+                add8(run_p, x, ref_p, c);
+                if (greedy) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) first_place(x[e], at + e);
+                    for (int e = 0; e < 8; ++e) first_place(x[e], at + 8 * u + e);
+                }
+                if (with_draft) {
+                    take_slot<T>(slot_of(held, 1, u), x);
+                    add8(run_q, x, ref_q, c);
+                }
             }
         });
-        const int single = single_of(row.head);
         if (single >= 0) {
-            take1(run_p, singles[held][0][tid], c);
-            if (row.q) take1(run_q, singles[held][1][tid], c);
-            if (greedy) first_place(singles[held][0][tid], single);
+            take1(run_p, one_p, c);
+            if (with_draft) take1(run_q, one_q, c);
+            if (greedy) first_place(one_p, single);
         }
         Stats stats = {over_warp(run_p, c), {-INFINITY, 0.f}};
-        if (row.q) stats.q = over_warp(run_q, c);
+        if (with_draft) stats.q = over_warp(run_q, c);
         if (greedy) better_over_warp(pick.key, pick.at);
         send(stats, pick);
-        // the row that the walk most likely goes on to
-        int base = here + 1;
-        const unsigned children = window(here, base);
-        const int guess = children ? base + __ffs(children) - 1 : -1;
-        Row ahead = {};
-        if (guess >= 0) {
-            int after = guess + 1;
-            ahead = row_at(guess, window(guess, after) != 0);
-            fetch(ahead, held ^ 1);
-        }
-        Order o = next_order();
-        while (o.what == kMass || o.what == kPick) {
+        const Order* o = next_order();
+        while (o->what == kMass || o->what == kPick) {
             // what is left of p times P.sum, of which a draft's exponential takes `less`
+            const float p_top = o->p_top, q_top = o->q_top, less = o->less;
             auto left = [&](float x, float y) {
-                const float p = ex2((x - o.p_top) * c);
-                return o.less > 0.f ? fmaxf(p - ex2((y - o.q_top) * c) * o.less, 0.f) : p;
+                const float p = ex2((x - p_top) * c);
+                return less > 0.f ? fmaxf(p - ex2((y - q_top) * c) * less, 0.f) : p;
             };
-            if (o.what == kMass) {
+            if (o->what == kMass) {
                 float sum = 0.f;
-                over([&](const float(&x8)[8], const float(&y8)[8], int, int) {
+                rounds(row, [&](int, int units) {
+#pragma unroll 2
+                    for (int u = tid; u < units; u += kThr) {
+                        float x8[8], y8[8];
+                        take_slot<T>(slot_of(held, 0, u), x8);
+                        take_slot<T>(slot_of(held, 1, u), y8);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) sum += left(x8[e], y8[e]);
+                        for (int e = 0; e < 8; ++e) sum += left(x8[e], y8[e]);
+                    }
                 });
-                if (single >= 0) sum += left(singles[held][0][tid], singles[held][1][tid]);
+                if (single >= 0) sum += left(one_p, one_q);
                 pick.key = warp_sum(sum);
             } else {
-                cp_wait<0>();
-                if (!with_noise && noise_head != row.head) {  // another alignment than the first row's
-                    fetch_noise(row.head);
-                    cp_commit();
-                    cp_wait<0>();
-                }
-                with_noise = true;
+                const bool wide = wide_at(noise + row.head), staged = noise_staged && noise_head == row.head;
+                if (staged) fine &= __all_sync(0xffffffffu, mbar_wait_ns(&noise_full, 0, kWaitNs));
                 float best = 0.f;
                 int best_at = V;
                 // rejected certain drafts among the n places from `at`, a bit each
                 auto out_of = [&](int at, unsigned n) {
                     unsigned bits = 0;
-                    for (int k = 0; k < o.dropped; ++k) {
+                    for (int k = 0; k < o->dropped; ++k) {
                         const unsigned d = unsigned(removed[k] - at);
                         if (d < n) bits |= 1u << d;
                     }
@@ -634,18 +692,25 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
                         best_at = at;
                     }
                 };
-                over([&](const float(&x8)[8], const float(&y8)[8], int at, int slot) {
-                    float e8[8];
-                    if (noise_wide(row.head))
-                        take_slot<float>(noise_slots + 2 * slot * kThr, e8);
-                    else
-                        read8(noise + at, a.noise, a.noise + int64_t(a.num_seqs) * V, e8);
-                    const unsigned out = out_of(at, 8);
+                rounds(row, [&](int at0, int units) {
+#pragma unroll 1
+                    for (int u = tid; u < units; u += kThr) {
+                        const int at = at0 + 8 * u;
+                        float x8[8], y8[8], e8[8];
+                        take_slot<T>(slot_of(held, 0, u), x8);
+                        if (row.q) take_slot<T>(slot_of(held, 1, u), y8);
+                        if (staged)
+                            take_slot<float>(noise_slots + 2 * u, e8);
+                        else if (wide)
+                            take_slot<float>(reinterpret_cast<const uint4*>(noise + at), e8);
+                        else
+                            read8(noise + at, a.noise, a.noise + int64_t(a.num_seqs) * V, e8);
+                        const unsigned out = out_of(at, 8);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) weigh(left(x8[e], y8[e]), e8[e], at + e, (out >> e) & 1u);
+                        for (int e = 0; e < 8; ++e) weigh(left(x8[e], y8[e]), e8[e], at + e, (out >> e) & 1u);
+                    }
                 });
-                if (single >= 0)
-                    weigh(left(singles[held][0][tid], singles[held][1][tid]), noise[single], single, out_of(single, 1));
+                if (single >= 0) weigh(left(one_p, one_q), noise[single], single, out_of(single, 1));
                 better_over_warp(best, best_at);
                 pick.key = best;
                 pick.at = best_at;
@@ -653,19 +718,15 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
             send(stats, pick);
             o = next_order();
         }
-        if (o.what == kStop) break;
-        here = o.went;
-        if (here == guess) {
-            row = ahead;
-        } else {
-            int after = here + 1;
-            row = row_at(here, window(here, after) != 0);
-            cp_wait<0>();  // the guess is still on its way there
-            fetch(row, held ^ 1);
-        }
+        if (o->what == kStop) break;
+        here = o->went;
+        phase = o->phase;
         held ^= 1;
+        int after = here + 1;
+        with_draft = draft && window(here, after);
     }
     cp_wait<0>();  // nobody leaves with copies under way
+    if (!fine) flag(a.dev_status, PA_DEV_TIMEOUT);
 }
 
 // Joins the sequences' lists: the walk left counts in accepted_cu and each
@@ -734,7 +795,7 @@ template <typename T> cudaError_t launch_walk(const VerifyCall& c, cudaStream_t 
     static std::atomic<uint64_t> wide{0}, allowed{0};
     const void* kern = reinterpret_cast<const void*>(verify_walk<T>);
     cudaError_t e = allow_wide_clusters(kern, wide);
-    if (e == cudaSuccess) e = allow_shared_memory(kern, Stage<T>::kBytes, allowed);
+    if (e == cudaSuccess) e = allow_shared_memory(kern, kRoom, allowed);
     if (e != cudaSuccess) return e;
     // as many CTAs as the GPU holds at once, each with a unit for every thread
     int size = kMaxCluster;
@@ -742,7 +803,7 @@ template <typename T> cudaError_t launch_walk(const VerifyCall& c, cudaStream_t 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(c.num_seqs) * size);
     cfg.blockDim = dim3(kThr + 32);
-    cfg.dynamicSmemBytes = Stage<T>::kBytes;
+    cfg.dynamicSmemBytes = kRoom;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
