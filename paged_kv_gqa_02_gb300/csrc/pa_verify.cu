@@ -251,7 +251,6 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
     pdl_launch_dependents();
     const int s = int(blockIdx.x) / C;
     const int r0 = a.cu_lens[s], r1 = a.cu_lens[s + 1], rows = r1 - r0;
-    const float heat = a.temperature[s];
     if (bad_rows(r0, r1, a.total_rows, a.max_rows) || rows == 0) {  // the whole cluster
         if (rank == 0 && tid == 0) {
             if (bad_rows(r0, r1, a.total_rows, a.max_rows)) flag(a.dev_status, PA_DEV_BAD_LEN);
@@ -260,6 +259,7 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
         }
         return;
     }
+    const float heat = a.temperature[s];  // not there where there are no rows at all
     const int V = a.vocab;
     const bool greedy = !(heat > 0.f);
     const float c = greedy ? kLog2e : fminf(kLog2e / heat, 3.402823466e38f);

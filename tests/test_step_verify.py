@@ -300,6 +300,17 @@ def test_no_rows_at_all():
     assert ends.tolist() == [0, 0, 0] and nexts.tolist() == [-1, -1] and lens.tolist() == [4, 5]
 
 
+def test_no_rows_need_no_pointers_of_rows():
+    p, r, b = ops.verify_params(num_seqs=2, dtype="bf16"), ops.make_rows(0, 0), 2
+    ends, nexts, status = (torch.full((n,), 9, dtype=torch.int32, device="cuda") for n in (b + 1, b, 1))
+    status.zero_()
+    starts = cu([0, 0])
+    assert ops.load().pa_verify(p, r, 50, None, None, None, None, starts.data_ptr(), None, None, None, None, None, ends.data_ptr(),
+                                nexts.data_ptr(), None, status.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert ends.tolist() == [0, 0, 0] and nexts.tolist() == [-1, -1] and int(status) == 0
+
+
 def test_many_sequences_join_in_order():
     rows = [(i * 7) % 4 for i in range(1500)]
     check(problem(rows, 40, "f32", True, True, 11), near=3)
