@@ -267,7 +267,8 @@ pa_status pa_rotate(const pa_params *p, const pa_rows *r, const pa_rope *t, cons
  *                 draft was certain to its drafter
  *   tokens, parents: [total_rows] int32; parents count within the sequence,
  *                 0 <= parents[t] < t; row 0's are not read
- *   temperature:  [num_seqs] f32; logits are divided by it; not above 0: greedy
+ *   temperature:  [num_seqs] f32; logits are divided by it; not above 0: greedy;
+ *                 infinity: all finite logits alike
  *   uniform:      [total_rows] f32 in [0, 1), one for each draft
  *   noise:        [num_seqs][vocab] f32, independent exponential numbers above 0
  * From row 0 on, with p = softmax(target), q = softmax(draft) of the row (q

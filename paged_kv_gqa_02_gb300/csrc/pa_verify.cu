@@ -262,7 +262,8 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
     const float heat = a.temperature[s];  // not there where there are no rows at all
     const int V = a.vocab;
     const bool greedy = !(heat > 0.f);
-    const float c = greedy ? kLog2e : fminf(kLog2e / heat, 3.402823466e38f);
+    // neither infinite nor 0: a difference of 0 stays 0, one of -infinity stays that
+    const float c = greedy ? kLog2e : fmaxf(fminf(kLog2e / heat, 3.402823466e38f), 1.175494351e-38f);
     const bool draft = !greedy && a.draft;
     const float* const noise = a.noise + int64_t(s) * V;
 

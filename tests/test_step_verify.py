@@ -200,6 +200,22 @@ def test_hot_and_cold_temperatures():
     check(x, near=1)
 
 
+def test_an_infinite_temperature_makes_finite_logits_alike():
+    x = problem((4, 4), 700, "f32", True, True, 24)
+    x["logits"][:, ::3] = -math.inf
+    x["draft"][:, ::3] = -math.inf
+    x["tokens"][:] = 1
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for heat in (math.inf, 3.4028234e38):
+        x["heat"][:] = heat
+        accepted, ends, nexts, _ = call(x, status=status)
+        assert int(status) == 0 and ends.tolist() == [0, 4, 8]  # p = q
+        for s, token in enumerate(nexts.tolist()):  # the smallest noise of a token that is not masked
+            masked = x["noise"][s].clone()
+            masked[::3] = math.inf
+            assert token == int(masked.argmin())
+
+
 def test_greedy_and_ties():
     x = problem((6, 9, 30), 333, "bf16", True, False, 3)
     x["heat"][0], x["heat"][1] = 0.0, -1.0
