@@ -263,10 +263,10 @@ pa_status pa_rotate(const pa_params *p, const pa_rows *r, const pa_rope *t, cons
  *                 elements from a row to the next (0: vocab)
  *   draft_logits: the same of the distributions that the drafts were drawn from
  *                 (independently: the children of a row from its row), stride
- *                 r->k_stride; rows without children are not read.  NULL: each
- *                 draft was certain to its drafter
+ *                 r->k_stride; nothing is made of rows without children.  NULL:
+ *                 each draft was certain to its drafter
  *   tokens, parents: [total_rows] int32; parents count within the sequence,
- *                 0 <= parents[t] < t; row 0's are not read
+ *                 0 <= parents[t] < t; row 0's are not looked at
  *   temperature:  [num_seqs] f32; logits are divided by it; not above 0: greedy;
  *                 infinity: all finite logits alike
  *   uniform:      [total_rows] f32 in [0, 1), one for each draft
@@ -279,7 +279,7 @@ pa_status pa_rotate(const pa_params *p, const pa_rows *r, const pa_rope *t, cons
  * token is the one with the largest p(i) / noise(i), ties to the lowest: the
  * tokens then follow the target's distribution.  Greedy: a child is accepted
  * when it is the target's largest logit, the next token is that one, ties to
- * the lowest; neither random numbers nor draft_logits are read.
+ * the lowest; nothing is made of the random numbers and draft_logits.
  *   accepted:    [total_rows] int32: the packed rows of the accepted tokens, row
  *                0 of each sequence among them, sequence after sequence, then -1
  *   accepted_cu: [num_seqs + 1] int32: where each sequence's begin.  The two are
@@ -293,8 +293,9 @@ pa_status pa_rotate(const pa_params *p, const pa_rows *r, const pa_rope *t, cons
  * largest logit (a NaN or +infinity, all -infinity) ends the walk with next
  * token -1 (PA_DEV_BAD_VALUE), as do random numbers that choose none.
  * -infinity in other logits is a probability of zero.
- * Uses of p: num_seqs, q_dtype.  vocab >= 1, max_rows <= 1024; logits and
- * noise aligned to their elements. */
+ * Uses of p: num_seqs, q_dtype.  vocab from 1 to 2^28, max_rows <= 1024; logits
+ * and noise aligned to their elements.  Where total_rows is 0, what has an entry
+ * or more a row, temperature and noise may be NULL. */
 pa_status pa_verify(const pa_params *p, const pa_rows *r, int32_t vocab, const void *logits,
                     const void *draft_logits, const int32_t *tokens, const int32_t *parents,
                     const int32_t *cu_lens, const float *temperature, const float *uniform,
@@ -319,8 +320,17 @@ pa_status pa_verify(const pa_params *p, const pa_rows *r, int32_t vocab, const v
  * Uses of p as in pa_tree (head_dim 64 or 128; out_dtype is not used; no
  * windows, splits or decode_q_rows); max_context_len is a bound on
  * every context_lens[s] (0: what a table holds): longer ones are
- * PA_DEV_BAD_LEN, their weights left as they were.
- * workspace: pa_key_weights_workspace_size bytes, 256-byte aligned (0: invalid). */
+ * PA_DEV_BAD_LEN, their weights left as they were.  deterministic: the work is
+ * shared out as on 152 SMs.  debug_timeout bears on the tensor-core kernel alone;
+ * after PA_DEV_TIMEOUT the weights are void.
+ * (max_rows G / 64 + 8) (longest context / 128 + 8) is at most 2^30,
+ * num_seqs num_kv_heads (longest context + 1) at most 2^40
+ * (PA_ERR_UNSUPPORTED).
+ * workspace: pa_key_weights_workspace_size bytes, 256-byte aligned (0: invalid).
+ * max_rows G up to 32 (decoding): the scores, num_seqs x num_kv_heads x
+ * longest context x max_rows G floats, and 3 % more, so a tight max_context_len
+ * pays.  Beyond: 8 bytes for each row and q head, and 1 MB at most.
+ * It carries nothing from one call to the next. */
 size_t pa_key_weights_workspace_size(const pa_params *p, const pa_rows *r);
 
 pa_status pa_key_weights(const pa_params *p, const pa_rows *r, const void *q, const int32_t *cu_lens,
@@ -345,11 +355,13 @@ pa_status pa_key_weights(const pa_params *p, const pa_rows *r, const void *q, co
  * pa_pages_resize with new_lens trims every sequence and frees its pages.
  * refcounts ([num_pages], may be NULL): a sequence of which a page from slot f
  * to slot n - 1 has more than one holder is not evicted (PA_DEV_SHARED_PAGE).
- * Without them no such page may belong to two sequences.  Keys whose old or new
+ * Without them no such page may belong to two sequences; nor may a page stand
+ * twice in one table, with or without them.  Keys whose old or new
  * page is outside the pool do not move (PA_DEV_BAD_PAGE); a length out of range
  * leaves the sequence out, new_lens -1 (PA_DEV_BAD_LEN).
  * Uses of p: num_seqs, num_kv_heads, head_dim (64, 128, 256), kv_dtype and the
- * pages.  max_blocks_per_seq * page_size is at most 2^22. */
+ * pages.  max_blocks_per_seq * page_size is at most 2^22, num_seqs * num_kv_heads
+ * at most 2^23 (PA_ERR_UNSUPPORTED). */
 pa_status pa_evict(const pa_params *p, void *k_cache, void *v_cache, const int32_t *block_tables,
                    const int32_t *context_lens, const int32_t *refcounts, const float *weights,
                    const int32_t *keep_lens, int32_t first, int32_t recent, float *weights_out,

@@ -11,7 +11,8 @@
 namespace {
 
 constexpr int kMaxVocab = 1 << 28;        // tokens of a vocabulary: indices with a tile stay in 32 bits
-constexpr int64_t kMaxEvictUnits = 1 << 24;  // sequences times kv heads of an eviction: its grids stay in 32 bits
+constexpr int64_t kMaxEvictUnits = 1 << 23;  // sequences times kv heads of an eviction: its grids stay in 31 bits
+constexpr int64_t kMaxWeights = int64_t(1) << 40;  // of a call: their scores' bytes stay in 64 bits
 
 // What pa_key_weights takes of the parameters.
 pa_status check_key_weights(const pa_params* p, const pa_rows* r, pa::KeyWeightsCall* c) {
@@ -32,6 +33,7 @@ pa_status check_key_weights(const pa_params* p, const pa_rows* r, pa::KeyWeights
     // products of a kv head are numbered in tiles of at least 65 x 128, in 32 bits
     if ((int64_t(c->r.max_rows) * (p->num_q_heads / p->num_kv_heads) / 64 + 8) * (len / 128 + 8) > (1 << 30))
         return PA_ERR_UNSUPPORTED;
+    if (int64_t(p->num_seqs) * p->num_kv_heads > kMaxWeights / (len + 1)) return PA_ERR_UNSUPPORTED;
     c->dtype = p->q_dtype;
     c->Hq = p->num_q_heads;
     c->Hkv = p->num_kv_heads;

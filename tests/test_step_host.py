@@ -138,6 +138,17 @@ def test_key_weights_refuses(lib):
     assert key_weights(lib, r=ops.make_rows(0, 0)) == 0
 
 
+def test_key_weights_refuses_more_than_it_can_count(lib):
+    big = dict(num_seqs=65535, num_kv_heads=65535, num_q_heads=65535, max_blocks_per_seq=1 << 27, max_context_len=0)
+    for bad, r in ((big, ops.make_rows(5, 3)), (dict(big, num_q_heads=16 * 4096, num_kv_heads=4096), ops.make_rows(5, 1)),
+                   (dict(max_blocks_per_seq=1 << 27, max_context_len=0), ops.make_rows(1 << 20, 1 << 20))):
+        assert key_weights(lib, p=params(**bad), r=r) == UNSUPPORTED, bad
+        assert ops.key_weights_workspace_size(params(**bad), r) == 0
+    # the longest table of one sequence: its scores and pieces count in 64 bits
+    p, r = params(num_seqs=1, num_q_heads=1, num_kv_heads=1, max_blocks_per_seq=1 << 26, max_context_len=0), ops.make_rows(1, 1)
+    assert ops.key_weights_workspace_size(p, r) >= 8 * p.page_size << 26
+
+
 def evict(lib, p=None, first=0, recent=0, **kw):
     a = dict(kc=BIG, vc=BIG, bt=BIG, cl=BIG, ref=BIG, w=BIG, keep=BIG)
     b = dict(out=ctypes.c_void_p(1 << 21), kept=BIG, lens=BIG)
@@ -155,6 +166,7 @@ def test_evict_refuses(lib):
     assert evict(lib, out=BIG) == SHAPE
     assert evict(lib, p=params(max_blocks_per_seq=1 << 20)) == UNSUPPORTED
     assert evict(lib, p=params(num_seqs=65535, num_kv_heads=65535, num_q_heads=65535)) == UNSUPPORTED
+    assert evict(lib, p=params(num_seqs=65535, num_kv_heads=129, num_q_heads=129)) == UNSUPPORTED
     assert evict(lib, p=params(head_dim=32)) == UNSUPPORTED
     assert evict(lib, p=params(strides=(0, 4, 0))) == ALIGN
 
