@@ -10,6 +10,8 @@
 // which are much smaller than K, and each part's largest scores and sums in
 // the workspace; the second joins the parts' and turns scores into weights.
 // Many columns: the second pass computes the scores again.
+#include <cooperative_groups.h>
+
 #include "pa_device.h"
 #include "pa_ptx.cuh"
 #include "pa_key_weights.h"
@@ -425,8 +427,16 @@ template <typename T> cudaError_t launch_few_of(const KwArgs& a, int D, int sms,
 }
 
 // ---- many columns, fp32: CUDA cores, 64 columns x 64 keys to a tile ---------------------------------
+// A cluster of CTAs to 64 columns, or to 64 keys, where there are fewer than two CTAs an
+// SM without it: they take the tiles in turn, and the first one joins what they
+// found, in order (four sequences of 4000 keys, 40 columns on 4 kv heads: 132 us, one CTA
+// each 493; a prompt of 500 rows 170 and 546).  Bound by shared memory's reads: 32
+// bytes of it for 16 multiply-adds a thread.
+namespace cg = cooperative_groups;
+
 constexpr int kThr = 256;
 constexpr int kTile = 64;
+constexpr int kTileCluster = 8;
 
 template <int D> constexpr size_t tile_smem() { return 2 * kTile * (D + 4) * sizeof(float); }
 
@@ -484,13 +494,16 @@ template <typename T, int D> __global__ void __launch_bounds__(kThr) kw_stats(co
     float* sq = smem;
     float* sk = smem + kTile * (D + 4);
     __shared__ int there[kTile];
+    __shared__ float2 found[kTile];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
     pdl_wait_primary();
     pdl_launch_dependents();
-    const int s = blockIdx.z, g = blockIdx.y, c0 = int(blockIdx.x) * kTile;
+    const int s = blockIdx.z, g = blockIdx.y, c0 = int(blockIdx.x) / C * kTile;
     const KwSeq q = kw_seq(a, s);
     if (q.bad && g == 0 && blockIdx.x == 0 && threadIdx.x == 0) flag(a.dev_status, PA_DEV_BAD_LEN);
     const int cols = q.T * a.G;
-    if (c0 >= cols) return;
+    if (c0 >= cols) return;  // the whole cluster
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     stage<T, D>(sq, [&](int r) -> const T* {
         const int c = c0 + r, t = c / a.G;
@@ -507,7 +520,7 @@ template <typename T, int D> __global__ void __launch_bounds__(kThr) kw_stats(co
         l[i] = 0.f;
     }
     const int end = q.L - q.T + min(cols - 1, c0 + kTile - 1) / a.G + 1;
-    for (int j0 = 0; j0 < end; j0 += kTile) {
+    for (int j0 = rank * kTile; j0 < end; j0 += C * kTile) {
         __syncthreads();
         stage<T, D>(sk, [&](int r) { return key_row<T>(a, s, g, j0 + r, q.L); });
         if (tid < kTile) {
@@ -532,16 +545,21 @@ template <typename T, int D> __global__ void __launch_bounds__(kThr) kw_stats(co
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) {
-            const float m2 = __shfl_xor_sync(0xffffffffu, m[i], o), l2 = __shfl_xor_sync(0xffffffffu, l[i], o);
-            const float top = fmaxf(m[i], m2);
-            l[i] = l[i] * ex2(m[i] - top) + l2 * ex2(m2 - top);
-            m[i] = top;
-        }
-        const int c = c0 + ty + 16 * i, t = c / a.G;
-        if (tx == 0 && c < cols)
-            a.stats[int64_t(q.row0 + t) * a.Hq + g * a.G + c - t * a.G] = make_float2(m[i], kw_reciprocal(l[i]));
+        for (int o = 8; o > 0; o >>= 1)
+            kw_join(m[i], l[i], __shfl_xor_sync(0xffffffffu, m[i], o), __shfl_xor_sync(0xffffffffu, l[i], o));
+        if (tx == 0) found[ty + 16 * i] = make_float2(m[i], l[i]);
     }
+    cluster.sync();
+    const int c = c0 + tid, t = c / a.G;
+    if (rank == 0 && tid < kTile && c < cols) {
+        float2 x = found[tid];
+        for (int i = 1; i < C; ++i) {
+            const float2 y = cluster.map_shared_rank(found, i)[tid];
+            kw_join(x.x, x.y, y.x, y.y);
+        }
+        a.stats[int64_t(q.row0 + t) * a.Hq + g * a.G + c - t * a.G] = make_float2(x.x, kw_reciprocal(x.y));
+    }
+    cluster.sync();  // nobody leaves while another may read what it found
 }
 
 // What 64 keys gather.
@@ -551,18 +569,22 @@ template <typename T, int D> __global__ void __launch_bounds__(kThr) kw_gather(c
     float* sk = smem + kTile * (D + 4);
     __shared__ int there[kTile];
     __shared__ float part[16][kTile];
+    __shared__ float found[kTile];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
     pdl_wait_primary();
     pdl_launch_dependents();
-    const int s = blockIdx.z, g = blockIdx.y, j0 = int(blockIdx.x) * kTile;
+    const int s = blockIdx.z, g = blockIdx.y, j0 = int(blockIdx.x) / C * kTile;
     const KwSeq q = kw_seq(a, s);
-    if (q.T == 0 || j0 >= q.L) return;
+    if (q.T == 0 || j0 >= q.L) return;  // the whole cluster
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int cols = q.T * a.G, before = q.L - q.T;
     stage<T, D>(sk, [&](int r) { return key_row<T>(a, s, g, j0 + r, q.L); });
     if (tid < kTile) there[tid] = key_row<T>(a, s, g, j0 + tid, q.L) != nullptr;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     // the first column that sees key j0
-    for (int c0 = max(0, j0 - before) * a.G / kTile * kTile; c0 < cols; c0 += kTile) {
+    const int first = max(0, j0 - before) * a.G / kTile * kTile;
+    for (int c0 = first + rank * kTile; c0 < cols; c0 += C * kTile) {
         __syncthreads();
         stage<T, D>(sq, [&](int r) -> const T* {
             const int c = c0 + r, t = c / a.G;
@@ -587,26 +609,53 @@ template <typename T, int D> __global__ void __launch_bounds__(kThr) kw_gather(c
 #pragma unroll
     for (int j = 0; j < 4; ++j) part[ty][tx + 16 * j] = sum[j];
     __syncthreads();
-    if (tid < kTile && j0 + tid < q.L) {
+    if (tid < kTile) {
         float w = 0.f;
         for (int i = 0; i < 16; ++i) w += part[i][tid];
+        found[tid] = w;
+    }
+    cluster.sync();
+    if (rank == 0 && tid < kTile && j0 + tid < q.L) {
+        float w = found[tid];
+        for (int i = 1; i < C; ++i) w += cluster.map_shared_rank(found, i)[tid];
         float* to = a.weights + (int64_t(s) * a.Hkv + g) * a.slots + j0 + tid;
         if (a.decay > 0.f && j0 + tid < before) w += a.decay * *to;
         *to = w;
     }
+    cluster.sync();  // nobody leaves while another may read what it found
 }
 
-template <typename T, int D> cudaError_t launch_tiles(const KwArgs& a, cudaStream_t st) {
+// A cluster to each of `tiles` tiles of every head.
+cudaError_t launch_clusters(void (*kern)(KwArgs), const KwArgs& a, int64_t tiles, int64_t others, int sms, size_t smem,
+                            cudaStream_t st) {
+    const int64_t heads = int64_t(a.Hkv) * a.num_seqs;
+    int size = 1;
+    while (size < kTileCluster && size < others && tiles * heads * size < 2 * sms) size *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(tiles * size), a.Hkv, a.num_seqs);
+    cfg.blockDim = dim3(kThr);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = size;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <typename T, int D> cudaError_t launch_tiles(const KwArgs& a, int sms, cudaStream_t st) {
     static std::atomic<uint64_t> done_stats{0}, done_gather{0};
     cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kw_stats<T, D>), tile_smem<D>(), done_stats);
     if (e == cudaSuccess)
         e = allow_shared_memory(reinterpret_cast<const void*>(kw_gather<T, D>), tile_smem<D>(), done_gather);
     if (e != cudaSuccess) return e;
-    const unsigned ct = unsigned((int64_t(a.max_rows) * a.G + kTile - 1) / kTile);
-    e = launch_pdl(kw_stats<T, D>, dim3(ct, a.Hkv, a.num_seqs), dim3(kThr), tile_smem<D>(), st, a);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(kw_gather<T, D>, dim3(unsigned((a.max_len + kTile - 1) / kTile), a.Hkv, a.num_seqs), dim3(kThr),
-                      tile_smem<D>(), st, a);
+    const int64_t columns = (int64_t(a.max_rows) * a.G + kTile - 1) / kTile, keys = (a.max_len + kTile - 1) / kTile;
+    e = launch_clusters(kw_stats<T, D>, a, columns, keys, sms, tile_smem<D>(), st);
+    return e == cudaSuccess ? launch_clusters(kw_gather<T, D>, a, keys, columns, sms, tile_smem<D>(), st) : e;
 }
 
 }  // namespace
@@ -670,7 +719,7 @@ cudaError_t launch_key_weights(const KeyWeightsCall& c, cudaStream_t st) {
         return c.dtype == PA_F16 ? launch_few_of<__half>(a, c.D, c.n_ctas, st)
                                  : launch_few_of<__nv_bfloat16>(a, c.D, c.n_ctas, st);
     }
-    if (c.dtype == PA_F32) return c.D == 64 ? launch_tiles<float, 64>(a, st) : launch_tiles<float, 128>(a, st);
+    if (c.dtype == PA_F32) return c.D == 64 ? launch_tiles<float, 64>(a, c.n_ctas, st) : launch_tiles<float, 128>(a, c.n_ctas, st);
     return launch_key_weights_tc(a, c.dtype, c.D, c.n_ctas, static_cast<char*>(c.workspace) + stats_bytes(c), st);
 }
 

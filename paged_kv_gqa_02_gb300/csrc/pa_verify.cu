@@ -40,7 +40,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kThr = 512;          // of the passes; the leader's warp comes behind them
 constexpr int kWarps = kThr / 32;
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 16;  // 2^4, of launch_walk
 constexpr int kMaxDrafts = 1024;  // rows of a sequence
 constexpr int kPackThr = 1024;
 constexpr uint64_t kWaitNs = 2000000000ull;  // an exchange gives up after 2 s
@@ -798,14 +798,27 @@ template <typename T> cudaError_t launch_walk(const VerifyCall& c, cudaStream_t 
     cudaError_t e = allow_wide_clusters(kern, wide);
     if (e == cudaSuccess) e = allow_shared_memory(kern, kRoom, allowed);
     if (e != cudaSuccess) return e;
-    // as many CTAs as the GPU holds at once, each with a unit for every thread
-    int size = kMaxCluster;
-    while (size > 1 && (int64_t(c.num_seqs) * size > 152 || c.vocab / 8 < size * kThr / 2)) size /= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(c.num_seqs) * size);
     cfg.blockDim = dim3(kThr + 32);
     cfg.dynamicSmemBytes = kRoom;
     cfg.stream = st;
+    // As wide a cluster as there is at once for every sequence, each CTA with a unit
+    // for every second thread of its passes (one sequence, 16000 tokens: 4 CTAs 20.2 us,
+    // 2 22.2, 8 21.8).  The GPU holds fewer clusters than its SMs divided by their size:
+    // 7 of 16 CTAs, and behind the last one a sequence waits (131072 tokens, chains of
+    // 5: 8 sequences 35 us with 16 CTAs each, 27 with 8).  Below 16, a seventh more
+    // is let in: 17 clusters of 8 run at once where the driver counts 15 (27 us, 40
+    // with 4 CTAs each), and trees of different sizes end one by one (16 trees: 43 us
+    // and 51).
+    static std::atomic<uint16_t> known[64][5];
+    auto room_for = [&](int log_size) {
+        const int n = clusters_at_once(kern, cfg, log_size, known);
+        return log_size < 4 ? n + n / 7 : n;
+    };
+    int log_size = 4;
+    while (log_size > 0 && ((c.vocab / 8 << 1) < (kThr << log_size) || c.num_seqs > room_for(log_size))) --log_size;
+    const int size = 1 << log_size;
+    cfg.gridDim = dim3(unsigned(c.num_seqs) * size);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -61,6 +61,8 @@ CASES = [  # rows, history, hq, hkv, d, page, decay, head_major
     ((300, 1, 129), (0, 500, 1), 16, 2, 128, 32, 1.0, False),
     ((511,), (1,), 3, 1, 128, 16, 0.0, False),
     ((700, 65), (60, 900), 8, 8, 64, 32, 1.0, False),
+    ((8, 9, 1), (3000, 2, 555), 16, 4, 128, 32, 1.0, False),
+    ((66, 33), (0, 1500), 2, 2, 64, 16, 0.5, False),
 ]
 
 

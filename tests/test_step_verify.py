@@ -147,6 +147,11 @@ def test_each_base_on_its_own_boundary(which, vocab, dtype):
     check(x)
 
 
+@pytest.mark.parametrize("seqs", [8, 9, 17, 40, 80])
+def test_as_many_sequences_as_the_gpu_holds_and_more(seqs):
+    check(problem((2,) * seqs, 16400, "bf16", True, True, 60 + seqs), near=1)
+
+
 @pytest.mark.parametrize("dtype,vocab", [("bf16", 300007), ("f32", 150001), ("f16", 8)])
 def test_vocabularies_beyond_the_slots(dtype, vocab):
     check(problem((3, 1, 5), vocab, dtype, True, False, 21), near=1)
