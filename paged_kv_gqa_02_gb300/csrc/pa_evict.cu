@@ -12,9 +12,19 @@
 // keys of one kv head, of K or of V, can work its way up tile by tile, reading a
 // tile before it writes it: what a tile overwrites belongs to keys that it or an
 // earlier tile has read.  A tile is 8 CTAs wide, so that a long sequence takes
-// few of them, and rows are read whole: columns of 32 or 64 bytes of them, which
-// need no cluster, were slower (86 and 100 us for eight long prompts, kernels
-// of both operations) as HBM reads scattered short pieces badly.
+// few of them (with 4: 87 us instead of 67, eight long prompts, kernels of both
+// operations), and a row goes to a cluster for each 128 bytes of it: whole rows of
+// 256 took 89 us, columns of 32 or 64 bytes, which need no cluster, 86 and 100, as HBM
+// reads scattered short pieces badly.  Two rows a thread instead of four: 72 us
+// (one long sequence 31 instead of 26); eight: 67 (23, but four short ones 13.6
+// instead of 12.2).
+//
+// Eight prompts of 10,000 to 16,000 tokens down to 2,048 and more, 8 heads of 128, bf16:
+// 67 us for 206 MB, of which 30 at a plain copy's rate.  13 are the selection; the
+// move waits for the tiles of the longest sequence, one after another.  The next
+// tile's loads before the cluster's wait take 74 registers for 40 and so half the
+// CTAs at once: 82 us.  Sequences in the order of their lengths: 59 us, but 1 to 3.5
+// more wherever they are alike (sixteen of 300 tokens 29 -> 32).
 #include <cooperative_groups.h>
 
 #include "pa_ptx.cuh"
