@@ -36,21 +36,21 @@ inline cudaError_t allow_wide_clusters(const void* kern, std::atomic<uint64_t>& 
     return e;
 }
 
-// How many clusters of 2^log_size CTAs of `kern` the current device holds at
-// once, `cfg` being their launch but for its grid; `known` keeps the answers, one
+// How many clusters of `size` CTAs (16 at most) of `kern` the current device holds
+// at once, `cfg` being their launch but for its grid; `known` keeps the answers, one
 // for each device and size.  0 where the question fails.
-inline int clusters_at_once(const void* kern, cudaLaunchConfig_t cfg, int log_size,
-                            std::atomic<uint16_t> (&known)[64][5]) {
+inline int clusters_at_once(const void* kern, cudaLaunchConfig_t cfg, int size,
+                            std::atomic<uint16_t> (&known)[64][17]) {
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     const bool kept = dev >= 0 && dev < 64;
-    const uint16_t before = kept ? known[dev][log_size].load(std::memory_order_relaxed) : 0;
+    const uint16_t before = kept ? known[dev][size].load(std::memory_order_relaxed) : 0;
     if (before) return before - 1;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 1u << log_size;
+    attr.val.clusterDim.x = unsigned(size);
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.gridDim = dim3(1u << log_size);
+    cfg.gridDim = dim3(unsigned(size));
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
@@ -58,7 +58,7 @@ inline int clusters_at_once(const void* kern, cudaLaunchConfig_t cfg, int log_si
         return 0;
     }
     if (n > 65534) n = 65534;
-    if (kept) known[dev][log_size].store(uint16_t(n + 1), std::memory_order_relaxed);
+    if (kept) known[dev][size].store(uint16_t(n + 1), std::memory_order_relaxed);
     return n;
 }
 

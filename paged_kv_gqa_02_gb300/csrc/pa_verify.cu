@@ -44,7 +44,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kThr = 512;          // of the passes; the leader's warp comes behind them
 constexpr int kWarps = kThr / 32;
-constexpr int kMaxCluster = 16;  // 2^4, of launch_walk
+constexpr int kMaxCluster = 16;
 constexpr int kMaxDrafts = 1024;  // rows of a sequence
 constexpr int kPackThr = 1024;
 constexpr uint64_t kWaitNs = 2000000000ull;  // an exchange gives up after 2 s
@@ -808,20 +808,21 @@ template <typename T> cudaError_t launch_walk(const VerifyCall& c, cudaStream_t 
     cfg.stream = st;
     // As wide a cluster as there is at once for every sequence, each CTA with a unit
     // for every second thread of its passes (one sequence, 16000 tokens: 4 CTAs 20.2 us,
-    // 2 22.2, 8 21.8).  The GPU holds fewer clusters than its SMs divided by their size:
-    // 7 of 16 CTAs, and behind the last one a sequence waits (131072 tokens, chains of
-    // 5: 8 sequences 35 us with 16 CTAs each, 27 with 8).  Below 16, a seventh more
-    // is let in: 17 clusters of 8 run at once where the driver counts 15 (27 us, 40
-    // with 4 CTAs each), and trees of different sizes end one by one (16 trees: 43 us
-    // and 51).
-    static std::atomic<uint16_t> known[64][5];
-    auto room_for = [&](int log_size) {
-        const int n = clusters_at_once(kern, cfg, log_size, known);
-        return log_size < 4 ? n + n / 7 : n;
+    // 2 22.2, 8 21.8).  A cluster lies in one group of SMs, so that the GPU holds 7 of 16
+    // CTAs, 15 of 8, 23 of 6, 28 of 5, 36 of 4, 46 of 3, 76 of 2, and behind the last
+    // one a sequence waits: chains of 5, 131072 tokens, 8 sequences 35 us with 16 CTAs
+    // each, 27 with 8; 18 45 us with 8, 31 with 6; 26 46 with 6, 38 with 5; 38 62 with 4,
+    // 54 with 3.  Of 8 two more run at once than the driver counts: 17 chains 27.5 us,
+    // with 6 CTAs each 31; 16 trees 37, with 6 45.
+    static std::atomic<uint16_t> known[64][17];
+    constexpr int kSizes[] = {kMaxCluster, 8, 6, 5, 4, 3, 2, 1};
+    auto fits = [&](int size) {
+        return (c.vocab / 8 << 1) >= kThr * size &&
+               c.num_seqs <= clusters_at_once(kern, cfg, size, known) + (size == 8 ? 2 : 0);
     };
-    int log_size = 4;
-    while (log_size > 0 && ((c.vocab / 8 << 1) < (kThr << log_size) || c.num_seqs > room_for(log_size))) --log_size;
-    const int size = 1 << log_size;
+    int pick = 0;
+    while (kSizes[pick] > 1 && !fits(kSizes[pick])) ++pick;
+    const int size = kSizes[pick];
     cfg.gridDim = dim3(unsigned(c.num_seqs) * size);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
