@@ -812,7 +812,7 @@ template <typename T> cudaError_t launch_walk(const VerifyCall& c, cudaStream_t 
     // CTAs, 15 of 8, 23 of 6, 28 of 5, 36 of 4, 46 of 3, 76 of 2, and behind the last
     // one a sequence waits: chains of 5, 131072 tokens, 8 sequences 35 us with 16 CTAs
     // each, 27 with 8; 18 45 us with 8, 31 with 6; 26 46 with 6, 38 with 5; 38 62 with 4,
-    // 54 with 3.  Of 8 two more run at once than the driver counts: 17 chains 27.5 us,
+    // 54 with 3.  Of 8 two more run at once than CUDA's query counts: 17 chains 27.5 us,
     // with 6 CTAs each 31; 16 trees 37, with 6 45.
     static std::atomic<uint16_t> known[64][17];
     constexpr int kSizes[] = {kMaxCluster, 8, 6, 5, 4, 3, 2, 1};
