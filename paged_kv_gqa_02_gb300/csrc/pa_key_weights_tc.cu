@@ -505,8 +505,10 @@ __global__ void __launch_bounds__(kThr, kPerSm)
                 return lane < PT && at * P < p.q.L ? table[at] : -1;
             };
             // The statistics of a tile's columns, to be read by the whole group: written
-            // a tile ahead.  Whoever writes a buffer has seen all warps begin the tile
-            // but one before, so nobody reads what stood in it three tiles ago.
+            // a tile ahead, in three buffers.  Whoever writes tile i + 1's has waited for
+            // all warps to write tile i's, which each does after it has waited for tile
+            // i - 1's, or once a part's last tile is done: so all are through with
+            // tile i - 2, whose buffer it is.
             auto show = [&](int b, float log, int to) {
                 const int lim = log == -INFINITY ? -1 : p.q.before + b * w.tq + my_t;  // a NaN counts as seen
                 sm_stats[128 * to + row] = -log;
@@ -531,12 +533,12 @@ __global__ void __launch_bounds__(kThr, kPerSm)
             for (int b = p.b0 + first; b < p.b1; b += 2, ++seen) {
                 uint32_t page_bits = 0;
                 if (kPass == 1) {
+                    ok = wait_warp(&st_full[3 * group + buf], turn, abort_flag);
+                    if (!ok) break;
                     if (b + 2 < p.b1) {
                         show(b + 2, ahead, buf == 2 ? 0 : buf + 1);
                         if (b + 4 < p.b1) ahead = column(b + 4);
                     }
-                    ok = wait_warp(&st_full[3 * group + buf], turn, abort_flag);
-                    if (!ok) break;
                 } else {
                     page_bits = __ballot_sync(0xffffffffu, page_ahead >= 0 && page_ahead < a.num_pages);
                     if (b + 2 < p.b1) page_ahead = pages(b + 2);
