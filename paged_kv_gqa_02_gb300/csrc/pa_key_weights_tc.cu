@@ -65,7 +65,7 @@ template <int D> struct Smem {
     static constexpr uint32_t kChunks = kLimits + 6 * 128 * 4;     // [2][3][4][2] lowest and highest of 32 columns'
     static constexpr uint32_t kHelp = kChunks + 6 * 4 * 2 * 4;     // [2][128] what a group leaves for the other
     static constexpr uint32_t kBars = kHelp + 2 * 128 * 8;
-    static constexpr int kNumBars = 2 + 2 * kStages + 4 + 6 + 4 + 1;
+    static constexpr int kNumBars = 2 + 2 * kStages + 4 + 6 + 4 + 2;
     static constexpr uint32_t kBytes = 1024 + kBars + kNumBars * 8 + 16;
 };
 
@@ -337,7 +337,8 @@ __global__ void __launch_bounds__(kThr, kPerSm)
     uint64_t* st_full = s_empty + 2;  // [group][3], gathering: the columns' statistics written
     uint64_t* help_full = st_full + 6;
     uint64_t* help_empty = help_full + 2;
-    uint64_t* never = help_empty + 2;  // never arrived on: the debug_timeout wait
+    uint64_t* mma_done = help_empty + 2;  // every product of the CTA has finished
+    uint64_t* never = mma_done + 1;       // never arrived on: the debug_timeout wait
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + S::kNumBars);
     volatile uint32_t* abort_flag = tslot + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -355,6 +356,7 @@ __global__ void __launch_bounds__(kThr, kPerSm)
             mbar_init(&help_full[i], 4);
             mbar_init(&help_empty[i], 4);
         }
+        mbar_init(mma_done, 1);
         mbar_init(never, 1);
         *abort_flag = 0u;
         mbar_fence_init();
@@ -472,6 +474,10 @@ __global__ void __launch_bounds__(kThr, kPerSm)
             }
         }
         if (!ok && lane == 0) raise_abort(abort_flag, a.dev_status);
+        // tensor memory is not freed, nor the operands' shared memory left, under a product
+        tc::commit_elect(mma_done);
+        if (!__all_sync(0xffffffffu, mbar_wait_ns(mma_done, 0, kWaitNs)) && lane == 0)
+            flag(a.dev_status, PA_DEV_TIMEOUT);
     } else {
         const int group = warp >> 2, row = tid & 127;  // the group's accumulator and buffers, the thread's lane of A
         float* sm_stats = reinterpret_cast<float*>(base + S::kStats) + 384 * group;
