@@ -293,7 +293,9 @@ pa_status pa_rotate(const pa_params *p, const pa_rows *r, const pa_rope *t, cons
  * largest logit (a NaN or +infinity, all -infinity) ends the walk with next
  * token -1 (PA_DEV_BAD_VALUE), as do random numbers that choose none.
  * -infinity in other logits is a probability of zero.
- * Uses of p: num_seqs, q_dtype.  vocab from 1 to 2^28, max_rows <= 1024; logits
+ * Uses of p: num_seqs, q_dtype, debug_timeout (1: the first exchange of a
+ * sequence's first CTA gives up at once, testing).  After PA_DEV_TIMEOUT what the
+ * call writes is void.  vocab from 1 to 2^28, max_rows <= 1024; logits
  * and noise aligned to their elements.  Where total_rows is 0, what has an entry
  * or more a row, temperature and noise may be NULL. */
 pa_status pa_verify(const pa_params *p, const pa_rows *r, int32_t vocab, const void *logits,

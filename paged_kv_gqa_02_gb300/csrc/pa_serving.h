@@ -118,6 +118,7 @@ struct VerifyCall {
     int32_t num_seqs, total_rows, max_rows, vocab;
     pa_dtype dtype;
     uint32_t* dev_status;
+    int32_t debug_timeout;
 };
 cudaError_t launch_verify(const VerifyCall& c, cudaStream_t st);
 

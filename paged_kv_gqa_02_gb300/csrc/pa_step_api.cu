@@ -166,6 +166,7 @@ PA_EXPORT pa_status pa_verify(const pa_params* p, const pa_rows* r, int32_t voca
     c.vocab = vocab;
     c.dtype = p->q_dtype;
     c.dev_status = dev_status;
+    c.debug_timeout = p->debug_timeout == 1;
     return cuda_status(pa::launch_verify(c, stream));
 }
 

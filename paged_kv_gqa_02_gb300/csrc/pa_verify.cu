@@ -48,6 +48,8 @@ constexpr int kMaxCluster = 16;
 constexpr int kMaxDrafts = 1024;  // rows of a sequence
 constexpr int kPackThr = 1024;
 constexpr uint64_t kWaitNs = 2000000000ull;  // an exchange gives up after 2 s
+constexpr uint64_t kTestNs = 2000000ull;     // or, testing, after 2 ms
+constexpr uint64_t kDrainNs = 1000000ull;    // what has been sent arrives within microseconds
 
 // The largest logit and the sum of 2^((x - largest) c); with a NaN or an
 // infinite largest one the sum is not finite.
@@ -358,10 +360,16 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
     if (warp == kWarps) {
         // ================================ leader ================================
         bool lost = false;  // an exchange gave up
+        const uint64_t limit = a.debug_timeout ? kTestNs : kWaitNs;
         // the cluster's results of an exchange
         auto wait = [&] {
             const int at = turn & 1;
-            if (!__all_sync(0xffffffffu, mbar_wait_ns(&arrived[at], (turn >> 1) & 1, kWaitNs))) lost = true;
+            // testing: the first CTA gives up on its first exchange, the others go on
+            const bool now = a.debug_timeout && rank == 0 && turn == 0;
+            if (now || !__all_sync(0xffffffffu, mbar_wait_ns(&arrived[at], (turn >> 1) & 1, limit))) {
+                lost = true;
+                return at;
+            }
             if (lane == 0) mbar_arrive_expect_tx(&arrived[at], bytes);  // for the exchange after the next
             ++turn;
             return at;
@@ -545,6 +553,13 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
             a.accepted_cu[s + 1] = count;
             a.next_tokens[s] = next;
         }
+        __syncwarp();
+        // Others may be an exchange ahead of a CTA that gave up, and send to its shared
+        // memory: it stays until all of them have stopped and what they sent is there.
+        // (Who did not give up has waited for all that is sent to it.)
+        cluster.sync();
+        if (lost)
+            for (int i = 0; i < 2; ++i) mbar_wait_ns(&arrived[(turn + i) & 1], ((turn + i) >> 1) & 1, kDrainNs);
         return;
     }
 
@@ -732,6 +747,8 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
     }
     cp_wait<0>();  // nobody leaves with copies under way
     if (!fine) flag(a.dev_status, PA_DEV_TIMEOUT);
+    __syncwarp();
+    cluster.sync();  // see the leader's
 }
 
 // Joins the sequences' lists: the walk left counts in accepted_cu and each

@@ -30,3 +30,17 @@ def test_products_end_before_their_tensor_memory_is_freed(name):
 
 def test_there_are_such_kernels():
     assert {"pa_key_weights_tc.cu", "pa_packed_tc.cu", "pa_prefill_tc.cu"} <= set(USERS)
+
+
+def test_the_walk_of_drafts_stays_until_its_cluster_has_stopped():
+    """Whoever may still be sent something by others of its cluster does not leave before a barrier of all of it."""
+    text = source("pa_verify.cu")
+    walk = text[text.index("verify_walk(const VerifyCall a)"):text.index("verify_pack(const VerifyCall a)")]
+    leader, passes = walk[walk.index("if (warp == kWarps) {"):].split("\n        return;\n    }\n", 1)
+    # the leader's last statements, and the passes': the barrier, then nothing that touches another CTA
+    for part in (leader, passes):
+        behind = part[part.rindex("cluster.sync()"):]
+        assert "order(" not in behind and "send(" not in behind and part.rindex("cluster.sync()") > part.rindex("PA_DEV_TIMEOUT")
+    # an exchange that was given up is not armed for the one after the next: its own bytes may still come
+    wait = leader[leader.index("auto wait = [&]"):leader.index("auto order")]
+    assert wait.index("return at;") < wait.index("mbar_arrive_expect_tx(")
