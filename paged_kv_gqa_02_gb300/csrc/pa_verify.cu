@@ -237,6 +237,10 @@ __device__ inline void better_over_warp(float& key, int& at) {
     at = __reduce_min_sync(0xffffffffu, key == top ? at : 0x7fffffff);
     key = top;
 }
+// A barrier of the cluster's CTAs that orders nothing in memory.
+__device__ inline void cluster_meet() {
+    asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
+}
 __device__ inline float rcp(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -557,7 +561,7 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
         // Others may be an exchange ahead of a CTA that gave up, and send to its shared
         // memory: it stays until all of them have stopped and what they sent is there.
         // (Who did not give up has waited for all that is sent to it.)
-        cluster.sync();
+        cluster_meet();
         if (lost)
             for (int i = 0; i < 2; ++i) mbar_wait_ns(&arrived[(turn + i) & 1], ((turn + i) >> 1) & 1, kDrainNs);
         return;
@@ -748,7 +752,7 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
     cp_wait<0>();  // nobody leaves with copies under way
     if (!fine) flag(a.dev_status, PA_DEV_TIMEOUT);
     __syncwarp();
-    cluster.sync();  // see the leader's
+    cluster_meet();  // see the leader's
 }
 
 // Joins the sequences' lists: the walk left counts in accepted_cu and each

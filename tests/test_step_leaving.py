@@ -39,8 +39,8 @@ def test_the_walk_of_drafts_stays_until_its_cluster_has_stopped():
     leader, passes = walk[walk.index("if (warp == kWarps) {"):].split("\n        return;\n    }\n", 1)
     # the leader's last statements, and the passes': the barrier, then nothing that touches another CTA
     for part in (leader, passes):
-        behind = part[part.rindex("cluster.sync()"):]
-        assert "order(" not in behind and "send(" not in behind and part.rindex("cluster.sync()") > part.rindex("PA_DEV_TIMEOUT")
+        behind = part[part.rindex("cluster_meet()"):]
+        assert "order(" not in behind and "send(" not in behind and part.rindex("cluster_meet()") > part.rindex("PA_DEV_TIMEOUT")
     # an exchange that was given up is not armed for the one after the next: its own bytes may still come
     wait = leader[leader.index("auto wait = [&]"):leader.index("auto order")]
     assert wait.index("return at;") < wait.index("mbar_arrive_expect_tx(")
