@@ -9,10 +9,14 @@
 // which is k times "subtract q, clamp, normalise" in one step, so a rejection
 // costs one sum over the vocabulary whatever came before it; the last child's
 // none, and certain drafts' (q a single token) none.  The next token is the
-// largest p_i / e_i for exponential e_i: a comparison of single terms, which
-// rounding can turn only where two are within a few units of 2^-24 of each
-// other, while a search in running sums would meet a border every few 2^-24 in a
-// vocabulary's tail.  M does not matter to it.
+// largest p_i / e_i for exponential e_i: a comparison of single terms, while a
+// search in running sums would meet a border every few 2^-24 in a vocabulary's
+// tail.  M does not matter to it.  A p is off by 2^-22 of its value at most for each
+// unit of its exponent (x - top) c, which is rounded, and by some more for the sums;
+// p - a q by that share of p and of a q, which is more of what is left.  Where the
+// draft's row is the target's, nothing is left, exactly: p - a q is one expression
+// everywhere, and its factor of the draft's exponentials, a times the sums' ratio, is
+// a where the sums are equal.
 //
 // The walk's time is a chain of passes, each bound by latency: the exponentials
 // of a row and one exchange, some 5 us together (64 chains of five drafts, 50021
@@ -71,7 +75,7 @@ enum { kGo, kMass, kPick, kStop };
 struct Order {
     int what, went, phase;    // phase: of the copies to the row's slots
     int dropped;              // certain drafts rejected
-    float p_top, q_top, less; // what is left: 2^((x - p_top) c) - less 2^((y - q_top) c), not below 0
+    float p_top, q_top, less; // what is left: left_of(2^((x - p_top) c), 2^((y - q_top) c), less)
 };
 // A thread's running Stat, the sum in two parts.
 struct Run {
@@ -226,6 +230,8 @@ __device__ inline Stat over_warp(const Run& s, float c) {
 __device__ inline bool usable(const Stat& s) {
     return s.top > -INFINITY && s.top < INFINITY && s.sum < INFINITY;  // false for a NaN
 }
+// What rejections left of a target's exponential: a draft's takes `less` of it.
+__device__ inline float left_of(float ex, float ey, float less) { return fmaxf(fmaf(-ey, less, ex), 0.f); }
 __device__ inline void better(float& key, int& at, float key2, int at2) {
     if (key2 > key || (key2 == key && at2 < at)) {
         key = key2;
@@ -449,6 +455,9 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
             }
             // what is left of p is max(p - used q, 0) / mass
             const float p_of = rcp(P.sum), q_of = row.q ? rcp(Q.sum) : 0.f;
+            // `used` of q in exponentials of the target's scale; 1 where the sums are equal (a division: 43.4 us
+            // for 16 trees instead of 43.0)
+            const float ratio = P.sum == Q.sum ? 1.f : P.sum * q_of;
             float used = 0.f, mass = 1.f, kept = -1.f;  // kept: what `used` was before the last child's rejection
             int dropped = 0;                            // certain drafts rejected here
             int went = 0;
@@ -463,11 +472,13 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
                 if (greedy) {
                     if (token == top_at) went = t;
                 } else {
-                    p = ex2((x - P.top) * c) * p_of;
+                    const float ex = ex2((x - P.top) * c);
                     float q = 1.f;
+                    p = ex * p_of;
                     if (row.q) {
-                        q = ex2((y - Q.top) * c) * q_of;
-                        p = fmaxf(p - used * q, 0.f) * rcp(mass);
+                        const float ey = ex2((y - Q.top) * c);
+                        q = ey * q_of;
+                        p = left_of(ex, ey, used * ratio) * p_of * rcp(mass);
                     } else {
                         for (int i = lane; i < dropped; i += 32) again |= removed[i] == token;
                         again = __any_sync(0xffffffffu, again);
@@ -495,7 +506,7 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
                     used += mass;
                 } else {
                     const float more = used + mass;
-                    order(Order{kMass, 0, 0, 0, P.top, Q.top, more * q_of * P.sum});
+                    order(Order{kMass, 0, 0, 0, P.top, Q.top, more * ratio});
                     const int from = wait();
                     if (lost) break;
                     float sum = 0.f;
@@ -527,7 +538,7 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
                 break;
             }
             for (;;) {
-                order(Order{kPick, 0, 0, dropped, P.top, Q.top, used * q_of * P.sum});
+                order(Order{kPick, 0, 0, dropped, P.top, Q.top, used * ratio});
                 const int from = wait();
                 if (lost) break;
                 float key = 0.f;
@@ -679,7 +690,7 @@ template <typename T> __global__ void __launch_bounds__(kThr + 32, 1) verify_wal
             const float p_top = o->p_top, q_top = o->q_top, less = o->less;
             auto left = [&](float x, float y) {
                 const float p = ex2((x - p_top) * c);
-                return less > 0.f ? fmaxf(p - ex2((y - q_top) * c) * less, 0.f) : p;
+                return less > 0.f ? left_of(p, ex2((y - q_top) * c), less) : p;
             };
             if (o->what == kMass) {
                 float sum = 0.f;
