@@ -352,7 +352,8 @@ pa_status pa_key_weights(const pa_params *p, const pa_rows *r, const void *q, co
  *   new_lens:    [num_seqs] int32: n, or -1 where nothing was evicted
  * Sequences with keep_lens[s] negative or not below context_lens[s] keep all:
  * kept and weights_out are filled as for n = context_lens[s].  Entries from n
- * on are left as they were.  weights_out must not overlap weights.
+ * on are left as they were.  weights_out must not overlap weights, nor new_lens
+ * keep_lens or context_lens (PA_ERR_SHAPE).
  * context_lens and the tables stay as they are: after the last layer,
  * pa_pages_resize with new_lens trims every sequence and frees its pages.
  * refcounts ([num_pages], may be NULL): a sequence of which a page from slot f

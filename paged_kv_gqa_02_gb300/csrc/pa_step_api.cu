@@ -14,6 +14,12 @@ constexpr int kMaxVocab = 1 << 28;        // tokens of a vocabulary: indices wit
 constexpr int64_t kMaxEvictUnits = 1 << 23;  // sequences times kv heads of an eviction: its grids stay in 31 bits
 constexpr int64_t kMaxWeights = int64_t(1) << 40;  // of a call: their scores' bytes stay in 64 bits
 
+// Whether n bytes at a and n at b have some in common.
+bool overlap(const void* a, const void* b, int64_t n) {
+    const int64_t d = static_cast<const char*>(a) - static_cast<const char*>(b);
+    return d < n && -d < n;
+}
+
 // What pa_key_weights takes of the parameters.
 pa_status check_key_weights(const pa_params* p, const pa_rows* r, pa::KeyWeightsCall* c) {
     if (!p || !r) return PA_ERR_NULL;
@@ -220,7 +226,11 @@ PA_EXPORT pa_status pa_evict(const pa_params* p, void* k_cache, void* v_cache, c
         !aligned(refcounts, 4) || !aligned(weights, 16) || !aligned(keep_lens, 4) || !aligned(weights_out, 16) ||
         !aligned(kept, 16) || !aligned(new_lens, 4))
         return PA_ERR_ALIGN;
-    if (weights_out == weights) return PA_ERR_SHAPE;
+    const int64_t lens = int64_t(p->num_seqs) * 4;
+    const int64_t table = lens * p->num_kv_heads * p->max_blocks_per_seq * p->page_size;
+    // new_lens of a sequence is written while CTAs of its other heads may still read its lengths
+    if (overlap(weights_out, weights, table) || overlap(new_lens, keep_lens, lens) || overlap(new_lens, context_lens, lens))
+        return PA_ERR_SHAPE;
     c.c.k = k_cache;
     c.c.v = v_cache;
     c.c.block_tables = block_tables;
