@@ -844,13 +844,15 @@ template <typename T> cudaError_t launch_walk(const VerifyCall& c, cudaStream_t 
     // CTAs, 15 of 8, 23 of 6, 28 of 5, 36 of 4, 46 of 3, 76 of 2, and behind the last
     // one a sequence waits: chains of 5, 131072 tokens, 8 sequences 35 us with 16 CTAs
     // each, 27 with 8; 18 45 us with 8, 31 with 6; 26 46 with 6, 38 with 5; 38 62 with 4,
-    // 54 with 3.  Of 8 two more run at once than CUDA's query counts: 17 chains 27.5 us,
-    // with 6 CTAs each 31; 16 trees 37, with 6 45.
+    // 54 with 3.  Of 8 two more run at once than the 15 that CUDA's query counts where all
+    // 152 SMs are there: 17 chains 27.5 us, with 6 CTAs each 31; 16 trees 37, with 6 45.
+    // Any other answer is taken as it is, 0 where the query fails.
     static std::atomic<uint16_t> known[64][17];
     constexpr int kSizes[] = {kMaxCluster, 8, 6, 5, 4, 3, 2, 1};
     auto fits = [&](int size) {
-        return (c.vocab / 8 << 1) >= kThr * size &&
-               c.num_seqs <= clusters_at_once(kern, cfg, size, known) + (size == 8 ? 2 : 0);
+        if ((c.vocab / 8 << 1) < kThr * size) return false;
+        const int n = clusters_at_once(kern, cfg, size, known);
+        return c.num_seqs <= (size == 8 && n == 15 ? 17 : n);
     };
     int pick = 0;
     while (kSizes[pick] > 1 && !fits(kSizes[pick])) ++pick;

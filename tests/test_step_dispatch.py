@@ -112,3 +112,33 @@ def test_evict_refuses_outputs_over_its_inputs(lib):
     for off in (2048, -2048):
         assert evict(lib, w=at(99, 0), out=at(99, off)) == 0, off
     assert evict(lib, keep=at(98, 0), cl=at(98, 0)) == 0  # both are read only
+
+
+ON_A_GB300 = {16: 7, 8: 15, 6: 23, 5: 28, 4: 36, 3: 46, 2: 76, 1: 152}
+
+
+def cluster_of(lib, seqs, vocab, dev, fits):
+    """CTAs to a sequence of a verification on a device that answers `fits`."""
+    for size in range(17):
+        lib.fake_fits(size, fits.get(size, -1))
+    lib.fake_device(dev)
+    p, r = ops.verify_params(num_seqs=seqs, dtype="bf16"), ops.make_rows(2 * seqs, 2)
+    assert lib.pa_verify(p, r, vocab, *[place(1)] * 13, None, None) == 0
+    sizes = (ctypes.c_int * 64)()
+    assert lib.fake_launches(sizes) == 2
+    return sizes[0]
+
+
+def test_clusters_of_a_verification(lib):
+    """As wide as fit at once for all sequences, by the device's own answer; one CTA where it has none."""
+    for seqs, size in ((1, 16), (7, 16), (8, 8), (15, 8), (17, 8), (18, 6), (23, 6), (24, 5), (28, 5), (36, 4), (46, 3), (76, 2), (77, 1), (500, 1)):
+        assert cluster_of(lib, seqs, 131072, 0, ON_A_GB300) == size, seqs
+    # a unit of eight tokens for every second thread of 512
+    for vocab, size in ((32768, 16), (32767, 8), (16384, 8), (8192, 4), (4096, 2), (4095, 1), (1, 1)):
+        assert cluster_of(lib, 1, vocab, 1, ON_A_GB300) == size, vocab
+    small = {16: 0, 8: 0, 6: 1, 5: 1, 4: 2, 3: 3, 2: 5, 1: 10}  # a part of a GPU
+    for seqs, size in ((1, 6), (2, 4), (3, 3), (5, 2), (6, 1)):
+        assert cluster_of(lib, seqs, 131072, 2, small) == size, seqs
+    assert cluster_of(lib, 14, 131072, 3, {**ON_A_GB300, 8: 12}) == 6  # no two more than it says
+    for seqs in (1, 2):  # the question fails
+        assert cluster_of(lib, seqs, 131072, 4, {}) == 1
