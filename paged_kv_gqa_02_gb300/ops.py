@@ -382,6 +382,16 @@ def _table(t, rows, width, dev, what):
     return t.data_ptr()
 
 
+def _float_table(t, rows, width, dev, what):
+    """As ``_table``, of float32."""
+    shape = t.shape
+    if (t.dtype is not _dtypes()[0] or t.get_device() != dev or not t.is_contiguous()
+            or (shape[0] < rows or shape[1] != width if len(shape) == 2
+                else t.numel() < rows * width or len(shape) > 1 and shape[-1] != width)):
+        raise ValueError(f"{what}: a contiguous float32 tensor of at least {rows} rows of {width} elements on cuda:{dev}")
+    return t.data_ptr()
+
+
 def _packed(t, code, rows, heads, dim, stride, dev, what):
     """Pointer of packed rows [rows or more][heads][dim], ``stride`` elements between rows."""
     shape = t.shape
@@ -597,7 +607,7 @@ def rotate(p: Params, r: Rows, rope: Rope, q, k, cu_lens, table=None, *, v=None,
           _packed(q, p.q_dtype, n, hq, d, r.q_stride, dev, "q"), _packed(k, p.kv_dtype, n, hkv, d, r.k_stride, dev, "k"),
           None if v is None else _packed(v, p.kv_dtype, n, hkv, d, r.v_stride, dev, "v"),
           _ints(cu_lens, b + 1, dev, "cu_lens"),
-          None if table is None else _floats(table, rope.table_rows * rope.rotary_dim, dev, "table"),
+          None if table is None or not rope.rotary_dim else _float_table(table, rope.table_rows, rope.rotary_dim, dev, "table"),
           None if positions is None else _table(positions, max(rope.axes, 1), n, dev, "positions"),
           None if context_lens is None else _ints(context_lens, b, dev, "context_lens"),
           _norm_weight(q_weight, p, dev, "q_weight"), _norm_weight(k_weight, p, dev, "k_weight"),
@@ -650,7 +660,7 @@ def verify(p: Params, r: Rows, logits, draft_logits, tokens, parents, cu_lens, t
           None if draft_logits is None else _logits(draft_logits, p.q_dtype, n, vocab, r.k_stride, dev, "draft_logits"),
           _ints(tokens, n, dev, "tokens"), _ints(parents, n, dev, "parents"), _ints(cu_lens, b + 1, dev, "cu_lens"),
           _floats(temperature, b, dev, "temperature"), _floats(uniform, n, dev, "uniform"),
-          _floats(noise, b * vocab, dev, "noise"),
+          _float_table(noise, b, vocab, dev, "noise"),
           None if context_lens is None else _ints(context_lens, b, dev, "context_lens"),
           _ints(accepted, n, dev, "accepted"), _ints(accepted_cu, b + 1, dev, "accepted_cu"),
           _ints(next_tokens, b, dev, "next_tokens"), None if new_lens is None else _ints(new_lens, b, dev, "new_lens"),
