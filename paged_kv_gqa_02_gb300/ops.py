@@ -601,8 +601,8 @@ def rotate(p: Params, r: Rows, rope: Rope, q, k, cu_lens, table=None, *, v=None,
         k_out = _new_rows(n, hkv, d, rope.k_out_stride, k, stream)
     cache = (None, None, None)
     if k_cache is not None:
-        cache = (_pool(k_cache, p, dev, "k_cache"), _pool(v_cache, p, dev, "v_cache"),
-                 _table(block_tables, b, p.max_blocks_per_seq, dev, "block_tables"))
+        cache = (_pool(k_cache, p, dev, "k_cache"), None if v_cache is None else _pool(v_cache, p, dev, "v_cache"),
+                 None if block_tables is None else _table(block_tables, b, p.max_blocks_per_seq, dev, "block_tables"))
     _call("pa_rotate", dev, stream, p, r, rope,
           _packed(q, p.q_dtype, n, hq, d, r.q_stride, dev, "q"), _packed(k, p.kv_dtype, n, hkv, d, r.k_stride, dev, "k"),
           None if v is None else _packed(v, p.kv_dtype, n, hkv, d, r.v_stride, dev, "v"),

@@ -41,3 +41,9 @@ def test_no_dims_turn_without_a_table(on_the_host):
         with pytest.raises(Passed):
             ops.rotate(params(), ops.make_rows(5, 3), ops.make_rope(0), bf16(5, 8, 64), bf16(5, 2, 64), i32(3), table, context_lens=i32(2),
                        q_out=bf16(5, 8, 64), k_out=bf16(5, 2, 64))
+
+
+def test_a_store_without_all_of_the_cache_is_the_librarys_to_refuse(on_the_host):
+    for missing in ("v_cache", "block_tables", "v"):
+        with pytest.raises(Passed):
+            rotate_call(**{missing: None})
