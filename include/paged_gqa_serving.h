@@ -318,7 +318,10 @@ pa_status pa_verify(const pa_params *p, const pa_rows *r, int32_t vocab, const v
  * decay in [0, 1].  A sequence without rows is left as it was.  Keys in pages
  * outside the pool take no part (PA_DEV_BAD_PAGE), theirs is decay alone.  A
  * score of -infinity weighs nothing; a NaN or +infinity makes what its row
- * adds NaN.  Sums, largest scores and weights are fp32.
+ * adds NaN.  Finite scores may have any size.  Sums, largest scores and weights are
+ * fp32; with 16-bit types and max_rows G above 32, a row's largest score below 128 (in
+ * base 2) and the logarithm of its sum are one fp32 number, whose rounding (2^-18 at
+ * most) is in that row's weights.
  * Uses of p as in pa_tree (head_dim 64 or 128; out_dtype is not used; no
  * windows, splits or decode_q_rows); max_context_len is a bound on
  * every context_lens[s] (0: what a table holds): longer ones are

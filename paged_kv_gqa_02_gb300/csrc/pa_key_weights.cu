@@ -281,7 +281,8 @@ __global__ void __launch_bounds__(kFewThr, Few<T, D>::kPerSm) few_scores(const K
                 if (8 * y + 2 * c >= a.width) continue;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    float s0 = x[y][k] * a.scale_log2, s1 = x[y][2 + k] * a.scale_log2;
+                    // rounded here, as the fold reads them: not to be contracted with a difference
+                    float s0 = __fmul_rn(x[y][k], a.scale_log2), s1 = __fmul_rn(x[y][2 + k], a.scale_log2);
                     if (edge) {
                         const int last = before + (early ? (8 * y + 2 * c + k) / a.G : 0);
                         if (j > last) s0 = -INFINITY;
@@ -546,7 +547,7 @@ template <typename T, int D> __global__ void __launch_bounds__(kThr) kw_stats(co
             for (int j = 0; j < 4; ++j) {
                 const int key = tx + 16 * j;
                 if (j0 + key <= last[i] && there[key]) {
-                    const float x = acc[i][j] * a.scale_log2, top = fmaxf(m[i], x);
+                    const float x = __fmul_rn(acc[i][j], a.scale_log2), top = fmaxf(m[i], x);  // rounded, in both kernels
                     l[i] = l[i] * ex2(m[i] - top) + ex2(x - top);
                     m[i] = top;
                 }
@@ -612,7 +613,7 @@ template <typename T, int D> __global__ void __launch_bounds__(kThr) kw_gather(c
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int key = tx + 16 * j;
-                if (j0 + key <= before + t && there[key]) sum[j] += ex2(acc[i][j] * a.scale_log2 - st.x) * st.y;
+                if (j0 + key <= before + t && there[key]) sum[j] += ex2(__fmul_rn(acc[i][j], a.scale_log2) - st.x) * st.y;
             }
         }
     }

@@ -19,8 +19,10 @@
 // pass, and 128 x 128 of them take longer than their product.  A column's m and l
 // go into one number, m + log2 l, which all lanes read from shared memory: with
 // two, 16 bytes for two scores, those reads bounded the second pass (92 us against
-// the first's 59, four prompts of 2560 rows and less); its rounding is half a step
-// of a number near the scores, as theirs is.
+// the first's 59, four prompts of 2560 rows and less).  Its rounding, 2^-18 where m
+// is below 128, goes into the column's weights.  Columns of larger scores, of which
+// it would take more and at last all of log2 l, keep both numbers, and their chunk
+// goes another way (which costs the others 2%: 114.0 -> 116.8 us).
 //
 // Units (an A tile with all its B tiles) are laid on a line, sequence by
 // sequence and kv head by kv head, each as long as it costs, and the line is cut
@@ -53,6 +55,8 @@ constexpr int kStart = 2;          // what beginning and ending a unit costs, in
 constexpr int kMinShare = 4;       // of the line, a CTA (300 rows, 64/8 heads: 22 us; 1: 24, 12: 31)
 constexpr uint32_t kHalf = kTile * 128;  // bytes of 64 dims of a tile
 constexpr uint32_t kNegInf = 0xff800000u;
+constexpr float kFar = 128.f;      // largest scores (base 2, scaled) below it: m + log2 l is off by 2^-18 at most
+constexpr int kFarColumn = -2;     // among a chunk's limits: a column of larger ones
 constexpr uint64_t kWaitNs = 2000000000ull;  // a role gives up after 2 s on one barrier
 constexpr uint32_t kSleepNs = 20000;
 
@@ -60,8 +64,9 @@ template <int D> struct Smem {
     static constexpr int kStages = D == 128 ? 2 : 4;
     static constexpr uint32_t kTileBytes = kTile * D * 2;
     static constexpr uint32_t kB = kTileBytes;
-    static constexpr uint32_t kStats = kB + kStages * kTileBytes;  // [group][3][128] of -(m + log2 l)
-    static constexpr uint32_t kLimits = kStats + 6 * 128 * 4;      // [2][3][128] last key that a column sees
+    static constexpr uint32_t kStats = kB + kStages * kTileBytes;  // [group][3][128] of -(m + log2 l), or -m
+    static constexpr uint32_t kFactors = kStats + 6 * 128 * 4;     // [2][3][128] 1, or 1 / l
+    static constexpr uint32_t kLimits = kFactors + 6 * 128 * 4;    // [2][3][128] last key that a column sees
     static constexpr uint32_t kChunks = kLimits + 6 * 128 * 4;     // [2][3][4][2] lowest and highest of 32 columns'
     static constexpr uint32_t kHelp = kChunks + 6 * 4 * 2 * 4;     // [2][128] what a group leaves for the other
     static constexpr uint32_t kBars = kHelp + 2 * 128 * 8;
@@ -72,7 +77,8 @@ template <int D> struct Smem {
 struct WideArgs {
     KwArgs a;
     int32_t tq, workers, head_first;
-    float* logs;          // [total_rows][Hq] of m + log2 l, -infinity where a column saw nothing
+    float* logs;          // [2][total_rows][Hq] of log_of
+    int64_t columns;      // total_rows Hq
     float2* parts_stats;  // [2 workers][128]
     float* parts_sums;    // [2 workers][128]
 };
@@ -291,11 +297,24 @@ __device__ inline uint64_t pair_of(uint32_t lo, uint32_t hi) {
     return pairs::pack(__uint_as_float(lo), __uint_as_float(hi));
 }
 
-// m + log2 l; -infinity for a column that saw nothing.
-__device__ inline float log_of(float m, float l) { return l == 0.f ? -INFINITY : m + log2f(l); }
+// A column's weights are 2^(s - x) y: (m + log2 l, 1), or, where that sum would lose
+// what matters of log2 l, (m, 1 / l).  x = -infinity: the column saw nothing.
+__device__ inline float2 log_of(float m, float l) {
+    if (l == 0.f) return make_float2(-INFINITY, 1.f);
+    return fabsf(m) < kFar ? make_float2(m + log2f(l), 1.f) : make_float2(m, 1.f / l);
+}
+__device__ inline void set_log(const WideArgs& w, int64_t column, float m, float l) {
+    const float2 x = log_of(m, l);
+    w.logs[column] = x.x;
+    w.logs[w.columns + column] = x.y;
+}
 
-// 32 scores of a lane: the running maximum (base 2, scaled) and sum.
-__device__ inline void take(float& m, uint64_t& l, uint64_t& l2, const uint32_t (&r)[32], float scale) {
+// 32 scores of a lane: the running maximum (base 2, scaled), whether it is far, and the
+// sum.  `real`: the lane's result is used.  A far maximum is a rounded product, and so are the scores that it is
+// taken from: a product that is not rounded can lie half a step of m beside it, which at
+// 2^30 is more than an exponent has room for.
+__device__ inline void take(float& m, bool& far, uint64_t& l, uint64_t& l2, const uint32_t (&r)[32], float scale,
+                            bool real) {
     float top = __uint_as_float(r[0]);
 #pragma unroll
     for (int i = 1; i < 31; i += 2) top = max3(top, __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
@@ -306,6 +325,17 @@ __device__ inline void take(float& m, uint64_t& l, uint64_t& l2, const uint32_t 
         l = pairs::mul(l, down2);
         l2 = pairs::mul(l2, down2);
         m = top;
+        far = real && fabsf(m) >= kFar;
+    }
+    if (far) {
+        // one by one: a paired product and sum become one operation, rounded once
+        auto term = [&](uint32_t v) { return ex2(__fsub_rn(__fmul_rn(__uint_as_float(v), scale), m)); };
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            l = pairs::add(l, pairs::pack(term(r[i]), term(r[i + 1])));
+            l2 = pairs::add(l2, pairs::pack(term(r[i + 2]), term(r[i + 3])));
+        }
+        return;
     }
     const uint64_t k = pairs::pack(scale, scale), minus = pairs::pack(-m, -m);
 #pragma unroll
@@ -315,6 +345,13 @@ __device__ inline void take(float& m, uint64_t& l, uint64_t& l2, const uint32_t 
         l = pairs::add(l, pairs::pack(ex2(x.x), ex2(x.y)));
         l2 = pairs::add(l2, pairs::pack(ex2(y.x), ex2(y.y)));
     }
+}
+
+// A score's weight where its column or a neighbour has a far maximum.  Above 1 only
+// where the two passes' products would differ; a NaN stays one.
+__device__ inline float far_weight(uint32_t v, float scale, float x, float y) {
+    const float e = ex2(__fadd_rn(__fmul_rn(__uint_as_float(v), scale), x));
+    return (e > 1.f ? 1.f : e) * y;
 }
 
 template <int kPass, typename T, int D>
@@ -481,6 +518,7 @@ __global__ void __launch_bounds__(kThr, kPerSm)
     } else {
         const int group = warp >> 2, row = tid & 127;  // the group's accumulator and buffers, the thread's lane of A
         float* sm_stats = reinterpret_cast<float*>(base + S::kStats) + 384 * group;
+        float* sm_factors = reinterpret_cast<float*>(base + S::kFactors) + 384 * group;
         int* sm_limits = reinterpret_cast<int*>(base + S::kLimits) + 384 * group;
         int* sm_chunks = reinterpret_cast<int*>(base + S::kChunks) + 24 * group;
         float2* sm_help = reinterpret_cast<float2*>(base + S::kHelp);
@@ -497,14 +535,16 @@ __global__ void __launch_bounds__(kThr, kPerSm)
             n += tiles;
             if (first >= tiles) continue;
             float m = kLowestScore, sum = 0.f;
+            bool far = false;
             uint64_t acc = 0, acc2 = 0;  // two sums each
             const int32_t* table = a.block_tables + int64_t(p.s) * a.max_blocks;
             // statistics: the lane's column; gathering: the lane's key
             const int t = p.unit * w.tq + my_t;
             const int key = kTile * p.unit + row;
-            auto column = [&](int b) {  // m + log2 l of the thread's column of Q tile b
+            auto stat_at = [&](int tt) { return w.logs + (int64_t(p.q.row0 + tt) * a.Hq + p.g * a.G + my_h); };
+            auto column = [&](int b) {  // the first number of log_of the thread's column of Q tile b
                 const int tt = b * w.tq + my_t;
-                return row < cols && tt < p.q.T ? w.logs[int64_t(p.q.row0 + tt) * a.Hq + p.g * a.G + my_h] : -INFINITY;
+                return row < cols && tt < p.q.T ? *stat_at(tt) : -INFINITY;
             };
             auto pages = [&](int b) {  // a lane of PT: the tile's page
                 const int at = b * PT + lane;
@@ -517,9 +557,12 @@ __global__ void __launch_bounds__(kThr, kPerSm)
             // tile i - 2, whose buffer it is.
             auto show = [&](int b, float log, int to) {
                 const int lim = log == -INFINITY ? -1 : p.q.before + b * w.tq + my_t;  // a NaN counts as seen
+                const bool far = lim >= 0 && fabsf(log) >= kFar;
                 sm_stats[128 * to + row] = -log;
+                sm_factors[128 * to + row] = far ? stat_at(b * w.tq + my_t)[w.columns] : 1.f;
                 sm_limits[128 * to + row] = lim;
-                const int low = __reduce_min_sync(0xffffffffu, lim), high = __reduce_max_sync(0xffffffffu, lim);
+                const int low = __reduce_min_sync(0xffffffffu, far ? kFarColumn : lim);
+                const int high = __reduce_max_sync(0xffffffffu, lim);
                 if (lane == 0) {
                     sm_chunks[8 * to + 2 * (warp & 3)] = low;
                     sm_chunks[8 * to + 2 * (warp & 3) + 1] = high;
@@ -576,7 +619,7 @@ __global__ void __launch_bounds__(kThr, kPerSm)
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] = (bits >> i) & 1u ? v[i] : kNegInf;
                         }
-                        take(m, acc, acc2, v, a.scale_log2);
+                        take(m, far, acc, acc2, v, a.scale_log2, row < cols);
                     } else {
                         const int low = sm_chunks[8 * buf + 2 * c], high = sm_chunks[8 * buf + 2 * c + 1];
                         if (high < kTile * p.unit) continue;  // no column sees a key of the tile
@@ -591,7 +634,7 @@ __global__ void __launch_bounds__(kThr, kPerSm)
                                 acc = pairs::add(acc, pairs::pack(ex2(e.x), ex2(e.y)));
                                 acc2 = pairs::add(acc2, pairs::pack(ex2(f.x), ex2(f.y)));
                             }
-                        } else {
+                        } else if (low != kFarColumn) {
                             const int* lim = sm_limits + 128 * buf + 32 * c;
 #pragma unroll
                             for (int i = 0; i < 32; i += 4) {
@@ -603,6 +646,18 @@ __global__ void __launch_bounds__(kThr, kPerSm)
                                 const float e3 = ex2(fmaf(__uint_as_float(v[i + 3]), a.scale_log2, y.w));
                                 sum += (key <= last4.x ? e0 : 0.f) + (key <= last4.y ? e1 : 0.f);
                                 sum += (key <= last4.z ? e2 : 0.f) + (key <= last4.w ? e3 : 0.f);
+                            }
+                        } else {
+                            const float4* factors = reinterpret_cast<const float4*>(sm_factors + 128 * buf + 32 * c);
+                            const int* lim = sm_limits + 128 * buf + 32 * c;
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                const float4 y = st[i / 4], f = factors[i / 4];
+                                const int4 last4 = *reinterpret_cast<const int4*>(lim + i);
+                                if (key <= last4.x) sum += far_weight(v[i], a.scale_log2, y.x, f.x);
+                                if (key <= last4.y) sum += far_weight(v[i + 1], a.scale_log2, y.y, f.y);
+                                if (key <= last4.z) sum += far_weight(v[i + 2], a.scale_log2, y.z, f.z);
+                                if (key <= last4.w) sum += far_weight(v[i + 3], a.scale_log2, y.w, f.w);
                             }
                         }
                     }
@@ -640,7 +695,7 @@ __global__ void __launch_bounds__(kThr, kPerSm)
                 if (!p.whole)
                     w.parts_stats[(2 * int64_t(blockIdx.x) + p.begins) * kTile + row] = make_float2(m, sum);
                 else if (row < cols && t < p.q.T)
-                    w.logs[int64_t(p.q.row0 + t) * a.Hq + p.g * a.G + my_h] = log_of(m, sum);
+                    set_log(w, int64_t(p.q.row0 + t) * a.Hq + p.g * a.G + my_h, m, sum);
             } else {
                 bool there = false;
                 if (key < p.q.L) {
@@ -691,7 +746,7 @@ template <int kPass> __global__ void __launch_bounds__(kTile) wide_join(const __
     if (kPass == 0) {
         const int t = p.unit * w.tq + tid / a.G;
         if (tid < w.tq * a.G && t < p.q.T)
-            w.logs[int64_t(p.q.row0 + t) * a.Hq + p.g * a.G + tid % a.G] = log_of(m, l);
+            set_log(w, int64_t(p.q.row0 + t) * a.Hq + p.g * a.G + tid % a.G, m, l);
     } else {
         const int key = kTile * p.unit + tid;
         if (key < p.q.L) {
@@ -728,6 +783,7 @@ cudaError_t launch_key_weights_tc(const KwArgs& a, pa_dtype dt, int D, int n_cta
     w.workers = kPerSm * n_ctas;
     w.head_first = a.head_stride <= a.token_stride;
     w.logs = reinterpret_cast<float*>(a.stats);
+    w.columns = int64_t(a.total_rows) * a.Hq;
     w.parts_stats = static_cast<float2*>(parts);
     w.parts_sums = reinterpret_cast<float*>(w.parts_stats + size_t(2) * w.workers * kTile);
     CUtensorMap mq, mk;
