@@ -17,6 +17,7 @@
 // against 121, 32 78 against 128.
 #include <cooperative_groups.h>
 
+#include "pa_cp_async.cuh"
 #include "pa_device.h"
 #include "pa_ptx.cuh"
 #include "pa_key_weights.h"
@@ -105,14 +106,6 @@ template <typename T, int D> struct Few {
     static constexpr size_t kSmem = size_t(kFewWarps) * kStages * kTileBytes;
     static constexpr int kPerSm = kTileBytes <= 4096 ? 4 : 2;  // CTAs: 192 KB of slots an SM at most
 };
-
-// K passes through L2 as the first to leave it: the scores are to be there still.
-__device__ inline void cp_async16(uint32_t to, const void* from, uint64_t policy) {
-    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "l"(policy)
-                 : "memory");
-}
-__device__ inline void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ inline void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // q of the columns as the lane meets them in a product, column 8 n + 2 c and
 // the next: fragments in registers; fp32 reads q where it lies.
@@ -211,7 +204,7 @@ __global__ void __launch_bounds__(kFewThr, Few<T, D>::kPerSm) few_scores(const K
     int64_t id = share * worker;
     uint4* mine = slots + warp * (kStages * Few<T, D>::kTileBytes / 16);
     const uint32_t mine_u32 = smem_u32(mine);
-    const uint64_t policy = l2_policy_evict_first();
+    const uint64_t policy = l2_policy_evict_first();  // K leaves L2 first: the scores are to be there still
     const bool early = a.max_rows > 1;  // rows that do not see all keys
     while (id < id1) {  // a head's part of the run
         const Place p = place_of(a, id, 16, lane);
@@ -451,18 +444,14 @@ constexpr int kTileCluster = 8;
 
 template <int D> constexpr size_t tile_smem() { return 2 * kTile * (D + 4) * sizeof(float); }
 
-// Rows of D elements to shared memory as floats; row r from from(r), nullptr: zeros.
-template <typename T, int D, typename F> __device__ inline void stage(float* to, F from) {
-    constexpr int kVec = Elt<T>::kVec, kUnits = D / kVec;
+// Rows of D elements to shared memory; row r from from(r), nullptr: zeros.
+template <int D, typename F> __device__ inline void stage(float* to, F from) {
+    constexpr int kUnits = D / 4;
     for (int i = threadIdx.x; i < kTile * kUnits; i += kThr) {
         const int r = i / kUnits, u = i - r * kUnits;
-        const T* p = from(r);
-        float x[kVec];
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (p) raw = reinterpret_cast<const uint4*>(p)[u];
-        vec_to_f32<T>(raw, x);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) to[r * (D + 4) + u * kVec + j] = x[j];
+        const float* p = from(r);
+        *reinterpret_cast<float4*>(to + r * (D + 4) + u * 4) =
+            p ? reinterpret_cast<const float4*>(p)[u] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 }
 
@@ -492,15 +481,15 @@ template <int D> __device__ inline void products(const float* sq, const float* s
     }
 }
 
-template <typename T> __device__ inline const T* key_row(const KwArgs& a, int s, int g, int j, int L) {
+__device__ inline const float* key_row(const KwArgs& a, int s, int g, int j, int L) {
     if (j >= L) return nullptr;
     const int pg = a.block_tables[int64_t(s) * a.max_blocks + (j >> a.page_shift)];
     if (pg < 0 || pg >= a.num_pages) return nullptr;
-    return static_cast<const T*>(a.k) + pg * a.page_stride + (j & (a.page_size - 1)) * a.token_stride +
+    return static_cast<const float*>(a.k) + pg * a.page_stride + (j & (a.page_size - 1)) * a.token_stride +
            g * a.head_stride;
 }
 // A column's largest score and sum over the keys that it sees.
-template <typename T, int D> __global__ void __launch_bounds__(kThr) kw_stats(const KwArgs a) {
+template <int D> __global__ void __launch_bounds__(kThr) kw_stats(const KwArgs a) {
     extern __shared__ float smem[];
     float* sq = smem;
     float* sk = smem + kTile * (D + 4);
@@ -516,10 +505,10 @@ template <typename T, int D> __global__ void __launch_bounds__(kThr) kw_stats(co
     const int cols = q.T * a.G;
     if (c0 >= cols) return;  // the whole cluster
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    stage<T, D>(sq, [&](int r) -> const T* {
+    stage<D>(sq, [&](int r) -> const float* {
         const int c = c0 + r, t = c / a.G;
         if (c >= cols) return nullptr;
-        return static_cast<const T*>(a.q) + int64_t(q.row0 + t) * a.q_stride + int64_t(g * a.G + c - t * a.G) * D;
+        return static_cast<const float*>(a.q) + int64_t(q.row0 + t) * a.q_stride + int64_t(g * a.G + c - t * a.G) * D;
     });
     int last[4];  // the last key that the thread's columns see
     float m[4], l[4];
@@ -533,9 +522,9 @@ template <typename T, int D> __global__ void __launch_bounds__(kThr) kw_stats(co
     const int end = q.L - q.T + min(cols - 1, c0 + kTile - 1) / a.G + 1;
     for (int j0 = rank * kTile; j0 < end; j0 += C * kTile) {
         __syncthreads();
-        stage<T, D>(sk, [&](int r) { return key_row<T>(a, s, g, j0 + r, q.L); });
+        stage<D>(sk, [&](int r) { return key_row(a, s, g, j0 + r, q.L); });
         if (tid < kTile) {
-            there[tid] = key_row<T>(a, s, g, j0 + tid, q.L) != nullptr;
+            there[tid] = key_row(a, s, g, j0 + tid, q.L) != nullptr;
             if (!there[tid] && j0 + tid < q.L) flag(a.dev_status, PA_DEV_BAD_PAGE);
         }
         __syncthreads();
@@ -574,7 +563,7 @@ template <typename T, int D> __global__ void __launch_bounds__(kThr) kw_stats(co
 }
 
 // What 64 keys gather.
-template <typename T, int D> __global__ void __launch_bounds__(kThr) kw_gather(const KwArgs a) {
+template <int D> __global__ void __launch_bounds__(kThr) kw_gather(const KwArgs a) {
     extern __shared__ float smem[];
     float* sq = smem;
     float* sk = smem + kTile * (D + 4);
@@ -590,17 +579,17 @@ template <typename T, int D> __global__ void __launch_bounds__(kThr) kw_gather(c
     if (q.T == 0 || j0 >= q.L) return;  // the whole cluster
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int cols = q.T * a.G, before = q.L - q.T;
-    stage<T, D>(sk, [&](int r) { return key_row<T>(a, s, g, j0 + r, q.L); });
-    if (tid < kTile) there[tid] = key_row<T>(a, s, g, j0 + tid, q.L) != nullptr;
+    stage<D>(sk, [&](int r) { return key_row(a, s, g, j0 + r, q.L); });
+    if (tid < kTile) there[tid] = key_row(a, s, g, j0 + tid, q.L) != nullptr;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     // the first column that sees key j0
     const int first = max(0, j0 - before) * a.G / kTile * kTile;
     for (int c0 = first + rank * kTile; c0 < cols; c0 += C * kTile) {
         __syncthreads();
-        stage<T, D>(sq, [&](int r) -> const T* {
+        stage<D>(sq, [&](int r) -> const float* {
             const int c = c0 + r, t = c / a.G;
             if (c >= cols) return nullptr;
-            return static_cast<const T*>(a.q) + int64_t(q.row0 + t) * a.q_stride + int64_t(g * a.G + c - t * a.G) * D;
+            return static_cast<const float*>(a.q) + int64_t(q.row0 + t) * a.q_stride + int64_t(g * a.G + c - t * a.G) * D;
         });
         __syncthreads();
         float acc[4][4];
@@ -658,15 +647,15 @@ cudaError_t launch_clusters(void (*kern)(KwArgs), const KwArgs& a, int64_t tiles
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-template <typename T, int D> cudaError_t launch_tiles(const KwArgs& a, int sms, cudaStream_t st) {
+template <int D> cudaError_t launch_tiles(const KwArgs& a, int sms, cudaStream_t st) {
     static std::atomic<uint64_t> done_stats{0}, done_gather{0};
-    cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kw_stats<T, D>), tile_smem<D>(), done_stats);
+    cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kw_stats<D>), tile_smem<D>(), done_stats);
     if (e == cudaSuccess)
-        e = allow_shared_memory(reinterpret_cast<const void*>(kw_gather<T, D>), tile_smem<D>(), done_gather);
+        e = allow_shared_memory(reinterpret_cast<const void*>(kw_gather<D>), tile_smem<D>(), done_gather);
     if (e != cudaSuccess) return e;
     const int64_t columns = (int64_t(a.max_rows) * a.G + kTile - 1) / kTile, keys = (a.max_len + kTile - 1) / kTile;
-    e = launch_clusters(kw_stats<T, D>, a, columns, keys, sms, tile_smem<D>(), st);
-    return e == cudaSuccess ? launch_clusters(kw_gather<T, D>, a, keys, columns, sms, tile_smem<D>(), st) : e;
+    e = launch_clusters(kw_stats<D>, a, columns, keys, sms, tile_smem<D>(), st);
+    return e == cudaSuccess ? launch_clusters(kw_gather<D>, a, keys, columns, sms, tile_smem<D>(), st) : e;
 }
 
 }  // namespace
@@ -730,7 +719,7 @@ cudaError_t launch_key_weights(const KeyWeightsCall& c, cudaStream_t st) {
         return c.dtype == PA_F16 ? launch_few_of<__half>(a, c.D, c.n_ctas, st)
                                  : launch_few_of<__nv_bfloat16>(a, c.D, c.n_ctas, st);
     }
-    if (c.dtype == PA_F32) return c.D == 64 ? launch_tiles<float, 64>(a, c.n_ctas, st) : launch_tiles<float, 128>(a, c.n_ctas, st);
+    if (c.dtype == PA_F32) return c.D == 64 ? launch_tiles<64>(a, c.n_ctas, st) : launch_tiles<128>(a, c.n_ctas, st);
     return launch_key_weights_tc(a, c.dtype, c.D, c.n_ctas, static_cast<char*>(c.workspace) + stats_bytes(c), st);
 }
 

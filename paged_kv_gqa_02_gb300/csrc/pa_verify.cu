@@ -34,6 +34,7 @@
 // writes.  A second kernel joins the sequences' lists.
 #include <cooperative_groups.h>
 
+#include "pa_cp_async.cuh"
 #include "pa_device.h"
 #include "pa_pairs.cuh"
 #include "pa_ptx.cuh"
@@ -86,21 +87,12 @@ struct Run {
 // Whether p lies on a 16-byte boundary.
 template <typename T> __device__ inline bool wide_at(const T* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-__device__ inline void cp_async16(uint32_t to, const void* from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
-__device__ inline void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ inline void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 // Shared memory for a CTA's part of two rows and their drafts', and of the
 // random numbers where they fit beside them: units of eight elements, in order.
 // Units beyond the room come to the slots of units that are done with.
 constexpr size_t kRoom = 203648;  // with what is laid out by the compiler, all that a CTA may have
 template <typename T> constexpr int kParts = 8 / Elt<T>::kVec;  // 16-byte parts of a unit
 
-__device__ inline void cp_async4(uint32_t to, const void* from) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
-}
 // A whole number of 16 bytes between 16-byte boundaries, counted by the mbarrier.
 __device__ inline void copy_bulk(void* to, const void* from, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
