@@ -346,7 +346,7 @@ pa_status pa_prefill_chunk(const pa_params *p, const void *q, const int32_t *cu_
 int32_t pa_version(void);
 
 /* How this library was built: PA_BUILD_CHECKED when PA_CHECKED was defined
- * (kernels range-check their computed global indices; see PA_DEV_OOB). */
+ * (decode and prefill kernels range-check their computed global indices; see PA_DEV_OOB). */
 #define PA_BUILD_CHECKED 1
 int32_t pa_build_flags(void);
 

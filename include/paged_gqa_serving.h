@@ -22,7 +22,8 @@
  * store the rows itself); then, per token or per drafted tree, pa_decode /
  * pa_tree, pa_verify, and pa_store of what was accepted.  A cache with a
  * budget calls pa_key_weights after the store and, when it is full, pa_evict
- * per layer and pa_pages_resize once.
+ * per layer and pa_pages_resize once; from then on a sequence's length is not its
+ * next position, and pa_rotate has to be given positions.
  * pa_pages_resize and pa_pages_compact change only the bookkeeping, once
  * per step; the (source, destination) pairs that they report go to
  * pa_pages_copy once per layer, before anything else touches the pages.
@@ -240,7 +241,9 @@ pa_rope *pa_rope_init(pa_rope *t);
  *   q_weight, k_weight: [D] in q_dtype, 16-byte aligned, either may be NULL
  *   table: [table_rows][rotary_dim] f32, cosines and sines of the angles, 16-byte aligned
  *   positions: [axes][total_rows] int32; NULL: the row's place in its sequence,
- *     context_lens[s] - n_s + t, on every axis
+ *     context_lens[s] - n_s + t, on every axis.  After an eviction that is less than
+ *     the tokens there have been: pass the positions, the rows are stored by
+ *     context_lens all the same
  *   q_out, k_out: may be q and k themselves, with the same stride; no other overlap
  * context_lens may be NULL with positions and no cache; v, v_cache and
  * block_tables without a cache.  k_out and k_cache may not both be NULL.
@@ -333,8 +336,14 @@ pa_status pa_verify(const pa_params *p, const pa_rows *r, int32_t vocab, const v
  * (PA_ERR_UNSUPPORTED).
  * workspace: pa_key_weights_workspace_size bytes, 256-byte aligned (0: invalid).
  * max_rows G up to 32 (decoding): the scores, num_seqs x num_kv_heads x
- * longest context x max_rows G floats, and 3 % more, so a tight max_context_len
- * pays.  Beyond: 8 bytes for each row and q head, and 1 MB at most.
+ * longest context x max_rows G floats (max_rows G rounded up to even), and a pair of
+ * floats for each of these columns and each 64 keys of the longest context and two
+ * more (3 % of the scores in long contexts, a quarter at 16 keys), so a tight
+ * max_context_len pays: it counts for every sequence.  Beyond: 8 bytes for each row
+ * and q head, and 1 MB at most.
+ * Which of the two a call is goes by max_rows for the whole call: a few rows more of
+ * one sequence cost the single tokens beside it twice their time, in a call of their
+ * own they would not.
  * It carries nothing from one call to the next. */
 size_t pa_key_weights_workspace_size(const pa_params *p, const pa_rows *r);
 
@@ -359,6 +368,8 @@ pa_status pa_key_weights(const pa_params *p, const pa_rows *r, const void *q, co
  * keep_lens or context_lens (PA_ERR_SHAPE).
  * context_lens and the tables stay as they are: after the last layer,
  * pa_pages_resize with new_lens trims every sequence and frees its pages.
+ * Kept keys have the positions that they were turned at; the caller counts on from
+ * the tokens there have been (positions of pa_rotate).
  * refcounts ([num_pages], may be NULL): a sequence of which a page from slot f
  * to slot n - 1 has more than one holder is not evicted (PA_DEV_SHARED_PAGE).
  * Without them no such page may belong to two sequences; nor may a page stand

@@ -3,9 +3,11 @@
 Each ``csrc/*.cu`` translation unit is compiled in parallel, then linked
 into one shared library with the CUDA runtime linked statically and only the
 ``pa_*`` entry points exported.  ``build(checked=True)`` builds the same
-sources with PA_CHECKED defined into libpaged_gqa_checked.so: every kernel
-range-checks its computed global indices and reports a violation through
-PA_DEV_OOB instead of making the access.
+sources with PA_CHECKED defined into libpaged_gqa_checked.so: the kernels of
+paged_gqa.h's entry points (decode, prefill) range-check their computed global
+indices and report a violation through PA_DEV_OOB instead of making the access.
+Those of paged_gqa_serving.h check the lengths, row ends, table entries and
+indices that they are given in every build, and are the same in both.
 """
 from __future__ import annotations
 

@@ -6,7 +6,9 @@
 // bits find the key of the last one that stays, from histograms in shared memory (the
 // cluster's added up), and how many of its equals stay with it.  Then ballots
 // number the keys that stay, in order; they leave where they came from and what
-// they weigh.  The passes are bound by latency: no weight is read twice.
+// they weigh, which is read again.  The passes themselves read what registers hold,
+// and again from memory what is beyond them (tables of more than 131,072 slots); they
+// are bound by latency.
 //
 // Move: key j comes from slot kept[j] >= j, so a cluster of CTAs that has the
 // keys of one kv head, of K or of V, can work its way up tile by tile, reading a

@@ -6,9 +6,11 @@
 // A column's largest score m and sum l are needed before any of its weights,
 // so there are two passes over the scores.
 //
-// Few columns (decoding): K is read once.  The first kernel leaves the scores,
-// which are much smaller than K, and each part's largest scores and sums in
-// the workspace; the second joins the parts' and turns scores into weights.
+// Few columns (decoding): K is read once.  The first kernel leaves the scores, and
+// each part's largest scores and sums, in the workspace; the second joins the parts'
+// and turns scores into weights.  A key's scores are 4 bytes a column out and 4 back:
+// with 16-bit types and head_dim 128 a quarter of its K at 8 columns, as much at 32;
+// at head_dim 64 twice that share.
 // Many columns: the second pass computes the scores again.  The border lies at 32
 // columns of a kv head (16 bits, 8 heads of 128; few columns against the tensor cores):
 //   8 sequences of 16000: 8 columns 60 against 125 us, 16 78, 32 141

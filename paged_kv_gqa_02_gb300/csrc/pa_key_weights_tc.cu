@@ -14,9 +14,11 @@
 // accumulators of 128 columns of tensor memory, one a group): while one CTA
 // begins or ends a unit, the other computes, and four warps to a scheduler hide
 // one another's latencies (one group: 58 and 69 us for the passes of four prompts
-// of 2560 rows and less).  Exponentials bound the
-// kernel: a score takes a multiply-add, an exponential and an addition in each
-// pass, and 128 x 128 of them take longer than their product.  A column's m and l
+// of 2560 rows and less).  A score takes a multiply-add, an exponential and an
+// addition in each pass, and 128 x 128 of them take longer than their product; yet no
+// pipe is saturated (special functions 42% and 32% busy, an SM's throughput 52% and
+// 42%): a warp waits for each chunk's load from tensor memory before it begins with
+// the chunk, so that latency and the order of a warp's own steps bound it.  A column's m and l
 // go into one number, m + log2 l, which all lanes read from shared memory: with
 // two, 16 bytes for two scores, those reads bounded the second pass (92 us against
 // the first's 59, four prompts of 2560 rows and less).  Its rounding, 2^-18 where m
@@ -32,8 +34,8 @@
 // division.  A unit inside one share is finished there; the pieces of others
 // are joined in ascending order by a kernel of its own.
 //
-// Four prompts of 2560, 130, 1999 and 37 rows, 32/8 heads of 128, bf16: 114 us, 52
-// for the statistics and 66 for the gathering when each runs by itself; 43.3 GFLOP of
+// Four prompts of 2560, 130, 1999 and 37 rows, 32/8 heads of 128, bf16: 117 us, 53
+// for the statistics and 67 for the gathering when each runs by itself; 43.3 GFLOP of
 // products twice over are 46 us at the measured rate of a large bf16 product.
 #include <type_traits>
 

@@ -10,7 +10,7 @@
 // needs no exchange, and a call may write over its input.  Only the norm's sum
 // crosses the D / 16 lanes of a head.  Heads go in groups as wide as a warp, q's
 // first, then k's and v's; the next groups' loads are in flight while a group is
-// turned, in paired fp32 arithmetic (without these two 87 us where it is 66 now).
+// turned, in paired fp32 arithmetic (without these two 87 us where it was then 66).
 // Each number is rounded once, to the output's type.
 //
 // Bound by HBM: four documents of 8192 rows, 64/8 heads of 128, bf16, with store,

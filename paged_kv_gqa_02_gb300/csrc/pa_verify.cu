@@ -20,7 +20,7 @@
 //
 // The walk's time is a chain of passes, each bound by latency: the exponentials
 // of a row and one exchange, some 5 us together (64 chains of five drafts, 50021
-// fp16 tokens: 7 passes, 38 us; one chain of four, 32000 fp32 tokens: 11 us; 16 trees
+// fp16 tokens: 7 passes, 39 us; one chain of four, 32000 fp32 tokens: 11 us; 16 trees
 // of up to 63, 131072 bf16 tokens: 35 to 43 us).  One CTA a sequence
 // that read rows from L2 took 232, 24 and 145 us.  The bytes, 24 MB for the chains,
 // would take 4 us.  A CTA has a run of the vocabulary, and its part of
